@@ -654,6 +654,59 @@ gg_status gg_moe_mlp_bwd_mx(const gg_bf16* dOut, const gg_bf16* x, const float* 
                             int pad_multiple, const gg_moe_options* opt, gg_bf16* dX,
                             float* dprob, const gg_mx_buffers* buf, gg_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * gg_route — the router in front of the layer: from the logits x[T][E] of the
+ * router's own linear layer to the (idx, prob) that every call above takes.
+ *   idx[t][j]   int32, the k experts with the largest logits of the row,
+ *               largest first, equal logits in ascending expert order (NaN
+ *               counts as larger than everything, both zeros as equal);
+ *   prob[t][j]  fp32, scale * w with w the expert's score s_e, s = softmax of
+ *               the whole row (GG_SCORE_SOFTMAX) or sigmoid(x_e)
+ *               (GG_SCORE_SIGMOID); with renormalize != 0, w = s_e / the sum
+ *               of the k picked scores.
+ * An expert is switched off for a row by the logit -inf: its score is 0. A
+ * row of nothing but -inf gets idx 0..k-1 and prob 0. A NaN or +inf makes
+ * the row's probabilities NaN where the formula does; its idx stay k
+ * different experts.
+ * Statistics of the batch, either pointer may be NULL:
+ *   counts[E]   int32, how often each expert was picked;
+ *   losses[2]   fp32: losses[0] = E * sum_e f_e * P_e, the balance loss, with
+ *               f_e = counts[e] / (T k) and P_e the mean over the tokens of
+ *               s_e / sum_e' s_e'; losses[1] = the mean of logsumexp(x_t)^2.
+ *               Rows of nothing but -inf add 0 to both.
+ * Sums are taken in fp32 in an order that depends on the sizes alone: results
+ * are bitwise repeatable. 1 <= k <= 32, k <= E <= 1024; logits fp32 or BF16
+ * (a gg_dtype) at their type's alignment. T = 0 writes zero counts and losses.
+ * Workspace: gg_route_workspace_size(T, E) bytes when counts or losses is not
+ * NULL, else ws may be NULL.
+ *
+ * gg_route_bwd — gradient of a loss L with respect to the logits, given
+ * dprob = dL/dprob[T][k] of the probabilities gg_route wrote, for
+ *   L + aux_coef * losses[0] + z_coef * losses[1]:
+ * dlogits[T][E] in the logits' type, accumulated in fp32 and rounded once.
+ * The picks and the counts are constants of the differentiation. score,
+ * renormalize and scale as in the forward; counts is read when aux_coef is
+ * not 0. dlogits may be the logits' own buffer. An idx outside [0, E) adds
+ * nothing and sets GG_ERR_DEVICE_BAD_EXPERT_ID in the status word of ws
+ * (ws may be NULL: then it is only skipped).
+ * ------------------------------------------------------------------------- */
+typedef enum gg_dtype {
+  GG_DTYPE_F32 = 0,
+  GG_DTYPE_BF16 = 1
+} gg_dtype;
+typedef enum gg_score {
+  GG_SCORE_SOFTMAX = 0,
+  GG_SCORE_SIGMOID = 1
+} gg_score;
+size_t gg_route_workspace_size(int T, int E);
+gg_status gg_route(const void* logits, int dtype, int T, int E, int k, int score,
+                   int renormalize, float scale, int32_t* idx, float* prob, int32_t* counts,
+                   float* losses, void* ws, size_t ws_bytes, gg_stream_t stream);
+gg_status gg_route_bwd(const void* logits, int dtype, int T, int E, int k, int score,
+                       int renormalize, float scale, const int32_t* idx, const float* dprob,
+                       const int32_t* counts, float aux_coef, float z_coef, void* dlogits,
+                       void* ws, size_t ws_bytes, gg_stream_t stream);
+
 /* Test hook for the bounded waits: one CTA waits on a barrier that nothing
  * completes, gives up after `limit_ns` nanoseconds (clamped to 1 s), writes
  * GG_ERR_DEVICE_TIMEOUT into the status word and returns normally. */

@@ -32,6 +32,10 @@ struct DevCache {
 };
 DevCache g_dev[kMaxDevices];
 
+inline bool aligned_to(const void* p, size_t n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline gg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GG_OK : GG_ERR_CUDA; }
@@ -996,6 +1000,85 @@ gg_status gg_moe_mlp_bwd_mx(const gg_bf16* dOut, const gg_bf16* x, const float* 
   return gg_unpermute_combine(buf->dXp, buf->row_of_slot, nullptr, T, k, H, R_cap, dX, rowdot,
                               gg_mx_rowdot_blocks(F), nullptr, dprob, buf->ws, buf->ws_bytes,
                               stream);
+}
+
+static gg_status route_checks(const void* logits, int dtype, int T, int E, int k, int score) {
+  if (T < 0 || E <= 0 || k <= 0 || k > 32 || k > E) return GG_ERR_INVALID_ARG;
+  if (dtype != GG_DTYPE_F32 && dtype != GG_DTYPE_BF16) return GG_ERR_INVALID_ARG;
+  if (score != GG_SCORE_SOFTMAX && score != GG_SCORE_SIGMOID) return GG_ERR_INVALID_ARG;
+  if (E > kMaxExperts) return GG_ERR_UNSUPPORTED_SHAPE;
+  if (T > 0 && logits == nullptr) return GG_ERR_INVALID_ARG;
+  return aligned_to(logits, dtype == GG_DTYPE_F32 ? 4 : 2) ? GG_OK : GG_ERR_MISALIGNED;
+}
+
+size_t gg_route_workspace_size(int T, int E) {
+  if (T < 0 || E <= 0) return 0;
+  const size_t words = static_cast<size_t>(route_blocks(T)) * (2 * static_cast<size_t>(E) + 1);
+  return kWsHeader + align256(words * sizeof(float));
+}
+
+gg_status gg_route(const void* logits, int dtype, int T, int E, int k, int score, int renormalize,
+                   float scale, int32_t* idx, float* prob, int32_t* counts, float* losses,
+                   void* ws, size_t ws_bytes, gg_stream_t stream) {
+  gg_status s = route_checks(logits, dtype, T, E, k, score);
+  if (s != GG_OK) return s;
+  if (T > 0 && (idx == nullptr || prob == nullptr)) return GG_ERR_INVALID_ARG;
+  if (!aligned_to(idx, 4) || !aligned_to(prob, 4) || !aligned_to(counts, 4) ||
+      !aligned_to(losses, 4))
+    return GG_ERR_MISALIGNED;
+  const bool stats = counts != nullptr || losses != nullptr;
+  if (stats && (s = check_ws(ws, ws_bytes, gg_route_workspace_size(T, E))) != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  RouteArgs a{};
+  a.logits = logits;
+  a.bf16 = dtype == GG_DTYPE_BF16;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.sigmoid = score == GG_SCORE_SIGMOID;
+  a.renorm = renormalize != 0;
+  a.scale = scale;
+  a.idx = idx;
+  a.prob = prob;
+  a.counts = counts;
+  a.losses = losses;
+  a.scratch = stats ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsHeader) : nullptr;
+  return from_cuda(launch_route(a, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gg_status gg_route_bwd(const void* logits, int dtype, int T, int E, int k, int score,
+                       int renormalize, float scale, const int32_t* idx, const float* dprob,
+                       const int32_t* counts, float aux_coef, float z_coef, void* dlogits,
+                       void* ws, size_t ws_bytes, gg_stream_t stream) {
+  gg_status s = route_checks(logits, dtype, T, E, k, score);
+  if (s != GG_OK) return s;
+  if (T > 0 && (idx == nullptr || dprob == nullptr || dlogits == nullptr))
+    return GG_ERR_INVALID_ARG;
+  if (aux_coef != 0.0f && counts == nullptr) return GG_ERR_INVALID_ARG;
+  if (!aligned_to(idx, 4) || !aligned_to(dprob, 4) || !aligned_to(counts, 4) ||
+      !aligned_to(dlogits, dtype == GG_DTYPE_F32 ? 4 : 2))
+    return GG_ERR_MISALIGNED;
+  if (ws != nullptr && (s = check_ws(ws, ws_bytes, kWsHeader)) != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  RouteBwdArgs a{};
+  a.logits = logits;
+  a.bf16 = dtype == GG_DTYPE_BF16;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.sigmoid = score == GG_SCORE_SIGMOID;
+  a.renorm = renormalize != 0;
+  a.scale = scale;
+  a.idx = idx;
+  a.dprob = dprob;
+  a.counts = counts;
+  a.aux = aux_coef;
+  a.z = z_coef;
+  a.dlogits = dlogits;
+  a.status = ws != nullptr ? status_ptr(ws) : nullptr;
+  return from_cuda(launch_route_bwd(a, dev, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 gg_status gg_selftest_bounded_wait(void* ws, size_t ws_bytes, uint64_t limit_ns,

@@ -202,6 +202,41 @@ cudaError_t launch_mx_prepare_weight(const gg_bf16* W, int E, int N, int K, bool
                                      int gated_F, int NT, uint8_t* Wq, uint8_t* S,
                                      cudaStream_t stream);
 
+// ------------------------------------------------------------------ gg_route.cu
+// Blocks that accumulate the router's batch statistics (two per SM of a
+// 152-SM device): rows of the scratch below.
+constexpr int kRouteMaxBlocks = 304;
+int route_blocks(long long T);
+
+struct RouteArgs {
+  const void* logits;  // [T][E] fp32 or BF16
+  bool bf16;
+  int T, E, k;
+  bool sigmoid, renorm;
+  float scale;
+  int32_t* idx;        // [T][k]
+  float* prob;         // [T][k]
+  int32_t* counts;     // [E] or null
+  float* losses;       // [2] or null
+  float* scratch;      // with counts or losses: route_blocks(T) x (2 E + 1) words
+};
+cudaError_t launch_route(const RouteArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
+struct RouteBwdArgs {
+  const void* logits;
+  bool bf16;
+  int T, E, k;
+  bool sigmoid, renorm;
+  float scale;
+  const int32_t* idx;
+  const float* dprob;
+  const int32_t* counts;  // read when aux is not 0
+  float aux, z;
+  void* dlogits;          // [T][E], the logits' type
+  int32_t* status;        // or null
+};
+cudaError_t launch_route_bwd(const RouteBwdArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
 // alpha of the gated activation of a gg_epilogue (1 for SwiGLU, 1.702 for
 // QuickGeGLU), 0 for epilogues without one.
 inline float glu_alpha(gg_epilogue epi) {

@@ -33,6 +33,7 @@ STATUS_NAMES = {
 
 # (name, restype, argtypes) of every exported symbol in include/gg.h
 _P, _I, _Z, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
+_F = ctypes.c_float
 SIGNATURES = [
     ("gg_status_string", ctypes.c_char_p, [_I]),
     ("gg_version", ctypes.c_char_p, []),
@@ -77,7 +78,15 @@ SIGNATURES = [
     ("gg_mx_buffers_bind", _I, [_P, _Z, _I, _I, _I, _I, _I, _I, _P]),
     ("gg_moe_mlp_fwd_mx", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
     ("gg_moe_mlp_bwd_mx", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    ("gg_route_workspace_size", _Z, [_I, _I]),
+    ("gg_route", _I, [_P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _Z, _P]),
+    ("gg_route_bwd", _I,
+     [_P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _F, _F, _P, _P, _Z, _P]),
 ]
+
+GG_DTYPE_F32, GG_DTYPE_BF16 = 0, 1
+GG_SCORE_SOFTMAX, GG_SCORE_SIGMOID = 0, 1
+_DTYPES = {torch.float32: GG_DTYPE_F32, torch.bfloat16: GG_DTYPE_BF16}
 
 GG_MX_FC1, GG_MX_FC2, GG_MX_DGRAD_FC2, GG_MX_DGRAD_FC1 = 0, 1, 2, 3
 
@@ -716,3 +725,78 @@ class MxMoeLayer:
 
     def status(self) -> int:
         return read_status(self.view("ws"))
+
+
+# ---------------------------------------------------------------- router
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return code
+
+
+def route_workspace(T: int, E: int, device) -> torch.Tensor:
+    """A zeroed workspace (status word first) for route calls on up to T tokens."""
+    return torch.zeros(int(LIB.gg_route_workspace_size(T, E)), dtype=torch.uint8, device=device)
+
+
+def route(logits, k: int, score: int = GG_SCORE_SOFTMAX, renormalize: bool = False,
+          scale: float = 1.0, idx=None, prob=None, counts=None, losses=None, ws=None):
+    """gg_route: the k largest of each row of logits [T, E] (fp32 or BF16) and their
+    probabilities. counts ([E] int32) and losses ([2] fp32: balance, z) are written when
+    a tensor, or True to allocate one, is passed; they need ws (route_workspace), which is
+    allocated when not passed. Returns dict(idx, prob, counts, losses)."""
+    T, E = logits.shape
+    dev = logits.device
+    dtype = _dtype(logits, "logits")
+    if idx is None:
+        idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    else:
+        _need(idx, torch.int32, (T, k), "idx")
+    if prob is None:
+        prob = torch.empty((T, k), dtype=torch.float32, device=dev)
+    else:
+        _need(prob, torch.float32, (T, k), "prob")
+    counts = None if counts is False else counts
+    losses = None if losses is False else losses
+    if counts is True:
+        counts = torch.empty((E,), dtype=torch.int32, device=dev)
+    elif counts is not None:
+        _need(counts, torch.int32, (E,), "counts")
+    if losses is True:
+        losses = torch.empty((2,), dtype=torch.float32, device=dev)
+    elif losses is not None:
+        _need(losses, torch.float32, (2,), "losses")
+    if ws is None and not (counts is None and losses is None):
+        ws = route_workspace(T, E, dev)
+    _check(LIB.gg_route(_ptr(logits), dtype, T, E, k, score, 1 if renormalize else 0, scale,
+                        _ptr(idx), _ptr(prob), _ptr(counts), _ptr(losses), _ptr(ws),
+                        0 if ws is None else ws.numel(), _stream(dev)),
+           "gg_route")
+    return dict(idx=idx, prob=prob, counts=counts, losses=losses)
+
+
+def route_bwd(logits, idx, dprob, score: int = GG_SCORE_SOFTMAX, renormalize: bool = False,
+              scale: float = 1.0, counts=None, aux_coef: float = 0.0, z_coef: float = 0.0,
+              dlogits=None, ws=None):
+    """gg_route_bwd: the gradient of the logits from dprob [T, k] and the coefficients of
+    the balance and z losses (the balance loss needs the forward's counts). With ws, an
+    idx outside [0, E) is reported in its status word."""
+    T, E = logits.shape
+    k = idx.shape[1]
+    dtype = _dtype(logits, "logits")
+    _need(idx, torch.int32, (T, k), "idx")
+    _need(dprob, torch.float32, (T, k), "dprob")
+    if counts is not None:
+        _need(counts, torch.int32, (E,), "counts")
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    else:
+        _need(dlogits, logits.dtype, (T, E), "dlogits")
+    _check(LIB.gg_route_bwd(_ptr(logits), dtype, T, E, k, score, 1 if renormalize else 0, scale,
+                            _ptr(idx), _ptr(dprob), _ptr(counts), aux_coef, z_coef,
+                            _ptr(dlogits), _ptr(ws), 0 if ws is None else ws.numel(),
+                            _stream(logits.device)),
+           "gg_route_bwd")
+    return dlogits
