@@ -707,6 +707,33 @@ gg_status gg_route_bwd(const void* logits, int dtype, int T, int E, int k, int s
                        const int32_t* counts, float aux_coef, float z_coef, void* dlogits,
                        void* ws, size_t ws_bytes, gg_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * gg_grouped_wgrad — weight gradient of gg_grouped_fwd, for layers whose
+ * expert weights are trained: one launch over all experts, each reducing over
+ * its own rows,
+ *   dB[e][n][c] = (base[e][n][c] +) sum_{offsets[e] <= r < offsets[e+1]}
+ *                                       dC[r][n] * A[r][c]
+ * with fp32 sums. dC[R_cap][N], A[R_cap][K] BF16 in the permuted row order;
+ * dB[E][N][K] and base (nullable: zero) in out_dtype, a gg_dtype: BF16 is
+ * rounded once, after the base is added; fp32 is not rounded further. base may
+ * be dB itself (accumulating in place).
+ * An expert without rows gets its base, or zeros. Rows outside
+ * [0, offsets[E]) are never read into a result, whatever they hold; padding
+ * rows below offsets[E] are read and must hold zeros in dC or A and finite
+ * values in the other (the permute and the GEMMs leave zeros).
+ * Where a probability p weighted the expert's output at the combine, dW2 =
+ * dOut_rows^T (p * A): pass gg_glu(..., prob_of_row) as A.
+ * K and N multiples of 64, E <= 1024, pointers 16-byte aligned. Offsets that
+ * are not monotone, do not start at 0 or end past R_cap set
+ * GG_ERR_DEVICE_BAD_OFFSETS and nothing is written. Results are bitwise
+ * repeatable for the same offsets. Workspace:
+ * gg_wgrad_workspace_size(E, R_cap, N, K) bytes.
+ * ------------------------------------------------------------------------- */
+size_t gg_wgrad_workspace_size(int E, int R_cap, int N, int K);
+gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* offsets, int E,
+                           int R_cap, int N, int K, int out_dtype, const void* base, void* dB,
+                           void* ws, size_t ws_bytes, gg_stream_t stream);
+
 /* Test hook for the bounded waits: one CTA waits on a barrier that nothing
  * completes, gives up after `limit_ns` nanoseconds (clamped to 1 s), writes
  * GG_ERR_DEVICE_TIMEOUT into the status word and returns normally. */

@@ -1002,6 +1002,44 @@ gg_status gg_moe_mlp_bwd_mx(const gg_bf16* dOut, const gg_bf16* x, const float* 
                               stream);
 }
 
+size_t gg_wgrad_workspace_size(int E, int R_cap, int N, int K) {
+  if (E <= 0 || R_cap < 0 || N <= 0 || K <= 0) return 0;
+  return kWsHeader;
+}
+
+gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* offsets, int E,
+                           int R_cap, int N, int K, int out_dtype, const void* base, void* dB,
+                           void* ws, size_t ws_bytes, gg_stream_t stream) {
+  if (E <= 0 || R_cap < 0 || N <= 0 || K <= 0) return GG_ERR_INVALID_ARG;
+  if (out_dtype != GG_DTYPE_F32 && out_dtype != GG_DTYPE_BF16) return GG_ERR_INVALID_ARG;
+  if (offsets == nullptr || dB == nullptr) return GG_ERR_INVALID_ARG;
+  if (R_cap > 0 && (dC == nullptr || A == nullptr)) return GG_ERR_INVALID_ARG;
+  if (E > kMaxExperts || N % 64 != 0 || K % 64 != 0) return GG_ERR_UNSUPPORTED_SHAPE;
+  // work items are counted in an int
+  if (static_cast<long long>(E) * ((N + 255) / 256) * ((K + 255) / 256) > 0x3FFFFFFFLL)
+    return GG_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(dC) || !aligned16(A) || !aligned16(base) || !aligned16(dB))
+    return GG_ERR_MISALIGNED;
+  gg_status s = check_ws(ws, ws_bytes, gg_wgrad_workspace_size(E, R_cap, N, K));
+  if (s != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  WgradArgs a{};
+  // without rows nothing is loaded: any aligned address will do for the maps
+  a.dC = R_cap > 0 ? dC : static_cast<const gg_bf16*>(dB);
+  a.A = R_cap > 0 ? A : static_cast<const gg_bf16*>(dB);
+  a.offsets = offsets;
+  a.E = E;
+  a.R_cap = R_cap;
+  a.N = N;
+  a.K = K;
+  a.f32 = out_dtype == GG_DTYPE_F32;
+  a.base = base;
+  a.dB = dB;
+  a.status = status_ptr(ws);
+  return from_cuda(launch_wgrad(a, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 static gg_status route_checks(const void* logits, int dtype, int T, int E, int k, int score) {
   if (T < 0 || E <= 0 || k <= 0 || k > 32 || k > E) return GG_ERR_INVALID_ARG;
   if (dtype != GG_DTYPE_F32 && dtype != GG_DTYPE_BF16) return GG_ERR_INVALID_ARG;

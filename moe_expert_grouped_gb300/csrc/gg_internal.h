@@ -202,6 +202,19 @@ cudaError_t launch_mx_prepare_weight(const gg_bf16* W, int E, int N, int K, bool
                                      int gated_F, int NT, uint8_t* Wq, uint8_t* S,
                                      cudaStream_t stream);
 
+// ------------------------------------------------------------------ gg_wgrad.cu
+struct WgradArgs {
+  const gg_bf16* dC;  // [R_cap][N]
+  const gg_bf16* A;   // [R_cap][K]
+  const int32_t* offsets;
+  int E, R_cap, N, K;
+  bool f32;           // type of base and dB
+  const void* base;   // [E][N][K] or null
+  void* dB;           // [E][N][K]
+  int32_t* status;
+};
+cudaError_t launch_wgrad(const WgradArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
 // ------------------------------------------------------------------ gg_route.cu
 // Blocks that accumulate the router's batch statistics (two per SM of a
 // 152-SM device): rows of the scratch below.

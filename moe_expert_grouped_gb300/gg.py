@@ -78,6 +78,8 @@ SIGNATURES = [
     ("gg_mx_buffers_bind", _I, [_P, _Z, _I, _I, _I, _I, _I, _I, _P]),
     ("gg_moe_mlp_fwd_mx", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
     ("gg_moe_mlp_bwd_mx", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    ("gg_wgrad_workspace_size", _Z, [_I, _I, _I, _I]),
+    ("gg_grouped_wgrad", _I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
     ("gg_route_workspace_size", _Z, [_I, _I]),
     ("gg_route", _I, [_P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _Z, _P]),
     ("gg_route_bwd", _I,
@@ -727,13 +729,46 @@ class MxMoeLayer:
         return read_status(self.view("ws"))
 
 
-# ---------------------------------------------------------------- router
-
 def _dtype(t: torch.Tensor, name: str) -> int:
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
     return code
+
+
+# ---------------------------------------------------------------- weight gradient
+
+def wgrad_workspace(E: int, R_cap: int, N: int, K: int, device) -> torch.Tensor:
+    """A zeroed workspace (status word first) for grouped_wgrad calls of these sizes."""
+    n = int(LIB.gg_wgrad_workspace_size(E, R_cap, N, K))
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def grouped_wgrad(dC, A, offsets, base=None, dB=None, out_dtype=torch.bfloat16, ws=None):
+    """gg_grouped_wgrad: dB [E, N, K] = (base +) dC_e^T A_e over each expert's rows of
+    dC [R_cap, N] and A [R_cap, K]. dB and base are BF16 or fp32 (dB's type, else base's,
+    else out_dtype); dB may be base itself, to accumulate in place."""
+    R_cap, N = dC.shape
+    K = A.shape[1]
+    E = offsets.numel() - 1
+    _need(dC, torch.bfloat16, (R_cap, N), "dC")
+    _need(A, torch.bfloat16, (R_cap, K), "A")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    if dB is None:
+        dB = torch.empty((E, N, K), dtype=out_dtype if base is None else base.dtype,
+                         device=dC.device)
+    dtype = _dtype(dB, "dB")
+    _need(dB, dB.dtype, (E, N, K), "dB")
+    if base is not None:
+        _need(base, dB.dtype, (E, N, K), "base")
+    ws = wgrad_workspace(E, R_cap, N, K, dC.device) if ws is None else ws
+    _check(LIB.gg_grouped_wgrad(_ptr(dC), _ptr(A), _ptr(offsets), E, R_cap, N, K, dtype,
+                                _ptr(base), _ptr(dB), _ptr(ws), ws.numel(), _stream(dC.device)),
+           "gg_grouped_wgrad")
+    return dB
+
+
+# ---------------------------------------------------------------- router
 
 
 def route_workspace(T: int, E: int, device) -> torch.Tensor:
