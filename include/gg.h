@@ -734,6 +734,58 @@ gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* o
                            int R_cap, int N, int K, int out_dtype, const void* base, void* dB,
                            void* ws, size_t ws_bytes, gg_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit integer expert weights, for serving: grouped linear layers on integers
+ * with one fp32 scale per row of the activations (token) and per row of the
+ * weight (output channel). A row x of either is held as
+ *   a = max(max_c |x_c|, 2^-100), q_c = rint(x_c * (127 / a)) (int8), s = a / 127
+ * in fp32 (ties to even). A row with a NaN or an infinity gets the codes 0
+ * and the scale NaN: its products are NaN.
+ *
+ * gg_q8_prepare_weight — codes Wq[E][N][K] and scales Ws[E][N] of a BF16 weight
+ * W[E][N][K], once per weight set. Codes made elsewhere are accepted too, any
+ * int8 and any fp32 scale.
+ *
+ * gg_q8_quantize_rows — codes Q and scales S of src[T][K] (BF16). With
+ * row_of_slot (from gg_permute) the codes of token t are written to its k rows
+ * of Q[R_cap][K], S[R_cap] (-1: no row; an entry outside [-1, R_cap) is
+ * skipped and sets GG_ERR_DEVICE_BAD_ROW); with row_of_slot NULL row t goes to
+ * row t (k is ignored, T <= R_cap).
+ *
+ * gg_q8_grouped_gemm — for every expert e and row r in [offsets[e],
+ * offsets[e+1]) of Aq[R_cap][K], As[R_cap]:
+ *   v[r][n] = As[r] * Ws[e][n] * sum_c Aq[r][c] * Wq[e][n][c]
+ * the sum exact below 2^24 and in fp32 above, v in fp32:
+ *   GG_EPI_NONE:   C[R_cap][N] = bf16(v)
+ *   GG_EPI_SWIGLU, GG_EPI_QGEGLU: N = 2F, C[R_cap][F] = bf16(act(v[:, :F]) *
+ *                  v[:, F:] [* prob_of_row[r]]): no rounding before the last.
+ * Other arguments, refusals and device errors as gg_grouped_fwd; rows outside
+ * [0, offsets[E]) are never written. Results of a row do not depend on the
+ * other rows of the batch beyond the choice of kernel, which goes by R_cap, E,
+ * K and N.
+ *
+ * gg_q8_grouped_fwd — quantise the rows of A[R_cap][K] (BF16, permuted order)
+ * and multiply, in one call; the codes stay in ws, gg_q8_workspace_size(R_cap,
+ * K) bytes. The other two need the 256-byte header of ws.
+ *
+ * K and N multiples of 64 (gated: N of 128), E <= 1024, matrices and Ws
+ * 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+size_t gg_q8_workspace_size(int R_cap, int K);
+gg_status gg_q8_prepare_weight(const gg_bf16* W, int E, int N, int K, int8_t* Wq, float* Ws,
+                               gg_stream_t stream);
+gg_status gg_q8_quantize_rows(const gg_bf16* src, int T, int K, const int32_t* row_of_slot, int k,
+                              int R_cap, int8_t* Q, float* S, void* ws, size_t ws_bytes,
+                              gg_stream_t stream);
+gg_status gg_q8_grouped_gemm(const int8_t* Aq, const float* As, const int8_t* Wq, const float* Ws,
+                             const int32_t* offsets, int E, int R_cap, int K, int N,
+                             gg_epilogue epi, const float* prob_of_row, gg_bf16* C, void* ws,
+                             size_t ws_bytes, gg_stream_t stream);
+gg_status gg_q8_grouped_fwd(const gg_bf16* A, const int8_t* Wq, const float* Ws,
+                            const int32_t* offsets, int E, int R_cap, int K, int N,
+                            gg_epilogue epi, const float* prob_of_row, gg_bf16* C, void* ws,
+                            size_t ws_bytes, gg_stream_t stream);
+
 /* Test hook for the bounded waits: one CTA waits on a barrier that nothing
  * completes, gives up after `limit_ns` nanoseconds (clamped to 1 s), writes
  * GG_ERR_DEVICE_TIMEOUT into the status word and returns normally. */

@@ -1040,6 +1040,122 @@ gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* o
   return from_cuda(launch_wgrad(a, dev, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t gg_q8_workspace_size(int R_cap, int K) {
+  if (R_cap < 0 || K <= 0) return 0;
+  return kWsHeader + align256(sizeof(float) * static_cast<size_t>(R_cap)) +
+         align256(static_cast<size_t>(R_cap) * static_cast<size_t>(K));
+}
+
+gg_status gg_q8_prepare_weight(const gg_bf16* W, int E, int N, int K, int8_t* Wq, float* Ws,
+                               gg_stream_t stream) {
+  if (E <= 0 || N <= 0 || K <= 0) return GG_ERR_INVALID_ARG;
+  if (W == nullptr || Wq == nullptr || Ws == nullptr) return GG_ERR_INVALID_ARG;
+  if (E > kMaxExperts || N % 64 != 0 || K % 64 != 0) return GG_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(W) || !aligned16(Wq) || !aligned16(Ws)) return GG_ERR_MISALIGNED;
+  DeviceInfo dev;
+  const gg_status s = device_ok(&dev);
+  if (s != GG_OK) return s;
+  return from_cuda(launch_q8_quantize(W, static_cast<long long>(E) * N, K, nullptr, 0, nullptr, 1,
+                                      0, Wq, Ws, nullptr, dev.sm_count,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gg_status gg_q8_quantize_rows(const gg_bf16* src, int T, int K, const int32_t* row_of_slot, int k,
+                              int R_cap, int8_t* Q, float* S, void* ws, size_t ws_bytes,
+                              gg_stream_t stream) {
+  if (T < 0 || K <= 0 || R_cap < 0) return GG_ERR_INVALID_ARG;
+  if (row_of_slot != nullptr ? (k <= 0 || k > 32) : T > R_cap) return GG_ERR_INVALID_ARG;
+  if (K % 64 != 0) return GG_ERR_UNSUPPORTED_SHAPE;
+  if (T > 0 && R_cap > 0 && (src == nullptr || Q == nullptr || S == nullptr))
+    return GG_ERR_INVALID_ARG;
+  if (!aligned16(src) || !aligned16(Q) || !aligned_to(S, 4) || !aligned_to(row_of_slot, 4))
+    return GG_ERR_MISALIGNED;
+  gg_status s = check_ws(ws, ws_bytes, kWsHeader);
+  if (s != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  if (R_cap == 0) return GG_OK;
+  return from_cuda(launch_q8_quantize(src, T, K, nullptr, 0, row_of_slot, k, R_cap, Q, S,
+                                      status_ptr(ws), dev.sm_count,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static gg_status q8_gemm_checks(const void* A, const int8_t* Wq, const float* Ws,
+                                const int32_t* offsets, int E, int R_cap, int K, int N,
+                                gg_epilogue epi, const float* prob_of_row, const gg_bf16* C) {
+  if (E <= 0 || R_cap < 0 || K <= 0 || N <= 0) return GG_ERR_INVALID_ARG;
+  const bool gated = epi == GG_EPI_SWIGLU || epi == GG_EPI_QGEGLU;
+  if (epi != GG_EPI_NONE && !gated) return GG_ERR_INVALID_ARG;
+  if (!gated && prob_of_row != nullptr) return GG_ERR_INVALID_ARG;
+  if (Wq == nullptr || Ws == nullptr || offsets == nullptr) return GG_ERR_INVALID_ARG;
+  if (R_cap > 0 && (A == nullptr || C == nullptr)) return GG_ERR_INVALID_ARG;
+  if (E > kMaxExperts || K % 64 != 0 || N % (gated ? 128 : 64) != 0)
+    return GG_ERR_UNSUPPORTED_SHAPE;
+  // work items are counted in an int
+  if ((static_cast<long long>(R_cap) / 256 + E) * ((N + 255) / 256) > 0x3FFFFFFFLL)
+    return GG_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(A) || !aligned16(Wq) || !aligned16(Ws) || !aligned16(C) ||
+      !aligned_to(prob_of_row, 4))
+    return GG_ERR_MISALIGNED;
+  return GG_OK;
+}
+
+static gg_status q8_gemm(const int8_t* Aq, const float* As, const int8_t* Wq, const float* Ws,
+                         const int32_t* offsets, int E, int R_cap, int K, int N, gg_epilogue epi,
+                         const float* prob_of_row, gg_bf16* C, void* ws, const DeviceInfo& dev,
+                         cudaStream_t stream) {
+  Q8GemmArgs a{};
+  a.A = Aq;
+  a.As = As;
+  a.B = Wq;
+  a.Bs = Ws;
+  a.offsets = offsets;
+  a.E = E;
+  a.R_cap = R_cap;
+  a.K = K;
+  a.N = N;
+  a.alpha = glu_alpha(epi);
+  a.row_scale = prob_of_row;
+  a.C = C;
+  a.status = status_ptr(ws);
+  return from_cuda(launch_q8_gemm(a, dev, stream));
+}
+
+gg_status gg_q8_grouped_gemm(const int8_t* Aq, const float* As, const int8_t* Wq, const float* Ws,
+                             const int32_t* offsets, int E, int R_cap, int K, int N,
+                             gg_epilogue epi, const float* prob_of_row, gg_bf16* C, void* ws,
+                             size_t ws_bytes, gg_stream_t stream) {
+  gg_status s = q8_gemm_checks(Aq, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C);
+  if (s != GG_OK) return s;
+  if (R_cap > 0 && As == nullptr) return GG_ERR_INVALID_ARG;
+  if (!aligned_to(As, 4)) return GG_ERR_MISALIGNED;
+  if ((s = check_ws(ws, ws_bytes, kWsHeader)) != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  if (R_cap == 0) return GG_OK;
+  return q8_gemm(Aq, As, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws, dev,
+                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+gg_status gg_q8_grouped_fwd(const gg_bf16* A, const int8_t* Wq, const float* Ws,
+                            const int32_t* offsets, int E, int R_cap, int K, int N,
+                            gg_epilogue epi, const float* prob_of_row, gg_bf16* C, void* ws,
+                            size_t ws_bytes, gg_stream_t stream) {
+  gg_status s = q8_gemm_checks(A, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C);
+  if (s != GG_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, gg_q8_workspace_size(R_cap, K))) != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  if (R_cap == 0) return GG_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  float* As = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsHeader);
+  int8_t* Aq = reinterpret_cast<int8_t*>(As) + align256(sizeof(float) * static_cast<size_t>(R_cap));
+  const cudaError_t e = launch_q8_quantize(A, R_cap, K, offsets, E, nullptr, 1, R_cap, Aq, As,
+                                           status_ptr(ws), dev.sm_count, st);
+  if (e != cudaSuccess) return GG_ERR_CUDA;
+  return q8_gemm(Aq, As, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws, dev, st);
+}
+
 static gg_status route_checks(const void* logits, int dtype, int T, int E, int k, int score) {
   if (T < 0 || E <= 0 || k <= 0 || k > 32 || k > E) return GG_ERR_INVALID_ARG;
   if (dtype != GG_DTYPE_F32 && dtype != GG_DTYPE_BF16) return GG_ERR_INVALID_ARG;

@@ -215,6 +215,29 @@ struct WgradArgs {
 };
 cudaError_t launch_wgrad(const WgradArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
+// ------------------------------------------------------------------ gg_q8_quant.cu
+// Codes Q and scales S of `rows` source rows (no more than offsets[E] when
+// offsets is not null). With row_of_slot, source row t goes to the rows
+// row_of_slot[t*k .. t*k+k) (-1: none) instead of row t.
+cudaError_t launch_q8_quantize(const gg_bf16* src, long long rows, int K, const int32_t* offsets,
+                               int E, const int32_t* row_of_slot, int k, int R_cap, int8_t* Q,
+                               float* S, int32_t* status, int sm_count, cudaStream_t stream);
+
+// ------------------------------------------------------------------ gg_gemm_q8.cu
+struct Q8GemmArgs {
+  const int8_t* A;         // [R_cap][K]
+  const float* As;         // [R_cap]
+  const int8_t* B;         // [E][N][K]
+  const float* Bs;         // [E][N]
+  const int32_t* offsets;
+  int E, R_cap, K, N;
+  float alpha;             // of the gated activation, 0: none
+  const float* row_scale;  // gated: [R_cap] or null
+  gg_bf16* C;
+  int32_t* status;
+};
+cudaError_t launch_q8_gemm(const Q8GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
 // ------------------------------------------------------------------ gg_route.cu
 // Blocks that accumulate the router's batch statistics (two per SM of a
 // 152-SM device): rows of the scratch below.

@@ -80,6 +80,12 @@ SIGNATURES = [
     ("gg_moe_mlp_bwd_mx", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
     ("gg_wgrad_workspace_size", _Z, [_I, _I, _I, _I]),
     ("gg_grouped_wgrad", _I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
+    ("gg_q8_workspace_size", _Z, [_I, _I]),
+    ("gg_q8_prepare_weight", _I, [_P, _I, _I, _I, _P, _P, _P]),
+    ("gg_q8_quantize_rows", _I, [_P, _I, _I, _P, _I, _I, _P, _P, _P, _Z, _P]),
+    ("gg_q8_grouped_gemm", _I,
+     [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
+    ("gg_q8_grouped_fwd", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
     ("gg_route_workspace_size", _Z, [_I, _I]),
     ("gg_route", _I, [_P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _Z, _P]),
     ("gg_route_bwd", _I,
@@ -766,6 +772,90 @@ def grouped_wgrad(dC, A, offsets, base=None, dB=None, out_dtype=torch.bfloat16, 
                                 _ptr(base), _ptr(dB), _ptr(ws), ws.numel(), _stream(dC.device)),
            "gg_grouped_wgrad")
     return dB
+
+
+# ---------------------------------------------------------------- 8-bit expert weights
+
+def q8_workspace(R_cap: int, K: int, device) -> torch.Tensor:
+    """A zeroed workspace (status word first) for q8_grouped_fwd on up to R_cap x K rows."""
+    return torch.zeros(int(LIB.gg_q8_workspace_size(R_cap, K)), dtype=torch.uint8, device=device)
+
+
+def q8_prepare_weight(W):
+    """gg_q8_prepare_weight: (codes [E, N, K] int8, scales [E, N] fp32) of W [E, N, K] BF16."""
+    E, N, K = W.shape
+    _need(W, torch.bfloat16, (E, N, K), "W")
+    Wq = torch.empty((E, N, K), dtype=torch.int8, device=W.device)
+    Ws = torch.empty((E, N), dtype=torch.float32, device=W.device)
+    _check(LIB.gg_q8_prepare_weight(_ptr(W), E, N, K, _ptr(Wq), _ptr(Ws), _stream(W.device)),
+           "gg_q8_prepare_weight")
+    return Wq, Ws
+
+
+def q8_quantize_rows(src, ws, row_of_slot=None, k: int = 1, R_cap=None, Q=None, S=None):
+    """gg_q8_quantize_rows: (codes [R_cap, K] int8, scales [R_cap] fp32) of src [T, K]; with
+    row_of_slot [T*k] each token's codes go to its k rows."""
+    T, K = src.shape
+    _need(src, torch.bfloat16, (T, K), "src")
+    if row_of_slot is not None:
+        _need(row_of_slot, torch.int32, (T * k,), "row_of_slot")
+    if R_cap is None:
+        R_cap = T if row_of_slot is None else T * k
+    Q = torch.empty((R_cap, K), dtype=torch.int8, device=src.device) if Q is None else Q
+    S = torch.empty((R_cap,), dtype=torch.float32, device=src.device) if S is None else S
+    _need(Q, torch.int8, (R_cap, K), "Q")
+    _need(S, torch.float32, (R_cap,), "S")
+    _check(LIB.gg_q8_quantize_rows(_ptr(src), T, K, _ptr(row_of_slot), k, R_cap, _ptr(Q),
+                                   _ptr(S), _ptr(ws), ws.numel(), _stream(src.device)),
+           "gg_q8_quantize_rows")
+    return Q, S
+
+
+def _q8_out(R_cap, Wq, Ws, offsets, epilogue, prob_of_row, C, device):
+    E, N, K = Wq.shape
+    _need(Wq, torch.int8, (E, N, K), "Wq")
+    _need(Ws, torch.float32, (E, N), "Ws")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    if prob_of_row is not None:
+        _need(prob_of_row, torch.float32, (R_cap,), "prob_of_row")
+    shape = (R_cap, N // 2 if epilogue in _GATED_FWD else N)
+    if C is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    _need(C, torch.bfloat16, shape, "C")
+    return C
+
+
+def q8_grouped_gemm(Aq, As, Wq, Ws, offsets, epilogue: int = GG_EPI_NONE, prob_of_row=None,
+                    C=None, ws=None):
+    """gg_q8_grouped_gemm on codes Aq [R_cap, K] with scales As [R_cap] and a weight Wq
+    [E, N, K], Ws [E, N]; returns C ([R_cap, N] or, gated, [R_cap, N/2])."""
+    R_cap, K = Aq.shape
+    E, N, _ = Wq.shape
+    _need(Aq, torch.int8, (R_cap, Wq.shape[2]), "Aq")
+    _need(As, torch.float32, (R_cap,), "As")
+    C = _q8_out(R_cap, Wq, Ws, offsets, epilogue, prob_of_row, C, Aq.device)
+    ws = workspace(0, 1, E, Aq.device) if ws is None else ws
+    _check(LIB.gg_q8_grouped_gemm(_ptr(Aq), _ptr(As), _ptr(Wq), _ptr(Ws), _ptr(offsets), E,
+                                  R_cap, K, N, epilogue, _ptr(prob_of_row), _ptr(C), _ptr(ws),
+                                  ws.numel(), _stream(Aq.device)),
+           "gg_q8_grouped_gemm")
+    return C
+
+
+def q8_grouped_fwd(A, Wq, Ws, offsets, epilogue: int = GG_EPI_NONE, prob_of_row=None, C=None,
+                   ws=None):
+    """gg_q8_grouped_fwd: quantises the rows of A [R_cap, K] (BF16) and multiplies them with
+    the 8-bit weight Wq [E, N, K], Ws [E, N]; ws from q8_workspace(R_cap, K)."""
+    R_cap, K = A.shape
+    E, N, _ = Wq.shape
+    _need(A, torch.bfloat16, (R_cap, Wq.shape[2]), "A")
+    C = _q8_out(R_cap, Wq, Ws, offsets, epilogue, prob_of_row, C, A.device)
+    ws = q8_workspace(R_cap, K, A.device) if ws is None else ws
+    _check(LIB.gg_q8_grouped_fwd(_ptr(A), _ptr(Wq), _ptr(Ws), _ptr(offsets), E, R_cap, K, N,
+                                 epilogue, _ptr(prob_of_row), _ptr(C), _ptr(ws), ws.numel(),
+                                 _stream(A.device)),
+           "gg_q8_grouped_fwd")
+    return C
 
 
 # ---------------------------------------------------------------- router
