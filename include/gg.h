@@ -654,6 +654,36 @@ gg_status gg_moe_mlp_bwd_mx(const gg_bf16* dOut, const gg_bf16* x, const float* 
                             int pad_multiple, const gg_moe_options* opt, gg_bf16* dX,
                             float* dprob, const gg_mx_buffers* buf, gg_stream_t stream);
 
+/* Buffers of the 8-bit layer, carved by gg_q8_buffers_bind(); R = T*k rows. */
+typedef struct gg_q8_buffers {
+  int8_t* Xq;           /* [R][H]  permuted input codes                   */
+  float* Xs;            /* [R]     and their scales                       */
+  gg_bf16* A;           /* [R][F]  activation                             */
+  int8_t* Aq;           /* [R][F]  its codes                              */
+  float* As;            /* [R]                                            */
+  gg_bf16* Yp;          /* [R][H]  FC2 output                             */
+  int32_t* offsets;     /* [E+1]                                          */
+  int32_t* row_of_slot; /* [T*k]                                          */
+  int32_t* slot_of_row; /* [R]                                            */
+  float* prob_of_row;   /* [R]                                            */
+  void* ws;             /* gg_workspace_size(T, k, E) bytes, status first */
+  size_t ws_bytes;
+} gg_q8_buffers;
+size_t gg_q8_buffers_size(int T, int H, int F, int k, int E);
+gg_status gg_q8_buffers_bind(void* base, size_t bytes, int T, int H, int F, int k, int E,
+                             gg_q8_buffers* out);
+
+/* The layer's forward on 8-bit weights (W1q[E][2F][H], W1s[E][2F], W2q[E][H][F],
+ * W2s[E][H]): permute maps -> quantise each token once into its k rows -> FC1
+ * and activation -> quantise the activation's rows -> FC2 -> combine into
+ * out[T][H]. Options as gg_moe_mlp_fwd_ex; GG_PROB_PRE_FC1 and recompute_h1
+ * are refused (GG_ERR_INVALID_ARG). */
+gg_status gg_moe_mlp_fwd_q8(const gg_bf16* x, const int32_t* idx, const float* prob,
+                            const int8_t* W1q, const float* W1s, const int8_t* W2q,
+                            const float* W2s, int T, int H, int F, int k, int E,
+                            const gg_moe_options* opt, gg_bf16* out, const gg_q8_buffers* buf,
+                            gg_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * gg_route — the router in front of the layer: from the logits x[T][E] of the
  * router's own linear layer to the (idx, prob) that every call above takes.
@@ -732,6 +762,19 @@ gg_status gg_route_bwd(const void* logits, int dtype, int T, int E, int k, int s
 size_t gg_wgrad_workspace_size(int E, int R_cap, int N, int K);
 gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* offsets, int E,
                            int R_cap, int N, int K, int out_dtype, const void* base, void* dB,
+                           void* ws, size_t ws_bytes, gg_stream_t stream);
+
+/* gg_moe_mlp_wgrad — both weight gradients of the layer, after gg_moe_mlp_bwd_ex
+ * on the same buffers with the same sizes and options:
+ *   dW1[E][2F][H] = (base1 +) dH_e^T Xp_e,  dW2[E][H][F] = (base2 +) dYp_e^T A_e,
+ * in out_dtype, base1 / base2 nullable or the outputs themselves. With the
+ * probability at the combine, buf->A is first rewritten as the weighted
+ * activation bf16(prob * act(H1)) (the kept H1 is not changed, so the call can
+ * be repeated). ws: a workspace of its own with the larger of
+ * gg_wgrad_workspace_size(E, R_cap, 2F, H) and (E, R_cap, H, F) bytes. */
+gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
+                           const gg_moe_options* opt, int out_dtype, const void* base1,
+                           void* dW1, const void* base2, void* dW2, const gg_moe_buffers* buf,
                            void* ws, size_t ws_bytes, gg_stream_t stream);
 
 /* ---------------------------------------------------------------------------

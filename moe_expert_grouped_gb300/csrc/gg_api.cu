@@ -1040,6 +1040,38 @@ gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* o
   return from_cuda(launch_wgrad(a, dev, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
+                           const gg_moe_options* opt, int out_dtype, const void* base1, void* dW1,
+                           const void* base2, void* dW2, const gg_moe_buffers* buf, void* ws,
+                           size_t ws_bytes, gg_stream_t stream) {
+  if (T < 0 || H <= 0 || k <= 0 || E <= 0 || pad_multiple <= 0 || F <= 0)
+    return GG_ERR_INVALID_ARG;
+  gg_epilogue fepi, bepi;
+  int mode;
+  bool recompute;
+  gg_status s = read_options(opt, &fepi, &bepi, &mode, &recompute);
+  if (s != GG_OK) return s;
+  if ((s = check_buffers(buf, T, k, E)) != GG_OK) return s;
+  if (dW1 == nullptr || dW2 == nullptr) return GG_ERR_INVALID_ARG;
+  if (H % 64 != 0 || F % 64 != 0 || E > kMaxExperts) return GG_ERR_UNSUPPORTED_SHAPE;
+  const long long rc = r_cap_of(T, k, E, pad_multiple);
+  if (rc > 0x7FFFFFFFLL) return GG_ERR_UNSUPPORTED_SHAPE;
+  const int R_cap = static_cast<int>(rc);
+  const size_t need1 = gg_wgrad_workspace_size(E, R_cap, 2 * F, H);
+  const size_t need2 = gg_wgrad_workspace_size(E, R_cap, H, F);
+  if ((s = check_ws(ws, ws_bytes, need1 > need2 ? need1 : need2)) != GG_OK) return s;
+  s = gg_grouped_wgrad(buf->dH, buf->Xp, buf->offsets, E, R_cap, 2 * F, H, out_dtype, base1, dW1,
+                       ws, ws_bytes, stream);
+  if (s != GG_OK) return s;
+  if (mode == GG_PROB_COMBINE) {
+    // out_t = sum_j p * (W2 A[row]): the probability goes with the activation
+    s = gg_glu(buf->H1, buf->offsets, E, R_cap, F, fepi, buf->prob_of_row, buf->A, stream);
+    if (s != GG_OK) return s;
+  }
+  return gg_grouped_wgrad(buf->dYp, buf->A, buf->offsets, E, R_cap, H, F, out_dtype, base2, dW2,
+                          ws, ws_bytes, stream);
+}
+
 size_t gg_q8_workspace_size(int R_cap, int K) {
   if (R_cap < 0 || K <= 0) return 0;
   return kWsHeader + align256(sizeof(float) * static_cast<size_t>(R_cap)) +
@@ -1154,6 +1186,95 @@ gg_status gg_q8_grouped_fwd(const gg_bf16* A, const int8_t* Wq, const float* Ws,
                                            status_ptr(ws), dev.sm_count, st);
   if (e != cudaSuccess) return GG_ERR_CUDA;
   return q8_gemm(Aq, As, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws, dev, st);
+}
+
+static bool q8_shape_ok(int E, int H, int F) {
+  return E > 0 && E <= kMaxExperts && H > 0 && F > 0 && H % 64 == 0 && F % 64 == 0;
+}
+
+size_t gg_q8_buffers_size(int T, int H, int F, int k, int E) {
+  if (T < 0 || k <= 0 || !q8_shape_ok(E, H, F) || r_cap_of(T, k, E, 1) > 0x7FFFFFFFLL) return 0;
+  const size_t R = static_cast<size_t>(T) * static_cast<size_t>(k);
+  const size_t h = static_cast<size_t>(H), f = static_cast<size_t>(F);
+  return align256(R * h) + align256(R * f) +              // Xq, Aq
+         align256(R * f * 2) + align256(R * h * 2) +      // A, Yp
+         align256(R * 4) * 5 +                            // scales, row maps, prob_of_row
+         align256(sizeof(int32_t) * (static_cast<size_t>(E) + 1)) +
+         align256(gg_workspace_size(T, k, E));
+}
+
+gg_status gg_q8_buffers_bind(void* base, size_t bytes, int T, int H, int F, int k, int E,
+                             gg_q8_buffers* out) {
+  if (base == nullptr || out == nullptr) return GG_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(base) & 255u) return GG_ERR_MISALIGNED;
+  const size_t need = gg_q8_buffers_size(T, H, F, k, E);
+  if (need == 0) return GG_ERR_INVALID_ARG;
+  if (bytes < need) return GG_ERR_WORKSPACE_TOO_SMALL;
+  const size_t R = static_cast<size_t>(T) * static_cast<size_t>(k);
+  const size_t h = static_cast<size_t>(H), f = static_cast<size_t>(F);
+  uint8_t* p = static_cast<uint8_t*>(base);
+  auto take = [&p](size_t n) {
+    uint8_t* q = p;
+    p += align256(n);
+    return q;
+  };
+  std::memset(out, 0, sizeof(*out));
+  out->Xq = reinterpret_cast<int8_t*>(take(R * h));
+  out->Xs = reinterpret_cast<float*>(take(R * 4));
+  out->A = reinterpret_cast<gg_bf16*>(take(R * f * 2));
+  out->Aq = reinterpret_cast<int8_t*>(take(R * f));
+  out->As = reinterpret_cast<float*>(take(R * 4));
+  out->Yp = reinterpret_cast<gg_bf16*>(take(R * h * 2));
+  out->offsets =
+      reinterpret_cast<int32_t*>(take(sizeof(int32_t) * (static_cast<size_t>(E) + 1)));
+  out->row_of_slot = reinterpret_cast<int32_t*>(take(R * 4));
+  out->slot_of_row = reinterpret_cast<int32_t*>(take(R * 4));
+  out->prob_of_row = reinterpret_cast<float*>(take(R * 4));
+  out->ws_bytes = align256(gg_workspace_size(T, k, E));
+  out->ws = take(out->ws_bytes);
+  return GG_OK;
+}
+
+gg_status gg_moe_mlp_fwd_q8(const gg_bf16* x, const int32_t* idx, const float* prob,
+                            const int8_t* W1q, const float* W1s, const int8_t* W2q,
+                            const float* W2s, int T, int H, int F, int k, int E,
+                            const gg_moe_options* opt, gg_bf16* out, const gg_q8_buffers* b,
+                            gg_stream_t stream) {
+  if (T < 0 || H <= 0 || F <= 0 || k <= 0 || E <= 0) return GG_ERR_INVALID_ARG;
+  gg_epilogue fepi, bepi;
+  int mode;
+  bool recompute;
+  gg_status s = read_options(opt, &fepi, &bepi, &mode, &recompute);
+  if (s != GG_OK) return s;
+  if (recompute || mode == GG_PROB_PRE_FC1) return GG_ERR_INVALID_ARG;
+  if (b == nullptr || b->Xq == nullptr || b->Xs == nullptr || b->A == nullptr ||
+      b->Aq == nullptr || b->As == nullptr || b->Yp == nullptr || b->offsets == nullptr ||
+      b->row_of_slot == nullptr || b->slot_of_row == nullptr || b->prob_of_row == nullptr)
+    return GG_ERR_INVALID_ARG;
+  if (W1q == nullptr || W1s == nullptr || W2q == nullptr || W2s == nullptr)
+    return GG_ERR_INVALID_ARG;
+  if (T > 0 && (x == nullptr || out == nullptr)) return GG_ERR_INVALID_ARG;
+  if (!q8_shape_ok(E, H, F) || r_cap_of(T, k, E, 1) > 0x7FFFFFFFLL)
+    return GG_ERR_UNSUPPORTED_SHAPE;
+  const int R = static_cast<int>(r_cap_of(T, k, E, 1));
+  // row maps only: the permuted copy is the quantised one below
+  s = gg_permute(x, idx, prob, T, H, k, E, 1, nullptr, b->offsets, b->row_of_slot, b->slot_of_row,
+                 b->prob_of_row, b->ws, b->ws_bytes, stream);
+  if (s != GG_OK || T == 0) return s;
+  s = gg_q8_quantize_rows(x, T, H, b->row_of_slot, k, R, b->Xq, b->Xs, b->ws, b->ws_bytes, stream);
+  if (s != GG_OK) return s;
+  s = gg_q8_grouped_gemm(b->Xq, b->Xs, W1q, W1s, b->offsets, E, R, H, 2 * F, fepi,
+                         mode == GG_PROB_ACTIVATION ? b->prob_of_row : nullptr, b->A, b->ws,
+                         b->ws_bytes, stream);
+  if (s != GG_OK) return s;
+  s = gg_q8_quantize_rows(b->A, R, F, nullptr, 1, R, b->Aq, b->As, b->ws, b->ws_bytes, stream);
+  if (s != GG_OK) return s;
+  s = gg_q8_grouped_gemm(b->Aq, b->As, W2q, W2s, b->offsets, E, R, F, H, GG_EPI_NONE, nullptr,
+                         b->Yp, b->ws, b->ws_bytes, stream);
+  if (s != GG_OK) return s;
+  return gg_unpermute_combine(b->Yp, b->row_of_slot, mode == GG_PROB_COMBINE ? prob : nullptr, T,
+                              k, H, R, out, nullptr, 0, nullptr, nullptr, b->ws, b->ws_bytes,
+                              stream);
 }
 
 static gg_status route_checks(const void* logits, int dtype, int T, int E, int k, int score) {

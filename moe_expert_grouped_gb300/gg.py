@@ -80,6 +80,12 @@ SIGNATURES = [
     ("gg_moe_mlp_bwd_mx", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
     ("gg_wgrad_workspace_size", _Z, [_I, _I, _I, _I]),
     ("gg_grouped_wgrad", _I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
+    ("gg_moe_mlp_wgrad", _I,
+     [_I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    ("gg_q8_buffers_size", _Z, [_I, _I, _I, _I, _I]),
+    ("gg_q8_buffers_bind", _I, [_P, _Z, _I, _I, _I, _I, _I, _P]),
+    ("gg_moe_mlp_fwd_q8", _I,
+     [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
     ("gg_q8_workspace_size", _Z, [_I, _I]),
     ("gg_q8_prepare_weight", _I, [_P, _I, _I, _I, _P, _P, _P]),
     ("gg_q8_quantize_rows", _I, [_P, _I, _I, _P, _I, _I, _P, _P, _P, _Z, _P]),
@@ -128,6 +134,14 @@ class GGMxBuffers(ctypes.Structure):
         "Xq", "Xs", "H1", "Aq", "As", "Yp", "dYq", "dYs", "dHq", "dHs", "dXp", "offsets",
         "row_of_slot", "slot_of_row", "prob_of_row", "tiles_before", "rowdot")] + [
         ("n_tiles", ctypes.c_int), ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
+class GGQ8Buffers(ctypes.Structure):
+    """Mirror of struct gg_q8_buffers."""
+
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "Xq", "Xs", "A", "Aq", "As", "Yp", "offsets", "row_of_slot", "slot_of_row",
+        "prob_of_row", "ws")] + [("ws_bytes", ctypes.c_size_t)]
 
 
 class GGError(RuntimeError):
@@ -458,6 +472,8 @@ class MoeLayer:
         self.opt = GGOptions(activation, prob_mode, 1 if recompute_h1 else 0)
         self._saved = None  # the forward's (x, prob): the pre-FC1 backward needs them
         self._rows = None   # the forward's batch size
+        self._backward_rows = None  # the backward's, once its buffers hold the gradients
+        self._wgrad_ws = None       # workspace of weight_grads, made at its first call
         self.R_cap = r_cap(T, k, E, P)
         self.device = torch.device(device)
         n = int(LIB.gg_moe_buffers_size(T, H, F, k, E, P))
@@ -511,6 +527,7 @@ class MoeLayer:
                "gg_moe_mlp_fwd_ex")
         self._saved = (x, prob)
         self._rows = T
+        self._backward_rows = None
         return out
 
     def backward(self, dOut, W1, W2, dX=None, dprob=None):
@@ -532,10 +549,49 @@ class MoeLayer:
                                      _ptr(dprob) if want else None, ctypes.byref(self.buf),
                                      _stream(self.device)),
                "gg_moe_mlp_bwd_ex")
+        self._backward_rows = T
         return (dX, dprob) if want else dX
 
+    def weight_grads(self, dW1=None, dW2=None, base1=None, base2=None,
+                     out_dtype=torch.bfloat16):
+        """(dW1 [E, 2F, H], dW2 [E, H, F]) of the last backward, in BF16 or fp32 (the
+        type of the tensors passed, else of the bases, else out_dtype); base1 / base2 are
+        added (pass the outputs themselves to accumulate in place). With the probability
+        at the combine, the view "A" then holds the weighted activation."""
+        T = self._backward_rows
+        if T is None:
+            raise GGError(1, "weight_grads before backward")
+        H, F, k, E = self.H, self.F, self.k, self.E
+        for t in (dW1, dW2, base1, base2):
+            if t is not None:
+                out_dtype = t.dtype
+                break
+        shapes = (E, 2 * F, H), (E, H, F)
+        if dW1 is None:
+            dW1 = torch.empty(shapes[0], dtype=out_dtype, device=self.device)
+        if dW2 is None:
+            dW2 = torch.empty(shapes[1], dtype=out_dtype, device=self.device)
+        dtype = _dtype(dW1, "dW1")
+        for t, shape, name in ((dW1, shapes[0], "dW1"), (dW2, shapes[1], "dW2"),
+                               (base1, shapes[0], "base1"), (base2, shapes[1], "base2")):
+            if t is not None:
+                _need(t, out_dtype, shape, name)
+        if self._wgrad_ws is None:
+            self._wgrad_ws = max((wgrad_workspace(E, self.R_cap, n, c, self.device)
+                                  for _, n, c in shapes), key=torch.Tensor.numel)
+        _check(LIB.gg_moe_mlp_wgrad(T, H, F, k, E, self.P, ctypes.byref(self.opt), dtype,
+                                    _ptr(base1), _ptr(dW1), _ptr(base2), _ptr(dW2),
+                                    ctypes.byref(self.buf), _ptr(self._wgrad_ws),
+                                    self._wgrad_ws.numel(), _stream(self.device)),
+               "gg_moe_mlp_wgrad")
+        return dW1, dW2
+
     def status(self) -> int:
-        return read_status(self.view("ws"))
+        """The first device-side error of the layer's calls, 0 for none."""
+        code = read_status(self.view("ws"))
+        if code == 0 and self._wgrad_ws is not None:
+            code = read_status(self._wgrad_ws)
+        return code
 
 
 def permute_noalloc(x, idx, prob, E: int, P: int = 1, out=None):
@@ -856,6 +912,53 @@ def q8_grouped_fwd(A, Wq, Ws, offsets, epilogue: int = GG_EPI_NONE, prob_of_row=
                                  _stream(A.device)),
            "gg_q8_grouped_fwd")
     return C
+
+
+class Q8MoeLayer:
+    """The expert layer's forward on 8-bit weights (gg_moe_mlp_fwd_q8) over one owned
+    buffer; weights as the (codes, scales) pairs of q8_prepare_weight."""
+
+    def __init__(self, T: int, H: int, F: int, k: int, E: int, device="cuda",
+                 activation: int = GG_ACT_SWIGLU, prob_mode: int = GG_PROB_COMBINE):
+        self.T, self.H, self.F, self.k, self.E = T, H, F, k, E
+        self.opt = GGOptions(activation, prob_mode, 0)
+        self.device = torch.device(device)
+        n = int(LIB.gg_q8_buffers_size(T, H, F, k, E))
+        if n == 0:
+            raise GGError(2, "gg_q8_buffers_size")
+        self.storage = torch.zeros(n + 256, dtype=torch.uint8, device=self.device)
+        self._base = self.storage.data_ptr() + ((-self.storage.data_ptr()) % 256)
+        self.buf = GGQ8Buffers()
+        _check(LIB.gg_q8_buffers_bind(ctypes.c_void_p(self._base), n, T, H, F, k, E,
+                                      ctypes.byref(self.buf)), "gg_q8_buffers_bind")
+
+    def forward(self, x, idx, prob, W1, W2, out=None):
+        """out [T, H] for x [T, H] with W1 = (codes [E, 2F, H], scales [E, 2F]) and W2 =
+        (codes [E, H, F], scales [E, H]); T is the bound size or any smaller batch."""
+        T = int(x.shape[0])
+        H, F, k, E = self.H, self.F, self.k, self.E
+        if T > self.T or int(LIB.gg_workspace_size(T, k, E)) > int(self.buf.ws_bytes):
+            raise GGError(4, f"{T} tokens do not fit a layer bound for {self.T}")
+        _need(x, torch.bfloat16, (T, H), "x")
+        _need(idx, torch.int32, (T, k), "idx")
+        _need(prob, torch.float32, (T, k), "prob")
+        for (q, s), shape, name in ((W1, (E, 2 * F, H), "W1"), (W2, (E, H, F), "W2")):
+            _need(q, torch.int8, shape, name)
+            _need(s, torch.float32, shape[:2], name + " scales")
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+        else:
+            _need(out, torch.bfloat16, (T, H), "out")
+        _check(LIB.gg_moe_mlp_fwd_q8(_ptr(x), _ptr(idx), _ptr(prob), _ptr(W1[0]), _ptr(W1[1]),
+                                     _ptr(W2[0]), _ptr(W2[1]), T, H, F, k, E,
+                                     ctypes.byref(self.opt), _ptr(out), ctypes.byref(self.buf),
+                                     _stream(self.device)),
+               "gg_moe_mlp_fwd_q8")
+        return out
+
+    def status(self) -> int:
+        off = self.buf.ws - self.storage.data_ptr()
+        return read_status(self.storage[off:off + int(self.buf.ws_bytes)])
 
 
 # ---------------------------------------------------------------- router
