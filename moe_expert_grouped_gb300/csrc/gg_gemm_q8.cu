@@ -244,7 +244,7 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait_bounded<true>(smem_u32(&st.ready[stage]), phase, abort_flag, p.status)) {
+          if (!mbar_wait_bounded(smem_u32(&st.ready[stage]), phase, abort_flag, p.status)) {
             ok = false;
             break;
           }
@@ -304,7 +304,7 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&st.raw_empty[rs]));
-          mbar_arrive_cluster(mapa_shared(smem_u32(&st.ready[ws]), 0));
+          mbar_arrive_cluster_cta(mapa_shared(smem_u32(&st.ready[ws]), 0));
         }
         used |= 1u << ws;
         last_phase = (last_phase & ~(1u << ws)) | (wp << ws);

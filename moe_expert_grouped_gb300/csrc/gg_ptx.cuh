@@ -79,34 +79,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// The same, acquiring what threads of either CTA of the cluster released to
-// the barrier.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, P;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Wait until the phase with the given parity has completed. Returns false if
 // the CTA-wide abort flag is raised or the wait ran past its limit (then the
 // status word gets GG_ERR_DEVICE_TIMEOUT and the abort flag is raised).
-// kCluster: the phase is completed by arrivals of both CTAs of the cluster
-// that publish shared-memory writes.
-template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
                                                   volatile int* abort_flag,
                                                   int32_t* status,
                                                   uint64_t limit_ns = kWaitLimitNs) {
-  if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1; i < kWaitMaxPolls; ++i) {
-    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 0) {
       if (abort_flag != nullptr && *abort_flag) return false;
       if (globaltimer_ns() - t0 > limit_ns) break;
@@ -282,6 +265,17 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
 // and pass no data through memory.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
+// The same arrive releasing to this CTA's scope: it orders this thread's
+// earlier accesses to its own shared memory (and, through a __syncwarp, its
+// warp's) before the arrive, without the device-wide fence that a
+// cluster-scope release costs (about 1 us). For handing operand tiles in this
+// CTA's shared memory, already fenced for the asynchronous proxy, to the
+// pair's MMAs: what reads them is this SM's own tensor core.
+__device__ __forceinline__ void mbar_arrive_cluster_cta(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
 }
 

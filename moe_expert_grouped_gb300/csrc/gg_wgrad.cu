@@ -223,7 +223,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap mapD, const __grid_constant__ C
           fence_proxy_async();
           __syncwarp();
         }
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&st.ready[stage]), 0));
+        if (lane == 0) mbar_arrive_cluster_cta(mapa_shared(smem_u32(&st.ready[stage]), 0));
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -247,7 +247,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap mapD, const __grid_constant__ C
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int r = 0; r < it.rows; r += BK) {
-          if (!mbar_wait_bounded<true>(smem_u32(&st.ready[stage]), phase, abort_flag, p.status)) {
+          if (!mbar_wait_bounded(smem_u32(&st.ready[stage]), phase, abort_flag, p.status)) {
             ok = false;
             break;
           }
