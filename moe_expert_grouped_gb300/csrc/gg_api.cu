@@ -1004,7 +1004,8 @@ gg_status gg_moe_mlp_bwd_mx(const gg_bf16* dOut, const gg_bf16* x, const float* 
 
 size_t gg_wgrad_workspace_size(int E, int R_cap, int N, int K) {
   if (E <= 0 || R_cap < 0 || N <= 0 || K <= 0) return 0;
-  return kWsHeader;
+  const size_t slots = static_cast<size_t>(wgrad_slots(R_cap, N, K));
+  return kWsHeader + (slots > 0 ? align256(sizeof(int)) + slots * wgrad_slot_bytes() : 0);
 }
 
 gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* offsets, int E,
@@ -1036,6 +1037,12 @@ gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* o
   a.f32 = out_dtype == GG_DTYPE_F32;
   a.base = base;
   a.dB = dB;
+  a.slots = wgrad_slots(R_cap, N, K);
+  if (a.slots > 0) {
+    uint8_t* scratch = static_cast<uint8_t*>(ws) + kWsHeader;
+    a.plan = reinterpret_cast<int*>(scratch);
+    a.partial = reinterpret_cast<float*>(scratch + align256(sizeof(int)));
+  }
   a.status = status_ptr(ws);
   return from_cuda(launch_wgrad(a, dev, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -211,8 +211,16 @@ struct WgradArgs {
   bool f32;           // type of base and dB
   const void* base;   // [E][N][K] or null
   void* dB;           // [E][N][K]
+  int slots;          // wgrad_slots(R_cap, N, K)
+  float* partial;     // slots partial blocks of wgrad_slot_bytes()
+  int* plan;          // one word of scratch
   int32_t* status;
 };
+// Partial blocks that the workspace holds for rows cut into slices; 0: too few
+// rows for that.
+constexpr int kWgradMaxSlots = 512;
+int wgrad_slots(int R_cap, int N, int K);
+size_t wgrad_slot_bytes();
 cudaError_t launch_wgrad(const WgradArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
 // ------------------------------------------------------------------ gg_q8_quant.cu
