@@ -1142,7 +1142,7 @@ static gg_status q8_gemm_checks(const void* A, const int8_t* Wq, const float* Ws
 static gg_status q8_gemm(const int8_t* Aq, const float* As, const int8_t* Wq, const float* Ws,
                          const int32_t* offsets, int E, int R_cap, int K, int N, gg_epilogue epi,
                          const float* prob_of_row, gg_bf16* C, void* ws, const DeviceInfo& dev,
-                         cudaStream_t stream) {
+                         bool behind_quantiser, cudaStream_t stream) {
   Q8GemmArgs a{};
   a.A = Aq;
   a.As = As;
@@ -1157,6 +1157,8 @@ static gg_status q8_gemm(const int8_t* Aq, const float* As, const int8_t* Wq, co
   a.row_scale = prob_of_row;
   a.C = C;
   a.status = status_ptr(ws);
+  if (q8_rows_fits(R_cap, E))
+    return from_cuda(launch_q8_rows(a, behind_quantiser, dev, stream));
   return from_cuda(launch_q8_gemm(a, dev, stream));
 }
 
@@ -1172,7 +1174,7 @@ gg_status gg_q8_grouped_gemm(const int8_t* Aq, const float* As, const int8_t* Wq
   DeviceInfo dev;
   if ((s = device_ok(&dev)) != GG_OK) return s;
   if (R_cap == 0) return GG_OK;
-  return q8_gemm(Aq, As, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws, dev,
+  return q8_gemm(Aq, As, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws, dev, false,
                  reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -1192,7 +1194,7 @@ gg_status gg_q8_grouped_fwd(const gg_bf16* A, const int8_t* Wq, const float* Ws,
   const cudaError_t e = launch_q8_quantize(A, R_cap, K, offsets, E, nullptr, 1, R_cap, Aq, As,
                                            status_ptr(ws), dev.sm_count, st);
   if (e != cudaSuccess) return GG_ERR_CUDA;
-  return q8_gemm(Aq, As, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws, dev, st);
+  return q8_gemm(Aq, As, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws, dev, true, st);
 }
 
 static bool q8_shape_ok(int E, int H, int F) {

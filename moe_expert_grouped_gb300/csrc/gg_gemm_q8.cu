@@ -29,7 +29,6 @@
 // GG_ERR_DEVICE_TIMEOUT, raises a CTA-wide abort flag, and the CTA drains
 // what is in flight, frees TMEM and exits after a final cluster barrier.
 
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -38,6 +37,7 @@
 #include "gg_internal.h"
 #include "gg_launch.cuh"
 #include "gg_ptx.cuh"
+#include "gg_q8.cuh"
 
 namespace gg {
 namespace {
@@ -95,18 +95,6 @@ struct QParams {
 // FP16 operands, fp32 sums: format fields 0.
 constexpr uint32_t kIdesc = (1u << 4) | ((static_cast<uint32_t>(BN) >> 3) << 17) |
                             ((static_cast<uint32_t>(2 * BM) >> 4) << 24);
-
-// Four 8-bit integers (bytes of w) -> four FP16 of the same value: byte + 128
-// under the exponent of 1024 reads 1152 + value.
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
-  const uint32_t x = w ^ 0x80808080u;
-  const uint32_t lo = __byte_perm(x, 0x64646464u, 0x4140);
-  const uint32_t hi = __byte_perm(x, 0x64646464u, 0x4342);
-  const __half2 bias = __half2half2(__ushort_as_half(static_cast<unsigned short>(0x6480)));
-  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
-  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
 
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)

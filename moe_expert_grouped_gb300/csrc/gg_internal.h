@@ -246,6 +246,13 @@ struct Q8GemmArgs {
 };
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
+// ------------------------------------------------------------------ gg_q8_rows.cu
+// The same for few rows per expert (q8_rows_fits). early: launched right
+// behind launch_q8_quantize, which makes A and As.
+bool q8_rows_fits(int R_cap, int E);
+cudaError_t launch_q8_rows(const Q8GemmArgs& a, bool early, const DeviceInfo& dev,
+                           cudaStream_t stream);
+
 // ------------------------------------------------------------------ gg_route.cu
 // Blocks that accumulate the router's batch statistics (two per SM of a
 // 152-SM device): rows of the scratch below.

@@ -34,6 +34,7 @@ q8_quantize_kernel(const uint4* __restrict__ src, long long rows, int K,
                    const int32_t* __restrict__ offsets, int E,
                    const int32_t* __restrict__ row_of_slot, int k, int R_cap,
                    uint2* __restrict__ Q, float* __restrict__ S, int32_t* status) {
+  grid_dependents_launch();  // the product's weight loads need not wait for the codes
   const int lane = threadIdx.x & 31;
   const int vec = K / 8;
   if (offsets != nullptr) {
