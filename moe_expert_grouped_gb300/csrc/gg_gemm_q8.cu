@@ -5,25 +5,44 @@
 //
 // This chip has no fast integer tensor path (its INT8 rate is far below the
 // 16-bit floating-point one), and FP16 holds every 8-bit integer exactly. So
-// the codes travel and lie in memory as 8 bits and are widened to FP16 in
-// shared memory, right before the FP16 tensor cores: products are exact, and
-// fp32 sums of them are too below 2^24 (any K up to 1040; longer sums of
-// larger magnitude round to fp32).
+// the codes travel and lie in memory as 8 bits and are widened to FP16 on the
+// SM, right before the FP16 tensor cores: products are exact, and fp32 sums of
+// them are too below 2^24 (any K up to 1040; longer sums of larger magnitude
+// round to fp32).
 //
-// One CTA per SM in clusters of two (one tcgen05 MMA pair, 448 threads per
+// The weights are the tensor core's A operand (M = 256 weight rows per pair
+// of CTAs), the tokens its B operand (N = up to 192 tokens, in steps of 32):
+// an expert's ragged token count then costs what it has, not a multiple of 256.
+// Shared-memory bandwidth is what widening strains, so the widened weights go
+// to tensor memory, which MMAs read as well (tcgen05.st, A in TMEM), and only
+// the widened tokens to shared memory: 52 KB per 64-deep step and SM against
+// 96 KB with both in shared memory.
+//
+// Bound by the instructions that widen (about 1350 per SM and 64 codes, 0.58
+// of the issue slots; the tensor pipe is 0.6 busy): without widening the
+// weights or the tokens it would run 1.16 times as fast each, with neither 1.4
+// times. Measured, 131072 rows: 4096 x 4096, one expert, 1576 TFLOP/s; 128
+// experts, 1536 x 2048 gated, 660 to 700 us (1180 to 1250 TFLOP/s).
+//
+// One CTA per SM in clusters of two (one tcgen05 MMA pair, 640 threads per
 // CTA, warp-specialised):
-//   warp 0       TMA producer: 128 rows x 64 codes of A and of B per step into
-//                a ring of raw steps (16 KB each);
+//   warp 0       TMA producer: 128 weight rows (gated: 64 gate rows and the
+//                matching 64 up rows) and half the tokens, 128 codes deep, into
+//                a ring of raw steps (rows of 64 bytes cost TMA as much as
+//                rows of 128 and held the kernel at 0.55 of the MMA rate);
 //   warp 1       allocates TMEM; in the even CTA one lane issues
-//                tcgen05.mma.cta_group::2 (M = 256, N = 256, K = 16);
-//   warps 2-5    epilogue: one TMEM lane = one row of C;
-//   warps 6-13   widen: raw step -> FP16 step (32 KB, K-major with the
-//                128-byte swizzle the descriptors name), passed to the even
-//                CTA's MMA issuer.
-// Work items are (expert, 256-row pair of row blocks, 256-column block; gated:
-// 128 gate and the matching 128 up columns) as in the BF16 grouped GEMM; rows
-// past an expert's end are computed from whatever codes lie there (any 8 bits
-// are a finite integer) and not stored.
+//                tcgen05.mma.cta_group::2 (M = 256, K = 16);
+//   warp 2       finds the work items ahead of the others;
+//   warps 4-11   widen the weights into TMEM, one thread per row;
+//   warps 12-15  widen the tokens into shared memory (K-major, 128-byte
+//                swizzle). Both in two groups, for the two halves of a step;
+//   warps 16-19  epilogue: one TMEM lane = one weight row, one column = one
+//                token. Gated: the up rows' warps hand their values to the
+//                gate rows' warps through shared memory.
+// TMEM: two accumulators of 192 columns and two steps of weights (64 columns
+// each). A step is 128 deep so that the issuer, whose loop costs it about 300
+// cycles, keeps ahead of the MMAs (400 per 64 codes). Work items are (expert, block of weight rows, block of tokens), the
+// token block fastest, so that neighbours share their weights in L2.
 //
 // Every wait is bounded (gg_ptx.cuh); a wait that runs out records
 // GG_ERR_DEVICE_TIMEOUT, raises a CTA-wide abort flag, and the CTA drains
@@ -32,6 +51,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstddef>
 
 #include "gg_epilogue.cuh"
 #include "gg_internal.h"
@@ -42,75 +62,173 @@
 namespace gg {
 namespace {
 
-constexpr int BM = 128;
-constexpr int BN = 256;
-constexpr int BK = 64;
-constexpr int RAW = 4;     // raw steps in flight
-constexpr int WIDE = 4;    // widened steps
+constexpr int BM = 128;     // weight rows per CTA
+constexpr int BN = 192;     // most tokens per work item
+constexpr int BK = 64;      // half a step: what a group of widening warps takes
+constexpr int RK = 128;     // codes of K per step
+constexpr int RAW = 4;      // raw steps in flight
+constexpr int WIDE = 2;     // widened steps
 constexpr uint16_t kPairMask = 0x3;
+constexpr int kItemWarp = 2;
+constexpr int kFirstA = 4, kFirstB = 12, kFirstEpi = 16;  // first warps of the roles
+constexpr int kGroups = 2;     // groups of widening warps, one for each half of a step:
+constexpr int kAWarps = 4;     // warps of a group for the weights
+constexpr int kBWarps = 2;     // and for the tokens
 constexpr int kEpiWarps = 4;
-constexpr int kWideWarps = 8;
-constexpr int kFirstWide = 2 + kEpiWarps;
-constexpr int kThreads = 32 * (kFirstWide + kWideWarps);
-constexpr uint32_t RAW_HALF = BM * BK;              // 8 KB: 128 rows of codes
-constexpr uint32_t RAW_BYTES = 2 * RAW_HALF;        // A rows, B rows
-constexpr uint32_t WIDE_HALF = 2 * RAW_HALF;        // the same as FP16
+constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+constexpr int kItems = 4;      // work items found ahead
+constexpr int kBoxRows = 16;                         // tokens per TMA box
+constexpr uint32_t RAW_A = BM * RK;                  // 16 KB of weight codes
+constexpr uint32_t RAW_BYTES = RAW_A + BN / 2 * RK;  // and up to 12 KB of token codes
+constexpr uint32_t WIDE_HALF = BN / 2 * BK * 2;      // half a step's tokens as FP16
 constexpr uint32_t WIDE_BYTES = 2 * WIDE_HALF;
 constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t kTmemA = 2 * BN;                  // TMEM column of the first weight step
+constexpr uint32_t kStepCols = RK / 2;               // two FP16 per column
+
+// A work item: expert, block of weight rows, its tokens (first row, number).
+// rows < 0: there are no more items.
+struct alignas(16) Item {
+  int e, nt, row0, rows;
+};
 
 struct SmemTail {
+  Item item[kItems];
+  uint64_t item_full[kItems];
+  uint64_t item_empty[kItems];
   uint64_t raw_full[RAW];
   uint64_t raw_empty[RAW];
   uint64_t ready[WIDE];    // even CTA: both CTAs widened the step
   uint64_t empty[WIDE];
   uint64_t tfull[2];
   uint64_t tempty[2];
+  uint64_t up_full[2];     // a chunk of up values, per pair of epilogue warps
+  uint64_t up_empty[2];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
   int total_tiles;
+  alignas(16) float scale[kEpiWarps][32];  // of the chunk's tokens, read as float4
   int tiles_before[kMaxExperts + 1];
   int row_start[kMaxExperts + 1];
 };
 
-constexpr uint32_t kWarpStagingBytes = 32 * 64;
-constexpr uint32_t kStagingBytes = kEpiWarps * kWarpStagingBytes;
 constexpr uint32_t kWideAt = RAW * RAW_BYTES;
 constexpr uint32_t kStagingAt = kWideAt + WIDE * WIDE_BYTES;
-constexpr size_t kSmemBytes = 1024 + kStagingAt + kStagingBytes + sizeof(SmemTail);
+constexpr uint32_t kWarpStagingBytes = 32 * 64;
+constexpr uint32_t kUpAt = kStagingAt + kEpiWarps * kWarpStagingBytes;
+constexpr uint32_t kUpBytes = 32 * 32 * 4;           // a chunk of up values, one buffer per pair
+constexpr uint32_t kTailAt = kUpAt + 2 * kUpBytes;
+constexpr size_t kSmemBytes = 1024 + kTailAt + sizeof(SmemTail);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+static_assert(offsetof(SmemTail, scale) % 16 == 0 && kTailAt % 16 == 0, "float4 reads");
+static_assert(32 % (16 * kBWarps) == 0, "an item's tokens per CTA are whole turns");
+static_assert(kTmemA + WIDE * kStepCols <= TMEM_COLS, "tensor memory budget");
+static_assert(kWideAt % 1024 == 0 && WIDE_BYTES % 1024 == 0, "128-byte swizzle");
 
 struct QParams {
   const int32_t* offsets;
   int E, R_cap, K, N;
   int F;               // gated: N / 2
-  int NT;
+  int NT;              // blocks of weight rows
   const float* As;     // [R_cap]
   const float* Bs;     // [E][N]
   const float* row_scale;
+  float alpha;
   gg_bf16* C;
   int32_t* status;
 };
 
-// FP16 operands, fp32 sums: format fields 0.
-constexpr uint32_t kIdesc = (1u << 4) | ((static_cast<uint32_t>(BN) >> 3) << 17) |
-                            ((static_cast<uint32_t>(2 * BM) >> 4) << 24);
+__device__ __forceinline__ int token_blocks(int rows) { return (rows + BN - 1) / BN; }
+
+__device__ __forceinline__ Item item_of(int tile, const QParams& p, const SmemTail& st) {
+  Item it;
+  int lo = 0, hi = p.E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (st.tiles_before[mid] <= tile)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  it.e = lo;
+  const int first = st.row_start[lo];
+  const int rows = st.row_start[lo + 1] - first;
+  const int blocks = token_blocks(rows);
+  const int local = tile - st.tiles_before[lo];
+  it.nt = local / blocks;
+  const int tb = local - it.nt * blocks;
+  const int each = ((rows + blocks - 1) / blocks + 31) / 32 * 32;  // as even as 32s allow
+  it.row0 = first + tb * each;
+  it.rows = max(0, min(each, rows - tb * each));
+  return it;
+}
+
+// The reader's side of the item ring (a whole warp or one thread; `arriver`
+// reports the slot free, once per reader). False: no more items.
+struct ItemReader {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ bool next(SmemTail& st, Item& it, bool warp, bool arriver,
+                                       volatile int* abort_flag, int32_t* status) {
+    if (!mbar_wait_bounded(smem_u32(&st.item_full[slot]), phase, abort_flag, status)) return false;
+    it = st.item[slot];
+    if (warp) __syncwarp();
+    if (arriver) mbar_arrive(smem_u32(&st.item_empty[slot]));
+    if (++slot == kItems) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    return it.rows >= 0;
+  }
+};
+
+// Columns of an item's MMAs.
+__device__ __forceinline__ int columns_of(const Item& it) { return max(32, (it.rows + 31) & ~31); }
+
+// FP16 operands (format fields 0), fp32 sums, M = 256, N = n; both K-major.
+__device__ __forceinline__ uint32_t idesc_f16(int n) {
+  return (1u << 4) | ((static_cast<uint32_t>(n) >> 3) << 17) |
+         ((static_cast<uint32_t>(2 * BM) >> 4) << 24);
+}
+
+// D[tmem of both CTAs] (+)= A[256 x 16, tensor memory] * B[N x 16, N/2 rows per
+// CTA, shared memory]^T.
+__device__ __forceinline__ void tc_mma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tmem,
+                                                   uint64_t bdesc, uint32_t idesc,
+                                                   uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Thread i of the warp writes 16 consecutive columns of lane (quadrant + i).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(taddr)
+      : "memory");
+}
 
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
-q8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-               const QParams p, const float alpha) {
+q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__ CUtensorMap mapW,
+               const QParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = raw_addr + pad;
-  SmemTail& st = *reinterpret_cast<SmemTail*>(smem + kStagingAt + kStagingBytes);
+  SmemTail& st = *reinterpret_cast<SmemTail*>(smem + kTailAt);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int E = p.E;
-  const int NT = p.NT;
-  const int KB = p.K / BK;
   const uint32_t crank = cluster_ctarank();
   const bool leader = crank == 0;
 
@@ -123,8 +241,8 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
       if (e < E) {
         const int o0 = p.offsets[e];
         const int o1 = p.offsets[e + 1];
-        if (o1 < o0) bad = true;
-        tiles = o1 > o0 ? (o1 - o0 + 2 * BM - 1) / (2 * BM) * NT : 0;
+        if (o1 < o0 || o0 < 0 || o1 > p.R_cap) bad = true;
+        tiles = o1 > o0 ? token_blocks(o1 - o0) * p.NT : 0;
         st.row_start[e] = o0;
       }
       int incl = tiles;
@@ -149,15 +267,23 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
       if (bad && blockIdx.x == 0) set_status(p.status, GG_ERR_DEVICE_BAD_OFFSETS);
       for (int s = 0; s < RAW; ++s) {
         mbar_init(smem_u32(&st.raw_full[s]), 1);
-        mbar_init(smem_u32(&st.raw_empty[s]), kWideWarps);
+        mbar_init(smem_u32(&st.raw_empty[s]), kGroups * (kAWarps + kBWarps));
       }
       for (int s = 0; s < WIDE; ++s) {
-        mbar_init(smem_u32(&st.ready[s]), 2 * kWideWarps);
+        mbar_init(smem_u32(&st.ready[s]), 2 * kGroups * (kAWarps + kBWarps));
         mbar_init(smem_u32(&st.empty[s]), 1);
       }
       for (int a = 0; a < 2; ++a) {
         mbar_init(smem_u32(&st.tfull[a]), 1);
         mbar_init(smem_u32(&st.tempty[a]), 2 * kEpiWarps);
+        mbar_init(smem_u32(&st.up_full[a]), 1);
+        mbar_init(smem_u32(&st.up_empty[a]), 1);
+      }
+      for (int i = 0; i < kItems; ++i) {
+        mbar_init(smem_u32(&st.item_full[i]), 1);
+        // readers: producer, widening and epilogue warps, and the even CTA's issuer
+        mbar_init(smem_u32(&st.item_empty[i]),
+                  1 + kGroups * (kAWarps + kBWarps) + kEpiWarps + (leader ? 1 : 0));
       }
       mbar_init(smem_u32(&st.mma_done), 1);
       mbar_fence_init();
@@ -181,19 +307,21 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------- TMA producer
-      tma_prefetch_desc(&mapA);
-      tma_prefetch_desc(&mapB);
+      tma_prefetch_desc(&mapT);
+      tma_prefetch_desc(&mapW);
       const int h = static_cast<int>(crank);
       int stage = 0;
       uint32_t phase = 0, used = 0, last_phase = 0;
       bool ok = true;
-      for (int tile = first; tile < total && ok; tile += step) {
-        int e, mp, nt;
-        decode_tile(tile, st.tiles_before, E, NT, e, mp, nt);
-        const int row0 = st.row_start[e] + (2 * mp + h) * BM;
-        // half 0 of a gated block: gate rows, half 1: the matching up rows
-        const int n0 = kGated ? h * p.F + nt * (BN / 2) : nt * BN + h * (BN / 2);
-        for (int kb = 0; kb < KB; ++kb) {
+      Item it;
+      ItemReader items;
+      while (ok && items.next(st, it, false, true, abort_flag, p.status)) {
+        // two boxes of 64 weight rows: gated, gate rows and the matching up rows
+        const int n0 = kGated ? it.nt * BM + h * (BM / 2) : it.nt * 2 * BM + h * BM;
+        const int n1 = kGated ? p.F + n0 : n0 + BM / 2;
+        const int half = columns_of(it) / 2;  // a multiple of 16
+        const int r0 = it.row0 + h * half;
+        for (int c = 0; c < p.K; c += RK) {
           if (!mbar_wait_bounded(smem_u32(&st.raw_empty[stage]), phase ^ 1u, abort_flag,
                                  p.status)) {
             ok = false;
@@ -201,9 +329,11 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
           }
           const uint32_t bar = smem_u32(&st.raw_full[stage]);
           const uint32_t sa = sbase + stage * RAW_BYTES;
-          mbar_arrive_expect_tx(bar, RAW_BYTES);
-          tma_load_2d(sa, &mapA, bar, kb * BK, row0);
-          tma_load_3d(sa + RAW_HALF, &mapB, bar, kb * BK, n0, e);
+          mbar_arrive_expect_tx(bar, RAW_A + half * RK);
+          tma_load_3d(sa, &mapW, bar, c, n0, it.e);
+          tma_load_3d(sa + RAW_A / 2, &mapW, bar, c, n1, it.e);
+          for (int i = 0; i < half; i += kBoxRows)
+            tma_load_2d(sa + RAW_A + i * RK, &mapT, bar, c, r0 + i);
           used |= 1u << stage;
           last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == RAW) {
@@ -218,82 +348,179 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
           (void)mbar_wait_bounded(smem_u32(&st.raw_full[s]), (last_phase >> s) & 1u, nullptr,
                                   p.status);
     }
+  } else if (warp == kItemWarp) {
+    if (lane == 0) {
+      // ------------------------------------------------------ work items
+      int slot = 0;
+      uint32_t phase = 0;
+      for (int i = first;; i += step) {
+        Item it{0, 0, 0, -1};
+        if (i < total) it = item_of(i, p, st);
+        if (!mbar_wait_bounded(smem_u32(&st.item_empty[slot]), phase ^ 1u, abort_flag, p.status))
+          break;
+        st.item[slot] = it;
+        mbar_arrive(smem_u32(&st.item_full[slot]));
+        if (i >= total) break;
+        if (++slot == kItems) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if ((blockIdx.x & 1u) == 0) {
       // ------------------------------------------------ MMA issuer (even CTA)
+      // The whole warp runs the loop and one lane issues: in a branch of one
+      // lane the compiler moves every operand of every MMA to a uniform
+      // register anew, 70 cycles an MMA. All of TMEM is ours, so it starts at
+      // column 0.
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      bool ok = true;
-      for (int tile = first; tile < total && ok; tile += step) {
+      bool ok = tmem_base == 0;
+      const uint64_t desc0 = make_sdesc(sbase + kWideAt, 16, 1024);
+      Item it;
+      ItemReader items;
+      while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
+        const uint32_t idesc = idesc_f16(__shfl_sync(0xFFFFFFFFu, columns_of(it), 0));
         if (!mbar_wait_bounded(smem_u32(&st.tempty[acc]), acc_phase ^ 1u, abort_flag, p.status))
           break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * BN;
-        for (int kb = 0; kb < KB; ++kb) {
+        const uint32_t d_tmem = acc * BN;
+        for (int c = 0; c < p.K; c += RK) {
           if (!mbar_wait_bounded(smem_u32(&st.ready[stage]), phase, abort_flag, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = sbase + kWideAt + stage * WIDE_BYTES;
+          const uint64_t desc = desc0 + stage * (WIDE_BYTES >> 4);
+          const uint32_t ta = kTmemA + stage * kStepCols;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            tc_mma_bf16_pair(d_tmem, make_sdesc(sa + kk * 32, 16, 1024),
-                             make_sdesc(sa + WIDE_HALF + kk * 32, 16, 1024), kIdesc,
-                             (kb | kk) != 0 ? 1u : 0u);
-          tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              tc_mma_f16_pair_ta(d_tmem, ta + kk * 8, desc + kk * 2, idesc,
+                                 (c | kk) != 0 ? 1u : 0u);
+            if (c + BK < p.K) {
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)
+                tc_mma_f16_pair_ta(d_tmem, ta + BK / 2 + kk * 8,
+                                   desc + (WIDE_HALF >> 4) + kk * 2, idesc, 1u);
+            }
+            tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
+          }
+          __syncwarp();
           if (++stage == WIDE) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        tc_commit_pair_mc(smem_u32(&st.tfull[acc]), kPairMask);
+        if (elect_one()) tc_commit_pair_mc(smem_u32(&st.tfull[acc]), kPairMask);
+        __syncwarp();
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      tc_commit_pair(smem_u32(&st.mma_done));
-      (void)mbar_wait_bounded(smem_u32(&st.mma_done), 0, nullptr, p.status);
+      if (elect_one()) {
+        tc_commit_pair(smem_u32(&st.mma_done));
+        (void)mbar_wait_bounded(smem_u32(&st.mma_done), 0, nullptr, p.status);
+      }
+      __syncwarp();
     }
-  } else if (warp >= kFirstWide) {
+  } else if (warp >= kFirstA && warp < kFirstEpi) {
     // -------------------------------------------------------------- widen
-    // 1024 pieces of 16 codes per step, A rows then B rows, four per row: a
-    // warp reads 512 consecutive bytes and writes two swizzled 16-byte
-    // pieces per lane, both free of bank conflicts.
-    const int t = threadIdx.x - 32 * kFirstWide;
+    const bool weights = warp < kFirstB;
+    const int q = warp & 3;
+    const int group = weights ? (warp - kFirstA) / kAWarps : (warp - kFirstB) / kBWarps;
+    // Raw rows are 128 bytes, their 16-byte pieces swizzled by TMA: eight lanes
+    // that read the same piece of eight rows hit all banks. A weight lane takes
+    // its row's four pieces of the group's half; a token warp widens eight rows
+    // at a time, a lane one piece of 16 codes into two swizzled 16-byte pieces,
+    // kBWarps * 8 rows further every turn. All offsets are set here: the loop
+    // is bound by its instructions.
+    const int row = weights ? q * 32 + lane
+                            : (warp - kFirstB - group * kBWarps) * 8 + (lane & 7);
+    const int piece = weights ? 0 : lane >> 3;
+    const uint8_t* from = smem + (weights ? 0 : RAW_A) + row * RK +
+                          (((4 * group + piece) ^ (row & 7)) << 4);
+    const uint32_t flip = (reinterpret_cast<uintptr_t>(from) & 0x70u);  // to reach piece i: ^ i << 4
+    uint8_t* to = smem + kWideAt + group * WIDE_HALF + row * 128;
+    const uint32_t to0 = ((2 * piece) ^ (row & 7)) << 4, to1 = ((2 * piece + 1) ^ (row & 7)) << 4;
+    const uint32_t ta0 = tmem_base + kTmemA + (static_cast<uint32_t>(q * 32) << 16) +
+                         group * (BK / 2);
+    const uint32_t bars = smem_u32(&st.raw_full[0]);
+    const uint32_t empty_raw = smem_u32(&st.raw_empty[0]);
+    const uint32_t empty_bar = smem_u32(&st.empty[0]);
+    const uint32_t ready_bar = mapa_shared(smem_u32(&st.ready[0]), 0);
     int rs = 0, ws = 0;
     uint32_t rp = 0, wp = 0, used = 0, last_phase = 0;
     bool ok = true;
-    for (int tile = first; tile < total && ok; tile += step) {
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!mbar_wait_bounded(smem_u32(&st.raw_full[rs]), rp, abort_flag, p.status) ||
-            !mbar_wait_bounded(smem_u32(&st.empty[ws]), wp ^ 1u, abort_flag, p.status)) {
+    Item it;
+    ItemReader items;
+    while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
+      const int turns = columns_of(it) / 2 / (8 * kBWarps);  // of a token warp
+      for (int k0 = 0; k0 < p.K; k0 += RK) {
+        // K an odd multiple of 64: the last step has one half
+        const bool there = k0 + group * BK < p.K;
+        if (!mbar_wait_bounded(bars + 8 * rs, rp, abort_flag, p.status)) {
           ok = false;
           break;
         }
-        const uint4* raw = reinterpret_cast<const uint4*>(smem + rs * RAW_BYTES);
-        uint8_t* wide = smem + kWideAt + ws * WIDE_BYTES;
+        const uint8_t* raw = from + rs * RAW_BYTES;
+        if (weights) {
+          uint4 c[4];
 #pragma unroll
-        for (int j = 0; j < 1024 / (32 * kWideWarps); ++j) {
-          const int i = t + j * 32 * kWideWarps;
-          const uint4 q = raw[i];
-          const int row = i >> 2;  // 0..255: A rows, then B rows
-          uint8_t* line = wide + row * 128;
-          const uint2 a = widen4(q.x), b = widen4(q.y), c = widen4(q.z), d = widen4(q.w);
-          const int piece = (i & 3) * 2;
-          *reinterpret_cast<uint4*>(line + ((piece ^ (row & 7)) << 4)) =
-              make_uint4(a.x, a.y, b.x, b.y);
-          *reinterpret_cast<uint4*>(line + (((piece + 1) ^ (row & 7)) << 4)) =
-              make_uint4(c.x, c.y, d.x, d.y);
+          for (int i = 0; i < 4; ++i)
+            c[i] = *reinterpret_cast<const uint4*>(raw - flip + (flip ^ (i << 4)));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty_raw + 8 * rs);
+          uint32_t w[2][16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint2 f = widen4((&c[i / 4].x)[i % 4]);
+            w[i / 8][2 * (i % 8)] = f.x;
+            w[i / 8][2 * (i % 8) + 1] = f.y;
+          }
+          if (!mbar_wait_bounded(empty_bar + 8 * ws, wp ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (there) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) tmem_st16(ta0 + ws * kStepCols + 16 * h, w[h]);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+        } else {
+          // the codes are read ahead of the wait for the place they go to
+          constexpr int kTurns = BN / 2 / (8 * kBWarps);
+          uint4 c[kTurns];
+#pragma unroll
+          for (int j = 0; j < kTurns; ++j)
+            if (j < turns) c[j] = *reinterpret_cast<const uint4*>(raw + j * 8 * kBWarps * RK);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty_raw + 8 * rs);
+          if (!mbar_wait_bounded(empty_bar + 8 * ws, wp ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          if (there) {
+            uint8_t* wide = to + ws * WIDE_BYTES;
+#pragma unroll
+            for (int j = 0; j < kTurns; ++j)
+              if (j < turns) {
+                uint8_t* line = wide + j * 8 * kBWarps * 128;
+                const uint2 a = widen4(c[j].x), b = widen4(c[j].y);
+                const uint2 d = widen4(c[j].z), e = widen4(c[j].w);
+                *reinterpret_cast<uint4*>(line + to0) = make_uint4(a.x, a.y, b.x, b.y);
+                *reinterpret_cast<uint4*>(line + to1) = make_uint4(d.x, d.y, e.x, e.y);
+              }
+          }
+          fence_proxy_async();
         }
-        fence_proxy_async();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&st.raw_empty[rs]));
-          mbar_arrive_cluster_cta(mapa_shared(smem_u32(&st.ready[ws]), 0));
-        }
+        if (lane == 0) mbar_arrive_cluster_cta(ready_bar + 8 * ws);
         used |= 1u << ws;
         last_phase = (last_phase & ~(1u << ws)) | (wp << ws);
         if (++rs == RAW) {
@@ -306,69 +533,108 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
         }
       }
     }
-    // the pair's MMAs read both CTAs' shared memory: wait for the last ones
+    // the pair's MMAs read both CTAs' memory: wait for the last ones
     if (lane == 0)
       for (int s = 0; s < WIDE; ++s)
         if (used & (1u << s))
           (void)mbar_wait_bounded(smem_u32(&st.empty[s]), (last_phase >> s) & 1u, nullptr,
                                   p.status);
-  } else {
+  } else if (warp >= kFirstEpi) {
     // ---------------------------------------------------------- epilogue
+    // One warp per lane quadrant, 32 tokens at a time. Gated: quadrants 0 and 1
+    // are gate rows, 2 and 3 the matching up rows.
     const int q = warp & 3;
-    const int half = (warp - 2) >> 2;
-    const int r = q * 32 + lane;
+    const int w = warp - kFirstEpi;
+    const bool up = kGated && q >= 2;
+    const int pair = q & 1;
+    const int width = kGated ? p.F : p.N;
+    uint4* stg = reinterpret_cast<uint4*>(smem + kStagingAt + w * kWarpStagingBytes);
+    float* ups = reinterpret_cast<float*>(smem + kUpAt + pair * kUpBytes);
     int acc = 0;
     uint32_t acc_phase = 0;
-    uint4* stg = reinterpret_cast<uint4*>(smem + kStagingAt + (warp - 2) * kWarpStagingBytes);
-    for (int tile = first; tile < total; tile += step) {
-      int e, mp, nt;
-      decode_tile(tile, st.tiles_before, E, NT, e, mp, nt);
-      const long long grow =
-          static_cast<long long>(st.row_start[e]) + (2 * mp + static_cast<int>(crank)) * BM + r;
-      const long long row_end = st.row_start[e + 1];
-      const long long grow0 = grow - lane;
-      const int nvalid = static_cast<int>(max(0LL, min(32LL, row_end - grow0)));
-      const float sr = grow < row_end ? p.As[grow] : 0.0f;
-      const float pr = kGated && p.row_scale != nullptr && grow < row_end ? p.row_scale[grow]
-                                                                          : 1.0f;
-      const int width = kGated ? p.F : p.N;
-      const int n0 = nt * (kGated ? BN / 2 : BN);
-      constexpr int kCols = (kGated ? BN / 2 : BN) / (kEpiWarps / 4);  // of the block's, per warp
-      const int c0 = half * kCols;
-      const float* bs = p.Bs + static_cast<long long>(e) * p.N + n0;
-      gg_bf16* crow0 = p.C + grow0 * width + n0;
+    uint32_t up_phase = 0;
+    bool ok = true;
+    Item it;
+    ItemReader items;
+    while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
+      const int n0 = kGated ? it.nt * BM + static_cast<int>(crank) * (BM / 2) + (q & 1) * 32
+                            : it.nt * 2 * BM + static_cast<int>(crank) * BM + q * 32;
+      const bool exists = n0 < width;  // 32 channels exist together: widths are multiples of 64
+      const float tn =
+          exists ? __ldg(p.Bs + static_cast<long long>(it.e) * p.N + (up ? p.F : 0) + n0 + lane)
+                 : 0.0f;
+      // the tokens' scales, lane by lane for every chunk, ahead of the sums
+      float sc[BN / 32];
+#pragma unroll
+      for (int i = 0; i < BN / 32; ++i) {
+        const int r = 32 * i + lane;
+        sc[i] = r < it.rows ? p.As[it.row0 + r] : 0.0f;
+        if (up && p.row_scale != nullptr && r < it.rows) sc[i] *= p.row_scale[it.row0 + r];
+      }
       if (!mbar_wait_bounded(smem_u32(&st.tfull[acc]), acc_phase, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
 #pragma unroll 1
-      for (int c = c0; c < c0 + kCols; c += 32) {
-        if (n0 + c >= width) break;
+      for (int c = 0; c < it.rows; c += 32) {
+        const int have = min(32, it.rows - c);
+        const long long r0 = static_cast<long long>(it.row0) + c;
+        st.scale[w][lane] = sc[0];
+#pragma unroll
+        for (int i = 0; i + 1 < BN / 32; ++i) sc[i] = sc[i + 1];
         float v[32];
         tmem_ld32(tbase + c, v);
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-          const float4 s = __ldg(reinterpret_cast<const float4*>(bs + c + i));
-          v[i] *= sr * s.x;
-          v[i + 1] *= sr * s.y;
-          v[i + 2] *= sr * s.z;
-          v[i + 3] *= sr * s.w;
+          const float4 f = *reinterpret_cast<const float4*>(&st.scale[w][i]);
+          v[i] *= tn * f.x;
+          v[i + 1] *= tn * f.y;
+          v[i + 2] *= tn * f.z;
+          v[i + 3] *= tn * f.w;
+        }
+        if (up) {
+          if (!mbar_wait_bounded(smem_u32(&st.up_empty[pair]), up_phase ^ 1u, abort_flag,
+                                 p.status)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ups[i * 32 + lane] = v[i];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&st.up_full[pair]));
+          up_phase ^= 1u;
+          continue;
         }
         if (kGated) {
-          float u[32];
-          tmem_ld32(tbase + BN / 2 + c, u);
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 s = __ldg(reinterpret_cast<const float4*>(bs + p.F + c + i));
-            v[i] = glu_mul(v[i], u[i] * (sr * s.x), alpha, true, pr);
-            v[i + 1] = glu_mul(v[i + 1], u[i + 1] * (sr * s.y), alpha, true, pr);
-            v[i + 2] = glu_mul(v[i + 2], u[i + 2] * (sr * s.z), alpha, true, pr);
-            v[i + 3] = glu_mul(v[i + 3], u[i + 3] * (sr * s.w), alpha, true, pr);
+          if (!mbar_wait_bounded(smem_u32(&st.up_full[pair]), up_phase, abort_flag, p.status)) {
+            ok = false;
+            break;
           }
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] = glu_mul(v[i], ups[i * 32 + lane], p.alpha, false, 1.0f);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&st.up_empty[pair]));
+          up_phase ^= 1u;
         }
-        uint4 w[4];
-        pack_bf16x32(v, 1.0f, w);
-        store_chunk(stg, w, crow0 + c, width, nvalid);
+        // [token][channel] through the staging buffer: four lanes then write each
+        // token's 64-byte segment
+        uint16_t* cell = reinterpret_cast<uint16_t*>(stg);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          cell[stage_slot(i, lane >> 3) * 8 + (lane & 7)] =
+              __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = 8 * j + (lane >> 2);
+          const uint4 x = stg[stage_slot(i, lane & 3)];
+          if (exists && i < have)
+            reinterpret_cast<uint4*>(p.C + (r0 + i) * width + n0)[lane & 3] = x;
+        }
+        __syncwarp();
       }
+      if (!ok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&st.tempty[acc]), 0));
@@ -387,32 +653,32 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
 }
 
 template <bool kGated>
-cudaError_t launch_q8_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const QParams& p,
-                             float alpha, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_q8_gemm_t(const CUtensorMap& mt, const CUtensorMap& mw, const QParams& p,
+                             const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<int> resident[kMaxDevices];
   // no more clusters than there can be work items
   const long long items =
-      (static_cast<long long>(p.R_cap) / (2 * BM) + (p.R_cap < p.E ? p.R_cap : p.E)) * p.NT;
+      (static_cast<long long>(p.R_cap) / BN + (p.R_cap < p.E ? p.R_cap : p.E)) * p.NT;
   const int most = static_cast<int>(items < 1 ? 1 : (items < 0x7FFFFFFF ? items : 0x7FFFFFFF));
   return launch_pairs(q8_gemm_kernel<kGated>, resident, kThreads, kSmemBytes, most, dev, stream,
-                      ma, mb, p, alpha);
+                      mt, mw, p);
 }
 
 }  // namespace
 
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  CUtensorMap ma, mb;
-  const cuuint64_t ad[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.R_cap)};
-  const cuuint64_t as[1] = {static_cast<cuuint64_t>(a.K)};
-  const cuuint32_t abox[2] = {BK, BM};
-  const cuuint64_t bd[3] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.N),
+  CUtensorMap mt, mw;
+  const cuuint64_t td[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.R_cap)};
+  const cuuint64_t ts[1] = {static_cast<cuuint64_t>(a.K)};
+  const cuuint32_t tbox[2] = {RK, kBoxRows};
+  const cuuint64_t wd[3] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.N),
                             static_cast<cuuint64_t>(a.E)};
-  const cuuint64_t bs[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.K) * a.N};
-  const cuuint32_t bbox[3] = {BK, BN / 2, 1};
-  if (!encode_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, 2, ad, as, abox,
-                  CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, bd, bs, bbox,
-                  CU_TENSOR_MAP_SWIZZLE_NONE))
+  const cuuint64_t ws[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.K) * a.N};
+  const cuuint32_t wbox[3] = {RK, BM / 2, 1};
+  if (!encode_map(&mt, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, 2, td, ts, tbox,
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, wd, ws, wbox,
+                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   QParams p{};
   p.offsets = a.offsets;
@@ -424,14 +690,15 @@ cudaError_t launch_q8_gemm(const Q8GemmArgs& a, const DeviceInfo& dev, cudaStrea
   p.As = a.As;
   p.Bs = a.Bs;
   p.row_scale = a.row_scale;
+  p.alpha = a.alpha;
   p.C = a.C;
   p.status = a.status;
   if (a.alpha != 0.0f) {
-    p.NT = (p.F + BN / 2 - 1) / (BN / 2);
-    return launch_q8_gemm_t<true>(ma, mb, p, a.alpha, dev, stream);
+    p.NT = (p.F + BM - 1) / BM;
+    return launch_q8_gemm_t<true>(mt, mw, p, dev, stream);
   }
-  p.NT = (a.N + BN - 1) / BN;
-  return launch_q8_gemm_t<false>(ma, mb, p, 1.0f, dev, stream);
+  p.NT = (a.N + 2 * BM - 1) / (2 * BM);
+  return launch_q8_gemm_t<false>(mt, mw, p, dev, stream);
 }
 
 }  // namespace gg

@@ -33,6 +33,17 @@ __device__ __forceinline__ void set_status(int32_t* status, int code) {
   if (status != nullptr) atomicCAS(status, 0, code);
 }
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xFFFFFFFF;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // ------------------------------------------- programmatic dependent launch
 // A kernel launched with programmatic stream serialisation may start while
 // the kernel ahead of it in the stream is still running. grid_dependency_wait
