@@ -500,55 +500,68 @@ wgrad_kernel(const __grid_constant__ CUtensorMap mapD, const __grid_constant__ C
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if ((blockIdx.x & 1u) == 0) {
       // ------------------------------------------------ MMA issuer (even CTA)
+      // The whole warp runs the loop and one lane issues: in a branch of one
+      // lane the compiler moves every operand of every MMA to a uniform
+      // register anew. All of TMEM is ours, so it starts at column 0.
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      bool ok = true;
+      bool ok = tmem_base == 0;
+      const uint64_t desc_d = make_sdesc(sbase, BOX_BYTES, 1024);
       Item it;
       ItemReader items;
-      while (ok && items.next(st, it, false, true, abort_flag, p.status)) {
-        const uint32_t idesc =
-            make_idesc_bf16(2 * BM, min(p.width, p.K - it.nt * p.width), true, true);
-        const int chunk = kF32 ? kChunk * BK : it.rows;
-        for (int c0 = 0; c0 < it.rows && ok; c0 += chunk) {
+      while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
+        const int rows = __shfl_sync(0xFFFFFFFFu, it.rows, 0);
+        const uint32_t idesc = make_idesc_bf16(
+            2 * BM, __shfl_sync(0xFFFFFFFFu, min(p.width, p.K - it.nt * p.width), 0), true, true);
+        const int chunk = kF32 ? kChunk * BK : rows;
+        for (int c0 = 0; c0 < rows && ok; c0 += chunk) {
           if (!mbar_wait_bounded(smem_u32(&st.tempty[acc]), acc_phase ^ 1u, abort_flag,
                                  p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t d_tmem = tmem_base + acc * BN;
-          const int c1 = min(it.rows, c0 + chunk);
+          const uint32_t d_tmem = acc * BN;
+          const int c1 = min(rows, c0 + chunk);
           for (int r = c0; r < c1; r += BK) {
             if (!mbar_wait_bounded(smem_u32(&st.ready[stage]), phase, abort_flag, p.status)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t sa = sbase + stage * STAGE_BYTES;
-            const int groups = min(BK / 16, (it.rows - r + 15) / 16);
-            for (int kk = 0; kk < groups; ++kk) {
-              const uint64_t adesc = make_sdesc(sa + kk * 2048, BOX_BYTES, 1024);
-              const uint64_t bdesc = make_sdesc(sa + A_BYTES + kk * 2048, BOX_BYTES, 1024);
-              tc_mma_bf16_pair(d_tmem, adesc, bdesc, idesc, (r - c0) | kk ? 1u : 0u);
+            const uint64_t desc = desc_d + stage * (STAGE_BYTES >> 4);
+            if (elect_one()) {
+              const int groups = min(BK / 16, (rows - r + 15) / 16);
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)
+                if (kk < groups)
+                  tc_mma_bf16_pair(d_tmem, desc + kk * (2048 >> 4),
+                                   desc + ((A_BYTES + kk * 2048) >> 4), idesc,
+                                   (r - c0) | kk ? 1u : 0u);
+              tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
             }
-            tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
+            __syncwarp();
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1u;
             }
           }
           if (!ok) break;
-          tc_commit_pair_mc(smem_u32(&st.tfull[acc]), kPairMask);
+          if (elect_one()) tc_commit_pair_mc(smem_u32(&st.tfull[acc]), kPairMask);
+          __syncwarp();
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1u;
         }
       }
-      tc_commit_pair(smem_u32(&st.mma_done));
-      (void)mbar_wait_bounded(smem_u32(&st.mma_done), 0, nullptr, p.status);
+      if (elect_one()) {
+        tc_commit_pair(smem_u32(&st.mma_done));
+        (void)mbar_wait_bounded(smem_u32(&st.mma_done), 0, nullptr, p.status);
+      }
+      __syncwarp();
     }
   } else {
     // ---------------------------------------------------------- epilogue
