@@ -2,13 +2,20 @@
 // logits per token with their probabilities, the tokens per expert, the
 // balance and z losses, and the gradient of the logits.
 //
-// One warp holds one token's logits in registers (column c in lane c % 32),
-// so every statistic of the row (maximum, sums of the scores, the picks) is a
-// warp reduction and the row is read once. Selection works on the logits
-// themselves, which both scores preserve the order of, as order-preserving
-// 32-bit keys: the picks do not depend on how an exponential rounds, and
-// equal logits go to the lower expert id. Everything is held in fp32; logits'
-// gradients are rounded once to the logits' type.
+// A token's logits lie in the registers of 8 lanes (four tokens per warp,
+// column c in lane c % 8), or of 32 where there are more than 256 experts or
+// 16 picks. The row is read once. With 8 lanes the picks come from sorting
+// networks: every lane keeps the largest of its own columns, block by block,
+// and three exchanges merge the lanes; sums over a row take three shuffles.
+// That is 90 (BF16) to 200 (fp32, 64-bit keys) instructions per token of 128
+// logits, against about 500 with one warp per token and a search and two
+// reductions per pick. Measured (events, 4 us of them launch): see the
+// launches below.
+//
+// Selection works on the logits themselves, which both scores preserve the
+// order of, as order-preserving keys: the picks do not depend on how an
+// exponential rounds, and equal logits go to the lower expert id. Everything
+// is held in fp32; logits' gradients are rounded once to the logits' type.
 
 #include <cuda_runtime.h>
 
@@ -67,6 +74,7 @@ struct RouteParams {
   int T, E, k;
   int sigmoid, renorm;
   float scale;
+  int words;         // BF16 rows are whole, aligned 32-bit words
   int32_t* idx;
   float* prob;
   float* part_p;     // [blocks][E] sums over the block's rows of score / row sum, or null
@@ -74,6 +82,24 @@ struct RouteParams {
   float* part_z;     // [blocks] sums of logsumexp^2
   int want_losses;
 };
+
+// A block's sums over its warps, as one row of the partials.
+__device__ __forceinline__ void store_partials(const float* sums, const int* hist, const float* zs,
+                                               const RouteParams& p) {
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    float a = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) a += sums[w * p.E + e];
+    p.part_p[static_cast<long long>(blockIdx.x) * p.E + e] = a;
+    p.part_n[static_cast<long long>(blockIdx.x) * p.E + e] = hist[e];
+  }
+  if (threadIdx.x == 0) {
+    float a = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) a += zs[w];
+    p.part_z[blockIdx.x] = a;
+  }
+}
 
 template <typename X, int V, bool kStats>
 __global__ void __launch_bounds__(kThreads)
@@ -88,6 +114,7 @@ route_kernel(const X* __restrict__ x, const RouteParams p) {
   if (kStats) {
 #pragma unroll
     for (int i = 0; i < V; ++i) pacc[i] = 0.0f;
+    grid_dependents_launch();
     for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
     __syncthreads();
   }
@@ -168,72 +195,74 @@ route_kernel(const X* __restrict__ x, const RouteParams p) {
     float* zs = reinterpret_cast<float*>(hist + E);
     if (lane == 0) zs[warp] = zacc;
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      float a = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) a += sh[w * E + e];
-      p.part_p[static_cast<long long>(blockIdx.x) * E + e] = a;
-      p.part_n[static_cast<long long>(blockIdx.x) * E + e] = hist[e];
-    }
-    if (threadIdx.x == 0) {
-      float a = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) a += zs[w];
-      p.part_z[blockIdx.x] = a;
-    }
+    store_partials(sh, hist, zs, p);
   }
 }
 
 // Sums the blocks' partials in a fixed order: counts[e], and losses[0] =
 // E sum_e f_e P_e with f_e = counts[e] / (T k) and P_e the mean share of e,
-// losses[1] = mean logsumexp^2.
+// losses[1] = mean logsumexp^2. One cluster: each of its blocks takes 32
+// columns at a time, 32 threads to a column (one block alone waited 27 us for
+// its loads at 256 experts).
 constexpr int kFinThreads = 1024;
-__global__ void __launch_bounds__(kFinThreads)
+constexpr int kFinBlocks = 8;
+__global__ void __cluster_dims__(kFinBlocks, 1, 1) __launch_bounds__(kFinThreads)
 route_finalise_kernel(const float* part_p, const int32_t* part_n, const float* part_z, int blocks,
                       int T, int E, int k, int32_t* counts, float* losses) {
-  __shared__ float sp[kFinThreads];
-  __shared__ int sn[kFinThreads];
-  const int tid = threadIdx.x;
-  int cols = 32;  // columns handled side by side, a power of two >= min(E, 1024)
-  while (cols < E) cols *= 2;
-  const int groups = kFinThreads / cols;
-  const int e = tid & (cols - 1), g = tid / cols;
-  float a = 0.0f;
-  int n = 0;
-  if (e < E)
-    for (int b = g; b < blocks; b += groups) {
-      a += part_p[static_cast<long long>(b) * E + e];
-      n += part_n[static_cast<long long>(b) * E + e];
+  __shared__ float sp[32][33];
+  __shared__ int sn[32][33];
+  __shared__ float terms[kFinBlocks];  // of block 0: every block's share of the balance loss
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int rank = static_cast<int>(cluster_ctarank());
+  grid_dependency_wait();
+  float term = 0.0f;  // warp 0, by lane
+  for (int e0 = rank * 32; e0 < E; e0 += 32 * kFinBlocks) {
+    const int e = e0 + lane;
+    float a = 0.0f;
+    int n = 0;
+    if (e < E)
+#pragma unroll 5
+      for (int b = warp; b < blocks; b += 32) {
+        a += part_p[static_cast<long long>(b) * E + e];
+        n += part_n[static_cast<long long>(b) * E + e];
+      }
+    sp[warp][lane] = a;
+    sn[warp][lane] = n;
+    __syncthreads();
+    if (warp == 0 && e < E) {
+      a = 0.0f;
+      n = 0;
+#pragma unroll
+      for (int q = 0; q < 32; ++q) {
+        a += sp[q][lane];
+        n += sn[q][lane];
+      }
+      if (counts != nullptr) counts[e] = n;
+      if (T > 0)
+        term += static_cast<float>(n) / (static_cast<float>(T) * static_cast<float>(k)) *
+                (a / static_cast<float>(T)) * static_cast<float>(E);
     }
-  sp[tid] = a;
-  sn[tid] = n;
-  __syncthreads();
-  float term = 0.0f;
-  if (g == 0 && e < E) {
-    for (int q = 1; q < groups; ++q) {
-      a += sp[q * cols + e];
-      n += sn[q * cols + e];
-    }
-    if (counts != nullptr) counts[e] = n;
-    if (T > 0)
-      term = static_cast<float>(n) / (static_cast<float>(T) * static_cast<float>(k)) *
-             (a / static_cast<float>(T)) * static_cast<float>(E);
+    __syncthreads();
   }
-  float z = 0.0f;
-  for (int b = tid; b < blocks; b += kFinThreads) z += part_z[b];
-  __syncthreads();
-  term = warp_sum(term);
-  z = warp_sum(z);
-  if ((tid & 31) == 0) {
-    sp[tid >> 5] = term;
-    sp[32 + (tid >> 5)] = z;
+  if (warp == 0) {
+    term = warp_sum(term);
+    if (lane == 0)
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(
+                       smem_u32(&terms[rank]), 0)),
+                   "f"(term)
+                   : "memory");
   }
-  __syncthreads();
-  if (tid < 32 && losses != nullptr) {
-    term = warp_sum(sp[tid]);
-    z = warp_sum(sp[32 + tid]);
-    if (tid == 0) {
-      losses[0] = term;
+  cluster_sync();
+  if (rank == 0 && warp == 0 && losses != nullptr) {
+    float z = 0.0f;
+    for (int b = lane; b < blocks; b += 32) z += part_z[b];
+    z = warp_sum(z);
+    if (lane == 0) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int r = 0; r < kFinBlocks; ++r) sum += terms[r];
+      losses[0] = sum;
       losses[1] = T > 0 ? z / static_cast<float>(T) : 0.0f;
     }
   }
@@ -250,118 +279,442 @@ struct RouteBwdParams {
   int32_t* status;        // or null
 };
 
-template <typename X, int V>
+// The fast exponential and divide: a few units of fp32, times the size of the
+// exponent, on gradients.
+__device__ __forceinline__ float fast_sigmoid(float v) {
+  return __fdividef(1.0f, 1.0f + __expf(-v));
+}
+
+// kL lanes per token, at least k (column c in lane c % kL). Every column's
+// gradient without its picks is written first, then the picks' lanes write
+// theirs over it. The sums over the row are taken together, and the next row
+// is on its way meanwhile. Eight lanes up to 64 experts and 8 picks, else a
+// warp: 121088 tokens, 32 experts 25 us against 41; 256 experts 242 against
+// 128 (more sums per lane than a warp's threads hide).
+template <typename X, int V, int kL>
 __global__ void __launch_bounds__(kThreads)
 route_bwd_kernel(const X* x, const RouteBwdParams p, X* dx) {
-  const int lane = threadIdx.x & 31;
-  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x % kL;
+  const int base = threadIdx.x & 31 & ~(kL - 1);  // the token's first lane
   const int E = p.E, k = p.k;
   const float inv_T = 1.0f / static_cast<float>(p.T);
+  const bool aux = p.aux != 0.0f, zl = p.z != 0.0f;
+  const bool soft = !p.sigmoid || zl;  // the softmax is needed
+  const float per_pick = static_cast<float>(E) / (static_cast<float>(p.T) * static_cast<float>(k));
   float load[V];  // E f_e: what the balance loss weighs expert e's mean share with
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = lane + 32 * i;
-    load[i] = p.counts != nullptr && c < E
-                  ? static_cast<float>(E) * static_cast<float>(p.counts[c]) /
-                        (static_cast<float>(p.T) * static_cast<float>(k))
-                  : 0.0f;
+    const int c = lane + kL * i;
+    load[i] = aux && c < E ? per_pick * static_cast<float>(p.counts[c]) : 0.0f;
   }
-  for (long long t = static_cast<long long>(blockIdx.x) * kWarps + warp; t < p.T;
-       t += static_cast<long long>(gridDim.x) * kWarps) {
-    float v[V];
-    const X* row = x + t * E;
-    load_row<X, V>(row, E, lane, v);
-    int id = -1;
-    float g = 0.0f, picked = -INFINITY;
-    if (lane < k) {
-      id = p.idx[t * k + lane];
-      if (id < 0 || id >= E) {
-        set_status(p.status, GG_ERR_DEVICE_BAD_EXPERT_ID);
-        id = -1;
-      } else {
-        g = p.dprob[t * k + lane];
-        picked = to_f32(row[id]);
-      }
+  constexpr int kTokens = kThreads / kL;  // per block
+  const long long step = static_cast<long long>(gridDim.x) * kTokens;
+  long long t = static_cast<long long>(blockIdx.x) * kTokens + threadIdx.x / kL;
+  float v[V];
+  int id = -1;
+  float g = 0.0f, picked = -INFINITY;
+  const auto fetch = [&](long long at, float(&to)[V], int& pick, float& grad) {
+    if (at >= p.T) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = lane + kL * i;
+      to[i] = c < E ? to_f32(x[at * E + c]) : -INFINITY;
     }
+    if (lane < k) {
+      pick = p.idx[at * k + lane];
+      grad = p.dprob[at * k + lane];
+    }
+  };
+  fetch(t, v, id, g);
+  // a warp's lanes stay together: tokens past the end do not load or store
+  for (long long first = t - (base / kL); first < p.T; first += step, t += step) {
+    const bool here = t < p.T;
+    const X* row = x + t * E;
+    if (here && lane < k && (id < 0 || id >= E)) {
+      set_status(p.status, GG_ERR_DEVICE_BAD_EXPERT_ID);
+      id = -1;
+      g = 0.0f;
+    }
+    picked = id >= 0 ? to_f32(row[id]) : -INFINITY;
+    float next[V];
+    int next_id = -1;
+    float next_g = 0.0f;
+    fetch(t + step, next, next_id, next_g);
+
     float m = v[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-    const bool dead = m == -INFINITY;
-    float soft[V], mass = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) mass += soft[i] = dead ? 0.0f : expf(v[i] - m);
-    mass = warp_sum(mass);
-    const float inv_mass = dead ? 0.0f : 1.0f / mass;
-#pragma unroll
-    for (int i = 0; i < V; ++i) soft[i] *= inv_mass;
-    const float zg = dead ? 0.0f : 2.0f * p.z * inv_T * (m + logf(mass));
-
-    // gradient of this lane's pick: of its score, or (renormalised softmax) of its logit
-    float ps = 0.0f;
-    if (id >= 0 && !dead) ps = p.sigmoid ? sigmoid_of(picked) : expf(picked - m) * inv_mass;
-    float gp = p.scale * g;
-    if (p.renorm) {
-      const float tot = warp_sum(ps);
-      const float share = tot > 0.0f || tot != tot ? ps / tot : 0.0f;
-      const float mean = warp_sum(g * share);
-      gp = p.scale * (g - mean);
-      if (p.sigmoid)
-        gp = tot > 0.0f || tot != tot ? gp / tot : 0.0f;
-      else
-        gp *= share;
-    }
-    const float dot = !p.sigmoid && !p.renorm ? warp_sum(gp * ps) : 0.0f;
-    float add[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) add[i] = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      const int c = __shfl_sync(kFull, id, j);
-      const float gj = __shfl_sync(kFull, gp, j);
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (c == lane + 32 * i) add[i] += gj;
-    }
-    if (p.sigmoid) {
-      float s[V], tot = 0.0f, cs = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        s[i] = sigmoid_of(v[i]);
-        tot += s[i];
-        cs += load[i] * s[i];
-      }
-      float ga = 0.0f, mean = 0.0f;
-      if (p.aux != 0.0f) {
-        tot = warp_sum(tot);
-        mean = warp_sum(cs) / tot;
-        ga = tot > 0.0f || tot != tot ? p.aux * inv_T / tot : 0.0f;
-        if (ga == 0.0f) mean = 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        soft[i] = (add[i] + ga * (load[i] - mean)) * s[i] * (1.0f - s[i]) + zg * soft[i];
+    if constexpr (kL == 32) {
+      m = value_of(__reduce_max_sync(kFull, key_of(m)));
     } else {
-      float cs = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) cs += load[i] * soft[i];
-      const float mean = p.aux != 0.0f ? warp_sum(cs) : 0.0f;
-      const float ga = p.aux * inv_T;
+      for (int d = kL / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+    }
+    const bool dead = m == -INFINITY;
+    // e: exp(v - m); sums of e, of the scores, of load * score, of the picks'
+    // scores and of gradient * score (softmax: all up to 1 / mass)
+    float e[V], sc[V];
+    float mass = 0.0f, st = 0.0f, cs = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float own = p.renorm ? add[i] : soft[i] * (add[i] - dot);
-        soft[i] = own + soft[i] * (ga * (load[i] - mean) + zg);
+    for (int i = 0; i < V; ++i) {
+      e[i] = soft && !dead ? __expf(v[i] - m) : 0.0f;
+      sc[i] = p.sigmoid ? fast_sigmoid(v[i]) : e[i];
+      mass += e[i];
+      st += sc[i];
+      cs += load[i] * sc[i];
+    }
+    float ps = 0.0f;
+    if (id >= 0 && !dead) ps = p.sigmoid ? fast_sigmoid(picked) : __expf(picked - m);
+    float tot = ps, gps = g * ps;
+#pragma unroll
+    for (int d = kL / 2; d > 0; d >>= 1) {
+      if (soft) mass += __shfl_xor_sync(kFull, mass, d);
+      if (aux) {
+        if (p.sigmoid) st += __shfl_xor_sync(kFull, st, d);
+        cs += __shfl_xor_sync(kFull, cs, d);
+      }
+      if (p.renorm) tot += __shfl_xor_sync(kFull, tot, d);
+      gps += __shfl_xor_sync(kFull, gps, d);
+    }
+    const float inv_mass = soft && !dead ? 1.0f / mass : 0.0f;
+    const float zg = dead || !zl ? 0.0f : 2.0f * p.z * inv_T * (m + logf(mass));
+    // gradient of this lane's pick: of its score, or (renormalised softmax) of its logit
+    float gp = p.scale * g, dot = 0.0f;
+    if (p.renorm) {
+      const bool some = tot > 0.0f || tot != tot;
+      gp = some ? p.scale * (g - gps / tot) / tot : 0.0f;
+      if (!p.sigmoid) gp *= ps;  // the factor 1 / mass of both scores cancels
+      if (id < 0) gp = 0.0f;
+    } else if (!p.sigmoid) {
+      dot = p.scale * gps * inv_mass;
+    }
+    float ga = 0.0f, mean = 0.0f;  // balance loss: gradient ga (load - mean) of each share
+    if (aux) {
+      const float total = p.sigmoid ? st : mass;
+      if (!dead && (total > 0.0f || total != total)) {
+        ga = p.sigmoid ? p.aux * inv_T / total : p.aux * inv_T;
+        mean = cs / total;
       }
     }
+    // a column's gradient, add: from its picks
+    const auto grad = [&](float sm, float score, float ld, float add) {
+      if (p.sigmoid) return (add + ga * (ld - mean)) * score * (1.0f - score) + zg * sm;
+      return (p.renorm ? add : sm * (add - dot)) + sm * (ga * (ld - mean) + zg);
+    };
+    X* out = dx + t * E;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < E) store_as(dx + t * E + lane + 32 * i, soft[i]);
+      if (here && lane + kL * i < E)
+        store_as(out + lane + kL * i, grad(e[i] * inv_mass, sc[i], load[i], 0.0f));
+    float add = 0.0f;  // an expert named in several slots gets them all
+    for (int j = 0; j < k; ++j) {
+      const int other = __shfl_sync(kFull, id, base + j);
+      const float gj = __shfl_sync(kFull, gp, base + j);
+      if (other == id) add += gj;
+    }
+    __syncwarp();  // the picks' columns are written after the others
+    if (here && id >= 0) {
+      const float sm = soft && !dead ? __expf(picked - m) * inv_mass : 0.0f;
+      const float ld = aux ? per_pick * static_cast<float>(p.counts[id]) : 0.0f;
+      store_as(out + id, grad(sm, p.sigmoid ? fast_sigmoid(picked) : 0.0f, ld, add));
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = next[i];
+    id = next_id;
+    g = next_g;
   }
+}
+
+// ------------------------------------------------------- eight lanes per token
+
+constexpr int kLanes = 8;
+
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  return v;
+}
+
+// A lane's share of a row in the eight-lane layout, V columns of it, and their
+// sort keys: the order-preserving key of the logit above the complement of its
+// column, all different; 0: no logit.
+template <typename X, int V>
+struct Share;
+
+// fp32: columns l + 8 i, 64-bit keys.
+template <int V>
+struct Share<float, V> {
+  using K = unsigned long long;
+  float v[V];
+  static __device__ __forceinline__ int column(int l, int i) { return l + kLanes * i; }
+  __device__ __forceinline__ void load(const float* row, int E, int l, bool) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = column(l, i) < E ? row[column(l, i)] : -INFINITY;
+  }
+  __device__ __forceinline__ float value(int i) const { return v[i]; }
+  __device__ __forceinline__ K key(int i, int E, int l) const {
+    const int c = column(l, i);
+    return c < E ? static_cast<K>(key_of(v[i])) << 32 | (0xFFFFFFFFu - c) : K(0);
+  }
+  static __device__ __forceinline__ int column_of(K k) {
+    return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k));
+  }
+  static __device__ __forceinline__ float value_of_key(K k) {
+    return value_of(static_cast<uint32_t>(k >> 32));
+  }
+};
+
+// BF16: pairs of columns 2 (l + 8 i), +1, one word each where rows are words;
+// 32-bit keys, made two at a time: adding 0 to the pair turns -0 into +0 and
+// every NaN into the positive one, then the sign's copies flip the bits.
+template <int V>
+struct Share<gg_bf16, V> {
+  using K = uint32_t;
+  uint32_t w[V / 2];
+  static __device__ __forceinline__ int column(int l, int i) {
+    return 2 * (l + kLanes * (i / 2)) + i % 2;
+  }
+  __device__ __forceinline__ void load(const gg_bf16* row, int E, int l, bool words) {
+    if (words) {  // E is even
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        w[i] = column(l, 2 * i) < E
+                   ? reinterpret_cast<const uint32_t*>(row)[l + kLanes * i]
+                   : 0xFF80FF80u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const int c = column(l, 2 * i);
+        const uint32_t lo = c < E ? row[c] : 0xFF80u, hi = c + 1 < E ? row[c + 1] : 0xFF80u;
+        w[i] = hi << 16 | lo;
+      }
+    }
+  }
+  __device__ __forceinline__ float value(int i) const {
+    return i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+  }
+  __device__ __forceinline__ K key(int i, int E, int l) const {
+    const int c = column(l, i);
+    __nv_bfloat162 q = *reinterpret_cast<const __nv_bfloat162*>(&w[i / 2]);
+    q = __hadd2(q, __floats2bfloat162_rn(0.0f, 0.0f));
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&q);
+    uint32_t signs;  // copies of each half's sign bit (selectors with their top bit set)
+    asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(signs) : "r"(u));
+    const uint32_t flip = u ^ (signs | 0x80008000u);
+    const uint32_t low = 0xFFFFu - c;
+    return c < E ? __byte_perm(flip, low, i % 2 ? 0x3254 : 0x1054) : K(0);
+  }
+  static __device__ __forceinline__ int column_of(K k) { return 0xFFFF - (k & 0xFFFFu); }
+  static __device__ __forceinline__ float value_of_key(K k) {
+    return __uint_as_float(__float_as_uint(value_of(k)) & 0xFFFF0000u);
+  }
+};
+
+template <typename K>
+__device__ __forceinline__ void order(K& a, K& b) {  // the larger first
+  const K hi = a > b ? a : b;
+  b = a > b ? b : a;
+  a = hi;
+}
+
+// Odd-even merge sort (Batcher 1968), descending: the network's comparators.
+template <int N>
+struct Network {
+  int n = 0;
+  int a[N * N / 2] = {}, b[N * N / 2] = {};
+  constexpr Network() {
+    for (int p = 1; p < N; p *= 2)
+      for (int k = p; k >= 1; k /= 2)
+        for (int j = k % p; j + k < N; j += 2 * k)
+          for (int i = 0; i < k; ++i)
+            if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+              a[n] = i + j;
+              b[n++] = i + j + k;
+            }
+  }
+};
+
+template <int N, int I = 0, typename K>
+__device__ __forceinline__ void sort_down(K (&v)[N]) {
+  constexpr Network<N> net;
+  if constexpr (I < net.n) {
+    order(v[net.a[I]], v[net.b[I]]);
+    sort_down<N, I + 1>(v);
+  }
+}
+
+// top = the N largest of top and v, both descending: the larger of each pair
+// from opposite ends is one of them, and what results is bitonic.
+template <int N, typename K>
+__device__ __forceinline__ void keep_top(K (&top)[N], const K (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) top[i] = top[i] > v[N - 1 - i] ? top[i] : v[N - 1 - i];
+#pragma unroll
+  for (int d = N / 2; d >= 1; d /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & d) == 0) order(top[i], top[i + d]);
+}
+
+// V: columns per lane; N: picks kept, at least k.
+template <typename X, int V, int N, bool kStats>
+__global__ void __launch_bounds__(kThreads)
+route_group_kernel(const X* __restrict__ x, const RouteParams p) {
+  using Key = Share<X, V>;
+  using K = typename Key::K;
+  constexpr int B = V < N ? V : N;      // block of columns sorted at once
+  constexpr int kMine = N > kLanes ? N / kLanes : 1;  // picks per lane
+  extern __shared__ float sh[];         // kStats: [kWarps][E] sums, int [E] picks, [kWarps] z
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int l = lane & (kLanes - 1);
+  const int E = p.E, k = p.k;
+  int* hist = reinterpret_cast<int*>(sh + kWarps * E);
+  float pacc[kStats ? V : 1];
+  float zacc = 0.0f;
+  if (kStats) {
+#pragma unroll
+    for (int i = 0; i < (kStats ? V : 1); ++i) pacc[i] = 0.0f;
+    grid_dependents_launch();
+    for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+  }
+  constexpr int kTokens = 32 / kLanes;
+  for (long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * kTokens; t0 < p.T;
+       t0 += static_cast<long long>(gridDim.x) * kWarps * kTokens) {
+    const bool here = t0 + lane / kLanes < p.T;
+    const long long t = here ? t0 + lane / kLanes : p.T - 1;
+    Key own;
+    own.load(x + t * E, E, l, p.words);
+    K top[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) top[i] = 0;
+#pragma unroll
+    for (int b = 0; b < V; b += B) {
+      K key[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) key[i] = own.key(b + i, E, l);
+      sort_down(key);
+      if (b == 0) {
+#pragma unroll
+        for (int i = 0; i < B; ++i) top[i] = key[i];
+      } else if constexpr (B == N) {
+        keep_top<N>(top, key);
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) {
+      K other[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) other[i] = __shfl_xor_sync(kFull, top[i], d);
+      keep_top<N>(top, other);
+    }
+    const float m = Key::value_of_key(top[0]);
+    const bool dead = m == -INFINITY;  // no expert left: everything of the row is zero
+    float mass = 0.0f;                 // sum of exp(v - m)
+    float e[kStats ? V : 1];
+    if (kStats) {
+#pragma unroll
+      for (int i = 0; i < (kStats ? V : 1); ++i) mass += e[i] = dead ? 0.0f : expf(own.value(i) - m);
+      mass = group_sum(mass);
+    } else if (!p.sigmoid && !p.renorm) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) mass += dead ? 0.0f : expf(own.value(i) - m);
+      mass = group_sum(mass);
+    }
+    // lane l writes picks l, l + 8, ..
+    int id[kMine];
+    float s[kMine], picked = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      K mine = top[q * kLanes < N ? q * kLanes : 0];
+#pragma unroll
+      for (int j = 1; j < kLanes; ++j)
+        if (q * kLanes + j < N && l == j) mine = top[q * kLanes + j < N ? q * kLanes + j : 0];
+      const float mv = Key::value_of_key(mine);
+      id[q] = Key::column_of(mine);
+      s[q] = q * kLanes + l >= k || dead ? 0.0f : (p.sigmoid ? sigmoid_of(mv) : expf(mv - m));
+      picked += s[q];
+    }
+    const float denom = p.renorm ? group_sum(picked) : mass;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const int j = q * kLanes + l;
+      if (j >= k || !here) continue;
+      float w = s[q];
+      if (p.renorm || !p.sigmoid) w = denom > 0.0f || denom != denom ? w / denom : 0.0f;
+      p.idx[t * k + j] = id[q];
+      p.prob[t * k + j] = p.scale * w;
+      if (kStats) atomicAdd(&hist[id[q]], 1);
+    }
+    if constexpr (kStats) {
+      if (p.want_losses) {
+        if (p.sigmoid) {
+          float tot = 0.0f;
+#pragma unroll
+          for (int i = 0; i < V; ++i) tot += e[i] = sigmoid_of(own.value(i));
+          tot = group_sum(tot);
+          const float inv = tot > 0.0f || tot != tot ? 1.0f / tot : 0.0f;
+          if (here) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) pacc[i] += e[i] * inv;
+          }
+        } else if (here && !dead) {
+          const float inv = 1.0f / mass;
+#pragma unroll
+          for (int i = 0; i < V; ++i) pacc[i] += e[i] * inv;
+        }
+        const float lse = m + logf(mass);
+        if (here && !dead && l == 0) zacc += lse * lse;
+      }
+    }
+  }
+  if constexpr (kStats) {
+    // the warp's four tokens' sums, then the block's warps'
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float a = pacc[i];
+      a += __shfl_xor_sync(kFull, a, 8);
+      a += __shfl_xor_sync(kFull, a, 16);
+      const int c = Key::column(l, i);
+      if (lane < kLanes && c < E) sh[warp * E + c] = a;
+    }
+    float* zs = reinterpret_cast<float*>(hist + E);
+    zacc = warp_sum(zacc);
+    if (lane == 0) zs[warp] = zacc;
+    __syncthreads();
+    store_partials(sh, hist, zs, p);
+  }
+}
+
+// Whether eight lanes hold a row and its picks.
+inline bool by_groups(int E, int k) { return E <= 32 * kLanes && k <= 2 * kLanes; }
+
+template <typename X, bool kStats, int V>
+cudaError_t launch_route_group(const RouteArgs& a, const RouteParams& p, int blocks, size_t smem,
+                               cudaStream_t stream) {
+  const X* x = static_cast<const X*>(a.logits);
+  if constexpr (V <= 4) {
+    if (a.k <= 4) route_group_kernel<X, V, 4, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
+    else if (a.k <= 8) route_group_kernel<X, V, 8, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
+    else route_group_kernel<X, V, 16, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
+  } else {
+    if (a.k <= 8) route_group_kernel<X, V, 8, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
+    else route_group_kernel<X, V, 16, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
+  }
+  count_launch();
+  return cudaGetLastError();
 }
 
 template <typename X, bool kStats>
 cudaError_t launch_route_t(const RouteArgs& a, const RouteParams& p, int blocks, size_t smem,
                            cudaStream_t stream) {
+  if (by_groups(a.E, a.k)) {
+    if (a.E <= 4 * kLanes) return launch_route_group<X, kStats, 4>(a, p, blocks, smem, stream);
+    if (a.E <= 8 * kLanes) return launch_route_group<X, kStats, 8>(a, p, blocks, smem, stream);
+    if (a.E <= 16 * kLanes) return launch_route_group<X, kStats, 16>(a, p, blocks, smem, stream);
+    return launch_route_group<X, kStats, 32>(a, p, blocks, smem, stream);
+  }
   const X* x = static_cast<const X*>(a.logits);
   const int v = (a.E + 31) / 32;
   if (v <= 1) route_kernel<X, 1, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
@@ -374,18 +727,24 @@ cudaError_t launch_route_t(const RouteArgs& a, const RouteParams& p, int blocks,
   return cudaGetLastError();
 }
 
+// Lanes per token of the backward.
+inline int bwd_lanes(int E, int k) { return E <= 64 && k <= 8 ? 8 : 32; }
+
 template <typename X>
 cudaError_t launch_route_bwd_t(const RouteBwdArgs& a, const RouteBwdParams& p, int blocks,
                                cudaStream_t stream) {
   const X* x = static_cast<const X*>(a.logits);
   X* dx = static_cast<X*>(a.dlogits);
   const int v = (a.E + 31) / 32;
-  if (v <= 1) route_bwd_kernel<X, 1><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  else if (v <= 2) route_bwd_kernel<X, 2><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  else if (v <= 4) route_bwd_kernel<X, 4><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  else if (v <= 8) route_bwd_kernel<X, 8><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  else if (v <= 16) route_bwd_kernel<X, 16><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  else route_bwd_kernel<X, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
+  if (bwd_lanes(a.E, a.k) == 8) {
+    if (v <= 1) route_bwd_kernel<X, 4, 8><<<blocks, kThreads, 0, stream>>>(x, p, dx);
+    else route_bwd_kernel<X, 8, 8><<<blocks, kThreads, 0, stream>>>(x, p, dx);
+  } else if (v <= 1) route_bwd_kernel<X, 1, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
+  else if (v <= 2) route_bwd_kernel<X, 2, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
+  else if (v <= 4) route_bwd_kernel<X, 4, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
+  else if (v <= 8) route_bwd_kernel<X, 8, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
+  else if (v <= 16) route_bwd_kernel<X, 16, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
+  else route_bwd_kernel<X, 32, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
   count_launch();
   return cudaGetLastError();
 }
@@ -407,8 +766,12 @@ cudaError_t launch_route(const RouteArgs& a, const DeviceInfo& dev, cudaStream_t
   p.scale = a.scale;
   p.idx = a.idx;
   p.prob = a.prob;
+  p.words = a.E % 2 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 3u) == 0;
   const bool stats = a.counts != nullptr || a.losses != nullptr;
-  const int blocks = route_blocks(a.T);
+  const int tokens = by_groups(a.E, a.k) ? 32 / kLanes : 1;  // per warp
+  const long long want =
+      (static_cast<long long>(a.T) + kWarps * tokens - 1) / (kWarps * tokens);
+  const int blocks = static_cast<int>(want < kRouteMaxBlocks ? want : kRouteMaxBlocks);
   cudaError_t e = cudaSuccess;
   if (stats) {
     p.part_p = a.scratch;
@@ -421,13 +784,12 @@ cudaError_t launch_route(const RouteArgs& a, const DeviceInfo& dev, cudaStream_t
                  : launch_route_t<float, true>(a, p, blocks, smem, stream);
       if (e != cudaSuccess) return e;
     }
-    route_finalise_kernel<<<1, kFinThreads, 0, stream>>>(p.part_p, p.part_n, p.part_z, blocks, a.T,
-                                                         a.E, a.k, a.counts, a.losses);
+    e = launch_early(route_finalise_kernel, dim3(kFinBlocks), dim3(kFinThreads), 0, stream,
+                     p.part_p, p.part_n, p.part_z, blocks, a.T, a.E, a.k, a.counts, a.losses);
     count_launch();
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
   }
   if (blocks == 0) return cudaSuccess;
-  const long long want = (static_cast<long long>(a.T) + kWarps - 1) / kWarps;
   const long long cap = static_cast<long long>(dev.sm_count) * 8;
   const int grid = static_cast<int>(want < cap ? want : cap);
   return a.bf16 ? launch_route_t<gg_bf16, false>(a, p, grid, 0, stream)
@@ -449,7 +811,8 @@ cudaError_t launch_route_bwd(const RouteBwdArgs& a, const DeviceInfo& dev, cudaS
   p.aux = a.aux;
   p.z = a.z;
   p.status = a.status;
-  const long long want = (static_cast<long long>(a.T) + kWarps - 1) / kWarps;
+  const int tokens = kThreads / bwd_lanes(a.E, a.k);  // per block
+  const long long want = (static_cast<long long>(a.T) + tokens - 1) / tokens;
   const long long cap = static_cast<long long>(dev.sm_count) * 8;
   const int grid = static_cast<int>(want < cap ? want : cap);
   return a.bf16 ? launch_route_bwd_t<gg_bf16>(a, p, grid, stream)
