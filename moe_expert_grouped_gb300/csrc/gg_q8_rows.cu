@@ -40,6 +40,8 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kPairs = kWarps / 2;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kTurns = kMaxExperts / 32;  // groups of 32 experts
+static_assert(kTurns <= 32 && kMaxExperts % kThreads == 0, "one warp scans the groups");
 constexpr int kRows = 32;    // weight rows per tile
 constexpr int kChunk = 128;  // codes of K per stage
 constexpr uint32_t kWeightBytes = kRows * kChunk;
@@ -56,7 +58,9 @@ template <int kTiles>
 struct SmemTail {
   uint64_t full[kWarps][Ring<kTiles>::kStages];
   int abort_flag;
+  int bad;
   int n_live;
+  int in_turn[kTurns];
   uint16_t live[kMaxExperts];  // experts that have rows
   float part[kPairs][2 * kTiles * 4][32];  // the second warp's sums, as its lanes hold them
 };
@@ -109,31 +113,51 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
 
-  if (warp == 0) {
-    int seen = 0;
-    bool bad = false;
-    for (int b = 0; b < p.E; b += 32) {
-      const int e = b + lane;
-      const int o0 = e < p.E ? p.offsets[e] : 0;
-      const int o1 = e < p.E ? p.offsets[e + 1] : 0;
-      if (o1 < o0 || o0 < 0 || o1 > p.R_cap || (e == 0 && o0 != 0)) bad = true;
-      const uint32_t live = __ballot_sync(0xFFFFFFFFu, o1 > o0);
-      if (o1 > o0) {
-        st.live[seen + __popc(live & ((1u << lane) - 1u))] = static_cast<uint16_t>(e);
-      }
-      seen += __popc(live);
+  // The live experts, in order: 32 experts per warp and turn, so that all
+  // offsets are on their way at once.
+  if (threadIdx.x == 0) {
+    st.abort_flag = 0;
+    st.bad = 0;
+    tma_prefetch_desc(&mapA);
+    tma_prefetch_desc(&mapB);
+  }
+  for (int i = threadIdx.x; i < kWarps * R::kStages; i += kThreads)
+    mbar_init(smem_u32(&st.full[i / R::kStages][i % R::kStages]), 1);
+  mbar_fence_init();
+  fence_proxy_async();
+  __syncthreads();
+  uint32_t live[kMaxExperts / kThreads];  // of the warp's turns: lanes with rows
+#pragma unroll
+  for (int i = 0; i < kMaxExperts / kThreads; ++i) {
+    const int e = i * kThreads + threadIdx.x;
+    const int o0 = e < p.E ? p.offsets[e] : 0;
+    const int o1 = e < p.E ? p.offsets[e + 1] : 0;
+    if (o1 < o0 || o0 < 0 || o1 > p.R_cap || (e == 0 && o0 != 0)) st.bad = 1;
+    live[i] = __ballot_sync(0xFFFFFFFFu, o1 > o0);
+    if (lane == 0) st.in_turn[i * kWarps + warp] = __popc(live[i]);
+  }
+  __syncthreads();
+  {
+    // experts of the turns before each of this warp's
+    const int mine = lane < kTurns ? st.in_turn[lane] : 0;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int n = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += n;
     }
-    bad = __any_sync(0xFFFFFFFFu, bad);
-    if (lane == 0) {
-      st.n_live = bad ? 0 : seen;
-      st.abort_flag = 0;
-      if (bad && blockIdx.x == 0) set_status(p.status, GG_ERR_DEVICE_BAD_OFFSETS);
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / kThreads; ++i) {
+      const int before = __shfl_sync(0xFFFFFFFFu, upto - mine, i * kWarps + warp);
+      if (live[i] >> lane & 1u)
+        st.live[before + __popc(live[i] & ((1u << lane) - 1u))] =
+            static_cast<uint16_t>(i * kThreads + threadIdx.x);
     }
-  } else if (warp == 1) {
-    for (int i = lane; i < kWarps * R::kStages; i += 32)
-      mbar_init(smem_u32(&st.full[i / R::kStages][i % R::kStages]), 1);
-    mbar_fence_init();
-    fence_proxy_async();
+    const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    if (threadIdx.x == 0) {
+      st.n_live = st.bad ? 0 : all;
+      if (st.bad && blockIdx.x == 0) set_status(p.status, GG_ERR_DEVICE_BAD_OFFSETS);
+    }
   }
   __syncthreads();
 

@@ -112,6 +112,46 @@ def test_gated_matches_oracle(gg, case, alpha, weighted):
     _check(C, Aq, As, Wq, Ws, off, alpha, prob)
 
 
+# few rows per expert on average, yet more in one than are multiplied in one go
+HEAVY = [
+    ([40] + [0] * 7, 192, 320, 0),
+    ([0] * 20 + [21] + [1] * 11, 64, 64, 0),
+    ([0, 100, 3, 0, 0, 9, 0, 0, 16], 128, 1088, 5),
+    ([33] + [0] * 600 + [1, 0, 17], 64, 192, 2),
+    ([1] + [0] * 1022 + [1], 128, 128, 0),
+]
+
+
+@pytest.mark.parametrize("case", range(len(HEAVY)))
+def test_one_expert_with_most_of_few_rows(gg, case):
+    counts, N, K, spare = HEAVY[case]
+    Aq, As, Wq, Ws, off = _random(counts, N, K, spare, 150 + case, lo=-128)
+    dA, dS, dW, dT, dO = _dev(Aq, As, Wq, Ws, off)
+    ws = gg.workspace(0, 1, len(counts), "cuda")
+    C = torch.full((Aq.shape[0], N), 3.0, dtype=torch.bfloat16, device="cuda")
+    gg.q8_grouped_gemm(dA, dS, dW, dT, dO, C=C, ws=ws)
+    assert gg.read_status(ws) == 0 and (C[int(off[-1]):] == 3).all()
+    _check(C, Aq, As, Wq, Ws, off)
+    if N % 128 == 0:
+        C = gg.q8_grouped_gemm(dA, dS, dW, dT, dO, gg.GG_EPI_SWIGLU, ws=ws)
+        _check(C, Aq, As, Wq, Ws, off, 1.0)
+
+
+@pytest.mark.parametrize("K", [128, 256, 320, 512, 576, 1024, 1088, 2112, 4096, 8192])
+def test_quantised_rows_of_every_width(gg, K):
+    g = torch.Generator().manual_seed(K)
+    x = torch.randn(19, K, generator=g) * torch.exp(torch.randn(19, 1, generator=g) * 4)
+    x = x.bfloat16()
+    x[7, K - 1] = 1e4
+    x[9, K - 3] = float("-inf")
+    Q, S = gg.q8_quantize_rows(x.cuda(), gg.workspace(0, 1, 1, "cuda"))
+    q, s = qo.quantize_rows(x.float().numpy())
+    np.testing.assert_array_equal(Q.cpu().numpy(), q)
+    ok = np.isfinite(s)
+    np.testing.assert_array_equal(S.cpu().numpy().view(np.int32)[ok], s.view(np.int32)[ok])
+    assert not ok[9] and ok.sum() == 18 and np.isnan(S.cpu().numpy()[9])
+
+
 @pytest.mark.parametrize("R,K", [(1, 64), (5, 192), (300, 2048), (33, 4160)])
 def test_quantised_rows_match_bit_for_bit(gg, R, K):
     g = torch.Generator().manual_seed(R + K)
