@@ -2,15 +2,19 @@
 // logits per token with their probabilities, the tokens per expert, the
 // balance and z losses, and the gradient of the logits.
 //
-// A token's logits lie in the registers of 8 lanes (four tokens per warp,
-// column c in lane c % 8), or of 32 where there are more than 256 experts or
+// A token's logits lie in the registers of 8 lanes (four tokens per warp, four
+// columns at a time), or of 32 where there are more than 256 experts or
 // 16 picks. The row is read once. With 8 lanes the picks come from sorting
 // networks: every lane keeps the largest of its own columns, block by block,
 // and three exchanges merge the lanes; sums over a row take three shuffles.
-// That is 90 (BF16) to 200 (fp32, 64-bit keys) instructions per token of 128
-// logits, against about 500 with one warp per token and a search and two
-// reductions per pick. Measured (events, 4 us of them launch): see the
-// launches below.
+// One warp per token, with a search and two reductions per pick, took 500
+// instructions per token of 128 logits and 2.8 times as long.
+//
+// Bound by the networks' comparisons (integer ALU 72% of its rate; memory is
+// at 2.1 TB/s). Measured (events on an empty queue, 4 us of them launch):
+// forward of 121088 x 256 BF16, k 8, sigmoid 29 us, with statistics 89;
+// 121088 x 128 fp32, k 8 54 and 68, gradient 68; 16384 x 128 fp32, k 8 15 and
+// 21, gradient 15; 121088 x 32 fp32, k 2 23 and 33, gradient 23.
 //
 // Selection works on the logits themselves, which both scores preserve the
 // order of, as order-preserving keys: the picks do not depend on how an
@@ -74,7 +78,7 @@ struct RouteParams {
   int T, E, k;
   int sigmoid, renorm;
   float scale;
-  int words;         // BF16 rows are whole, aligned 32-bit words
+  int pieces;        // rows are whole, aligned pieces of four logits
   int32_t* idx;
   float* prob;
   float* part_p;     // [blocks][E] sums over the block's rows of score / row sum, or null
@@ -435,26 +439,57 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// A lane's share of a row in the eight-lane layout, V columns of it, and their
-// sort keys: the order-preserving key of the logit above the complement of its
-// column, all different; 0: no logit.
+// A lane's share of a row in the eight-lane layout, V columns of it: of every
+// 32 columns, lane l has columns 4 l to 4 l + 3; past the row's end it holds
+// -inf. Their sort keys are the order-preserving key of the logit above the
+// complement of its column, all different: those past the end come after the
+// row's own, of which there are at least k. 0 is below every key.
 template <typename X, int V>
 struct Share;
 
-// fp32: columns l + 8 i, 64-bit keys.
 template <int V>
-struct Share<float, V> {
+struct ShareColumns {
+  static __device__ __forceinline__ int column(int l, int i) {
+    return 4 * (l + kLanes * (i / 4)) + i % 4;
+  }
+};
+
+// fp32: 64-bit keys.
+template <int V>
+struct Share<float, V> : ShareColumns<V> {
   using K = unsigned long long;
+  using ShareColumns<V>::column;
   float v[V];
-  static __device__ __forceinline__ int column(int l, int i) { return l + kLanes * i; }
-  __device__ __forceinline__ void load(const float* row, int E, int l, bool) {
+  __device__ __forceinline__ void load(const float* row, int E, int l, bool pieces) {
+    if (pieces) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = column(l, i) < E ? row[column(l, i)] : -INFINITY;
+      for (int i = 0; i < V; i += 4) {
+        const int c = column(l, i);
+        const float4 q = c < E ? *reinterpret_cast<const float4*>(row + c)
+                               : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        v[i] = q.x;
+        v[i + 1] = q.y;
+        v[i + 2] = q.z;
+        v[i + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = column(l, i) < E ? row[column(l, i)] : -INFINITY;
+    }
   }
   __device__ __forceinline__ float value(int i) const { return v[i]; }
-  __device__ __forceinline__ K key(int i, int E, int l) const {
-    const int c = column(l, i);
-    return c < E ? static_cast<K>(key_of(v[i])) << 32 | (0xFFFFFFFFu - c) : K(0);
+  static __device__ __forceinline__ K make(float value, int c) {
+    return static_cast<K>(key_of(value)) << 32 | (0xFFFFFFFFu - c);
+  }
+  __device__ __forceinline__ K key(int i, int l) const { return make(v[i], column(l, i)); }
+  // Of four columns from i on: the largest logit's, as column i's.
+  __device__ __forceinline__ K lead(int i, int l) const {
+    const auto larger = [](float a, float b) {  // NaN above all
+      float r;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+      return r;
+    };
+    return make(larger(larger(v[i], v[i + 1]), larger(v[i + 2], v[i + 3])), column(l, i));
   }
   static __device__ __forceinline__ int column_of(K k) {
     return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k));
@@ -464,45 +499,50 @@ struct Share<float, V> {
   }
 };
 
-// BF16: pairs of columns 2 (l + 8 i), +1, one word each where rows are words;
-// 32-bit keys, made two at a time: adding 0 to the pair turns -0 into +0 and
-// every NaN into the positive one, then the sign's copies flip the bits.
+// BF16: two columns to a word, 32-bit keys, made two at a time: adding 0 to
+// the pair turns -0 into +0 and every NaN into the positive one, then the
+// sign's copies flip the bits.
 template <int V>
-struct Share<gg_bf16, V> {
+struct Share<gg_bf16, V> : ShareColumns<V> {
   using K = uint32_t;
+  using ShareColumns<V>::column;
   uint32_t w[V / 2];
-  static __device__ __forceinline__ int column(int l, int i) {
-    return 2 * (l + kLanes * (i / 2)) + i % 2;
-  }
-  __device__ __forceinline__ void load(const gg_bf16* row, int E, int l, bool words) {
-    if (words) {  // E is even
+  __device__ __forceinline__ void load(const gg_bf16* row, int E, int l, bool pieces) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i)
-        w[i] = column(l, 2 * i) < E
-                   ? reinterpret_cast<const uint32_t*>(row)[l + kLanes * i]
-                   : 0xFF80FF80u;
-    } else {
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        const int c = column(l, 2 * i);
-        const uint32_t lo = c < E ? row[c] : 0xFF80u, hi = c + 1 < E ? row[c + 1] : 0xFF80u;
-        w[i] = hi << 16 | lo;
+    for (int i = 0; i < V; i += 4) {
+      const int c = column(l, i);
+      uint2 q = make_uint2(0xFF80FF80u, 0xFF80FF80u);
+      if (pieces) {
+        if (c < E) q = *reinterpret_cast<const uint2*>(row + c);
+      } else {
+        if (c < E) q.x = 0xFF800000u | row[c];
+        if (c + 1 < E) q.x = (q.x & 0xFFFFu) | static_cast<uint32_t>(row[c + 1]) << 16;
+        if (c + 2 < E) q.y = 0xFF800000u | row[c + 2];
+        if (c + 3 < E) q.y = (q.y & 0xFFFFu) | static_cast<uint32_t>(row[c + 3]) << 16;
       }
+      w[i / 2] = q.x;
+      w[i / 2 + 1] = q.y;
     }
   }
   __device__ __forceinline__ float value(int i) const {
     return i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
   }
-  __device__ __forceinline__ K key(int i, int E, int l) const {
-    const int c = column(l, i);
-    __nv_bfloat162 q = *reinterpret_cast<const __nv_bfloat162*>(&w[i / 2]);
+  __device__ __forceinline__ uint32_t pair(int word) const {  // two logits' keys
+    __nv_bfloat162 q = *reinterpret_cast<const __nv_bfloat162*>(&w[word]);
     q = __hadd2(q, __floats2bfloat162_rn(0.0f, 0.0f));
     const uint32_t u = *reinterpret_cast<const uint32_t*>(&q);
     uint32_t signs;  // copies of each half's sign bit (selectors with their top bit set)
     asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(signs) : "r"(u));
-    const uint32_t flip = u ^ (signs | 0x80008000u);
-    const uint32_t low = 0xFFFFu - c;
-    return c < E ? __byte_perm(flip, low, i % 2 ? 0x3254 : 0x1054) : K(0);
+    return u ^ (signs | 0x80008000u);
+  }
+  __device__ __forceinline__ K key(int i, int l) const {
+    return __byte_perm(pair(i / 2), 0xFFFFu - column(l, i), i % 2 ? 0x3254 : 0x1054);
+  }
+  // Of four columns from i on: the largest logit's, as column i's.
+  __device__ __forceinline__ K lead(int i, int l) const {
+    const uint32_t two = __vmaxu2(pair(i / 2), pair(i / 2 + 1));
+    const uint32_t low = 0xFFFFu - column(l, i);
+    return max(__byte_perm(two, low, 0x3254), __byte_perm(two, low, 0x1054));
   }
   static __device__ __forceinline__ int column_of(K k) { return 0xFFFF - (k & 0xFFFFu); }
   static __device__ __forceinline__ float value_of_key(K k) {
@@ -543,17 +583,50 @@ __device__ __forceinline__ void sort_down(K (&v)[N]) {
   }
 }
 
-// top = the N largest of top and v, both descending: the larger of each pair
-// from opposite ends is one of them, and what results is bitonic.
 template <int N, typename K>
-__device__ __forceinline__ void keep_top(K (&top)[N], const K (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) top[i] = top[i] > v[N - 1 - i] ? top[i] : v[N - 1 - i];
+__device__ __forceinline__ void sort_bitonic(K (&v)[N]) {
 #pragma unroll
   for (int d = N / 2; d >= 1; d /= 2)
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if ((i & d) == 0) order(top[i], top[i + d]);
+      if ((i & d) == 0) order(v[i], v[i + d]);
+}
+
+// top = the N largest of top and v, both descending: the larger of each pair
+// from opposite ends is one of them, and what results is bitonic.
+template <int N, typename K>
+__device__ __forceinline__ void larger_ones(K (&top)[N], const K (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) top[i] = top[i] > v[N - 1 - i] ? top[i] : v[N - 1 - i];
+}
+
+// top: the N largest of all lanes' v, each descending; where kSet, unordered,
+// and the upper half of the lanes in the other half's order reversed. M < N: lanes' keys are joined until there are N.
+template <bool kSet, int D = 1, int M, int N, typename K>
+__device__ __forceinline__ void over_lanes(K (&v)[M], K (&top)[N]) {
+  if constexpr (D == kLanes) {
+    static_assert(M == N, "too few lanes for N keys");
+#pragma unroll
+    for (int i = 0; i < N; ++i) top[i] = v[i];
+  } else {
+    K other[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) other[i] = __shfl_xor_sync(kFull, v[i], D);
+    if constexpr (M < N) {
+      K both[2 * M];
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        both[i] = v[i];
+        both[2 * M - 1 - i] = other[i];
+      }
+      sort_bitonic(both);
+      over_lanes<kSet, 2 * D>(both, top);
+    } else {
+      larger_ones(v, other);
+      if constexpr (!kSet || 2 * D < kLanes) sort_bitonic(v);
+      over_lanes<kSet, 2 * D>(v, top);
+    }
+  }
 }
 
 // V: columns per lane; N: picks kept, at least k.
@@ -563,6 +636,12 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
   using Key = Share<X, V>;
   using K = typename Key::K;
   constexpr int B = V < N ? V : N;      // block of columns sorted at once
+  // Eight picks of more than 64 columns: no pick is outside the eight pieces
+  // of four columns with the largest leaders (of equal ones the first), since
+  // a better piece's leader comes before all of this one. So the networks run
+  // on leaders, and then on the eight pieces, one per lane, read once more:
+  // 121088 x 256 BF16 40 -> 29 us, 121088 x 128 fp32 68 -> 54.
+  constexpr bool kLead = V >= 16 && N == kLanes;
   constexpr int kMine = N > kLanes ? N / kLanes : 1;  // picks per lane
   extern __shared__ float sh[];         // kStats: [kWarps][E] sums, int [E] picks, [kWarps] z
   const int lane = threadIdx.x & 31;
@@ -585,29 +664,44 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
     const bool here = t0 + lane / kLanes < p.T;
     const long long t = here ? t0 + lane / kLanes : p.T - 1;
     Key own;
-    own.load(x + t * E, E, l, p.words);
+    own.load(x + t * E, E, l, p.pieces);
     K top[N];
+    if constexpr (kLead) {
+      K lead[V / 4];
 #pragma unroll
-    for (int i = 0; i < N; ++i) top[i] = 0;
+      for (int i = 0; i < V / 4; ++i) lead[i] = own.lead(4 * i, l);
+      sort_down(lead);
+      over_lanes<true>(lead, top);
+      const int at = l < kLanes / 2 ? l : N - 1 - l;  // lane l's is l in the first lanes' order
+      K mine = top[0];
 #pragma unroll
-    for (int b = 0; b < V; b += B) {
-      K key[B];
+      for (int j = 1; j < kLanes / 2; ++j)
+        if (at == j) mine = top[j];
+      const int piece = Key::column_of(mine) / 4;
+      Share<X, 4> four;
+      four.load(x + t * E, E, piece, p.pieces);
+      K key[4];
 #pragma unroll
-      for (int i = 0; i < B; ++i) key[i] = own.key(b + i, E, l);
+      for (int i = 0; i < 4; ++i) key[i] = four.key(i, piece);
       sort_down(key);
-      if (b == 0) {
+      over_lanes<false>(key, top);
+    } else {
+      K best[B];
 #pragma unroll
-        for (int i = 0; i < B; ++i) top[i] = key[i];
-      } else if constexpr (B == N) {
-        keep_top<N>(top, key);
+      for (int b = 0; b < V; b += B) {
+        K key[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) key[i] = own.key(b + i, l);
+        sort_down(key);
+        if (b == 0) {
+#pragma unroll
+          for (int i = 0; i < B; ++i) best[i] = key[i];
+        } else {
+          larger_ones(best, key);
+          sort_bitonic(best);
+        }
       }
-    }
-#pragma unroll
-    for (int d = 1; d < kLanes; d *= 2) {
-      K other[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) other[i] = __shfl_xor_sync(kFull, top[i], d);
-      keep_top<N>(top, other);
+      over_lanes<false>(best, top);
     }
     const float m = Key::value_of_key(top[0]);
     const bool dead = m == -INFINITY;  // no expert left: everything of the row is zero
@@ -766,7 +860,8 @@ cudaError_t launch_route(const RouteArgs& a, const DeviceInfo& dev, cudaStream_t
   p.scale = a.scale;
   p.idx = a.idx;
   p.prob = a.prob;
-  p.words = a.E % 2 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 3u) == 0;
+  p.pieces =
+      a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (a.bf16 ? 8 : 16) == 0;
   const bool stats = a.counts != nullptr || a.losses != nullptr;
   const int tokens = by_groups(a.E, a.k) ? 32 / kLanes : 1;  // per warp
   const long long want =

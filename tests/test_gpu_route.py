@@ -113,6 +113,41 @@ def test_nan_and_infinities_keep_valid_ids(gg):
             assert torch.isnan(r["prob"][:2]).all()
 
 
+@pytest.mark.parametrize("E", [29, 33, 64, 65, 70, 127, 128, 130, 200, 254, 256])
+@pytest.mark.parametrize("k", [1, 3, 8, 16])
+def test_picks_among_many_equal_logits(gg, E, k):
+    # few values, infinities and NaN among them, in rows that start at any element; NaN is the
+    # largest, and equals go to the lower id
+    rng = np.random.default_rng(E * 100 + k)
+    few = np.array([-np.inf, -2.0, -0.0, 0.0, 0.0, 1.0, 1.5, np.inf, np.nan])
+    x = few[rng.integers(0, rng.integers(1, 10, (203, 1)), (203, E))]
+    x[5] = -np.inf
+    x[6] = np.nan
+    x[7, E - 1] = 3.0
+    rank = np.where(np.isnan(x), 1e6, np.clip(x, -1e5, 1e5))
+    want = np.argsort(-rank, axis=1, kind="stable")[:, :k]
+    for dtype in (torch.float32, torch.bfloat16):
+        for shift in (0, 1, 4):
+            room = torch.empty(203 * E + shift, dtype=dtype, device="cuda")
+            t = room[shift:].view(203, E)
+            t.copy_(torch.from_numpy(x))
+            r = gg.route(t, k, 1, counts=True)
+            np.testing.assert_array_equal(r["idx"].cpu().numpy(), want)
+            np.testing.assert_array_equal(r["counts"].cpu().numpy(),
+                                          np.bincount(want.ravel(), minlength=E))
+            assert torch.equal(gg.route(t, k, 1)["idx"], r["idx"])
+
+
+@pytest.mark.parametrize("T,E,k", [(700, 70, 8), (700, 128, 8), (301, 200, 5), (300, 255, 8),
+                                   (300, 256, 12), (40, 96, 16)])
+def test_wide_rows_match_oracle(gg, T, E, k):
+    for dtype in (torch.float32, torch.bfloat16):
+        t, x = _logits(T + E + k, T, E, dtype, masked=E // 9, dead=0.05)
+        for sig, ren in VARIANTS:
+            r, f = _check_forward(gg, t, x, k, sig, ren, 1.5)
+            _check_backward(gg, t, x, r, f, sig, ren, 1.5, 3)
+
+
 def test_extreme_logits_stay_finite(gg):
     for dtype in (torch.float32, torch.bfloat16):
         lim = torch.finfo(dtype).max
