@@ -13,8 +13,8 @@
 // Bound by the networks' comparisons (integer ALU 72% of its rate; memory is
 // at 2.1 TB/s). Measured (events on an empty queue, 4 us of them launch):
 // forward of 121088 x 256 BF16, k 8, sigmoid 29 us, with statistics 89;
-// 121088 x 128 fp32, k 8 54 and 68, gradient 68; 16384 x 128 fp32, k 8 15 and
-// 21, gradient 15; 121088 x 32 fp32, k 2 23 and 33, gradient 23.
+// gradient 85; 121088 x 128 fp32, k 8 54 and 68, gradient 42; 16384 x 128 fp32,
+// k 8 15 and 21, gradient 13; 121088 x 32 fp32, k 2 23 and 33, gradient 21.
 //
 // Selection works on the logits themselves, which both scores preserve the
 // order of, as order-preserving keys: the picks do not depend on how an
@@ -272,164 +272,7 @@ route_finalise_kernel(const float* part_p, const int32_t* part_n, const float* p
   }
 }
 
-struct RouteBwdParams {
-  int T, E, k;
-  int sigmoid, renorm;
-  float scale;
-  const int32_t* idx;
-  const float* dprob;
-  const int32_t* counts;  // null when aux is 0
-  float aux, z;           // coefficients of the two losses
-  int32_t* status;        // or null
-};
-
-// The fast exponential and divide: a few units of fp32, times the size of the
-// exponent, on gradients.
-__device__ __forceinline__ float fast_sigmoid(float v) {
-  return __fdividef(1.0f, 1.0f + __expf(-v));
-}
-
-// kL lanes per token, at least k (column c in lane c % kL). Every column's
-// gradient without its picks is written first, then the picks' lanes write
-// theirs over it. The sums over the row are taken together, and the next row
-// is on its way meanwhile. Eight lanes up to 64 experts and 8 picks, else a
-// warp: 121088 tokens, 32 experts 25 us against 41; 256 experts 242 against
-// 128 (more sums per lane than a warp's threads hide).
-template <typename X, int V, int kL>
-__global__ void __launch_bounds__(kThreads)
-route_bwd_kernel(const X* x, const RouteBwdParams p, X* dx) {
-  const int lane = threadIdx.x % kL;
-  const int base = threadIdx.x & 31 & ~(kL - 1);  // the token's first lane
-  const int E = p.E, k = p.k;
-  const float inv_T = 1.0f / static_cast<float>(p.T);
-  const bool aux = p.aux != 0.0f, zl = p.z != 0.0f;
-  const bool soft = !p.sigmoid || zl;  // the softmax is needed
-  const float per_pick = static_cast<float>(E) / (static_cast<float>(p.T) * static_cast<float>(k));
-  float load[V];  // E f_e: what the balance loss weighs expert e's mean share with
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = lane + kL * i;
-    load[i] = aux && c < E ? per_pick * static_cast<float>(p.counts[c]) : 0.0f;
-  }
-  constexpr int kTokens = kThreads / kL;  // per block
-  const long long step = static_cast<long long>(gridDim.x) * kTokens;
-  long long t = static_cast<long long>(blockIdx.x) * kTokens + threadIdx.x / kL;
-  float v[V];
-  int id = -1;
-  float g = 0.0f, picked = -INFINITY;
-  const auto fetch = [&](long long at, float(&to)[V], int& pick, float& grad) {
-    if (at >= p.T) return;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = lane + kL * i;
-      to[i] = c < E ? to_f32(x[at * E + c]) : -INFINITY;
-    }
-    if (lane < k) {
-      pick = p.idx[at * k + lane];
-      grad = p.dprob[at * k + lane];
-    }
-  };
-  fetch(t, v, id, g);
-  // a warp's lanes stay together: tokens past the end do not load or store
-  for (long long first = t - (base / kL); first < p.T; first += step, t += step) {
-    const bool here = t < p.T;
-    const X* row = x + t * E;
-    if (here && lane < k && (id < 0 || id >= E)) {
-      set_status(p.status, GG_ERR_DEVICE_BAD_EXPERT_ID);
-      id = -1;
-      g = 0.0f;
-    }
-    picked = id >= 0 ? to_f32(row[id]) : -INFINITY;
-    float next[V];
-    int next_id = -1;
-    float next_g = 0.0f;
-    fetch(t + step, next, next_id, next_g);
-
-    float m = v[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-    if constexpr (kL == 32) {
-      m = value_of(__reduce_max_sync(kFull, key_of(m)));
-    } else {
-#pragma unroll
-      for (int d = kL / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-    }
-    const bool dead = m == -INFINITY;
-    // e: exp(v - m); sums of e, of the scores, of load * score, of the picks'
-    // scores and of gradient * score (softmax: all up to 1 / mass)
-    float e[V], sc[V];
-    float mass = 0.0f, st = 0.0f, cs = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      e[i] = soft && !dead ? __expf(v[i] - m) : 0.0f;
-      sc[i] = p.sigmoid ? fast_sigmoid(v[i]) : e[i];
-      mass += e[i];
-      st += sc[i];
-      cs += load[i] * sc[i];
-    }
-    float ps = 0.0f;
-    if (id >= 0 && !dead) ps = p.sigmoid ? fast_sigmoid(picked) : __expf(picked - m);
-    float tot = ps, gps = g * ps;
-#pragma unroll
-    for (int d = kL / 2; d > 0; d >>= 1) {
-      if (soft) mass += __shfl_xor_sync(kFull, mass, d);
-      if (aux) {
-        if (p.sigmoid) st += __shfl_xor_sync(kFull, st, d);
-        cs += __shfl_xor_sync(kFull, cs, d);
-      }
-      if (p.renorm) tot += __shfl_xor_sync(kFull, tot, d);
-      gps += __shfl_xor_sync(kFull, gps, d);
-    }
-    const float inv_mass = soft && !dead ? 1.0f / mass : 0.0f;
-    const float zg = dead || !zl ? 0.0f : 2.0f * p.z * inv_T * (m + logf(mass));
-    // gradient of this lane's pick: of its score, or (renormalised softmax) of its logit
-    float gp = p.scale * g, dot = 0.0f;
-    if (p.renorm) {
-      const bool some = tot > 0.0f || tot != tot;
-      gp = some ? p.scale * (g - gps / tot) / tot : 0.0f;
-      if (!p.sigmoid) gp *= ps;  // the factor 1 / mass of both scores cancels
-      if (id < 0) gp = 0.0f;
-    } else if (!p.sigmoid) {
-      dot = p.scale * gps * inv_mass;
-    }
-    float ga = 0.0f, mean = 0.0f;  // balance loss: gradient ga (load - mean) of each share
-    if (aux) {
-      const float total = p.sigmoid ? st : mass;
-      if (!dead && (total > 0.0f || total != total)) {
-        ga = p.sigmoid ? p.aux * inv_T / total : p.aux * inv_T;
-        mean = cs / total;
-      }
-    }
-    // a column's gradient, add: from its picks
-    const auto grad = [&](float sm, float score, float ld, float add) {
-      if (p.sigmoid) return (add + ga * (ld - mean)) * score * (1.0f - score) + zg * sm;
-      return (p.renorm ? add : sm * (add - dot)) + sm * (ga * (ld - mean) + zg);
-    };
-    X* out = dx + t * E;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (here && lane + kL * i < E)
-        store_as(out + lane + kL * i, grad(e[i] * inv_mass, sc[i], load[i], 0.0f));
-    float add = 0.0f;  // an expert named in several slots gets them all
-    for (int j = 0; j < k; ++j) {
-      const int other = __shfl_sync(kFull, id, base + j);
-      const float gj = __shfl_sync(kFull, gp, base + j);
-      if (other == id) add += gj;
-    }
-    __syncwarp();  // the picks' columns are written after the others
-    if (here && id >= 0) {
-      const float sm = soft && !dead ? __expf(picked - m) * inv_mass : 0.0f;
-      const float ld = aux ? per_pick * static_cast<float>(p.counts[id]) : 0.0f;
-      store_as(out + id, grad(sm, p.sigmoid ? fast_sigmoid(picked) : 0.0f, ld, add));
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = next[i];
-    id = next_id;
-    g = next_g;
-  }
-}
-
-// ------------------------------------------------------- eight lanes per token
+// --------------------------------------------------- several tokens per warp
 
 constexpr int kLanes = 8;
 
@@ -439,26 +282,25 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// A lane's share of a row in the eight-lane layout, V columns of it: of every
-// 32 columns, lane l has columns 4 l to 4 l + 3; past the row's end it holds
-// -inf. Their sort keys are the order-preserving key of the logit above the
+// A lane's share of a row on kL lanes, V columns of it: of every 4 kL columns,
+// lane l has columns 4 l to 4 l + 3; past the row's end it holds -inf. Their sort keys are the order-preserving key of the logit above the
 // complement of its column, all different: those past the end come after the
 // row's own, of which there are at least k. 0 is below every key.
-template <typename X, int V>
+template <typename X, int V, int kL = kLanes>
 struct Share;
 
-template <int V>
+template <int V, int kL>
 struct ShareColumns {
   static __device__ __forceinline__ int column(int l, int i) {
-    return 4 * (l + kLanes * (i / 4)) + i % 4;
+    return 4 * (l + kL * (i / 4)) + i % 4;
   }
 };
 
 // fp32: 64-bit keys.
-template <int V>
-struct Share<float, V> : ShareColumns<V> {
+template <int V, int kL>
+struct Share<float, V, kL> : ShareColumns<V, kL> {
   using K = unsigned long long;
-  using ShareColumns<V>::column;
+  using ShareColumns<V, kL>::column;
   float v[V];
   __device__ __forceinline__ void load(const float* row, int E, int l, bool pieces) {
     if (pieces) {
@@ -502,10 +344,10 @@ struct Share<float, V> : ShareColumns<V> {
 // BF16: two columns to a word, 32-bit keys, made two at a time: adding 0 to
 // the pair turns -0 into +0 and every NaN into the positive one, then the
 // sign's copies flip the bits.
-template <int V>
-struct Share<gg_bf16, V> : ShareColumns<V> {
+template <int V, int kL>
+struct Share<gg_bf16, V, kL> : ShareColumns<V, kL> {
   using K = uint32_t;
-  using ShareColumns<V>::column;
+  using ShareColumns<V, kL>::column;
   uint32_t w[V / 2];
   __device__ __forceinline__ void load(const gg_bf16* row, int E, int l, bool pieces) {
 #pragma unroll
@@ -709,7 +551,8 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
     float e[kStats ? V : 1];
     if (kStats) {
 #pragma unroll
-      for (int i = 0; i < (kStats ? V : 1); ++i) mass += e[i] = dead ? 0.0f : expf(own.value(i) - m);
+      for (int i = 0; i < (kStats ? V : 1); ++i)
+        mass += e[i] = dead ? 0.0f : expf(own.value(i) - m);
       mass = group_sum(mass);
     } else if (!p.sigmoid && !p.renorm) {
 #pragma unroll
@@ -781,6 +624,192 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
   }
 }
 
+struct RouteBwdParams {
+  int T, E, k;
+  int sigmoid, renorm;
+  float scale;
+  const int32_t* idx;
+  const float* dprob;
+  const int32_t* counts;  // null when aux is 0
+  float aux, z;           // coefficients of the two losses
+  int pieces;             // both tensors' rows are whole, aligned pieces of four
+  int32_t* status;        // or null
+};
+
+// The fast exponential and divide: a few units of fp32, times the size of the
+// exponent, on gradients.
+__device__ __forceinline__ float fast_sigmoid(float v) {
+  return __fdividef(1.0f, 1.0f + __expf(-v));
+}
+
+// Four columns' gradients from column c on, as the logits' type.
+__device__ __forceinline__ void store_piece(float* row, int c, int E, bool pieces,
+                                            const float (&g)[4]) {
+  if (pieces) {
+    if (c < E) *reinterpret_cast<float4*>(row + c) = make_float4(g[0], g[1], g[2], g[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < E) row[c + j] = g[j];
+  }
+}
+__device__ __forceinline__ void store_piece(gg_bf16* row, int c, int E, bool pieces,
+                                            const float (&g)[4]) {
+  if (pieces) {
+    if (c < E)
+      *reinterpret_cast<uint2*>(row + c) =
+          make_uint2(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < E) store_as(row + c + j, g[j]);
+  }
+}
+
+// kL lanes per token, at least k. Every column's gradient without its picks is
+// written first, then the picks' lanes write theirs over it. The sums over the
+// row are taken together, and the next row is on its way meanwhile.
+template <typename X, int V, int kL>
+__global__ void __launch_bounds__(kThreads)
+route_bwd_kernel(const X* x, const RouteBwdParams p, X* dx) {
+  using Row = Share<X, V, kL>;
+  __shared__ float4 load[kL * V / 4];  // E f_e: what the balance loss weighs a mean share with
+  const int lane = threadIdx.x % kL;
+  const int base = threadIdx.x & 31 & ~(kL - 1);  // the token's first lane
+  const int E = p.E, k = p.k;
+  const float inv_T = 1.0f / static_cast<float>(p.T);
+  const bool aux = p.aux != 0.0f, zl = p.z != 0.0f;
+  const bool soft = !p.sigmoid || zl;  // the softmax is needed
+  const float per_pick = static_cast<float>(E) / (static_cast<float>(p.T) * static_cast<float>(k));
+  for (int c = threadIdx.x; c < kL * V; c += kThreads)
+    reinterpret_cast<float*>(load)[c] =
+        aux && c < E ? per_pick * static_cast<float>(p.counts[c]) : 0.0f;
+  __syncthreads();
+  constexpr int kTokens = kThreads / kL;  // per block
+  const long long step = static_cast<long long>(gridDim.x) * kTokens;
+  long long t = static_cast<long long>(blockIdx.x) * kTokens + threadIdx.x / kL;
+  Row own{}, next{};
+  int id = -1, next_id = -1;
+  float g = 0.0f, next_g = 0.0f;
+  const auto fetch = [&](long long at, Row& to, int& pick, float& grad) {
+    pick = -1;
+    grad = 0.0f;
+    if (at >= p.T) return;
+    to.load(x + at * E, E, lane, p.pieces);
+    if (lane < k) {
+      pick = p.idx[at * k + lane];
+      grad = p.dprob[at * k + lane];
+    }
+  };
+  fetch(t, own, id, g);
+  // a warp's lanes stay together: tokens past the end do not load or store
+  for (long long first = t - (base / kL); first < p.T; first += step, t += step) {
+    const bool here = t < p.T;
+    if (here && lane < k && (id < 0 || id >= E)) {
+      set_status(p.status, GG_ERR_DEVICE_BAD_EXPERT_ID);
+      id = -1;
+      g = 0.0f;
+    }
+    const float picked = id >= 0 ? to_f32(x[t * E + id]) : -INFINITY;
+    fetch(t + step, next, next_id, next_g);
+
+    float m = own.value(0);
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = fmaxf(m, own.value(i));
+    if constexpr (kL == 32) {
+      m = value_of(__reduce_max_sync(kFull, key_of(m)));
+    } else {
+#pragma unroll
+      for (int d = kL / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+    }
+    const bool dead = m == -INFINITY;
+    // e: exp(v - m); sums of e, of the scores, of load * score, of the picks'
+    // scores and of gradient * score (softmax: all up to 1 / mass)
+    float e[V], sc[V];
+    float mass = 0.0f, st = 0.0f, cs = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 ld = load[Row::column(lane, i) / 4];
+      const float four[4] = {ld.x, ld.y, ld.z, ld.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v = own.value(i + j);
+        e[i + j] = soft && !dead ? __expf(v - m) : 0.0f;
+        sc[i + j] = p.sigmoid ? fast_sigmoid(v) : e[i + j];
+        mass += e[i + j];
+        st += sc[i + j];
+        cs += four[j] * sc[i + j];
+      }
+    }
+    float ps = 0.0f;
+    if (id >= 0 && !dead) ps = p.sigmoid ? fast_sigmoid(picked) : __expf(picked - m);
+    float tot = ps, gps = g * ps;
+#pragma unroll
+    for (int d = kL / 2; d > 0; d >>= 1) {
+      if (soft) mass += __shfl_xor_sync(kFull, mass, d);
+      if (aux) {
+        if (p.sigmoid) st += __shfl_xor_sync(kFull, st, d);
+        cs += __shfl_xor_sync(kFull, cs, d);
+      }
+      if (p.renorm) tot += __shfl_xor_sync(kFull, tot, d);
+      gps += __shfl_xor_sync(kFull, gps, d);
+    }
+    const float inv_mass = soft && !dead ? 1.0f / mass : 0.0f;
+    const float zg = dead || !zl ? 0.0f : 2.0f * p.z * inv_T * (m + logf(mass));
+    // gradient of this lane's pick: of its score, or (renormalised softmax) of its logit
+    float gp = p.scale * g, dot = 0.0f;
+    if (p.renorm) {
+      const bool some = tot > 0.0f || tot != tot;
+      gp = some ? p.scale * (g - gps / tot) / tot : 0.0f;
+      if (!p.sigmoid) gp *= ps;  // the factor 1 / mass of both scores cancels
+      if (id < 0) gp = 0.0f;
+    } else if (!p.sigmoid) {
+      dot = p.scale * gps * inv_mass;
+    }
+    float ga = 0.0f, mean = 0.0f;  // balance loss: gradient ga (load - mean) of each share
+    if (aux) {
+      const float total = p.sigmoid ? st : mass;
+      if (!dead && (total > 0.0f || total != total)) {
+        ga = p.sigmoid ? p.aux * inv_T / total : p.aux * inv_T;
+        mean = cs / total;
+      }
+    }
+    // a column's gradient, add: from its picks
+    const auto grad = [&](float sm, float score, float ld, float add) {
+      if (p.sigmoid) return (add + ga * (ld - mean)) * score * (1.0f - score) + zg * sm;
+      return (p.renorm ? add : sm * (add - dot)) + sm * (ga * (ld - mean) + zg);
+    };
+    X* out = dx + t * E;
+    if (here) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const int c = Row::column(lane, i);
+        const float4 ld = load[c / 4];
+        const float four[4] = {ld.x, ld.y, ld.z, ld.w};
+        float to[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[j] = grad(e[i + j] * inv_mass, sc[i + j], four[j], 0.0f);
+        store_piece(out, c, E, p.pieces, to);
+      }
+    }
+    float add = 0.0f;  // an expert named in several slots gets them all
+    for (int j = 0; j < k; ++j) {
+      const int other = __shfl_sync(kFull, id, base + j);
+      const float gj = __shfl_sync(kFull, gp, base + j);
+      if (other == id) add += gj;
+    }
+    __syncwarp();  // the picks' columns are written after the others
+    if (here && id >= 0) {
+      const float sm = soft && !dead ? __expf(picked - m) * inv_mass : 0.0f;
+      const float ld = reinterpret_cast<const float*>(load)[id];
+      store_as(out + id, grad(sm, p.sigmoid ? fast_sigmoid(picked) : 0.0f, ld, add));
+    }
+    own = next;
+    id = next_id;
+    g = next_g;
+  }
+}
+
 // Whether eight lanes hold a row and its picks.
 inline bool by_groups(int E, int k) { return E <= 32 * kLanes && k <= 2 * kLanes; }
 
@@ -821,24 +850,37 @@ cudaError_t launch_route_t(const RouteArgs& a, const RouteParams& p, int blocks,
   return cudaGetLastError();
 }
 
-// Lanes per token of the backward.
-inline int bwd_lanes(int E, int k) { return E <= 64 && k <= 8 ? 8 : 32; }
+// Lanes per token of the backward: as few as hold the row at 16 columns each,
+// and its picks (121088 x 128 fp32: 42 us, 52 at 8 columns each, 66 at 4;
+// 121088 x 256 BF16, sigmoid: 85 us, 97 at 8 columns, 242 at 32).
+inline int bwd_lanes(int E, int k) {
+  if (E <= 128 && k <= 8) return 8;
+  if (E <= 256 && k <= 16) return 16;
+  return 32;
+}
+
+template <typename X, int kL, int V>
+void launch_route_bwd_v(const RouteBwdArgs& a, const RouteBwdParams& p, int blocks,
+                        cudaStream_t stream) {
+  route_bwd_kernel<X, V, kL><<<blocks, kThreads, 0, stream>>>(
+      static_cast<const X*>(a.logits), p, static_cast<X*>(a.dlogits));
+}
 
 template <typename X>
 cudaError_t launch_route_bwd_t(const RouteBwdArgs& a, const RouteBwdParams& p, int blocks,
                                cudaStream_t stream) {
-  const X* x = static_cast<const X*>(a.logits);
-  X* dx = static_cast<X*>(a.dlogits);
-  const int v = (a.E + 31) / 32;
-  if (bwd_lanes(a.E, a.k) == 8) {
-    if (v <= 1) route_bwd_kernel<X, 4, 8><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-    else route_bwd_kernel<X, 8, 8><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  } else if (v <= 1) route_bwd_kernel<X, 1, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  else if (v <= 2) route_bwd_kernel<X, 2, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  else if (v <= 4) route_bwd_kernel<X, 4, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  else if (v <= 8) route_bwd_kernel<X, 8, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  else if (v <= 16) route_bwd_kernel<X, 16, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
-  else route_bwd_kernel<X, 32, 32><<<blocks, kThreads, 0, stream>>>(x, p, dx);
+  const int lanes = bwd_lanes(a.E, a.k);
+  const int v = (a.E + lanes - 1) / lanes;  // columns per lane
+  if (lanes == 8) {
+    if (v <= 4) launch_route_bwd_v<X, 8, 4>(a, p, blocks, stream);
+    else if (v <= 8) launch_route_bwd_v<X, 8, 8>(a, p, blocks, stream);
+    else launch_route_bwd_v<X, 8, 16>(a, p, blocks, stream);
+  } else if (lanes == 16) {
+    if (v <= 8) launch_route_bwd_v<X, 16, 8>(a, p, blocks, stream);
+    else launch_route_bwd_v<X, 16, 16>(a, p, blocks, stream);
+  } else if (v <= 8) launch_route_bwd_v<X, 32, 8>(a, p, blocks, stream);
+  else if (v <= 16) launch_route_bwd_v<X, 32, 16>(a, p, blocks, stream);
+  else launch_route_bwd_v<X, 32, 32>(a, p, blocks, stream);
   count_launch();
   return cudaGetLastError();
 }
@@ -906,6 +948,8 @@ cudaError_t launch_route_bwd(const RouteBwdArgs& a, const DeviceInfo& dev, cudaS
   p.aux = a.aux;
   p.z = a.z;
   p.status = a.status;
+  p.pieces = a.E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) |
+                              reinterpret_cast<uintptr_t>(a.dlogits)) % (a.bf16 ? 8 : 16) == 0;
   const int tokens = kThreads / bwd_lanes(a.E, a.k);  // per block
   const long long want = (static_cast<long long>(a.T) + tokens - 1) / tokens;
   const long long cap = static_cast<long long>(dev.sm_count) * 8;
