@@ -2,11 +2,11 @@
 // logits per token with their probabilities, the tokens per expert, the
 // balance and z losses, and the gradient of the logits.
 //
-// A token's logits lie in the registers of 8 lanes (four tokens per warp, four
-// columns at a time), or of 32 where there are more than 256 experts or
-// 16 picks. The row is read once. With 8 lanes the picks come from sorting
-// networks: every lane keeps the largest of its own columns, block by block,
-// and three exchanges merge the lanes; sums over a row take three shuffles.
+// A token's logits lie in the registers of 8 lanes (up to 256 experts) or 16
+// (up to 512), four columns at a time, or of 32 where there are more of them
+// or more than 16 picks. The row is read once. With 8 or 16 lanes the picks
+// come from sorting networks: every lane keeps the largest of its own columns,
+// block by block, and three or four exchanges merge the lanes.
 // One warp per token, with a search and two reductions per pick, took 500
 // instructions per token of 128 logits and 2.8 times as long.
 //
@@ -274,19 +274,19 @@ route_finalise_kernel(const float* part_p, const int32_t* part_n, const float* p
 
 // --------------------------------------------------- several tokens per warp
 
-constexpr int kLanes = 8;
-
+template <int kL>
 __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-  for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  for (int d = kL / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
   return v;
 }
 
 // A lane's share of a row on kL lanes, V columns of it: of every 4 kL columns,
-// lane l has columns 4 l to 4 l + 3; past the row's end it holds -inf. Their sort keys are the order-preserving key of the logit above the
-// complement of its column, all different: those past the end come after the
-// row's own, of which there are at least k. 0 is below every key.
-template <typename X, int V, int kL = kLanes>
+// lane l has columns 4 l to 4 l + 3; past the row's end it holds -inf. Their
+// sort keys are the order-preserving key of the logit above the complement of
+// its column, all different: those past the end come after the row's own, of
+// which there are at least k. 0 is below every key.
+template <typename X, int V, int kL>
 struct Share;
 
 template <int V, int kL>
@@ -442,11 +442,12 @@ __device__ __forceinline__ void larger_ones(K (&top)[N], const K (&v)[N]) {
   for (int i = 0; i < N; ++i) top[i] = top[i] > v[N - 1 - i] ? top[i] : v[N - 1 - i];
 }
 
-// top: the N largest of all lanes' v, each descending; where kSet, unordered,
-// and the upper half of the lanes in the other half's order reversed. M < N: lanes' keys are joined until there are N.
-template <bool kSet, int D = 1, int M, int N, typename K>
+// top: the N largest of all kL lanes' v, each descending; where kSet,
+// unordered, and the upper half of the lanes in the other half's order
+// reversed. M < N: lanes' keys are joined until there are N.
+template <int kL, bool kSet, int D = 1, int M, int N, typename K>
 __device__ __forceinline__ void over_lanes(K (&v)[M], K (&top)[N]) {
-  if constexpr (D == kLanes) {
+  if constexpr (D == kL) {
     static_assert(M == N, "too few lanes for N keys");
 #pragma unroll
     for (int i = 0; i < N; ++i) top[i] = v[i];
@@ -462,33 +463,33 @@ __device__ __forceinline__ void over_lanes(K (&v)[M], K (&top)[N]) {
         both[2 * M - 1 - i] = other[i];
       }
       sort_bitonic(both);
-      over_lanes<kSet, 2 * D>(both, top);
+      over_lanes<kL, kSet, 2 * D>(both, top);
     } else {
       larger_ones(v, other);
-      if constexpr (!kSet || 2 * D < kLanes) sort_bitonic(v);
-      over_lanes<kSet, 2 * D>(v, top);
+      if constexpr (!kSet || 2 * D < kL) sort_bitonic(v);
+      over_lanes<kL, kSet, 2 * D>(v, top);
     }
   }
 }
 
 // V: columns per lane; N: picks kept, at least k.
-template <typename X, int V, int N, bool kStats>
+template <typename X, int kL, int V, int N, bool kStats>
 __global__ void __launch_bounds__(kThreads)
 route_group_kernel(const X* __restrict__ x, const RouteParams p) {
-  using Key = Share<X, V>;
+  using Key = Share<X, V, kL>;
   using K = typename Key::K;
   constexpr int B = V < N ? V : N;      // block of columns sorted at once
-  // Eight picks of more than 64 columns: no pick is outside the eight pieces
-  // of four columns with the largest leaders (of equal ones the first), since
-  // a better piece's leader comes before all of this one. So the networks run
-  // on leaders, and then on the eight pieces, one per lane, read once more:
+  // From 16 columns per lane on: no pick is outside the N pieces of four
+  // columns with the largest leaders (of equal ones the first), since a better
+  // piece's leader comes before all of this one. So the networks run on
+  // leaders, and then on those pieces, one per lane, read once more:
   // 121088 x 256 BF16 40 -> 29 us, 121088 x 128 fp32 68 -> 54.
-  constexpr bool kLead = V >= 16 && N == kLanes;
-  constexpr int kMine = N > kLanes ? N / kLanes : 1;  // picks per lane
+  constexpr bool kLead = V >= 16 && N <= kL;
+  constexpr int kMine = N > kL ? N / kL : 1;  // picks per lane
   extern __shared__ float sh[];         // kStats: [kWarps][E] sums, int [E] picks, [kWarps] z
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
-  const int l = lane & (kLanes - 1);
+  const int l = lane & (kL - 1);
   const int E = p.E, k = p.k;
   int* hist = reinterpret_cast<int*>(sh + kWarps * E);
   float pacc[kStats ? V : 1];
@@ -500,11 +501,11 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
     for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
     __syncthreads();
   }
-  constexpr int kTokens = 32 / kLanes;
+  constexpr int kTokens = 32 / kL;
   for (long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * kTokens; t0 < p.T;
        t0 += static_cast<long long>(gridDim.x) * kWarps * kTokens) {
-    const bool here = t0 + lane / kLanes < p.T;
-    const long long t = here ? t0 + lane / kLanes : p.T - 1;
+    const bool here = t0 + lane / kL < p.T;
+    const long long t = here ? t0 + lane / kL : p.T - 1;
     Key own;
     own.load(x + t * E, E, l, p.pieces);
     K top[N];
@@ -513,20 +514,21 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) lead[i] = own.lead(4 * i, l);
       sort_down(lead);
-      over_lanes<true>(lead, top);
-      const int at = l < kLanes / 2 ? l : N - 1 - l;  // lane l's is l in the first lanes' order
+      over_lanes<kL, true>(lead, top);
+      // lane l's piece is l in the order of the first lanes
+      const int at = l < kL / 2 ? l : N - 1 - l;
       K mine = top[0];
 #pragma unroll
-      for (int j = 1; j < kLanes / 2; ++j)
+      for (int j = 1; j < (N < kL ? N : kL / 2); ++j)
         if (at == j) mine = top[j];
       const int piece = Key::column_of(mine) / 4;
-      Share<X, 4> four;
+      Share<X, 4, kL> four;
       four.load(x + t * E, E, piece, p.pieces);
       K key[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) key[i] = four.key(i, piece);
+      for (int i = 0; i < 4; ++i) key[i] = N < kL && l >= N ? K(0) : four.key(i, piece);
       sort_down(key);
-      over_lanes<false>(key, top);
+      over_lanes<kL, false>(key, top);
     } else {
       K best[B];
 #pragma unroll
@@ -543,7 +545,7 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
           sort_bitonic(best);
         }
       }
-      over_lanes<false>(best, top);
+      over_lanes<kL, false>(best, top);
     }
     const float m = Key::value_of_key(top[0]);
     const bool dead = m == -INFINITY;  // no expert left: everything of the row is zero
@@ -553,30 +555,30 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
 #pragma unroll
       for (int i = 0; i < (kStats ? V : 1); ++i)
         mass += e[i] = dead ? 0.0f : expf(own.value(i) - m);
-      mass = group_sum(mass);
+      mass = group_sum<kL>(mass);
     } else if (!p.sigmoid && !p.renorm) {
 #pragma unroll
       for (int i = 0; i < V; ++i) mass += dead ? 0.0f : expf(own.value(i) - m);
-      mass = group_sum(mass);
+      mass = group_sum<kL>(mass);
     }
-    // lane l writes picks l, l + 8, ..
+    // lane l writes picks l, l + kL, ..
     int id[kMine];
     float s[kMine], picked = 0.0f;
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
-      K mine = top[q * kLanes < N ? q * kLanes : 0];
+      K mine = top[q * kL];
 #pragma unroll
-      for (int j = 1; j < kLanes; ++j)
-        if (q * kLanes + j < N && l == j) mine = top[q * kLanes + j < N ? q * kLanes + j : 0];
+      for (int j = 1; j < kL; ++j)
+        if (q * kL + j < N && l == j) mine = top[q * kL + j < N ? q * kL + j : 0];
       const float mv = Key::value_of_key(mine);
       id[q] = Key::column_of(mine);
-      s[q] = q * kLanes + l >= k || dead ? 0.0f : (p.sigmoid ? sigmoid_of(mv) : expf(mv - m));
+      s[q] = q * kL + l >= k || dead ? 0.0f : (p.sigmoid ? sigmoid_of(mv) : expf(mv - m));
       picked += s[q];
     }
-    const float denom = p.renorm ? group_sum(picked) : mass;
+    const float denom = p.renorm ? group_sum<kL>(picked) : mass;
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
-      const int j = q * kLanes + l;
+      const int j = q * kL + l;
       if (j >= k || !here) continue;
       float w = s[q];
       if (p.renorm || !p.sigmoid) w = denom > 0.0f || denom != denom ? w / denom : 0.0f;
@@ -590,7 +592,7 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
           float tot = 0.0f;
 #pragma unroll
           for (int i = 0; i < V; ++i) tot += e[i] = sigmoid_of(own.value(i));
-          tot = group_sum(tot);
+          tot = group_sum<kL>(tot);
           const float inv = tot > 0.0f || tot != tot ? 1.0f / tot : 0.0f;
           if (here) {
 #pragma unroll
@@ -607,14 +609,14 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
     }
   }
   if constexpr (kStats) {
-    // the warp's four tokens' sums, then the block's warps'
+    // the sums over the warp's tokens, then the block's warps
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float a = pacc[i];
-      a += __shfl_xor_sync(kFull, a, 8);
-      a += __shfl_xor_sync(kFull, a, 16);
+#pragma unroll
+      for (int d = kL; d < 32; d *= 2) a += __shfl_xor_sync(kFull, a, d);
       const int c = Key::column(l, i);
-      if (lane < kLanes && c < E) sh[warp * E + c] = a;
+      if (lane < kL && c < E) sh[warp * E + c] = a;
     }
     float* zs = reinterpret_cast<float*>(hist + E);
     zacc = warp_sum(zacc);
@@ -810,33 +812,35 @@ route_bwd_kernel(const X* x, const RouteBwdParams p, X* dx) {
   }
 }
 
-// Whether eight lanes hold a row and its picks.
-inline bool by_groups(int E, int k) { return E <= 32 * kLanes && k <= 2 * kLanes; }
+// Lanes per token of the forward: eight or 16 hold a row and its picks, else a
+// warp (121088 x 512 fp32, k 8: 167 us against 202).
+inline int fwd_lanes(int E, int k) { return E > 512 || k > 16 ? 32 : E > 256 ? 16 : 8; }
 
-template <typename X, bool kStats, int V>
-cudaError_t launch_route_group(const RouteArgs& a, const RouteParams& p, int blocks, size_t smem,
-                               cudaStream_t stream) {
-  const X* x = static_cast<const X*>(a.logits);
+template <typename X, bool kStats, int kL, int V>
+void launch_route_group(const RouteArgs& a, const RouteParams& p, int blocks, size_t smem,
+                        cudaStream_t stream) {
+  const auto go = [&](auto kernel) {
+    kernel<<<blocks, kThreads, smem, stream>>>(static_cast<const X*>(a.logits), p);
+  };
   if constexpr (V <= 4) {
-    if (a.k <= 4) route_group_kernel<X, V, 4, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
-    else if (a.k <= 8) route_group_kernel<X, V, 8, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
-    else route_group_kernel<X, V, 16, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
-  } else {
-    if (a.k <= 8) route_group_kernel<X, V, 8, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
-    else route_group_kernel<X, V, 16, kStats><<<blocks, kThreads, smem, stream>>>(x, p);
+    if (a.k <= 4) return go(route_group_kernel<X, kL, V, 4, kStats>);
   }
-  count_launch();
-  return cudaGetLastError();
+  if (a.k <= 8) go(route_group_kernel<X, kL, V, 8, kStats>);
+  else go(route_group_kernel<X, kL, V, 16, kStats>);
 }
 
 template <typename X, bool kStats>
 cudaError_t launch_route_t(const RouteArgs& a, const RouteParams& p, int blocks, size_t smem,
                            cudaStream_t stream) {
-  if (by_groups(a.E, a.k)) {
-    if (a.E <= 4 * kLanes) return launch_route_group<X, kStats, 4>(a, p, blocks, smem, stream);
-    if (a.E <= 8 * kLanes) return launch_route_group<X, kStats, 8>(a, p, blocks, smem, stream);
-    if (a.E <= 16 * kLanes) return launch_route_group<X, kStats, 16>(a, p, blocks, smem, stream);
-    return launch_route_group<X, kStats, 32>(a, p, blocks, smem, stream);
+  const int lanes = fwd_lanes(a.E, a.k);
+  if (lanes < 32) {
+    if (a.E <= 32) launch_route_group<X, kStats, 8, 4>(a, p, blocks, smem, stream);
+    else if (a.E <= 64) launch_route_group<X, kStats, 8, 8>(a, p, blocks, smem, stream);
+    else if (a.E <= 128) launch_route_group<X, kStats, 8, 16>(a, p, blocks, smem, stream);
+    else if (lanes == 8) launch_route_group<X, kStats, 8, 32>(a, p, blocks, smem, stream);
+    else launch_route_group<X, kStats, 16, 32>(a, p, blocks, smem, stream);
+    count_launch();
+    return cudaGetLastError();
   }
   const X* x = static_cast<const X*>(a.logits);
   const int v = (a.E + 31) / 32;
@@ -905,7 +909,7 @@ cudaError_t launch_route(const RouteArgs& a, const DeviceInfo& dev, cudaStream_t
   p.pieces =
       a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (a.bf16 ? 8 : 16) == 0;
   const bool stats = a.counts != nullptr || a.losses != nullptr;
-  const int tokens = by_groups(a.E, a.k) ? 32 / kLanes : 1;  // per warp
+  const int tokens = 32 / fwd_lanes(a.E, a.k);  // per warp
   const long long want =
       (static_cast<long long>(a.T) + kWarps * tokens - 1) / (kWarps * tokens);
   const int blocks = static_cast<int>(want < kRouteMaxBlocks ? want : kRouteMaxBlocks);

@@ -113,7 +113,8 @@ def test_nan_and_infinities_keep_valid_ids(gg):
             assert torch.isnan(r["prob"][:2]).all()
 
 
-@pytest.mark.parametrize("E", [29, 33, 64, 65, 70, 127, 128, 130, 200, 254, 256])
+@pytest.mark.parametrize("E", [29, 33, 64, 65, 70, 127, 128, 130, 200, 254, 256, 257, 300,
+                               511, 512])
 @pytest.mark.parametrize("k", [1, 3, 8, 16])
 def test_picks_among_many_equal_logits(gg, E, k):
     # few values, infinities and NaN among them, in rows that start at any element; NaN is the
@@ -139,7 +140,7 @@ def test_picks_among_many_equal_logits(gg, E, k):
 
 
 @pytest.mark.parametrize("T,E,k", [(700, 70, 8), (700, 128, 8), (301, 200, 5), (300, 255, 8),
-                                   (300, 256, 12), (40, 96, 16)])
+                                   (300, 256, 12), (40, 96, 16), (200, 512, 8), (201, 390, 10)])
 def test_wide_rows_match_oracle(gg, T, E, k):
     for dtype in (torch.float32, torch.bfloat16):
         t, x = _logits(T + E + k, T, E, dtype, masked=E // 9, dead=0.05)
