@@ -11,20 +11,22 @@
 // round to fp32).
 //
 // The weights are the tensor core's A operand (M = 256 weight rows per pair
-// of CTAs), the tokens its B operand (N = up to 192 tokens, in steps of 32):
+// of CTAs), the tokens its B operand (N = up to 256 tokens, in steps of 32):
 // an expert's ragged token count then costs what it has, not a multiple of 256.
 // Shared-memory bandwidth is what widening strains, so the widened weights go
 // to tensor memory, which MMAs read as well (tcgen05.st, A in TMEM), and only
-// the widened tokens to shared memory: 52 KB per 64-deep step and SM against
-// 96 KB with both in shared memory.
+// the widened tokens to shared memory.
 //
-// Bound by the instructions that widen (about 1350 per SM and 64 codes, 0.58
-// of the issue slots; the tensor pipe is 0.6 busy): without widening the
-// weights or the tokens it would run 1.16 times as fast each, with neither 1.4
-// times. Measured, 131072 rows: 4096 x 4096, one expert, 1576 TFLOP/s; 128
-// experts, 1536 x 2048 gated, 660 to 700 us (1180 to 1250 TFLOP/s).
+// Large products run at 0.9 of the rate the FP16 pipe reaches elsewhere: 65536
+// rows, 4096 x 4096, one expert 1290 us (1700 TFLOP/s); 131072 rows of 128
+// experts, 1536 x 2048 gated, 600 us (1370 TFLOP/s); 32768 rows of 32 experts,
+// 4096 x 4096 gated, 656 us (1676 TFLOP/s). With blocks of up to 192 tokens
+// these took 1397, 650 and 791: every block widens its weights anew. Below
+// about 128 rows per expert the weights bound it (4096 rows of those 128
+// experts: 91 us, 4.6 TB/s), and the way of a step through its two widened
+// places: widening, arrival at the issuer, MMAs, release.
 //
-// One CTA per SM in clusters of two (one tcgen05 MMA pair, 640 threads per
+// One CTA per SM in clusters of two (one tcgen05 MMA pair, 768 threads per
 // CTA, warp-specialised):
 //   warp 0       TMA producer: 128 weight rows (gated: 64 gate rows and the
 //                matching 64 up rows) and half the tokens, 128 codes deep, into
@@ -34,15 +36,17 @@
 //                tcgen05.mma.cta_group::2 (M = 256, K = 16);
 //   warp 2       finds the work items ahead of the others;
 //   warps 4-11   widen the weights into TMEM, one thread per row;
-//   warps 12-15  widen the tokens into shared memory (K-major, 128-byte
+//   warps 12-19  widen the tokens into shared memory (K-major, 128-byte
 //                swizzle). Both in two groups, for the two halves of a step;
-//   warps 16-19  epilogue: one TMEM lane = one weight row, one column = one
+//   warps 20-23  epilogue: one TMEM lane = one weight row, one column = one
 //                token. Gated: the up rows' warps hand their values to the
 //                gate rows' warps through shared memory.
-// TMEM: two accumulators of 192 columns and two steps of weights (64 columns
-// each). A step is 128 deep so that the issuer, whose loop costs it about 300
-// cycles, keeps ahead of the MMAs (400 per 64 codes). Work items are (expert, block of weight rows, block of tokens), the
-// token block fastest, so that neighbours share their weights in L2.
+// TMEM: 384 columns of sums, given to the items in turn, and two steps of
+// weights (64 columns each). A step is 128 deep so that the issuer, whose loop
+// costs it about 300 cycles, keeps ahead of the MMAs (256 tokens: 512 cycles
+// per 64 codes). Work items are (expert, block of weight rows, block of
+// tokens), the token block fastest, so that neighbours share their weights in
+// L2.
 //
 // Every wait is bounded (gg_ptx.cuh); a wait that runs out records
 // GG_ERR_DEVICE_TIMEOUT, raises a CTA-wide abort flag, and the CTA drains
@@ -52,6 +56,7 @@
 
 #include <atomic>
 #include <cstddef>
+#include <type_traits>
 
 #include "gg_epilogue.cuh"
 #include "gg_internal.h"
@@ -63,33 +68,40 @@ namespace gg {
 namespace {
 
 constexpr int BM = 128;     // weight rows per CTA
-constexpr int BN = 192;     // most tokens per work item
+constexpr int BN = 256;     // most tokens per work item
 constexpr int BK = 64;      // half a step: what a group of widening warps takes
 constexpr int RK = 128;     // codes of K per step
 constexpr int RAW = 4;      // raw steps in flight
 constexpr int WIDE = 2;     // widened steps
+constexpr int UNITS = 6;    // TMEM for sums, in units of 64 columns
+constexpr int kUnit = 64;
 constexpr uint16_t kPairMask = 0x3;
 constexpr int kItemWarp = 2;
-constexpr int kFirstA = 4, kFirstB = 12, kFirstEpi = 16;  // first warps of the roles
+constexpr int kFirstA = 4, kFirstB = 12, kFirstEpi = 20;  // first warps of the roles
 constexpr int kGroups = 2;     // groups of widening warps, one for each half of a step:
 constexpr int kAWarps = 4;     // warps of a group for the weights
-constexpr int kBWarps = 2;     // and for the tokens
+constexpr int kBWarps = 4;     // and for the tokens, eight rows at a time each
+constexpr int kFew = 2;        // turns of a token warp that have code of their own
 constexpr int kEpiWarps = 4;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kItems = 4;      // work items found ahead
-constexpr int kBoxRows = 16;                         // tokens per TMA box
+constexpr int kBoxes = 3;      // heights of token boxes: 64, 32 and 16 rows
 constexpr uint32_t RAW_A = BM * RK;                  // 16 KB of weight codes
-constexpr uint32_t RAW_BYTES = RAW_A + BN / 2 * RK;  // and up to 12 KB of token codes
+constexpr uint32_t RAW_BYTES = RAW_A + BN / 2 * RK;  // and up to 16 KB of token codes
 constexpr uint32_t WIDE_HALF = BN / 2 * BK * 2;      // half a step's tokens as FP16
 constexpr uint32_t WIDE_BYTES = 2 * WIDE_HALF;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t kTmemA = 2 * BN;                  // TMEM column of the first weight step
+constexpr uint32_t kTmemA = UNITS * kUnit;           // TMEM column of the first weight step
 constexpr uint32_t kStepCols = RK / 2;               // two FP16 per column
 
-// A work item: expert, block of weight rows, its tokens (first row, number).
-// rows < 0: there are no more items.
+// A work item: expert, block of weight rows, its tokens (first row, number;
+// rows < 0: there are no more items). Its sums take `cols` columns of TMEM, a
+// multiple of 32: `first` from column `col` on, and any others from column 0
+// on, by MMAs of their own.
 struct alignas(16) Item {
   int e, nt, row0, rows;
+  int col, cols, first;
+  int pad_;
 };
 
 struct SmemTail {
@@ -100,8 +112,8 @@ struct SmemTail {
   uint64_t raw_empty[RAW];
   uint64_t ready[WIDE];    // even CTA: both CTAs widened the step
   uint64_t empty[WIDE];
-  uint64_t tfull[2];
-  uint64_t tempty[2];
+  uint64_t tfull[UNITS];   // of the item that starts in this unit
+  uint64_t tempty[UNITS];
   uint64_t up_full[2];     // a chunk of up values, per pair of epilogue warps
   uint64_t up_empty[2];
   uint64_t mma_done;
@@ -122,7 +134,6 @@ constexpr uint32_t kTailAt = kUpAt + 2 * kUpBytes;
 constexpr size_t kSmemBytes = 1024 + kTailAt + sizeof(SmemTail);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(offsetof(SmemTail, scale) % 16 == 0 && kTailAt % 16 == 0, "float4 reads");
-static_assert(32 % (16 * kBWarps) == 0, "an item's tokens per CTA are whole turns");
 static_assert(kTmemA + WIDE * kStepCols <= TMEM_COLS, "tensor memory budget");
 static_assert(kWideAt % 1024 == 0 && WIDE_BYTES % 1024 == 0, "128-byte swizzle");
 
@@ -160,7 +171,7 @@ __device__ __forceinline__ Item item_of(int tile, const QParams& p, const SmemTa
   const int tb = local - it.nt * blocks;
   const int each = ((rows + blocks - 1) / blocks + 31) / 32 * 32;  // as even as 32s allow
   it.row0 = first + tb * each;
-  it.rows = max(0, min(each, rows - tb * each));
+  it.rows = min(each, rows - tb * each);  // each <= BN: no block is empty
   return it;
 }
 
@@ -183,8 +194,28 @@ struct ItemReader {
   }
 };
 
-// Columns of an item's MMAs.
-__device__ __forceinline__ int columns_of(const Item& it) { return max(32, (it.rows + 31) & ~31); }
+// Gives the items their columns in turn. Up to 192 lie together (narrow MMAs
+// cost what one of 128 columns does: two of 96 took 1.2 times as long as one
+// of 192). More than that take four units from an even one on: two such items
+// do not fit, so every third one goes over the end in two halves, and the next
+// item's MMAs can start as the first units are read out.
+struct Columns {
+  int at = 0;  // unit
+  __device__ __forceinline__ void give(Item& it) {
+    it.cols = (it.rows + 31) & ~31;
+    it.first = it.cols;
+    const int units = (it.cols + kUnit - 1) / kUnit;
+    if (units > UNITS / 2) {
+      at = (at + 1) & ~1;
+      if (at == UNITS) at = 0;
+      it.first = min(it.cols, (UNITS - at) * kUnit);
+    } else if (at + units > UNITS) {
+      at = 0;
+    }
+    it.col = at * kUnit;
+    at = (at + units) % UNITS;
+  }
+};
 
 // FP16 operands (format fields 0), fp32 sums, M = 256, N = n; both K-major.
 __device__ __forceinline__ uint32_t idesc_f16(int n) {
@@ -216,9 +247,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+struct TokenMaps {
+  CUtensorMap box[kBoxes];
+};
+
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
-q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__ CUtensorMap mapW,
+q8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ CUtensorMap mapW,
                const QParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -273,9 +308,11 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
         mbar_init(smem_u32(&st.ready[s]), 2 * kGroups * (kAWarps + kBWarps));
         mbar_init(smem_u32(&st.empty[s]), 1);
       }
-      for (int a = 0; a < 2; ++a) {
+      for (int a = 0; a < UNITS; ++a) {
         mbar_init(smem_u32(&st.tfull[a]), 1);
         mbar_init(smem_u32(&st.tempty[a]), 2 * kEpiWarps);
+      }
+      for (int a = 0; a < 2; ++a) {
         mbar_init(smem_u32(&st.up_full[a]), 1);
         mbar_init(smem_u32(&st.up_empty[a]), 1);
       }
@@ -307,7 +344,7 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------- TMA producer
-      tma_prefetch_desc(&mapT);
+      for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&mapT.box[i]);
       tma_prefetch_desc(&mapW);
       const int h = static_cast<int>(crank);
       int stage = 0;
@@ -319,8 +356,11 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
         // two boxes of 64 weight rows: gated, gate rows and the matching up rows
         const int n0 = kGated ? it.nt * BM + h * (BM / 2) : it.nt * 2 * BM + h * BM;
         const int n1 = kGated ? p.F + n0 : n0 + BM / 2;
-        const int half = columns_of(it) / 2;  // a multiple of 16
-        const int r0 = it.row0 + h * half;
+        // this CTA's half of the tokens of either MMA, multiples of 16
+        const int half = it.cols / 2;
+        const int half0 = it.first / 2;
+        const int r0 = it.row0 + h * half0;
+        const int r1 = it.row0 + half0 + h * (half - half0);  // of token half0 on
         for (int c = 0; c < p.K; c += RK) {
           if (!mbar_wait_bounded(smem_u32(&st.raw_empty[stage]), phase ^ 1u, abort_flag,
                                  p.status)) {
@@ -332,8 +372,18 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
           mbar_arrive_expect_tx(bar, RAW_A + half * RK);
           tma_load_3d(sa, &mapW, bar, c, n0, it.e);
           tma_load_3d(sa + RAW_A / 2, &mapW, bar, c, n1, it.e);
-          for (int i = 0; i < half; i += kBoxRows)
-            tma_load_2d(sa + RAW_A + i * RK, &mapT, bar, c, r0 + i);
+          // few boxes: 16 rows at a time, this thread held the others up
+          const auto rows = [&](int i, int end, int from) {
+            for (; i + 64 <= end; i += 64)
+              tma_load_2d(sa + RAW_A + i * RK, &mapT.box[0], bar, c, from + i);
+            if (i + 32 <= end) {
+              tma_load_2d(sa + RAW_A + i * RK, &mapT.box[1], bar, c, from + i);
+              i += 32;
+            }
+            if (i < end) tma_load_2d(sa + RAW_A + i * RK, &mapT.box[2], bar, c, from + i);
+          };
+          rows(0, half0, r0);
+          if (half > half0) rows(half0, half, r1);
           used |= 1u << stage;
           last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == RAW) {
@@ -353,9 +403,13 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
       // ------------------------------------------------------ work items
       int slot = 0;
       uint32_t phase = 0;
+      Columns columns;
       for (int i = first;; i += step) {
         Item it{0, 0, 0, -1};
-        if (i < total) it = item_of(i, p, st);
+        if (i < total) {
+          it = item_of(i, p, st);
+          columns.give(it);
+        }
         if (!mbar_wait_bounded(smem_u32(&st.item_empty[slot]), phase ^ 1u, abort_flag, p.status))
           break;
         st.item[slot] = it;
@@ -376,18 +430,26 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
       // column 0.
       int stage = 0;
       uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
+      uint32_t unit_phase = 0;  // one bit per unit
       bool ok = tmem_base == 0;
       const uint64_t desc0 = make_sdesc(sbase + kWideAt, 16, 1024);
       Item it;
       ItemReader items;
       while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
-        const uint32_t idesc = idesc_f16(__shfl_sync(0xFFFFFFFFu, columns_of(it), 0));
-        if (!mbar_wait_bounded(smem_u32(&st.tempty[acc]), acc_phase ^ 1u, abort_flag, p.status))
-          break;
+        // reductions, for their results are in uniform registers
+        const int n = __reduce_max_sync(0xFFFFFFFFu, it.cols);
+        const int n0 = __reduce_max_sync(0xFFFFFFFFu, it.first);
+        const uint32_t d0 = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(it.col));
+        const uint32_t idesc0 = idesc_f16(n0), idesc1 = idesc_f16(n - n0);
+        const uint64_t second = (n0 / 2 * 128) >> 4;  // where the others' tokens begin
+        for (int i = 0; i < n && ok; i += kUnit) {
+          const int u = i < n0 ? d0 / kUnit + i / kUnit : (i - n0) / kUnit;
+          ok = mbar_wait_bounded(smem_u32(&st.tempty[u]), (unit_phase >> u & 1u) ^ 1u, abort_flag,
+                                 p.status);
+          unit_phase ^= 1u << u;
+        }
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d_tmem = acc * BN;
         for (int c = 0; c < p.K; c += RK) {
           if (!mbar_wait_bounded(smem_u32(&st.ready[stage]), phase, abort_flag, p.status)) {
             ok = false;
@@ -396,16 +458,25 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
           tc_fence_after();
           const uint64_t desc = desc0 + stage * (WIDE_BYTES >> 4);
           const uint32_t ta = kTmemA + stage * kStepCols;
-          if (elect_one()) {
+          const auto half_step = [&](uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                     uint32_t more) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              tc_mma_f16_pair_ta(d_tmem, ta + kk * 8, desc + kk * 2, idesc,
-                                 (c | kk) != 0 ? 1u : 0u);
+              tc_mma_f16_pair_ta(d, a + kk * 8, b + kk * 2, idesc, (more | kk) != 0 ? 1u : 0u);
+          };
+          if (n == n0) {
+            if (elect_one()) {
+              half_step(d0, ta, desc, idesc0, c);
+              if (c + BK < p.K)
+                half_step(d0, ta + BK / 2, desc + (WIDE_HALF >> 4), idesc0, 1u);
+              tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
+            }
+          } else if (elect_one()) {
+            half_step(d0, ta, desc, idesc0, c);
+            half_step(0, ta, desc + second, idesc1, c);
             if (c + BK < p.K) {
-#pragma unroll
-              for (int kk = 0; kk < BK / 16; ++kk)
-                tc_mma_f16_pair_ta(d_tmem, ta + BK / 2 + kk * 8,
-                                   desc + (WIDE_HALF >> 4) + kk * 2, idesc, 1u);
+              half_step(d0, ta + BK / 2, desc + (WIDE_HALF >> 4), idesc0, 1u);
+              half_step(0, ta + BK / 2, desc + second + (WIDE_HALF >> 4), idesc1, 1u);
             }
             tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
           }
@@ -416,10 +487,8 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
           }
         }
         if (!ok) break;
-        if (elect_one()) tc_commit_pair_mc(smem_u32(&st.tfull[acc]), kPairMask);
+        if (elect_one()) tc_commit_pair_mc(smem_u32(&st.tfull[d0 / kUnit]), kPairMask);
         __syncwarp();
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
       }
       if (elect_one()) {
         tc_commit_pair(smem_u32(&st.mma_done));
@@ -443,7 +512,7 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
     const int piece = weights ? 0 : lane >> 3;
     const uint8_t* from = smem + (weights ? 0 : RAW_A) + row * RK +
                           (((4 * group + piece) ^ (row & 7)) << 4);
-    const uint32_t flip = (reinterpret_cast<uintptr_t>(from) & 0x70u);  // to reach piece i: ^ i << 4
+    const uint32_t flip = reinterpret_cast<uintptr_t>(from) & 0x70u;  // piece i is at ^ i << 4
     uint8_t* to = smem + kWideAt + group * WIDE_HALF + row * 128;
     const uint32_t to0 = ((2 * piece) ^ (row & 7)) << 4, to1 = ((2 * piece + 1) ^ (row & 7)) << 4;
     const uint32_t ta0 = tmem_base + kTmemA + (static_cast<uint32_t>(q * 32) << 16) +
@@ -458,7 +527,9 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
     Item it;
     ItemReader items;
     while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
-      const int turns = columns_of(it) / 2 / (8 * kBWarps);  // of a token warp
+      // of a token warp: turns of eight rows, 8 kBWarps rows apart
+      const int turns =
+          (it.cols / 2 - 8 * ((warp - kFirstB) % kBWarps) + 8 * kBWarps - 1) / (8 * kBWarps);
       for (int k0 = 0; k0 < p.K; k0 += RK) {
         // K an odd multiple of 64: the last step has one half
         const bool there = k0 + group * BK < p.K;
@@ -494,18 +565,17 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
           tc_fence_before();
         } else {
           // the codes are read ahead of the wait for the place they go to
-          constexpr int kTurns = BN / 2 / (8 * kBWarps);
-          uint4 c[kTurns];
+          const auto tokens = [&](auto most) {
+            constexpr int kTurns = decltype(most)::value;
+            uint4 c[kTurns];
 #pragma unroll
-          for (int j = 0; j < kTurns; ++j)
-            if (j < turns) c[j] = *reinterpret_cast<const uint4*>(raw + j * 8 * kBWarps * RK);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty_raw + 8 * rs);
-          if (!mbar_wait_bounded(empty_bar + 8 * ws, wp ^ 1u, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          if (there) {
+            for (int j = 0; j < kTurns; ++j)
+              if (j < turns) c[j] = *reinterpret_cast<const uint4*>(raw + j * 8 * kBWarps * RK);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_raw + 8 * rs);
+            if (!mbar_wait_bounded(empty_bar + 8 * ws, wp ^ 1u, abort_flag, p.status))
+              return false;
+            if (!there) return true;
             uint8_t* wide = to + ws * WIDE_BYTES;
 #pragma unroll
             for (int j = 0; j < kTurns; ++j)
@@ -516,7 +586,14 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
                 *reinterpret_cast<uint4*>(line + to0) = make_uint4(a.x, a.y, b.x, b.y);
                 *reinterpret_cast<uint4*>(line + to1) = make_uint4(d.x, d.y, e.x, e.y);
               }
-          }
+            return true;
+          };
+          // few turns have code of their own: masked ones are not free (4096 rows
+          // of 128 experts: 99 us with the one code, 91)
+          constexpr int kMost = BN / 2 / (8 * kBWarps);
+          ok = turns <= kFew ? tokens(std::integral_constant<int, kFew>())
+                             : tokens(std::integral_constant<int, kMost>());
+          if (!ok) break;
           fence_proxy_async();
         }
         __syncwarp();
@@ -550,8 +627,7 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
     const int width = kGated ? p.F : p.N;
     uint4* stg = reinterpret_cast<uint4*>(smem + kStagingAt + w * kWarpStagingBytes);
     float* ups = reinterpret_cast<float*>(smem + kUpAt + pair * kUpBytes);
-    int acc = 0;
-    uint32_t acc_phase = 0;
+    uint32_t unit_phase = 0;  // one bit per unit
     uint32_t up_phase = 0;
     bool ok = true;
     Item it;
@@ -571,9 +647,13 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
         sc[i] = r < it.rows ? p.As[it.row0 + r] : 0.0f;
         if (up && p.row_scale != nullptr && r < it.rows) sc[i] *= p.row_scale[it.row0 + r];
       }
-      if (!mbar_wait_bounded(smem_u32(&st.tfull[acc]), acc_phase, abort_flag, p.status)) break;
+      const int start = it.col / kUnit;
+      if (!mbar_wait_bounded(smem_u32(&st.tfull[start]), unit_phase >> start & 1u, abort_flag,
+                             p.status))
+        break;
+      unit_phase ^= 1u << start;
       tc_fence_after();
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
+      const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
       for (int c = 0; c < it.rows; c += 32) {
         const int have = min(32, it.rows - c);
@@ -582,8 +662,13 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
 #pragma unroll
         for (int i = 0; i + 1 < BN / 32; ++i) sc[i] = sc[i + 1];
         float v[32];
-        tmem_ld32(tbase + c, v);
+        const int col = c < it.first ? it.col + c : c - it.first;
+        tmem_ld32(lanes + col, v);
+        const bool unit_read = (c & 32) != 0 || c + 32 >= it.rows;
+        if (unit_read) tc_fence_before();
         __syncwarp();
+        if (unit_read && lane == 0)
+          mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&st.tempty[col / kUnit]), 0));
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&st.scale[w][i]);
@@ -634,12 +719,6 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
         }
         __syncwarp();
       }
-      if (!ok) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&st.tempty[acc]), 0));
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
     }
   }
 
@@ -653,7 +732,7 @@ q8_gemm_kernel(const __grid_constant__ CUtensorMap mapT, const __grid_constant__
 }
 
 template <bool kGated>
-cudaError_t launch_q8_gemm_t(const CUtensorMap& mt, const CUtensorMap& mw, const QParams& p,
+cudaError_t launch_q8_gemm_t(const TokenMaps& mt, const CUtensorMap& mw, const QParams& p,
                              const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<int> resident[kMaxDevices];
   // no more clusters than there can be work items
@@ -667,17 +746,21 @@ cudaError_t launch_q8_gemm_t(const CUtensorMap& mt, const CUtensorMap& mw, const
 }  // namespace
 
 cudaError_t launch_q8_gemm(const Q8GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  CUtensorMap mt, mw;
+  TokenMaps mt;
+  CUtensorMap mw;
   const cuuint64_t td[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.R_cap)};
   const cuuint64_t ts[1] = {static_cast<cuuint64_t>(a.K)};
-  const cuuint32_t tbox[2] = {RK, kBoxRows};
   const cuuint64_t wd[3] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.N),
                             static_cast<cuuint64_t>(a.E)};
   const cuuint64_t ws[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.K) * a.N};
   const cuuint32_t wbox[3] = {RK, BM / 2, 1};
-  if (!encode_map(&mt, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, 2, td, ts, tbox,
-                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, wd, ws, wbox,
+  for (int i = 0; i < kBoxes; ++i) {
+    const cuuint32_t tbox[2] = {RK, 64u >> i};
+    if (!encode_map(&mt.box[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, 2, td, ts, tbox,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  if (!encode_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, wd, ws, wbox,
                   CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   QParams p{};

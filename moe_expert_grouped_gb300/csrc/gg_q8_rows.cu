@@ -356,6 +356,9 @@ cudaError_t launch_rows_t(const CUtensorMap& ma, const CUtensorMap& mb, const Ro
 
 }  // namespace
 
+// Up to 16 rows per expert that can have any, which are multiplied in one pass
+// over the weights: 16 rows for each of 128 experts, 1536 x 2048 gated, take 80
+// us against the many-row kernel's 91, 32 take 138.
 bool q8_rows_fits(int R_cap, int E) {
   const int experts = R_cap < E ? R_cap : E;
   return R_cap <= 16 * experts;

@@ -137,6 +137,22 @@ def test_one_expert_with_most_of_few_rows(gg, case):
         _check(C, Aq, As, Wq, Ws, off, 1.0)
 
 
+@pytest.mark.parametrize("seed,gated", [(0, False), (1, True), (2, False), (3, True)])
+def test_many_blocks_of_mixed_sizes(gg, seed, gated):
+    # several work items per SM pair, from one token to 256, in every order
+    r = np.random.default_rng(900 + seed)
+    counts = r.choice([0, 1, 31, 33, 64, 70, 128, 129, 150, 190, 193, 224, 240, 256, 257, 300, 513],
+                      48).tolist()
+    N, K = (2048, 192) if gated else (1536, 320)
+    Aq, As, Wq, Ws, off = _random(counts, N, K, 3, 950 + seed)
+    dA, dS, dW, dT, dO = _dev(Aq, As, Wq, Ws, off)
+    ws = gg.workspace(0, 1, len(counts), "cuda")
+    epi = gg.GG_EPI_SWIGLU if gated else gg.GG_EPI_NONE
+    C = gg.q8_grouped_gemm(dA, dS, dW, dT, dO, epi, ws=ws)
+    assert gg.read_status(ws) == 0
+    _check(C, Aq, As, Wq, Ws, off, 1.0 if gated else 0.0)
+
+
 @pytest.mark.parametrize("K", [128, 256, 320, 512, 576, 1024, 1088, 2112, 4096, 8192])
 def test_quantised_rows_of_every_width(gg, K):
     g = torch.Generator().manual_seed(K)
