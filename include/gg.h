@@ -805,8 +805,8 @@ gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
  *                  v[:, F:] [* prob_of_row[r]]): no rounding before the last.
  * Other arguments, refusals and device errors as gg_grouped_fwd; rows outside
  * [0, offsets[E]) are never written. Results of a row do not depend on the
- * other rows of the batch beyond the choice of kernel, which goes by R_cap, E,
- * K and N.
+ * other rows of the batch beyond the choice of kernel, which goes by R_cap and
+ * E (both kernels' sums are exact below 2^24).
  *
  * gg_q8_grouped_fwd — quantise the rows of A[R_cap][K] (BF16, permuted order)
  * and multiply, in one call; the codes stay in ws, gg_q8_workspace_size(R_cap,
