@@ -93,6 +93,7 @@ constexpr int kMinSlice = 8;
 // What a partial block costs, in steps: writing 256 KB per pair and reading it
 // back take about as long as 10 steps of MMAs.
 constexpr int kPartialCost = 10;
+constexpr int kJoinCost = 24;
 
 // A work item: block (row block mt, column block nt) of expert e's dB over a
 // slice of its rows; slot: its partial block, -1 for the whole sum. rows < 0:
@@ -223,7 +224,8 @@ __device__ float cost_of(const WParams& p, const int* row_start, int slice) {
   }
   if (slots > static_cast<float>(p.slots)) return INFINITY;
   const float c = static_cast<float>(p.clusters);
-  return fmaxf(ceilf(items / c) * (work / items), longest) + slots * kPartialCost / c;
+  return fmaxf(ceilf(items / c) * (work / items), longest) + slots * kPartialCost / c +
+         (slots > 0.0f ? kJoinCost : 0.0f);
 }
 
 __device__ __forceinline__ Item item_of(int i, const WParams& p, const SmemTail& st) {
@@ -401,52 +403,60 @@ wgrad_kernel(const __grid_constant__ CUtensorMap mapD, const __grid_constant__ C
   volatile int* abort_flag = &st.abort_flag;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------- TMA producer
+    // ------------------------------------------------------ TMA producer
+    // The whole warp runs the loop and one lane issues, as the MMA issuer's
+    // does: its values go into uniform registers (by reductions) once per item.
+    if (elect_one()) {
       tma_prefetch_desc(&mapD);
       tma_prefetch_desc(&mapA);
-      const int h = static_cast<int>(crank);
-      int stage = 0;
-      uint32_t phase = 0, used = 0, last_phase = 0;
-      bool ok = true;
-      Item it;
-      ItemReader items;
-      while (ok && items.next(st, it, false, true, abort_flag, p.status)) {
-        const int n0 = it.mt * (2 * BM) + h * BM;
-        const int half = min(p.width, p.K - it.nt * p.width) / 2;  // a multiple of 32
-        const int k0 = it.nt * p.width + h * half;
-        const int boxes = (half + 63) / 64;
-        for (int r = 0; r < it.rows; r += BK) {
-          if (!mbar_wait_bounded(smem_u32(&st.empty[stage]), phase ^ 1u, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = smem_u32(&st.full[stage]);
-          const uint32_t sa = sbase + stage * STAGE_BYTES;
+    }
+    __syncwarp();
+    const int h = static_cast<int>(crank);
+    int stage = 0;
+    uint32_t phase = 0, used = 0, last_phase = 0;
+    bool ok = true;
+    Item it;
+    ItemReader items;
+    while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
+      const int nt = __reduce_max_sync(0xFFFFFFFFu, it.nt);
+      const int n0 = __reduce_max_sync(0xFFFFFFFFu, it.mt) * (2 * BM) + h * BM;
+      const int half = min(p.width, p.K - nt * p.width) / 2;  // a multiple of 32
+      const int k0 = nt * p.width + h * half;
+      const int boxes = (half + 63) / 64;
+      const int row0 = __reduce_max_sync(0xFFFFFFFFu, it.row0);
+      const int rows = __reduce_max_sync(0xFFFFFFFFu, it.rows);
+      for (int r = 0; r < rows; r += BK) {
+        if (!mbar_wait_bounded(smem_u32(&st.empty[stage]), phase ^ 1u, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = smem_u32(&st.full[stage]);
+        const uint32_t sa = sbase + stage * STAGE_BYTES;
+        if (elect_one()) {
           mbar_arrive_expect_tx(bar, A_BYTES + boxes * BOX_BYTES);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            tma_load_2d(sa + j * BOX_BYTES, &mapD, bar, n0 + 64 * j, it.row0 + r);
+            tma_load_2d(sa + j * BOX_BYTES, &mapD, bar, n0 + 64 * j, row0 + r);
             if (j < boxes)
-              tma_load_2d(sa + A_BYTES + j * BOX_BYTES, &mapA, bar, k0 + 64 * j, it.row0 + r);
+              tma_load_2d(sa + A_BYTES + j * BOX_BYTES, &mapA, bar, k0 + 64 * j, row0 + r);
           }
-          used |= 1u << stage;
-          last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        used |= 1u << stage;
+        last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // the CTA may not exit before its loads have landed and been consumed
-      for (int s = 0; s < kStages; ++s)
-        if (used & (1u << s)) {
-          (void)mbar_wait_bounded(smem_u32(&st.full[s]), (last_phase >> s) & 1u, nullptr,
-                                  p.status);
-          (void)mbar_wait_bounded(smem_u32(&st.empty[s]), (last_phase >> s) & 1u, nullptr,
-                                  p.status);
-        }
     }
+    // the CTA may not exit before its loads have landed and been consumed
+    for (int s = 0; s < kStages; ++s)
+      if (used & (1u << s)) {
+        (void)mbar_wait_bounded(smem_u32(&st.full[s]), (last_phase >> s) & 1u, nullptr, p.status);
+        (void)mbar_wait_bounded(smem_u32(&st.empty[s]), (last_phase >> s) & 1u, nullptr,
+                                p.status);
+      }
   } else if (warp == kPassWarp) {
     // ------------------------------------------------ pass on, zero the tail
     int stage = 0;
