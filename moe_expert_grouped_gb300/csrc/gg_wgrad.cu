@@ -2,8 +2,8 @@
 // dB[e] = dC_e^T A_e for every expert e in one persistent launch, the
 // reduction running over the expert's own (ragged) rows.
 //
-// One CTA per SM in clusters of two (one tcgen05 MMA pair, 384 or 640
-// threads per CTA, warp-specialised):
+// One CTA per SM in clusters of two (one tcgen05 MMA pair, 384 threads
+// per CTA, warp-specialised):
 //   warp 0      TMA producer: per 64-row step its CTA's 128 columns of dC and
 //               its half of up to 256 columns of A, 64 x 64 boxes of BF16
 //               with 128-byte swizzle. Both operands are used as they lie in
@@ -20,8 +20,7 @@
 //   warp 3      finds the work items (a search and divisions) ahead of the
 //               others and hands them on through a ring: found by the MMA
 //               issuer itself, each item cost it 1.5 us of idle tensor core;
-//   the others  epilogue (8 warps, 16 for fp32 results): one TMEM lane = one
-//               row of dB.
+//   the others  epilogue (8 warps): one TMEM lane = one row of dB.
 //
 // Work items are (expert, slice of its rows, block of dB), expert-major with
 // the block fastest: the blocks that share rows run side by side and find
@@ -30,8 +29,8 @@
 // clusters idle. Then the rows of an expert are cut into slices whose fp32
 // partial blocks go to the workspace, and a second kernel adds them in slice
 // order (the slice length is chosen at the kernel's start; results depend on
-// the offsets and sizes alone). 8 experts, 60000 rows, 768 x 320 fp32: 57 us,
-// of which the second kernel 8; whole blocks 68.
+// the offsets and sizes alone). 60000 rows, 768 x 320 fp32: one expert 46 us,
+// whole blocks 229; 4 experts 46 and 70; 8 experts, whole blocks, 46, slices 51.
 //
 // fp32 results: the tensor core truncates each of its additions, by up to
 // 2^-23 of the running sum and always towards zero, so a sum over 7500 rows
@@ -45,9 +44,9 @@
 // other (2048 x 768 over 128 experts, 32768 rows: 587 us against 285).
 //
 // Bound by the tensor pipe where experts have rows enough: 131072 rows, 4096 x
-// 4096, one expert 1865 TFLOP/s; 128 experts, 1536 x 2048 487 us (1693), 2048 x
-// 768 261 us. fp32 results over few rows are bound by memory: 32768 rows of 128
-// experts, 2048 x 768 with a base 285 to 309 us (6.3 to 5.8 TB/s), without 167.
+// 4096, one expert 1840 TFLOP/s; 128 experts, 1536 x 2048 482 us (1710), 2048 x
+// 768 255 us. fp32 results over few rows are bound by memory: 32768 rows of 128
+// experts, 2048 x 768 with a base 320 us (5.6 TB/s), without one 216.
 //
 // Every wait is bounded (gg_ptx.cuh); a wait that runs out records
 // GG_ERR_DEVICE_TIMEOUT, raises a CTA-wide abort flag, and the CTA drains
@@ -91,7 +90,7 @@ constexpr int kTried = 11;
 __constant__ const int kSlices[kTried] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 40, 76};
 constexpr int kMinSlice = 8;
 // What a partial block costs, in steps: writing 256 KB per pair and reading it
-// back take about as long as 10 steps of MMAs.
+// back take about as long as 10 steps of MMAs. The second kernel takes 24.
 constexpr int kPartialCost = 10;
 constexpr int kJoinCost = 24;
 
@@ -588,7 +587,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap mapD, const __grid_constant__ C
     const int c0 = ((warp - kFirstEpi) >> 2) * kCols;
     int acc = 0;
     uint32_t acc_phase = 0;
-    uint4* stg = reinterpret_cast<uint4*>(smem + L::kStagingAt + (warp - kFirstEpi) * kWarpStagingBytes);
+    uint4* stg =
+        reinterpret_cast<uint4*>(smem + L::kStagingAt + (warp - kFirstEpi) * kWarpStagingBytes);
     const uint32_t piece_at = L::kBaseAt + (warp - kFirstEpi) * kBaseBufs * kPieceBytes;
     uint32_t piece_phase = 0, pending = 0;
     bool ok = true;
