@@ -14,7 +14,7 @@
 // at 2.1 TB/s). Measured (events on an empty queue, 4 us of them launch):
 // forward of 121088 x 256 BF16, k 8, sigmoid 29 us, with statistics 89;
 // gradient 85; 121088 x 128 fp32, k 8 54 and 68, gradient 42; 16384 x 128 fp32,
-// k 8 15 and 21, gradient 13; 121088 x 32 fp32, k 2 23 and 33, gradient 21.
+// k 8 15 and 21, gradient 13; 121088 x 32 fp32, k 2 23 and 31, gradient 21.
 //
 // Selection works on the logits themselves, which both scores preserve the
 // order of, as order-preserving keys: the picks do not depend on how an
@@ -502,12 +502,23 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
     __syncthreads();
   }
   constexpr int kTokens = 32 / kL;
-  for (long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * kTokens; t0 < p.T;
-       t0 += static_cast<long long>(gridDim.x) * kWarps * kTokens) {
+  // With statistics there are two blocks per SM: too few warps to hide a row's
+  // loads, so the next row's are on their way meanwhile (121088 x 32 fp32, k 2:
+  // 35 -> 31 us; 16 columns per lane gain nothing by it).
+  constexpr bool kAhead = kStats && V <= 8;
+  const long long step = static_cast<long long>(gridDim.x) * kWarps * kTokens;
+  const auto row_of = [&](long long t0) { return min(t0 + lane / kL, p.T - 1LL); };
+  long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * kTokens;
+  Key own;
+  if (kAhead) own.load(x + row_of(t0) * E, E, l, p.pieces);
+  for (; t0 < p.T; t0 += step) {
     const bool here = t0 + lane / kL < p.T;
-    const long long t = here ? t0 + lane / kL : p.T - 1;
-    Key own;
-    own.load(x + t * E, E, l, p.pieces);
+    const long long t = row_of(t0);
+    Key next;
+    if (kAhead)
+      next.load(x + row_of(t0 + step) * E, E, l, p.pieces);
+    else
+      own.load(x + t * E, E, l, p.pieces);
     K top[N];
     if constexpr (kLead) {
       K lead[V / 4];
@@ -607,6 +618,7 @@ route_group_kernel(const X* __restrict__ x, const RouteParams p) {
         if (here && !dead && l == 0) zacc += lse * lse;
       }
     }
+    if (kAhead) own = next;
   }
   if constexpr (kStats) {
     // the sums over the warp's tokens, then the block's warps
