@@ -18,12 +18,13 @@
 // the widened tokens to shared memory.
 //
 // Large products run at 0.9 of the rate the FP16 pipe reaches elsewhere: 65536
-// rows, 4096 x 4096, one expert 1290 us (1700 TFLOP/s); 131072 rows of 128
-// experts, 1536 x 2048 gated, 600 us (1370 TFLOP/s); 32768 rows of 32 experts,
-// 4096 x 4096 gated, 656 us (1676 TFLOP/s). With blocks of up to 192 tokens
-// these took 1397, 650 and 791: every block widens its weights anew. Below
-// about 128 rows per expert the weights bound it (4096 rows of those 128
-// experts: 91 us, 4.6 TB/s), and the way of a step through its two widened
+// rows, 4096 x 4096, one expert 1255 to 1300 us (1690 to 1750 TFLOP/s); 131072
+// rows of 128 experts, 1536 x 2048 gated, 541 us (1523 TFLOP/s); 32768 rows of
+// 32 experts, 4096 x 4096 gated, 615 us (1788 TFLOP/s). With blocks of up to
+// 192 tokens these took 1397, 650 and 791: every block widens its weights anew;
+// with the activation in the gate rows' warps alone the last two 592 and 660.
+// Below about 128 rows per expert the weights bound it (4096 rows of those 128
+// experts: 92 us, 4.5 TB/s), and the way of a step through its two widened
 // places: widening, arrival at the issuer, MMAs, release.
 //
 // One CTA per SM in clusters of two (one tcgen05 MMA pair, 768 threads per
@@ -39,8 +40,9 @@
 //   warps 12-19  widen the tokens into shared memory (K-major, 128-byte
 //                swizzle). Both in two groups, for the two halves of a step;
 //   warps 20-23  epilogue: one TMEM lane = one weight row, one column = one
-//                token. Gated: the up rows' warps hand their values to the
-//                gate rows' warps through shared memory.
+//                token. Gated: of every two chunks of 32 tokens the up rows'
+//                warps hand the first one's values to the gate rows' warps and
+//                get the gate values of the second, through shared memory.
 // TMEM: 384 columns of sums, given to the items in turn, and two steps of
 // weights (64 columns each). A step is 128 deep so that the issuer, whose loop
 // costs it about 300 cycles, keeps ahead of the MMAs (256 tokens: 512 cycles
@@ -114,8 +116,10 @@ struct SmemTail {
   uint64_t empty[WIDE];
   uint64_t tfull[UNITS];   // of the item that starts in this unit
   uint64_t tempty[UNITS];
-  uint64_t up_full[2];     // a chunk of up values, per pair of epilogue warps
-  uint64_t up_empty[2];
+  // a chunk of values handed on, per pair of epilogue warps: to the gate rows'
+  // warp, to the up rows' warp
+  uint64_t hand_full[2][2];
+  uint64_t hand_empty[2][2];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
@@ -128,9 +132,9 @@ struct SmemTail {
 constexpr uint32_t kWideAt = RAW * RAW_BYTES;
 constexpr uint32_t kStagingAt = kWideAt + WIDE * WIDE_BYTES;
 constexpr uint32_t kWarpStagingBytes = 32 * 64;
-constexpr uint32_t kUpAt = kStagingAt + kEpiWarps * kWarpStagingBytes;
-constexpr uint32_t kUpBytes = 32 * 32 * 4;           // a chunk of up values, one buffer per pair
-constexpr uint32_t kTailAt = kUpAt + 2 * kUpBytes;
+constexpr uint32_t kHandAt = kStagingAt + kEpiWarps * kWarpStagingBytes;
+constexpr uint32_t kHandBytes = 32 * 32 * 4;         // a chunk of values, two per pair of warps
+constexpr uint32_t kTailAt = kHandAt + 4 * kHandBytes;
 constexpr size_t kSmemBytes = 1024 + kTailAt + sizeof(SmemTail);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(offsetof(SmemTail, scale) % 16 == 0 && kTailAt % 16 == 0, "float4 reads");
@@ -313,8 +317,10 @@ q8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
         mbar_init(smem_u32(&st.tempty[a]), 2 * kEpiWarps);
       }
       for (int a = 0; a < 2; ++a) {
-        mbar_init(smem_u32(&st.up_full[a]), 1);
-        mbar_init(smem_u32(&st.up_empty[a]), 1);
+        for (int d = 0; d < 2; ++d) {
+          mbar_init(smem_u32(&st.hand_full[a][d]), 1);
+          mbar_init(smem_u32(&st.hand_empty[a][d]), 1);
+        }
       }
       for (int i = 0; i < kItems; ++i) {
         mbar_init(smem_u32(&st.item_full[i]), 1);
@@ -623,12 +629,16 @@ q8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
     const int q = warp & 3;
     const int w = warp - kFirstEpi;
     const bool up = kGated && q >= 2;
+    constexpr int kChunks = kGated ? 2 : 1;  // a turn's
     const int pair = q & 1;
     const int width = kGated ? p.F : p.N;
     uint4* stg = reinterpret_cast<uint4*>(smem + kStagingAt + w * kWarpStagingBytes);
-    float* ups = reinterpret_cast<float*>(smem + kUpAt + pair * kUpBytes);
+    // what this warp hands on, and what it is handed
+    float* given = reinterpret_cast<float*>(smem + kHandAt + (2 * pair + up) * kHandBytes);
+    const float* taken =
+        reinterpret_cast<const float*>(smem + kHandAt + (2 * pair + !up) * kHandBytes);
     uint32_t unit_phase = 0;  // one bit per unit
-    uint32_t up_phase = 0;
+    uint32_t give_phase = 0, take_phase = 0;
     bool ok = true;
     Item it;
     ItemReader items;
@@ -654,21 +664,16 @@ q8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
       unit_phase ^= 1u << start;
       tc_fence_after();
       const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll 1
-      for (int c = 0; c < it.rows; c += 32) {
-        const int have = min(32, it.rows - c);
-        const long long r0 = static_cast<long long>(it.row0) + c;
-        st.scale[w][lane] = sc[0];
-#pragma unroll
-        for (int i = 0; i + 1 < BN / 32; ++i) sc[i] = sc[i + 1];
-        float v[32];
-        const int col = c < it.first ? it.col + c : c - it.first;
-        tmem_ld32(lanes + col, v);
-        const bool unit_read = (c & 32) != 0 || c + 32 >= it.rows;
-        if (unit_read) tc_fence_before();
+      const auto column = [&](int c) { return c < it.first ? it.col + c : c - it.first; };
+      // a chunk's scaled sums; scale: of the lane's token; done: with it the
+      // unit's sums are in registers
+      const auto load = [&](int c, float scale, bool done, float(&v)[32]) {
+        st.scale[w][lane] = scale;
+        tmem_ld32(lanes + column(c), v);
+        if (done) tc_fence_before();
         __syncwarp();
-        if (unit_read && lane == 0)
-          mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&st.tempty[col / kUnit]), 0));
+        if (done && lane == 0)
+          mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&st.tempty[column(c) / kUnit]), 0));
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&st.scale[w][i]);
@@ -677,33 +682,12 @@ q8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
           v[i + 2] *= tn * f.z;
           v[i + 3] *= tn * f.w;
         }
-        if (up) {
-          if (!mbar_wait_bounded(smem_u32(&st.up_empty[pair]), up_phase ^ 1u, abort_flag,
-                                 p.status)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) ups[i * 32 + lane] = v[i];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&st.up_full[pair]));
-          up_phase ^= 1u;
-          continue;
-        }
-        if (kGated) {
-          if (!mbar_wait_bounded(smem_u32(&st.up_full[pair]), up_phase, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            v[i] = glu_mul(v[i], ups[i * 32 + lane], p.alpha, false, 1.0f);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&st.up_empty[pair]));
-          up_phase ^= 1u;
-        }
-        // [token][channel] through the staging buffer: four lanes then write each
-        // token's 64-byte segment
+      };
+      // [token][channel] through the staging buffer: four lanes then write each
+      // token's 64-byte segment
+      const auto store = [&](int c, const float(&v)[32]) {
+        const int have = min(32, it.rows - c);
+        const long long r0 = static_cast<long long>(it.row0) + c;
         uint16_t* cell = reinterpret_cast<uint16_t*>(stg);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -718,6 +702,50 @@ q8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
             reinterpret_cast<uint4*>(p.C + (r0 + i) * width + n0)[lane & 3] = x;
         }
         __syncwarp();
+      };
+#pragma unroll 1
+      for (int c = 0; c < it.rows; c += 32 * kChunks) {
+        const bool second = c + 32 < it.rows;
+        float v[32];
+        if constexpr (kGated) {
+          const bool keep = !up || second;
+          if (up || second) {
+            load(up ? c : c + 32, up ? sc[0] : sc[1], !keep, v);
+            if (!mbar_wait_bounded(smem_u32(&st.hand_empty[pair][up]), give_phase ^ 1u, abort_flag,
+                                   p.status)) {
+              ok = false;
+              break;
+            }
+            give_phase ^= 1u;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) given[i * 32 + lane] = v[i];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&st.hand_full[pair][up]));
+          }
+          if (keep) {
+            const int at = up ? c + 32 : c;
+            load(at, up ? sc[1] : sc[0], true, v);
+            if (!mbar_wait_bounded(smem_u32(&st.hand_full[pair][!up]), take_phase, abort_flag,
+                                   p.status)) {
+              ok = false;
+              break;
+            }
+            take_phase ^= 1u;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float other = taken[i * 32 + lane];
+              v[i] = glu_mul(up ? other : v[i], up ? v[i] : other, p.alpha, false, 1.0f);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&st.hand_empty[pair][!up]));
+            store(at, v);
+          }
+        } else {
+          load(c, sc[0], (c & 32) != 0 || !second, v);
+          store(c, v);
+        }
+#pragma unroll
+        for (int i = 0; i + kChunks < BN / 32; ++i) sc[i] = sc[i + kChunks];
       }
     }
   }
