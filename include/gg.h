@@ -798,8 +798,8 @@ gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
  *
  * gg_q8_grouped_gemm — for every expert e and row r in [offsets[e],
  * offsets[e+1]) of Aq[R_cap][K], As[R_cap]:
- *   v[r][n] = As[r] * Ws[e][n] * sum_c Aq[r][c] * Wq[e][n][c]
- * the sum exact below 2^24 and in fp32 above, v in fp32:
+ *   v[r][n] = (sum_c Aq[r][c] * Wq[e][n][c]) * Ws[e][n] * As[r]
+ * the sum exact below 2^24 and in fp32 above, v in fp32, from left to right:
  *   GG_EPI_NONE:   C[R_cap][N] = bf16(v)
  *   GG_EPI_SWIGLU, GG_EPI_QGEGLU: N = 2F, C[R_cap][F] = bf16(act(v[:, :F]) *
  *                  v[:, F:] [* prob_of_row[r]]): no rounding before the last.

@@ -649,6 +649,7 @@ q8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
       const float tn =
           exists ? __ldg(p.Bs + static_cast<long long>(it.e) * p.N + (up ? p.F : 0) + n0 + lane)
                  : 0.0f;
+      const float2 tn2 = make_float2(tn, tn);
       // the tokens' scales, lane by lane for every chunk, ahead of the sums
       float sc[BN / 32];
 #pragma unroll
@@ -677,10 +678,15 @@ q8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&st.scale[w][i]);
-          v[i] *= tn * f.x;
-          v[i + 1] *= tn * f.y;
-          v[i + 2] *= tn * f.z;
-          v[i + 3] *= tn * f.w;
+          // one scale after the other: their product alone may leave fp32's range
+          const float2 a = __fmul2_rn(__fmul2_rn(make_float2(v[i], v[i + 1]), tn2),
+                                      make_float2(f.x, f.y));
+          const float2 b = __fmul2_rn(__fmul2_rn(make_float2(v[i + 2], v[i + 3]), tn2),
+                                      make_float2(f.z, f.w));
+          v[i] = a.x;
+          v[i + 1] = a.y;
+          v[i + 2] = b.x;
+          v[i + 3] = b.y;
         }
       };
       // [token][channel] through the staging buffer: four lanes then write each

@@ -304,9 +304,10 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
             const int r = at.row0 + first + tok;
             const float sr = p.As[r];
             gg_bf16* out = p.C + r * width + at.n0 + c;
-            const float lo = (acc[0][i][v] + sums[4 * i + v][lane]) * (sr * __ldg(bs + c));
+            // one scale after the other: their product alone may leave fp32's range
+            const float lo = (acc[0][i][v] + sums[4 * i + v][lane]) * __ldg(bs + c) * sr;
             const float hi = (acc[1][i][v] + sums[4 * (kTiles + i) + v][lane]) *
-                             (sr * __ldg(bs + (kGated ? p.F : 16) + c));
+                             __ldg(bs + (kGated ? p.F : 16) + c) * sr;
             if (kGated) {
               const float pr = p.row_scale != nullptr ? p.row_scale[r] : 1.0f;
               *out = __bfloat16_as_ushort(

@@ -314,3 +314,23 @@ def test_empty_batch(gg):
     Wq = torch.zeros(2, 128, 64, dtype=torch.int8, device="cuda")
     off = torch.zeros(3, dtype=torch.int32, device="cuda")
     assert gg.q8_grouped_fwd(x, Wq, torch.zeros(2, 128, device="cuda"), off).shape == (0, 128)
+
+
+@pytest.mark.parametrize("counts", [[5, 0, 3], [300, 0, 70]])
+def test_scales_whose_product_leaves_the_fp32_range(gg, counts):
+    # Scales of 1e-24 and 1e-19: their product, 1e-43, has six bits left in fp32, yet the results
+    # (sums near 8e6, exact) are normal numbers. Scales of 1e25 and 1e20: their product is
+    # infinite, the result of a row of zero codes is zero.
+    K, N = 1024, 128
+    Aq, As, Wq, Ws, off = _random(counts, N, K, 0, 300)
+    Aq, Wq = np.abs(Aq) | 64, np.abs(Wq) | 64
+    As, Ws = (As * 1e-22).astype(np.float32) + np.float32(1e-24), (Ws * 1e-16).astype(np.float32)
+    assert (As.astype(np.float64).min() * Ws.min() < 2.0 ** -143)
+    dA, dS, dW, dT, dO = _dev(Aq, As, Wq, Ws, off)
+    _check(gg.q8_grouped_gemm(dA, dS, dW, dT, dO), Aq, As, Wq, Ws, off)
+    Aq[1::2] = 0
+    As[1::2], Ws[:] = 1e25, 1e20
+    dA, dS, dT = _dev(Aq, As, Ws)
+    C = gg.q8_grouped_gemm(dA, dS, dW, dT, dO)
+    assert (C[1::2] == 0).all()
+    _check(C, Aq, As, Wq, Ws, off)
