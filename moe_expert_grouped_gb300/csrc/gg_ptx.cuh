@@ -148,6 +148,15 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 }
 
 // All threads of every CTA of the cluster (release / acquire).
+// cluster_sync in two halves, with work between them; every thread of the
+// cluster runs both.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");

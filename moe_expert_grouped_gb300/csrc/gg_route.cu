@@ -219,6 +219,7 @@ route_finalise_kernel(const float* part_p, const int32_t* part_n, const float* p
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
+  cluster_arrive();
   grid_dependency_wait();
   float term = 0.0f;  // warp 0, by lane
   for (int e0 = rank * 32; e0 < E; e0 += 32 * kFinBlocks) {
@@ -249,6 +250,7 @@ route_finalise_kernel(const float* part_p, const int32_t* part_n, const float* p
     }
     __syncthreads();
   }
+  cluster_wait();  // block 0 has started: its shared memory may be written
   if (warp == 0) {
     term = warp_sum(term);
     if (lane == 0)
