@@ -696,8 +696,8 @@ gg_status gg_moe_mlp_fwd_q8(const gg_bf16* x, const int32_t* idx, const float* p
  *               of the k picked scores.
  * An expert is switched off for a row by the logit -inf: its score is 0. A
  * row of nothing but -inf gets idx 0..k-1 and prob 0. A NaN or +inf makes
- * the row's probabilities NaN where the formula does; its idx stay k
- * different experts.
+ * the row's probabilities and the losses NaN where the formula does; its idx
+ * stay k different experts.
  * Statistics of the batch, either pointer may be NULL:
  *   counts[E]   int32, how often each expert was picked;
  *   losses[2]   fp32: losses[0] = E * sum_e f_e * P_e, the balance loss, with

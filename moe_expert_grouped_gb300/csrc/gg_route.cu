@@ -184,7 +184,8 @@ route_kernel(const X* __restrict__ x, const RouteParams p) {
           for (int i = 0; i < V; ++i) tot += ss[i] = sigmoid_of(v[i]);
           tot = warp_sum(tot);
 #pragma unroll
-          for (int i = 0; i < V; ++i) pacc[i] += tot > 0.0f ? ss[i] / tot : 0.0f;
+          for (int i = 0; i < V; ++i)
+            pacc[i] += tot > 0.0f || tot != tot ? ss[i] / tot : 0.0f;
         } else {
 #pragma unroll
           for (int i = 0; i < V; ++i) pacc[i] += expf(v[i] - m) / row_sum;

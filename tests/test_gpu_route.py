@@ -265,3 +265,14 @@ def test_losses_repeat_over_many_calls(gg, E):
     for r in got:
         assert torch.equal(r["losses"], first["losses"]) and torch.equal(r["counts"],
                                                                          first["counts"])
+
+
+@pytest.mark.parametrize("sig", [0, 1])
+@pytest.mark.parametrize("E,k", [(6, 2), (60, 4), (200, 8), (400, 8), (600, 8), (70, 20)])
+def test_a_nan_logit_makes_both_losses_nan(gg, E, k, sig):
+    # whatever kernel the sizes choose
+    for dtype in (torch.float32, torch.bfloat16):
+        t, _ = _logits(51, 40, E, dtype)
+        assert torch.isfinite(gg.route(t, k, sig, losses=True)["losses"]).all()
+        t[17, E // 2] = float("nan")
+        assert torch.isnan(gg.route(t, k, sig, losses=True)["losses"]).all()
