@@ -714,7 +714,8 @@ gg_status gg_moe_mlp_fwd_q8(const gg_bf16* x, const int32_t* idx, const float* p
  * dprob = dL/dprob[T][k] of the probabilities gg_route wrote, for
  *   L + aux_coef * losses[0] + z_coef * losses[1]:
  * dlogits[T][E] in the logits' type, accumulated in fp32 and rounded once.
- * The picks and the counts are constants of the differentiation. score,
+ * The picks and the counts are constants of the differentiation. A row of
+ * nothing but -inf gets 0, one with a NaN gets NaN where the formula does. score,
  * renormalize and scale as in the forward; counts is read when aux_coef is
  * not 0. dlogits may be the logits' own buffer. An idx outside [0, E) adds
  * nothing and sets GG_ERR_DEVICE_BAD_EXPERT_ID in the status word of ws

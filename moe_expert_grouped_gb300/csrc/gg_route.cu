@@ -56,6 +56,12 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key ^ 0x80000000u) : ~key);
 }
 
+__device__ __forceinline__ float larger(float a, float b) {  // NaN above all
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
@@ -329,11 +335,6 @@ struct Share<float, V, kL> : ShareColumns<V, kL> {
   __device__ __forceinline__ K key(int i, int l) const { return make(v[i], column(l, i)); }
   // Of four columns from i on: the largest logit's, as column i's.
   __device__ __forceinline__ K lead(int i, int l) const {
-    const auto larger = [](float a, float b) {  // NaN above all
-      float r;
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-      return r;
-    };
     return make(larger(larger(v[i], v[i + 1]), larger(v[i + 2], v[i + 3])), column(l, i));
   }
   static __device__ __forceinline__ int column_of(K k) {
@@ -732,12 +733,12 @@ route_bwd_kernel(const X* x, const RouteBwdParams p, X* dx) {
 
     float m = own.value(0);
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = fmaxf(m, own.value(i));
+    for (int i = 1; i < V; ++i) m = larger(m, own.value(i));
     if constexpr (kL == 32) {
       m = value_of(__reduce_max_sync(kFull, key_of(m)));
     } else {
 #pragma unroll
-      for (int d = kL / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+      for (int d = kL / 2; d > 0; d >>= 1) m = larger(m, __shfl_xor_sync(kFull, m, d));
     }
     const bool dead = m == -INFINITY;
     // e: exp(v - m); sums of e, of the scores, of load * score, of the picks'

@@ -276,3 +276,32 @@ def test_a_nan_logit_makes_both_losses_nan(gg, E, k, sig):
         assert torch.isfinite(gg.route(t, k, sig, losses=True)["losses"]).all()
         t[17, E // 2] = float("nan")
         assert torch.isnan(gg.route(t, k, sig, losses=True)["losses"]).all()
+
+
+@pytest.mark.parametrize("ren", [False, True])
+@pytest.mark.parametrize("E,k", [(6, 2), (60, 4), (128, 8), (200, 8), (400, 8), (600, 8), (70, 20)])
+def test_a_nan_logit_makes_the_rows_gradient_nan(gg, E, k, ren):
+    # softmax: every share of the row depends on the NaN, also where the other experts are
+    # switched off; the other rows' gradients, and a row with none left, stay as they are
+    for dtype in (torch.float32, torch.bfloat16):
+        t, _ = _logits(52, 40, E, dtype, dead=0.1)
+        t[9] = float("-inf")
+        t[9, E // 3] = float("nan")
+        t[17, E - 1] = float("nan")
+        t[23] = float("nan")
+        t[31] = float("-inf")
+        bad = torch.zeros(40, dtype=torch.bool, device="cuda")
+        bad[[9, 17, 23]] = True
+        r = gg.route(t, k, 0, ren)
+        dprob = torch.randn(40, k, generator=torch.Generator().manual_seed(3)).cuda()
+        assert torch.isnan(r["prob"][bad]).all()
+        d = gg.route_bwd(t, r["idx"], dprob, 0, ren, z_coef=0.1)
+        assert torch.isnan(d[bad]).all() and torch.isfinite(d[~bad]).all()
+        assert (d[31] == 0).all()
+        assert torch.isnan(gg.route_bwd(t, r["idx"], dprob, 0, ren)[bad]).all()
+        # sigmoid scores of other columns do not depend on it: those of the losses do
+        r = gg.route(t, k, 1, False)
+        d = gg.route_bwd(t, r["idx"], dprob, 1, False)
+        assert torch.equal(torch.isnan(d), torch.isnan(t))
+        d = gg.route_bwd(t, r["idx"], dprob, 1, False, z_coef=0.1)
+        assert torch.isnan(d[bad]).all() and torch.isfinite(d[~bad]).all()
