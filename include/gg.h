@@ -803,11 +803,13 @@ gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
  * the sum exact below 2^24 and in fp32 above, v in fp32, from left to right:
  *   GG_EPI_NONE:   C[R_cap][N] = bf16(v)
  *   GG_EPI_SWIGLU, GG_EPI_QGEGLU: N = 2F, C[R_cap][F] = bf16(act(v[:, :F]) *
- *                  v[:, F:] [* prob_of_row[r]]): no rounding before the last.
+ *                  v[:, F:] [* prob_of_row[r]]): no rounding to fewer bits before
+ *                  the last (the probability multiplies As[r] of the second half).
  * Other arguments, refusals and device errors as gg_grouped_fwd; rows outside
  * [0, offsets[E]) are never written. Results of a row do not depend on the
- * other rows of the batch beyond the choice of kernel, which goes by R_cap and
- * E (both kernels' sums are exact below 2^24).
+ * other rows of the batch. Two kernels share the sizes by R_cap and E; up to
+ * K = 1024 a row's bits are the same in both, above as long as its sums stay
+ * below 2^24, where both are exact and what follows is the same arithmetic.
  *
  * gg_q8_grouped_fwd — quantise the rows of A[R_cap][K] (BF16, permuted order)
  * and multiply, in one call; the codes stay in ws, gg_q8_workspace_size(R_cap,

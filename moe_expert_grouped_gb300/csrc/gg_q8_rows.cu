@@ -304,14 +304,16 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
             const int r = at.row0 + first + tok;
             const float sr = p.As[r];
             gg_bf16* out = p.C + r * width + at.n0 + c;
-            // one scale after the other: their product alone may leave fp32's range
+            // one scale after the other: their product alone may leave fp32's range.
+            // The probability goes with the token's scale of the up half, as
+            // gg_gemm_q8.cu has it: a row's bits are the same there.
+            const float up = kGated && p.row_scale != nullptr ? sr * p.row_scale[r] : sr;
             const float lo = (acc[0][i][v] + sums[4 * i + v][lane]) * __ldg(bs + c) * sr;
             const float hi = (acc[1][i][v] + sums[4 * (kTiles + i) + v][lane]) *
-                             __ldg(bs + (kGated ? p.F : 16) + c) * sr;
+                             __ldg(bs + (kGated ? p.F : 16) + c) * up;
             if (kGated) {
-              const float pr = p.row_scale != nullptr ? p.row_scale[r] : 1.0f;
               *out = __bfloat16_as_ushort(
-                  __float2bfloat16_rn(glu_mul(lo, hi, p.alpha, true, pr)));
+                  __float2bfloat16_rn(glu_mul(lo, hi, p.alpha, false, 1.0f)));
             } else {
               out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
               out[16] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));

@@ -334,3 +334,27 @@ def test_scales_whose_product_leaves_the_fp32_range(gg, counts):
     C = gg.q8_grouped_gemm(dA, dS, dW, dT, dO)
     assert (C[1::2] == 0).all()
     _check(C, Aq, As, Wq, Ws, off)
+
+
+@pytest.mark.parametrize("K", [64, 320, 1024])
+@pytest.mark.parametrize("N", [128, 4096])
+@pytest.mark.parametrize("epi", [0, 1, 3])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_a_rows_bits_do_not_depend_on_the_kernel(gg, K, N, epi, weighted):
+    # the sizes choose the kernel by the rows there is room for: the same rows, with room for few
+    # and for many, where every sum is exact (K * 127 * 127 < 2^24)
+    if weighted and epi == 0:
+        pytest.skip("no probability without an activation")
+    counts = [9, 0, 40, 1, 33, 2, 0, 8, 64, 70]
+    Aq, As, Wq, Ws, off = _random(counts, N, K, 4000, 500 + K)
+    prob = np.random.default_rng(2).random(Aq.shape[0]).astype(np.float32)
+    n = int(off[-1])
+    assert n > 16 * len(counts)
+    got = []
+    for room, E in ((n + 4000, 10), (n, 30)):
+        pad = np.zeros((E - 10, N, K), np.int8)
+        offs = np.concatenate([off, np.full(E - 10, n, np.int32)])
+        dev = _dev(Aq[:room], As[:room], np.concatenate([Wq, pad]),
+                   np.concatenate([Ws, np.ones((E - 10, N), np.float32)]), offs, prob[:room])
+        got.append(gg.q8_grouped_gemm(*dev[:5], epi, prob_of_row=dev[5] if weighted else None)[:n])
+    assert torch.equal(got[0], got[1])
