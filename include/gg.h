@@ -746,9 +746,10 @@ gg_status gg_route_bwd(const void* logits, int dtype, int T, int E, int k, int s
  *                                       dC[r][n] * A[r][c]
  * with fp32 sums. dC[R_cap][N], A[R_cap][K] BF16 in the permuted row order;
  * dB[E][N][K] and base (nullable: zero) in out_dtype, a gg_dtype: BF16 is
- * rounded once, after the base is added; fp32 is not rounded further, and its
- * sums are carried outside the tensor cores, whose additions truncate, every
- * 256 rows. base may be dB itself (accumulating in place).
+ * rounded once, after the base is added; fp32 is not rounded further. The sums
+ * are carried outside the tensor cores, whose additions truncate by up to 2^-23
+ * every 16 rows: every 256 rows for fp32 results (2^-19 in all), every 8192 for
+ * BF16 ones (2^-14). base may be dB itself (accumulating in place).
  * An expert without rows gets its base, or zeros. Rows outside
  * [0, offsets[E]) are never read into a result, whatever they hold; padding
  * rows below offsets[E] are read and must hold zeros in dC or A and finite

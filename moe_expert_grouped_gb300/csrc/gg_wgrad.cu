@@ -32,12 +32,13 @@
 // the offsets and sizes alone). 60000 rows, 768 x 320 fp32: one expert 46 us,
 // whole blocks 229; 4 experts 46 and 70; 8 experts, whole blocks, 46, slices 51.
 //
-// fp32 results: the tensor core truncates each of its additions, by up to
-// 2^-23 of the running sum and always towards zero, so a sum over 7500 rows
-// (469 additions) is 8e-6 off. The sums are therefore carried in fp32
-// registers every kChunk steps (256 rows, 16 additions: 3e-7 off), which the
-// epilogue warps do while the next chunk runs. A BF16 result is rounded to
-// 4e-3 and takes the whole slice in TMEM.
+// The tensor core truncates each of its additions, by up to 2^-23 of the
+// running sum and always towards zero, so a sum over 7500 rows (469 additions)
+// is 8e-6 off. fp32 results are therefore carried in fp32 registers every
+// kChunk steps (256 rows, 16 additions: 3e-7 off), which the epilogue warps do
+// while the next chunk runs. BF16 results, rounded by up to 2^-9 in the end,
+// are carried every kChunkBf16 steps (8192 rows, 512 additions: at most 2^-14;
+// 131072 rows of one sign left in TMEM were 3e-4 low on average).
 //
 // An fp32 base is loaded by TMA into shared memory, piece by piece ahead of
 // the sums: held in registers it spilled, and the loads then waited for each
@@ -68,6 +69,7 @@ constexpr int BM = 128;            // rows of dB per CTA (columns of dC)
 constexpr int BN = 256;            // most columns of dB per work item (columns of A)
 constexpr int BK = 64;             // rows of dC and A per step
 constexpr int kChunk = 4;          // fp32 results: steps summed inside TMEM
+constexpr int kChunkBf16 = 128;    // and BF16 results
 constexpr int kMaxStages = 6;
 constexpr uint16_t kPairMask = 0x3;
 constexpr int kItems = 4;          // work items found ahead
@@ -533,7 +535,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap mapD, const __grid_constant__ C
         const int rows = __shfl_sync(0xFFFFFFFFu, it.rows, 0);
         const uint32_t idesc = make_idesc_bf16(
             2 * BM, __shfl_sync(0xFFFFFFFFu, min(p.width, p.K - it.nt * p.width), 0), true, true);
-        const int chunk = kF32 ? kChunk * BK : rows;
+        const int chunk = (kF32 ? kChunk : kChunkBf16) * BK;
         for (int c0 = 0; c0 < rows && ok; c0 += chunk) {
           if (!mbar_wait_bounded(smem_u32(&st.tempty[acc]), acc_phase ^ 1u, abort_flag,
                                  p.status)) {
@@ -705,6 +707,85 @@ wgrad_kernel(const __grid_constant__ CUtensorMap mapD, const __grid_constant__ C
           }
         }
       } else {
+        // 32 columns of dB; raw: the base's
+        const auto put = [&](int c, float(&v)[32], const uint4(&raw)[4]) {
+          uint4 w[4];
+          if (add) {
+            transpose_chunk(stg, raw, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                v[8 * i + 2 * j] += bf16_lo(u[j]);
+                v[8 * i + 2 * j + 1] += bf16_hi(u[j]);
+              }
+            }
+          }
+          pack_bf16x32(v, 1.0f, w);
+          store_chunk(stg, w, static_cast<gg_bf16*>(p.dB) + at + c, p.K, nvalid);
+        };
+        if (it.rows > kChunkBf16 * BK) {
+          // several chunks, carried in registers; with a base in local memory, that
+          // is in L2 (registers spilled what shorter items load ahead: 128 experts,
+          // 1536 x 2048 onto a BF16 base 568 -> 703 us; in local memory one expert of
+          // 131072 rows, 4096 x 4096, takes 2770 us, left in TMEM 2600)
+          float4 sum[kCols / 4];
+          constexpr int kUnroll = kBase ? 1 : kCols / 32;
+#pragma unroll
+          for (int i = 0; i < kCols / 4; ++i) sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int r = 0; r < it.rows; r += kChunkBf16 * BK) {
+            if (!mbar_wait_bounded(smem_u32(&st.tfull[acc]), acc_phase, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll kUnroll * 2
+            for (int c = 0; c < kCols; c += 16) {
+              if (c >= cols) continue;
+              float v[16];
+              tmem_ld16(lanes + acc * BN + c, v);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float4& f = sum[c / 4 + i];
+                f.x += v[4 * i];
+                f.y += v[4 * i + 1];
+                f.z += v[4 * i + 2];
+                f.w += v[4 * i + 3];
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&st.tempty[acc]), 0));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+          }
+          if (!ok) break;
+#pragma unroll kUnroll
+          for (int c = 0; c < kCols; c += 32) {
+            if (c >= cols) continue;
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 f = sum[c / 4 + i];
+              v[4 * i] = f.x;
+              v[4 * i + 1] = f.y;
+              v[4 * i + 2] = f.z;
+              v[4 * i + 3] = f.w;
+            }
+            if (part != nullptr) {
+              store_f32x16(stg, v, part + c, BN, nvalid);
+              store_f32x16(stg, v + 16, part + c + 16, BN, nvalid);
+            } else {
+              uint4 raw[4];
+              if (add)
+                load_chunk_raw(raw, static_cast<const gg_bf16*>(p.base) + at + c, p.K, nvalid);
+              put(c, v, raw);
+            }
+          }
+          continue;
+        }
+        // one chunk: straight from TMEM
         uint4 raw[BN / 64][4];  // the base's 32-column chunks, loaded ahead of the sums
         if (add) {
 #pragma unroll
@@ -732,21 +813,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap mapD, const __grid_constant__ C
               store_f32x16(stg, v, part + c, BN, nvalid);
               store_f32x16(stg, v + 16, part + c + 16, BN, nvalid);
             } else {
-              uint4 w[4];
-              if (add) {
-                transpose_chunk(stg, raw[b], w);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    v[8 * i + 2 * j] += bf16_lo(u[j]);
-                    v[8 * i + 2 * j + 1] += bf16_hi(u[j]);
-                  }
-                }
-              }
-              pack_bf16x32(v, 1.0f, w);
-              store_chunk(stg, w, static_cast<gg_bf16*>(p.dB) + at + c, p.K, nvalid);
+              put(c, v, raw[b]);
             }
           }
         }

@@ -199,3 +199,31 @@ def test_host_refusals(gg):
                          dB=torch.zeros(1, 64, 64, device="cuda", dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         gg.grouped_wgrad(x.t().contiguous().t(), x, off)
+
+
+@pytest.mark.parametrize("with_base", [False, True])
+@pytest.mark.parametrize("counts,N,K", [([65536], 4096, 4352), ([20000, 0, 8192, 8193, 30001], 2048, 2112),
+                                        ([1048576], 256, 256)])
+def test_long_bf16_sums_of_one_sign(gg, counts, N, K, with_base):
+    # Sums of one sign over many rows, where truncations add up. A BF16 result's sums leave the
+    # tensor core every 8192 rows, 512 additions that each lose up to 2^-23 of the running sum:
+    # 2^-14 in all, next to which fp32 additions do not count; then half a BF16 step, 2^-9 to
+    # 2^-8 of the value by its mantissa. The first case has too many blocks for slices, the last
+    # cuts one block's rows into slices of more than 8192.
+    g = torch.Generator(device="cuda").manual_seed(31)
+    R = sum(counts)
+    dC, A = ((torch.rand(R, n, generator=g, device="cuda") + 0.5).bfloat16() for n in (N, K))
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    base = None
+    if with_base:
+        base = (torch.rand(len(counts), N, K, generator=g, device="cuda") * 1e4).bfloat16()
+    got = gg.grouped_wgrad(dC, A, torch.from_numpy(off).cuda(), base=base, out_dtype=torch.bfloat16)
+    some = torch.randperm(N, generator=g, device="cuda")[:48]  # rows of dB
+    a, d = A.double(), dC[:, some].double()
+    for e, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        want = d[lo:hi].t() @ a[lo:hi]
+        if with_base:
+            want = want + base[e, some].double()
+        half = torch.exp2(torch.floor(torch.log2(want.clamp_min(1e-30))) - 8)
+        err = (got[e, some].double() - want).abs()
+        assert (err <= 2.0 ** -14 * want + half * (1 + 2.0 ** -14)).all(), float((err / half).max())
