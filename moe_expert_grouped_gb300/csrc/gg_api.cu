@@ -1008,9 +1008,9 @@ size_t gg_wgrad_workspace_size(int E, int R_cap, int N, int K) {
   return kWsHeader + (slots > 0 ? align256(sizeof(int)) + slots * wgrad_slot_bytes() : 0);
 }
 
-gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* offsets, int E,
-                           int R_cap, int N, int K, int out_dtype, const void* base, void* dB,
-                           void* ws, size_t ws_bytes, gg_stream_t stream) {
+static gg_status wgrad_checks(const gg_bf16* dC, const gg_bf16* A, const int32_t* offsets, int E,
+                              int R_cap, int N, int K, int out_dtype, const void* base,
+                              const void* dB, const void* ws, size_t ws_bytes) {
   if (E <= 0 || R_cap < 0 || N <= 0 || K <= 0) return GG_ERR_INVALID_ARG;
   if (out_dtype != GG_DTYPE_F32 && out_dtype != GG_DTYPE_BF16) return GG_ERR_INVALID_ARG;
   if (offsets == nullptr || dB == nullptr) return GG_ERR_INVALID_ARG;
@@ -1021,7 +1021,13 @@ gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* o
     return GG_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(dC) || !aligned16(A) || !aligned16(base) || !aligned16(dB))
     return GG_ERR_MISALIGNED;
-  gg_status s = check_ws(ws, ws_bytes, gg_wgrad_workspace_size(E, R_cap, N, K));
+  return check_ws(ws, ws_bytes, gg_wgrad_workspace_size(E, R_cap, N, K));
+}
+
+gg_status gg_grouped_wgrad(const gg_bf16* dC, const gg_bf16* A, const int32_t* offsets, int E,
+                           int R_cap, int N, int K, int out_dtype, const void* base, void* dB,
+                           void* ws, size_t ws_bytes, gg_stream_t stream) {
+  gg_status s = wgrad_checks(dC, A, offsets, E, R_cap, N, K, out_dtype, base, dB, ws, ws_bytes);
   if (s != GG_OK) return s;
   DeviceInfo dev;
   if ((s = device_ok(&dev)) != GG_OK) return s;
@@ -1060,13 +1066,18 @@ gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
   if (s != GG_OK) return s;
   if ((s = check_buffers(buf, T, k, E)) != GG_OK) return s;
   if (dW1 == nullptr || dW2 == nullptr) return GG_ERR_INVALID_ARG;
-  if (H % 64 != 0 || F % 64 != 0 || E > kMaxExperts) return GG_ERR_UNSUPPORTED_SHAPE;
+  if (H % 64 != 0 || F % 64 != 0 || F > 0x3FFFFFFF || E > kMaxExperts)
+    return GG_ERR_UNSUPPORTED_SHAPE;
   const long long rc = r_cap_of(T, k, E, pad_multiple);
   if (rc > 0x7FFFFFFFLL) return GG_ERR_UNSUPPORTED_SHAPE;
   const int R_cap = static_cast<int>(rc);
-  const size_t need1 = gg_wgrad_workspace_size(E, R_cap, 2 * F, H);
-  const size_t need2 = gg_wgrad_workspace_size(E, R_cap, H, F);
-  if ((s = check_ws(ws, ws_bytes, need1 > need2 ? need1 : need2)) != GG_OK) return s;
+  // both products' arguments before the first is enqueued
+  if ((s = wgrad_checks(buf->dH, buf->Xp, buf->offsets, E, R_cap, 2 * F, H, out_dtype, base1, dW1,
+                        ws, ws_bytes)) != GG_OK ||
+      (s = wgrad_checks(buf->dYp, buf->A, buf->offsets, E, R_cap, H, F, out_dtype, base2, dW2, ws,
+                        ws_bytes)) != GG_OK)
+    return s;
+  if (!aligned16(buf->H1)) return GG_ERR_MISALIGNED;
   s = gg_grouped_wgrad(buf->dH, buf->Xp, buf->offsets, E, R_cap, 2 * F, H, out_dtype, base1, dW1,
                        ws, ws_bytes, stream);
   if (s != GG_OK) return s;
@@ -1198,7 +1209,8 @@ gg_status gg_q8_grouped_fwd(const gg_bf16* A, const int8_t* Wq, const float* Ws,
 }
 
 static bool q8_shape_ok(int E, int H, int F) {
-  return E > 0 && E <= kMaxExperts && H > 0 && F > 0 && H % 64 == 0 && F % 64 == 0;
+  return E > 0 && E <= kMaxExperts && H > 0 && F > 0 && H % 64 == 0 && F % 64 == 0 &&
+         F <= 0x3FFFFFFF;
 }
 
 size_t gg_q8_buffers_size(int T, int H, int F, int k, int E) {
@@ -1266,6 +1278,16 @@ gg_status gg_moe_mlp_fwd_q8(const gg_bf16* x, const int32_t* idx, const float* p
   if (!q8_shape_ok(E, H, F) || r_cap_of(T, k, E, 1) > 0x7FFFFFFFLL)
     return GG_ERR_UNSUPPORTED_SHAPE;
   const int R = static_cast<int>(r_cap_of(T, k, E, 1));
+  // what the calls below check of their arguments, before the first is enqueued
+  const float* weight = mode == GG_PROB_ACTIVATION ? b->prob_of_row : nullptr;
+  if ((s = q8_gemm_checks(b->Xq, W1q, W1s, b->offsets, E, R, H, 2 * F, fepi, weight, b->A)) !=
+          GG_OK ||
+      (s = q8_gemm_checks(b->Aq, W2q, W2s, b->offsets, E, R, F, H, GG_EPI_NONE, nullptr,
+                          b->Yp)) != GG_OK)
+    return s;
+  if (!aligned16(out) || !aligned_to(b->Xs, 4) || !aligned_to(b->As, 4) ||
+      !aligned_to(b->row_of_slot, 4))
+    return GG_ERR_MISALIGNED;
   // row maps only: the permuted copy is the quantised one below
   s = gg_permute(x, idx, prob, T, H, k, E, 1, nullptr, b->offsets, b->row_of_slot, b->slot_of_row,
                  b->prob_of_row, b->ws, b->ws_bytes, stream);
@@ -1273,8 +1295,7 @@ gg_status gg_moe_mlp_fwd_q8(const gg_bf16* x, const int32_t* idx, const float* p
   s = gg_q8_quantize_rows(x, T, H, b->row_of_slot, k, R, b->Xq, b->Xs, b->ws, b->ws_bytes, stream);
   if (s != GG_OK) return s;
   s = gg_q8_grouped_gemm(b->Xq, b->Xs, W1q, W1s, b->offsets, E, R, H, 2 * F, fepi,
-                         mode == GG_PROB_ACTIVATION ? b->prob_of_row : nullptr, b->A, b->ws,
-                         b->ws_bytes, stream);
+                         weight, b->A, b->ws, b->ws_bytes, stream);
   if (s != GG_OK) return s;
   s = gg_q8_quantize_rows(b->A, R, F, nullptr, 1, R, b->Aq, b->As, b->ws, b->ws_bytes, stream);
   if (s != GG_OK) return s;

@@ -328,3 +328,43 @@ def test_mx_layout_and_validation(gg):
                                None) == 2
     assert L.gg_moe_mlp_fwd_mx(p, p, p, None, T, H, F, k, E, P, None, p, ctypes.byref(buf),
                                None) == 1
+
+
+def test_whole_layer_calls_check_everything_before_they_enqueue(gg):
+    # an argument that only the last product reads is refused like one of the first (without a
+    # device, a call that got past its checks returns GG_ERR_CUDA or GG_ERR_UNSUPPORTED_DEVICE)
+    L = gg.LIB
+    p = ctypes.c_void_p(1 << 40)
+    mis = ctypes.c_void_p((1 << 40) + 8)
+    T, H, F, k, E = 8, 64, 128, 2, 4
+    n0 = gg.launch_count()
+    b = gg.GGBuffers()
+    n = L.gg_moe_buffers_size(T, H, F, k, E, 1)
+    assert L.gg_moe_buffers_bind(p, n, T, H, F, k, E, 1, ctypes.byref(b)) == 0
+
+    def wgrad(dt=0, b1=None, d1=p, b2=None, d2=p, buf=b, f=F, wb=1 << 40):
+        return L.gg_moe_mlp_wgrad(T, H, f, k, E, 1, None, dt, b1, d1, b2, d2, ctypes.byref(buf), p,
+                                  wb, None)
+
+    assert wgrad(d1=mis) == 3 and wgrad(b1=mis) == 3 and wgrad(d2=mis) == 3 and wgrad(b2=mis) == 3
+    assert wgrad(dt=2) == 1 and wgrad(wb=16) == 4 and wgrad(f=1 << 30) == 2
+    for name in ("dH", "Xp", "dYp", "A", "H1"):
+        off = gg.GGBuffers.from_buffer_copy(b)
+        setattr(off, name, getattr(b, name) + 8)
+        assert wgrad(buf=off) == 3, name
+
+    q = gg.GGQ8Buffers()
+    n = L.gg_q8_buffers_size(T, H, F, k, E)
+    assert L.gg_q8_buffers_bind(p, n, T, H, F, k, E, ctypes.byref(q)) == 0
+
+    def fwd(x=p, w1=p, s1=p, w2=p, s2=p, out=p, buf=q, kk=k, f=F):
+        return L.gg_moe_mlp_fwd_q8(x, p, p, w1, s1, w2, s2, T, H, f, kk, E, None, out,
+                                   ctypes.byref(buf), None)
+
+    assert fwd(x=mis) == 3 and fwd(w1=mis) == 3 and fwd(s1=mis) == 3 and fwd(w2=mis) == 3
+    assert fwd(s2=mis) == 3 and fwd(out=mis) == 3 and fwd(kk=33) == 1 and fwd(f=1 << 30) == 2
+    for name in ("Xq", "A", "Aq", "Yp"):
+        off = gg.GGQ8Buffers.from_buffer_copy(q)
+        setattr(off, name, getattr(q, name) + 8)
+        assert fwd(buf=off) == 3, name
+    assert gg.launch_count() == n0
