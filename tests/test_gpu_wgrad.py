@@ -227,3 +227,48 @@ def test_long_bf16_sums_of_one_sign(gg, counts, N, K, with_base):
         half = torch.exp2(torch.floor(torch.log2(want.clamp_min(1e-30))) - 8)
         err = (got[e, some].double() - want).abs()
         assert (err <= 2.0 ** -14 * want + half * (1 + 2.0 ** -14)).all(), float((err / half).max())
+
+
+MIXED = [0, 1, 63, 64, 65, 100, 128, 256, 257, 300, 512, 600]
+
+
+@pytest.mark.parametrize("N,K", [(576, 320), (320, 576), (64, 1088)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_work_items_of_mixed_sizes(gg, N, K, dtype):
+    # several items per pair of SMs, in every order of lengths, experts without rows among them,
+    # blocks that are cut off on both sides; with and without a base, and in place
+    counts = np.random.default_rng(N + K).choice(MIXED, 90).tolist()
+    dC, A, offsets, off = _inputs(counts, N, K, 5, 200 + N)
+    want, mag = _want(dC, A, off)
+    ws = gg.wgrad_workspace(len(counts), dC.shape[0], N, K, "cuda")
+    _check(gg.grouped_wgrad(dC, A, offsets, out_dtype=dtype, ws=ws), want, mag, off)
+    base = torch.randn(len(counts), N, K, generator=torch.Generator().manual_seed(1)).to(dtype)
+    base = base.cuda()
+    got = gg.grouped_wgrad(dC, A, offsets, base=base, ws=ws)
+    _check(got, want, mag, off, base)
+    gg.grouped_wgrad(dC, A, offsets, base=base, dB=base, ws=ws)
+    assert torch.equal(base, got) and gg.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("counts,N,K", [([3000, 0, 2500, 7, 4000], 320, 320),
+                                        ([64, 5000, 1, 5001, 0, 4999, 5063], 64, 448),
+                                        ([1] * 30 + [3000, 2999, 0, 2000] + [2] * 9, 64, 64),
+                                        ([9000, 8000, 100, 7000], 256, 320)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_several_experts_cut_into_slices(gg, counts, N, K, dtype):
+    # experts that are cut next to ones that are not; the word behind the workspace's header
+    # says how many steps of 64 rows a slice has
+    dC, A, offsets, off = _inputs(counts, N, K, 3, 300 + N)
+    want, mag = _want(dC, A, off)
+    ws = gg.wgrad_workspace(len(counts), dC.shape[0], N, K, "cuda")
+    got = gg.grouped_wgrad(dC, A, offsets, out_dtype=dtype, ws=ws)
+    steps = int(ws[256:260].view(torch.int32).item())
+    assert steps > 0 and sum(-(-c // 64) > steps for c in counts) >= 3
+    _check(got, want, mag, off)
+    assert torch.equal(got, gg.grouped_wgrad(dC, A, offsets, out_dtype=dtype, ws=ws))
+    base = torch.randn(len(counts), N, K, generator=torch.Generator().manual_seed(1)).to(dtype)
+    base = base.cuda()
+    got = gg.grouped_wgrad(dC, A, offsets, base=base, ws=ws)
+    _check(got, want, mag, off, base)
+    gg.grouped_wgrad(dC, A, offsets, base=base, dB=base, ws=ws)
+    assert torch.equal(base, got) and gg.read_status(ws) == 0
