@@ -305,3 +305,23 @@ def test_a_nan_logit_makes_the_rows_gradient_nan(gg, E, k, ren):
         assert torch.equal(torch.isnan(d), torch.isnan(t))
         d = gg.route_bwd(t, r["idx"], dprob, 1, False, z_coef=0.1)
         assert torch.isnan(d[bad]).all() and torch.isfinite(d[~bad]).all()
+
+
+# tokens enough that every block of the forward with and without statistics, and of the gradient,
+# takes several turns, the last of them in part
+@pytest.mark.parametrize("T,E,k", [(80003, 30, 3), (80003, 60, 4), (40009, 64, 6), (80003, 128, 8),
+                                   (40007, 200, 8), (20011, 300, 8), (20011, 1024, 8),
+                                   (20011, 90, 20)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sig,ren", [(False, False), (True, True)])
+def test_many_turns_match_oracle(gg, T, E, k, dtype, sig, ren):
+    t, x = _logits(T + E, T, E, dtype, masked=E // 9, dead=0.03)
+    r, f = _check_forward(gg, t, x, k, sig, ren, 1.5)
+    assert int(r["counts"].sum()) == T * k
+    _check_backward(gg, t, x, r, f, sig, ren, 1.5, 5)
+    # into the logits' own buffer: the same bits
+    dprob = torch.randn(T, k, generator=torch.Generator().manual_seed(6)).cuda()
+    args = dict(counts=r["counts"], aux_coef=0.7, z_coef=0.3)
+    d = gg.route_bwd(t, r["idx"], dprob, int(sig), ren, 1.5, **args)
+    gg.route_bwd(t, r["idx"], dprob, int(sig), ren, 1.5, dlogits=t, **args)
+    assert torch.equal(t, d)
