@@ -694,6 +694,8 @@ gg_status gg_moe_mlp_fwd_q8(const gg_bf16* x, const int32_t* idx, const float* p
  *               the whole row (GG_SCORE_SOFTMAX) or sigmoid(x_e)
  *               (GG_SCORE_SIGMOID); with renormalize != 0, w = s_e / the sum
  *               of the k picked scores.
+ * Scores are fp32: those below its range (sigmoid: logits under -87) may be 0,
+ * and where all that a sum runs over are, its quotients are 0 too.
  * An expert is switched off for a row by the logit -inf: its score is 0. A
  * row of nothing but -inf gets idx 0..k-1 and prob 0. A NaN or +inf makes
  * the row's probabilities and the losses NaN where the formula does; its idx

@@ -7,7 +7,7 @@
 // matching 16 up rows). One block of 16 warps per SM; two warps share a tile,
 // each taking every other 128-code chunk of K, and go from tile to tile.
 // Every warp has a ring of its own in shared memory that TMA fills with 32 x
-// 128 weight codes and the 128 codes of up to 8 kTiles tokens per stage, so
+// 128 weight codes and the 128 codes of up to eight tokens per stage, so
 // 128 KB of weights per SM are always on their way, across tiles too; the
 // first are asked for before the kernel waits for the quantiser that makes the
 // token codes. Measured at 4 rows for each of 128 experts, 1536 x 2048 gated
@@ -44,32 +44,24 @@ constexpr int kTurns = kMaxExperts / 32;  // groups of 32 experts
 static_assert(kTurns <= 32 && kMaxExperts % kThreads == 0, "one warp scans the groups");
 constexpr int kRows = 32;    // weight rows per tile
 constexpr int kChunk = 128;  // codes of K per stage
+constexpr int kTokens = 8;   // tokens multiplied with each piece of weight
 constexpr uint32_t kWeightBytes = kRows * kChunk;
+constexpr int kStages = 2;   // of a warp's ring
+constexpr uint32_t kStageBytes = kWeightBytes + kTokens * kChunk;
+constexpr uint32_t kWarpBytes = kStages * kStageBytes;
 
-// kTiles: groups of eight tokens multiplied with each piece of weight.
-template <int kTiles>
-struct Ring {
-  static constexpr int kStages = 2;
-  static constexpr uint32_t kStageBytes = kWeightBytes + kTiles * 8 * kChunk;
-  static constexpr uint32_t kWarpBytes = kStages * kStageBytes;
-};
-
-template <int kTiles>
 struct SmemTail {
-  uint64_t full[kWarps][Ring<kTiles>::kStages];
+  uint64_t full[kWarps][kStages];
   int abort_flag;
   int bad;
   int n_live;
   int in_turn[kTurns];
   uint16_t live[kMaxExperts];  // experts that have rows
-  float part[kPairs][2 * kTiles * 4][32];  // the second warp's sums, as its lanes hold them
+  float part[kPairs][2 * 4][32];  // the second warp's sums, as its lanes hold them
 };
 
-template <int kTiles>
-constexpr size_t rows_smem() {
-  return 1024 + kWarps * Ring<kTiles>::kWarpBytes + sizeof(SmemTail<kTiles>);
-}
-static_assert(rows_smem<1>() <= 227 * 1024 && rows_smem<2>() <= 227 * 1024, "shared memory");
+constexpr size_t kSmemBytes = 1024 + kWarps * kWarpBytes + sizeof(SmemTail);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 struct RowsParams {
   const float* As;
@@ -99,16 +91,15 @@ struct Cursor {
   int row0, rows;  // the expert's rows
 };
 
-template <bool kGated, int kTiles>
+template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
 q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                const RowsParams p) {
-  using R = Ring<kTiles>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
-  SmemTail<kTiles>& st = *reinterpret_cast<SmemTail<kTiles>*>(smem + kWarps * R::kWarpBytes);
+  SmemTail& st = *reinterpret_cast<SmemTail*>(smem + kWarps * kWarpBytes);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -121,8 +112,8 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
     tma_prefetch_desc(&mapA);
     tma_prefetch_desc(&mapB);
   }
-  for (int i = threadIdx.x; i < kWarps * R::kStages; i += kThreads)
-    mbar_init(smem_u32(&st.full[i / R::kStages][i % R::kStages]), 1);
+  for (int i = threadIdx.x; i < kWarps * kStages; i += kThreads)
+    mbar_init(smem_u32(&st.full[i / kStages][i % kStages]), 1);
   mbar_fence_init();
   fence_proxy_async();
   __syncthreads();
@@ -169,8 +160,8 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   const int pair = warp >> 1, part_of = warp & 1;
   const int first_tile = pair * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
   const int tile_step = kPairs * static_cast<int>(gridDim.x);
-  uint8_t* ring = smem + warp * R::kWarpBytes;
-  const uint32_t ring_addr = raw_addr + pad + warp * R::kWarpBytes;
+  uint8_t* ring = smem + warp * kWarpBytes;
+  const uint32_t ring_addr = raw_addr + pad + warp * kWarpBytes;
 
   const auto enter = [&](Cursor& c) {  // c.tile has changed
     if (c.tile >= total) return;
@@ -184,7 +175,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
     c.chunk += 2;
     if (c.chunk < chunks) return;
     c.chunk = part_of;
-    c.first += 8 * kTiles;
+    c.first += kTokens;
     if (c.first < c.rows) return;
     c.first = 0;
     c.tile += tile_step;
@@ -192,14 +183,14 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   };
   const auto load_weights = [&](const Cursor& c, int s) {
     const uint32_t bar = smem_u32(&st.full[warp][s]);
-    const uint32_t dst = ring_addr + s * R::kStageBytes;
-    mbar_arrive_expect_tx(bar, R::kStageBytes);
+    const uint32_t dst = ring_addr + s * kStageBytes;
+    mbar_arrive_expect_tx(bar, kStageBytes);
     tma_load_3d(dst, &mapB, bar, c.chunk * kChunk, c.n0, c.e);
     if (kGated)
       tma_load_3d(dst + kWeightBytes / 2, &mapB, bar, c.chunk * kChunk, p.F + c.n0, c.e);
   };
   const auto load_tokens = [&](const Cursor& c, int s) {
-    tma_load_2d(ring_addr + s * R::kStageBytes + kWeightBytes, &mapA, smem_u32(&st.full[warp][s]),
+    tma_load_2d(ring_addr + s * kStageBytes + kWeightBytes, &mapA, smem_u32(&st.full[warp][s]),
                 c.chunk * kChunk, c.row0 + c.first);
   };
 
@@ -209,7 +200,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   uint32_t pending = 0;                 // stages with a load that was not waited for
   const bool works = part_of < chunks;  // K <= 128: the second warp has nothing
   if (works) {
-    for (int s = 0; s < R::kStages && ahead.tile < total; ++s) {
+    for (int s = 0; s < kStages && ahead.tile < total; ++s) {
       if (lane == 0) load_weights(ahead, s);
       pending |= 1u << s;
       advance(ahead);
@@ -218,7 +209,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   if (p.early) grid_dependency_wait();
   if (works && lane == 0) {
     Cursor c = at;
-    for (int s = 0; s < R::kStages && c.tile < total; ++s) {
+    for (int s = 0; s < kStages && c.tile < total; ++s) {
       load_tokens(c, s);
       advance(c);
     }
@@ -230,8 +221,8 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   int failed = 0;
   uint32_t failed_phase = 0;
   for (; at.tile < total; at.tile += tile_step, enter(at)) {
-    for (int first = 0; first < at.rows; first += 8 * kTiles) {
-      float acc[2][kTiles][4] = {};
+    for (int first = 0; first < at.rows; first += kTokens) {
+      float acc[2][4] = {};
       for (int chunk = part_of; chunk < chunks; chunk += 2) {
         if (ok) {
           ok = mbar_wait_bounded(smem_u32(&st.full[warp][s]), phase, abort_flag, p.status);
@@ -240,32 +231,27 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
           else
             failed = s, failed_phase = phase;
         }
-        const uint8_t* stage = ring + s * R::kStageBytes;
+        const uint8_t* stage = ring + s * kStageBytes;
         // 16-byte piece 2t + h of the swizzled 128-byte rows: the eight lanes
         // of an access, two neighbouring rows, then hit all banks
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t piece = ((2 * t + h) ^ g) << 4;
-          uint4 w[4], x[kTiles];
+          uint4 w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             w[i] = *reinterpret_cast<const uint4*>(stage + (8 * i + g) * kChunk + piece);
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i)
-            x[i] = *reinterpret_cast<const uint4*>(stage + kWeightBytes + (8 * i + g) * kChunk +
-                                                   piece);
+          const uint4 x =
+              *reinterpret_cast<const uint4*>(stage + kWeightBytes + g * kChunk + piece);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint2 r0 = widen4((&w[0].x)[q]), r1 = widen4((&w[1].x)[q]);
             const uint2 r2 = widen4((&w[2].x)[q]), r3 = widen4((&w[3].x)[q]);
             const uint32_t a0[4] = {r0.x, r1.x, r0.y, r1.y};
             const uint32_t a1[4] = {r2.x, r3.x, r2.y, r3.y};
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-              const uint2 b = widen4((&x[i].x)[q]);
-              mma_f16(acc[0][i], a0, b.x, b.y);
-              mma_f16(acc[1][i], a1, b.x, b.y);
-            }
+            const uint2 b = widen4((&x.x)[q]);
+            mma_f16(acc[0], a0, b.x, b.y);
+            mma_f16(acc[1], a1, b.x, b.y);
           }
         }
         __syncwarp();  // every lane has read the stage
@@ -278,7 +264,7 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
           pending |= 1u << s;
           advance(ahead);
         }
-        if (++s == R::kStages) {
+        if (++s == kStages) {
           s = 0;
           phase ^= 1u;
         }
@@ -287,60 +273,56 @@ q8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
       float(*sums)[32] = st.part[pair];
       if (part_of == 1) {
 #pragma unroll
-        for (int i = 0; i < 2 * kTiles * 4; ++i)
-          sums[i][lane] = acc[i / (4 * kTiles)][i / 4 % kTiles][i % 4];
+        for (int i = 0; i < 8; ++i) sums[i][lane] = acc[i / 4][i % 4];
       }
       asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
       if (part_of == 0) {
-        const int have = ok ? min(8 * kTiles, at.rows - first) : 0;
+        const int have = ok ? min(kTokens, at.rows - first) : 0;
         const long long width = kGated ? p.F : p.N;
         const float* bs = p.Bs + static_cast<long long>(at.e) * p.N + at.n0;
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int tok = 8 * i + 2 * t + (v & 1), c = g + (v & 2 ? 8 : 0);
-            if (tok >= have) continue;
-            const int r = at.row0 + first + tok;
-            const float sr = p.As[r];
-            gg_bf16* out = p.C + r * width + at.n0 + c;
-            // one scale after the other: their product alone may leave fp32's range.
-            // The probability goes with the token's scale of the up half, as
-            // gg_gemm_q8.cu has it: a row's bits are the same there.
-            const float up = kGated && p.row_scale != nullptr ? sr * p.row_scale[r] : sr;
-            const float lo = (acc[0][i][v] + sums[4 * i + v][lane]) * __ldg(bs + c) * sr;
-            const float hi = (acc[1][i][v] + sums[4 * (kTiles + i) + v][lane]) *
-                             __ldg(bs + (kGated ? p.F : 16) + c) * up;
-            if (kGated) {
-              *out = __bfloat16_as_ushort(
-                  __float2bfloat16_rn(glu_mul(lo, hi, p.alpha, false, 1.0f)));
-            } else {
-              out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
-              out[16] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
-            }
+        for (int v = 0; v < 4; ++v) {
+          const int tok = 2 * t + (v & 1), c = g + (v & 2 ? 8 : 0);
+          if (tok >= have) continue;
+          const int r = at.row0 + first + tok;
+          const float sr = p.As[r];
+          gg_bf16* out = p.C + r * width + at.n0 + c;
+          // one scale after the other: their product alone may leave fp32's range.
+          // The probability goes with the token's scale of the up half, as
+          // gg_gemm_q8.cu has it: a row's bits are the same there.
+          const float up = kGated && p.row_scale != nullptr ? sr * p.row_scale[r] : sr;
+          const float lo = (acc[0][v] + sums[v][lane]) * __ldg(bs + c) * sr;
+          const float hi =
+              (acc[1][v] + sums[4 + v][lane]) * __ldg(bs + (kGated ? p.F : 16) + c) * up;
+          if (kGated) {
+            *out = __bfloat16_as_ushort(
+                __float2bfloat16_rn(glu_mul(lo, hi, p.alpha, false, 1.0f)));
+          } else {
+            out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
+            out[16] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
           }
+        }
       }
       asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");  // the sums were read
     }
   }
   // after a wait that ran out: no load may still be on its way at the exit
   if (!ok)
-    for (int i = 0; i < R::kStages; ++i)
+    for (int i = 0; i < kStages; ++i)
       if (pending & (1u << i))
         (void)mbar_wait_bounded(smem_u32(&st.full[warp][i]),
                                 i >= failed ? failed_phase : failed_phase ^ 1u, nullptr,
                                 p.status);
 }
 
-template <bool kGated, int kTiles>
+template <bool kGated>
 cudaError_t launch_rows_t(const CUtensorMap& ma, const CUtensorMap& mb, const RowsParams& p,
                           const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<int> opted[kMaxDevices];
-  constexpr size_t smem = rows_smem<kTiles>();
   if (opted[dev.device].load(std::memory_order_relaxed) == 0) {
     const cudaError_t o =
-        cudaFuncSetAttribute(q8_rows_kernel<kGated, kTiles>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        cudaFuncSetAttribute(q8_rows_kernel<kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemBytes));
     if (o != cudaSuccess) return o;
     opted[dev.device].store(1, std::memory_order_relaxed);
   }
@@ -349,33 +331,37 @@ cudaError_t launch_rows_t(const CUtensorMap& ma, const CUtensorMap& mb, const Ro
   const dim3 grid(static_cast<unsigned>(tiles < dev.sm_count ? tiles : dev.sm_count));
   cudaError_t e = cudaSuccess;
   if (p.early)
-    e = launch_early(q8_rows_kernel<kGated, kTiles>, grid, dim3(kThreads), smem, stream, ma, mb,
-                     p);
+    e = launch_early(q8_rows_kernel<kGated>, grid, dim3(kThreads), kSmemBytes, stream, ma, mb, p);
   else
-    q8_rows_kernel<kGated, kTiles><<<grid, kThreads, smem, stream>>>(ma, mb, p);
+    q8_rows_kernel<kGated><<<grid, kThreads, kSmemBytes, stream>>>(ma, mb, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-// Up to 16 rows per expert that can have any, which are multiplied in one pass
-// over the weights: 16 rows for each of 128 experts, 1536 x 2048 gated, take 80
-// us against the many-row kernel's 91, 32 take 138.
+// Up to four rows per expert that can have any. The offsets are on the device,
+// so the rule cannot see a hot expert, whose rows take a pass over its weights
+// for every eight, one after the other in each tile. us here : many-row kernel,
+// rows dealt evenly, and by Zipf's law (1.2, at most an eighth to one expert):
+//   rows per expert                     1                2               4
+//   128 experts, 1536 x 2048 gated  72:92   39:49    72:92  57:57   72:92  98:78
+//   128 experts, 2048 x 768         41:51   23:29    41:51  33:35   41:51  45:43
+//   32 experts, 4096 x 4096 gated   90:111  49:68    90:111 72:96   91:111 92:109
+// At eight rows, passes of 16 tokens took 77:92, 45:51 and 96:111, by Zipf's law
+// 113:87, 63:49 and 120:111; at 16 rows 80:93 and 180:100 on the first.
 bool q8_rows_fits(int R_cap, int E) {
   const int experts = R_cap < E ? R_cap : E;
-  return R_cap <= 16 * experts;
+  return R_cap <= 4 * experts;
 }
 
 cudaError_t launch_q8_rows(const Q8GemmArgs& a, bool early, const DeviceInfo& dev,
                            cudaStream_t stream) {
   const bool gated = a.alpha != 0.0f;
-  const int experts = a.R_cap < a.E ? a.R_cap : a.E;
-  const bool wide = a.R_cap > 4 * experts;
   CUtensorMap ma, mb;
   const cuuint64_t ad[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.R_cap)};
   const cuuint64_t as[1] = {static_cast<cuuint64_t>(a.K)};
-  const cuuint32_t abox[2] = {kChunk, wide ? 16u : 8u};
+  const cuuint32_t abox[2] = {kChunk, kTokens};
   const cuuint64_t bd[3] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.N),
                             static_cast<cuuint64_t>(a.E)};
   const cuuint64_t bs[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.K) * a.N};
@@ -399,11 +385,8 @@ cudaError_t launch_q8_rows(const Q8GemmArgs& a, bool early, const DeviceInfo& de
   p.C = a.C;
   p.status = a.status;
   p.early = early ? 1 : 0;
-  if (!wide)
-    return gated ? launch_rows_t<true, 1>(ma, mb, p, dev, stream)
-                 : launch_rows_t<false, 1>(ma, mb, p, dev, stream);
-  return gated ? launch_rows_t<true, 2>(ma, mb, p, dev, stream)
-               : launch_rows_t<false, 2>(ma, mb, p, dev, stream);
+  return gated ? launch_rows_t<true>(ma, mb, p, dev, stream)
+               : launch_rows_t<false>(ma, mb, p, dev, stream);
 }
 
 }  // namespace gg

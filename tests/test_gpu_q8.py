@@ -351,7 +351,7 @@ def test_a_rows_bits_do_not_depend_on_the_kernel(gg, K, N, epi, weighted):
     n = int(off[-1])
     assert n > 16 * len(counts)
     got = []
-    for room, E in ((n + 4000, 10), (n, 30)):
+    for room, E in ((n + 4000, 10), (n, 60)):
         pad = np.zeros((E - 10, N, K), np.int8)
         offs = np.concatenate([off, np.full(E - 10, n, np.int32)])
         dev = _dev(Aq[:room], As[:room], np.concatenate([Wq, pad]),
