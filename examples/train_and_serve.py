@@ -9,6 +9,7 @@ A student layer (router, E experts) learns to reproduce a fixed teacher layer. O
     MoeLayer.forward, .backward             out, dX, dprob
     MoeLayer.weight_grads                   dW1, dW2 of the experts, in fp32
     route_bwd  -> dlogits                   from dprob and the balance and z losses
+    grad_norm, AdamW.step                   all weights in one launch, skipped unless finite
 
 Serving quantises the trained experts once (q8_prepare_weight) and runs Q8MoeLayer, for the whole
 batch and for a single token. Needs a GB300 and the built library.
@@ -30,22 +31,6 @@ E, H, F, K = 16, 256, 128, 2
 AUX, ZCO, LR = 1e-2, 1e-3, 2e-3
 
 
-class Adam:
-    """Adam on fp32 master weights; `half` is the BF16 copy that the kernels read."""
-
-    def __init__(self, w):
-        self.w, self.m, self.v, self.t = w, torch.zeros_like(w), torch.zeros_like(w), 0
-        self.half = w.bfloat16()
-
-    def step(self, g):
-        self.t += 1
-        self.m.lerp_(g, 0.1)
-        self.v.lerp_(g * g, 0.01)
-        m, v = self.m / (1 - 0.9 ** self.t), self.v / (1 - 0.99 ** self.t)
-        self.w -= LR * m / (v.sqrt() + 1e-8)
-        self.half.copy_(self.w)
-
-
 def experts(g, scale):
     return [torch.randn(s, generator=g, device="cuda") * scale / s[2] ** 0.5
             for s in ((E, 2 * F, H), (E, H, F))]
@@ -60,33 +45,36 @@ def train(tokens: int, steps: int, seed: int = 0, log=print):
     layer = gg.MoeLayer(tokens, H, F, K, E)
     r = gg.route(x.float() @ tr, K, renormalize=True)
     target = layer.forward(x, r["idx"], r["prob"], t1.bfloat16(), t2.bfloat16()).float()
-    W1, W2 = (Adam(w) for w in experts(g, 1.0))
-    R = Adam(tr + 0.3 * torch.randn(H, E, generator=g, device="cuda") / H ** 0.5)
+    weights = experts(g, 1.0)  # fp32 masters; the kernels read the BF16 copies W1 and W2
+    weights.append(tr + 0.3 * torch.randn(H, E, generator=g, device="cuda") / H ** 0.5)
+    R = weights[2]
+    W1, W2, _ = half = [w.bfloat16() for w in weights]
+    dW1, dW2, dR = grads = [torch.empty_like(w) for w in weights]
+    opt = gg.AdamW(weights, grads, half=half, betas=(0.9, 0.99))
+    norm = gg.GradPlan(grads)
     ws = gg.route_workspace(tokens, E, "cuda")
-    dW1, dW2 = (torch.empty_like(p.w) for p in (W1, W2))
     losses = []
     for i in range(steps):
-        logits = x.float() @ R.w
+        logits = x.float() @ R
         r = gg.route(logits, K, renormalize=True, counts=True, losses=True, ws=ws)
-        out = layer.forward(x, r["idx"], r["prob"], W1.half, W2.half)
+        out = layer.forward(x, r["idx"], r["prob"], W1, W2)
         err = out.float() - target
         losses.append(err.square().mean())
         dOut = (err * (2.0 / tokens)).bfloat16()
-        _, dprob = layer.backward(dOut, W1.half, W2.half, dprob=True)
+        _, dprob = layer.backward(dOut, W1, W2, dprob=True)
         layer.weight_grads(dW1, dW2)
         dlogits = gg.route_bwd(logits, r["idx"], dprob, renormalize=True, counts=r["counts"],
                                aux_coef=AUX, z_coef=ZCO)
-        W1.step(dW1)
-        W2.step(dW2)
-        R.step(x.float().t() @ dlogits)
+        torch.mm(x.float().t(), dlogits, out=dR)
+        opt.step(LR, grad_scale=gg.grad_norm(norm)[1:])
         if i % 20 == 0 or i == steps - 1:
             log(f"step {i:4d}  loss {losses[-1].item():.5f}  balance {r['losses'][0].item():.3f}"
                 f"  busiest expert {int(r['counts'].max())} of {tokens * K} pairs")
     if layer.status() != 0:
         raise RuntimeError(gg.status_string(layer.status()))
-    r = gg.route(x.float() @ R.w, K, renormalize=True)
-    out = layer.forward(x, r["idx"], r["prob"], W1.half, W2.half)
-    return dict(first=losses[0].item(), last=losses[-1].item(), W1=W1.half, W2=W2.half, R=R.w,
+    r = gg.route(x.float() @ R, K, renormalize=True)
+    out = layer.forward(x, r["idx"], r["prob"], W1, W2)
+    return dict(first=losses[0].item(), last=losses[-1].item(), W1=W1, W2=W2, R=R,
                 x=x, route=r, out=out)
 
 

@@ -783,6 +783,91 @@ gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
                            void* ws, size_t ws_bytes, gg_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * gg_adamw_step — one AdamW step over many tensors, in one launch for every
+ * 310 of them. For each element, every operation rounded to fp32:
+ *   g' = s g                          s = *grad_scale, 1 if that is NULL
+ *   m  = beta1 m + (1 - beta1) g'
+ *   v  = beta2 v + (1 - beta2) g'^2
+ *   w  = w (1 - l weight_decay) - (m c1) / (sqrt(v) c2 + eps)
+ * with l = lr * lr_scale, c1 = l / (1 - beta1^t), c2 = 1 / sqrt(1 - beta2^t)
+ * and t = step, counted from 1.
+ *   w        weights [n], fp32 or BF16 (options.w_dtype), updated in place;
+ *   g        gradient [n], fp32 or BF16 (options.g_dtype);
+ *   m, v     states, updated in place; all zero before the first step.
+ *            state_bits 32: fp32 [n], m_scale and v_scale NULL. state_bits 8:
+ *            E4M3 codes [n] of m and of sqrt(v), with one fp32 scale for each
+ *            256 elements, m_scale and v_scale [ceil(n / 256)]: a cell's scale
+ *            is max(largest magnitude, 2^-100) / 448, its values are code *
+ *            scale (v: squared). A NaN or infinity in a cell makes its scale
+ *            NaN;
+ *   half     (nullable, fp32 weights only) BF16 copy [n] of the new weights,
+ *            rounded to nearest: the weight that the layer's calls read;
+ *   lr_scale, weight_decay   of this tensor.
+ * What is kept from step to step in fewer than 32 bits (8-bit states, BF16
+ * weights) is rounded stochastically: up with the probability of the part cut
+ * off, to within 2^-16 of a step, by bits that depend on (seed, step, the
+ * tensor's place in the list, the element) alone; equal inputs give equal
+ * bits. A positive sqrt(v) keeps at least the smallest code.
+ * grad_scale, lr_dev and step_dev (nullable, device) are read when the step
+ * runs: a captured step follows their values, which take the place of lr and
+ * step. A grad_scale that is NaN or infinite skips the step: nothing is
+ * written (gg_grad_norm gives NaN for gradients that are not finite). A
+ * *step_dev below 1 skips it too.
+ * Arrays need their type's alignment (faster: that of four elements) and may
+ * not overlap each other. `tensors` and `options` are host memory, read during
+ * the call; n = 0 and tensors of 0 elements are legal.
+ * Returns GG_ERR_INVALID_ARG for a missing pointer, step < 1 (without
+ * step_dev), beta1 or beta2 outside [0, 1), an eps that is not positive, a
+ * half next to BF16 weights, state_bits other than 8 and 32, or scales next to
+ * fp32 states; GG_ERR_UNSUPPORTED_SHAPE for a tensor of 2^40 or more elements.
+ * ------------------------------------------------------------------------- */
+typedef struct gg_adamw_tensor {
+  void* w;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  gg_bf16* half;
+  int64_t n;
+  double lr_scale;
+  double weight_decay;
+} gg_adamw_tensor;
+typedef struct gg_adamw_options {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  uint32_t seed;
+  int w_dtype, g_dtype;     /* gg_dtype */
+  int state_bits;           /* 32 or 8 */
+  const float* grad_scale;  /* device, nullable */
+  const float* lr_dev;      /* device, nullable */
+  const int32_t* step_dev;  /* device, nullable */
+} gg_adamw_options;
+gg_status gg_adamw_step(const gg_adamw_tensor* tensors, int n, const gg_adamw_options* options,
+                        gg_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * gg_grad_norm — the norm of all gradients together and the factor that clips
+ * them, for gg_adamw_step's grad_scale:
+ *   out[0] = sqrt(sum over all tensors and elements of g^2)
+ *   out[1] = min(1, max_norm / (out[0] + 1e-6)), 1 for max_norm <= 0, NaN
+ *            when out[0] is NaN or infinite
+ * out: two floats on the device. Squares are taken in fp32 (beyond 1.8e19
+ * they are infinite), added up 32 at a time in fp32 and from there on in 64
+ * bits, in an order that depends on the sizes alone. g fp32 or BF16 (a
+ * gg_dtype) at its type's alignment (faster: 16 bytes). `tensors` is host
+ * memory; n = 0 gives out = {0, 1}. Workspace: gg_grad_norm_workspace_size(n)
+ * bytes; overlapping calls need one each.
+ * ------------------------------------------------------------------------- */
+typedef struct gg_grad_tensor {
+  const void* g;
+  int64_t n;
+} gg_grad_tensor;
+size_t gg_grad_norm_workspace_size(int n);
+gg_status gg_grad_norm(const gg_grad_tensor* tensors, int n, int g_dtype, float max_norm,
+                       float* out, void* ws, size_t ws_bytes, gg_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * 8-bit integer expert weights, for serving: grouped linear layers on integers
  * with one fp32 scale per row of the activations (token) and per row of the
  * weight (output channel). A row x of either is held as

@@ -1,0 +1,635 @@
+// gg_adamw.cu — the optimizer step over many tensors in one launch, and the
+// norm of all gradients that clips it.
+//
+// For each element, every operation rounded to fp32 (fused multiply-adds would
+// move a result by an ulp, and a code of an 8-bit state at a border by a step):
+//   g' = s g,  m' = b1 m + (1 - b1) g',  v' = b2 v + (1 - b2) g'^2,
+//   w' = w (1 - lr wd) - (m' c1) / (sqrt(v') c2 + eps),
+//   c1 = lr / (1 - b1^t),  c2 = 1 / sqrt(1 - b2^t).
+//
+// 8-bit states are E4M3 codes of m' and of sqrt(v') (half of v's range of
+// exponents), with one fp32 scale a / 448 for each cell of 256 elements, a the
+// cell's largest magnitude. A state moves by less than half a code's step in
+// most steps (b2 near 1: 0.05 of a percent of sqrt(v), a step is 6 to 12), and
+// rounding to nearest would leave it where it is. So what is kept from one
+// step to the next in fewer than 32 bits, the states and BF16 weights, is
+// rounded up with the probability of the part cut off, by bits of a hash
+// (Wellons' two-multiplication mixer) of seed, step, tensor and element. A
+// sqrt(v') above 0 keeps at least the smallest code: as 0 it would divide m'
+// by eps alone.
+//
+// A warp takes a cell of 256 elements, a block eight of them; the blocks go
+// through all tensors' cells together, so that small tensors cost what they
+// hold and not a launch each. The list of tensors travels in the launch's
+// parameters: nothing is copied to the device ahead of it, and a captured
+// launch keeps its own.
+
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "gg_internal.h"
+#include "gg_launch.cuh"
+#include "gg_ptx.cuh"
+
+namespace gg {
+namespace {
+
+constexpr int kCell = 256;        // elements that share a scale
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kFew = 8, kMany = 310;  // tensors in a launch's parameters (at most 32 KB)
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr uint32_t kInf = 0x7F800000u;
+constexpr float kTop = 448.0f;                       // largest E4M3 value
+constexpr float kAmaxFloor = 7.888609052210118e-31f; // 2^-100
+
+struct Entry {
+  void* w;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  gg_bf16* half;
+  long long n;
+  long long first;         // blocks' turns of kWarps cells before this tensor's
+  double lr_scale, decay;
+  float c1, kept;          // from the host's lr and step
+  int position;            // in the caller's list
+  int wide;                // every array aligned for four elements at a time
+};
+static_assert(sizeof(Entry) == 104, "parameter space");
+
+template <int kCap>
+struct List {
+  Entry t[kCap];
+};
+
+struct StepParams {
+  int count;
+  long long turns;
+  float b1, b2, ib1, ib2, c2, eps;
+  uint32_t run_key;
+  const float* grad_scale;
+  // values that a captured launch reads anew
+  const float* lr_dev;
+  const int32_t* step_dev;
+  double lr, beta1, beta2;
+  long long step;
+  uint32_t seed_key;
+};
+
+// ----------------------------------------------------- randomness and powers
+
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x7FEB352Du;
+  x ^= x >> 15;
+  x *= 0x846CA68Bu;
+  return x ^ (x >> 16);
+}
+
+__host__ __device__ __forceinline__ double times(double a, double b) {
+#ifdef __CUDA_ARCH__
+  return __dmul_rn(a, b);
+#else
+  volatile double r = a * b;  // a rounded product on every host
+  return r;
+#endif
+}
+
+// beta^t by squaring: the same products, so the same bits, on host and device.
+__host__ __device__ inline double power(double beta, long long t) {
+  double r = 1.0, b = beta;
+  for (; t > 0; t >>= 1) {
+    if (t & 1) r = times(r, b);
+    b = times(b, b);
+  }
+  return r;
+}
+
+struct Factors {
+  double lr, per_step;  // lr / (1 - b1^t)
+  float c2;
+};
+
+__host__ __device__ inline Factors factors(double lr, double beta1, double beta2, long long t) {
+  Factors f;
+  const double p1 = power(beta1, t), p2 = power(beta2, t);
+  f.lr = lr;
+  f.per_step = lr / (1.0 - p1);
+  f.c2 = static_cast<float>(1.0 / sqrt(1.0 - p2));
+  return f;
+}
+
+__host__ __device__ inline float c1_of(const Factors& f, double lr_scale) {
+  return static_cast<float>(times(f.per_step, lr_scale));
+}
+
+__host__ __device__ inline float kept_of(const Factors& f, double lr_scale, double decay) {
+  return static_cast<float>(1.0 - times(times(f.lr, lr_scale), decay));
+}
+
+// -------------------------------------------------------------- the elements
+
+__device__ __forceinline__ void e4m3_values(uint32_t codes, float* to) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(codes >> (16 * h) & 0xFFFFu), __NV_E4M3);
+    const float2 f = __half22float2(__half2(r));
+    to[2 * h] = f.x;
+    to[2 * h + 1] = f.y;
+  }
+}
+
+// E4M3 code of y in [0, 448], rounded up where the part cut off exceeds
+// 1 - bits16 / 65536. Below 2^-6 codes are 2^-9 apart, as mantissas of 3 bits
+// are from 2^-6 to 2^-5: y + 2^-6 is cut there.
+__device__ __forceinline__ uint32_t round_code(float y, uint32_t bits16) {
+  const bool small = y < 0.015625f;
+  const float z = small ? __fadd_rn(y, 0.015625f) : y;
+  const uint32_t t = (__float_as_uint(z) + (bits16 << 4)) >> 20;
+  return min(t - (small ? 968u : 960u), 126u);
+}
+
+struct Cell {
+  float w[8], g[8], m[8], v[8];
+};
+
+template <typename T>
+__device__ __forceinline__ void load4(float* to, const void* from, long long at) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(from) + at);
+    to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(from) + at);
+    to[0] = bf16_lo(x.x), to[1] = bf16_hi(x.x), to[2] = bf16_lo(x.y), to[3] = bf16_hi(x.y);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float load1(const void* from, long long at) {
+  if constexpr (sizeof(T) == 4)
+    return static_cast<const float*>(from)[at];
+  else
+    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(from)[at]) << 16);
+}
+
+template <int kCap, typename W, typename G, bool k8>
+__global__ void __launch_bounds__(kThreads)
+adamw_kernel(const __grid_constant__ List<kCap> list, const __grid_constant__ StepParams p) {
+  float gs = 1.0f;
+  if (p.grad_scale != nullptr) {
+    gs = *p.grad_scale;
+    if ((__float_as_uint(gs) & kInf) == kInf) return;  // the step is skipped
+  }
+  const bool on_device = p.lr_dev != nullptr || p.step_dev != nullptr;
+  __shared__ Factors shared;
+  uint32_t run_key = p.run_key;
+  float c2 = p.c2;
+  if (on_device) {
+    const long long t = p.step_dev != nullptr ? *p.step_dev : p.step;
+    if (t < 1) return;
+    if (threadIdx.x == 0)
+      shared = factors(p.lr_dev != nullptr ? static_cast<double>(*p.lr_dev) : p.lr, p.beta1,
+                       p.beta2, t);
+    __syncthreads();
+    c2 = shared.c2;
+    run_key = mix(p.seed_key + static_cast<uint32_t>(t));
+  }
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  int at = 0;
+  for (long long turn = blockIdx.x; turn < p.turns; turn += gridDim.x) {
+    while (at + 1 < p.count && list.t[at + 1].first <= turn) ++at;
+    const Entry& t = list.t[at];
+    const long long cell = (turn - t.first) * kWarps + warp;
+    const long long e0 = cell * kCell;
+    if (e0 >= t.n) continue;
+    // The lane's elements: four neighbours of either half of the cell, or one of
+    // every 32, which loads and stores of single elements bring together.
+    const bool whole = t.wide && e0 + kCell <= t.n;
+    const int n = static_cast<int>(min(static_cast<long long>(kCell), t.n - e0));
+    const auto place = [&](int i) {
+      return whole ? 128 * (i / 4) + 4 * lane + i % 4 : 32 * i + lane;
+    };
+    Cell c;
+    float ms = 0.0f, vs = 0.0f;
+    if constexpr (k8) {
+      ms = t.ms[cell];
+      vs = t.vs[cell];
+    }
+    const uint8_t* mq = static_cast<const uint8_t*>(t.m) + e0;
+    const uint8_t* vq = static_cast<const uint8_t*>(t.v) + e0;
+    uint32_t mw[2] = {}, vw[2] = {};
+    if (whole) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = 128 * h + 4 * lane;
+        load4<W>(c.w + 4 * h, t.w, e0 + j);
+        load4<G>(c.g + 4 * h, t.g, e0 + j);
+        if constexpr (k8) {
+          mw[h] = *reinterpret_cast<const uint32_t*>(mq + j);
+          vw[h] = *reinterpret_cast<const uint32_t*>(vq + j);
+        } else {
+          load4<float>(c.m + 4 * h, t.m, e0 + j);
+          load4<float>(c.v + 4 * h, t.v, e0 + j);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = 32 * i + lane;
+        const bool there = j < n;
+        c.w[i] = there ? load1<W>(t.w, e0 + j) : 0.0f;
+        c.g[i] = there ? load1<G>(t.g, e0 + j) : 0.0f;
+        if constexpr (k8) {
+          mw[i / 4] |= (there ? static_cast<uint32_t>(mq[j]) : 0u) << (8 * (i % 4));
+          vw[i / 4] |= (there ? static_cast<uint32_t>(vq[j]) : 0u) << (8 * (i % 4));
+        } else {
+          c.m[i] = there ? load1<float>(t.m, e0 + j) : 0.0f;
+          c.v[i] = there ? load1<float>(t.v, e0 + j) : 0.0f;
+        }
+      }
+    }
+    const float c1 = on_device ? c1_of(shared, t.lr_scale) : t.c1;
+    const float kept = on_device ? kept_of(shared, t.lr_scale, t.decay) : t.kept;
+    uint32_t mtop = 0, vtop = 0;
+    float r[8];
+    if constexpr (k8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        e4m3_values(mw[h], c.m + 4 * h);
+        e4m3_values(vw[h], c.v + 4 * h);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float g = __fmul_rn(c.g[i], gs);
+      if constexpr (k8) {
+        c.m[i] = __fmul_rn(c.m[i], ms);
+        const float old = __fmul_rn(c.v[i], vs);
+        c.v[i] = __fmul_rn(old, old);
+      }
+      c.m[i] = __fadd_rn(__fmul_rn(c.m[i], p.b1), __fmul_rn(g, p.ib1));
+      c.v[i] = __fadd_rn(__fmul_rn(c.v[i], p.b2), __fmul_rn(__fmul_rn(g, g), p.ib2));
+      r[i] = __fsqrt_rn(c.v[i]);
+      c.w[i] = __fadd_rn(__fmul_rn(c.w[i], kept),
+                         -__fdiv_rn(__fmul_rn(c.m[i], c1), __fadd_rn(__fmul_rn(r[i], c2), p.eps)));
+      if constexpr (k8) {
+        const bool there = whole || 32 * i + lane < n;
+        // as bits: ordered, a NaN above infinity
+        mtop = max(mtop, there ? __float_as_uint(c.m[i]) & 0x7FFFFFFFu : 0u);
+        vtop = max(vtop, there ? __float_as_uint(r[i]) & 0x7FFFFFFFu : 0u);
+      }
+    }
+    uint32_t noise[8];
+    if constexpr (k8 || sizeof(W) == 2) {
+      const uint32_t key = mix(mix(run_key + static_cast<uint32_t>(t.position)) +
+                               static_cast<uint32_t>(cell));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) noise[i] = mix(key + place(i));
+    }
+    uint32_t mo[2] = {}, vo[2] = {};
+    if constexpr (k8) {
+      mtop = __reduce_max_sync(kFull, mtop);
+      vtop = __reduce_max_sync(kFull, vtop);
+      // a NaN or infinity makes the cell's scale NaN, and so all its values
+      const bool mfine = mtop < kInf, vfine = vtop < kInf;
+      const float ma = fmaxf(__uint_as_float(mtop), kAmaxFloor);
+      const float va = fmaxf(__uint_as_float(vtop), kAmaxFloor);
+      const float minv = __fmul_rn(__frcp_rn(ma), kTop);
+      const float vinv = __fmul_rn(__frcp_rn(va), kTop);
+      if (lane == 0) {
+        t.ms[cell] = mfine ? __fmul_rn(ma, 1.0f / kTop) : __uint_as_float(0x7FC00000u);
+        t.vs[cell] = vfine ? __fmul_rn(va, 1.0f / kTop) : __uint_as_float(0x7FC00000u);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t a = round_code(__fmul_rn(fabsf(c.m[i]), minv), noise[i] & 0xFFFFu);
+        uint32_t b = round_code(__fmul_rn(r[i], vinv), noise[i] >> 16);
+        if (c.m[i] < 0.0f) a |= 128u;
+        if (r[i] > 0.0f) b = max(b, 1u);
+        mo[i / 4] |= (mfine ? a : 0u) << (8 * (i % 4));
+        vo[i / 4] |= (vfine ? b : 0u) << (8 * (i % 4));
+      }
+    }
+    if constexpr (sizeof(W) == 2) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __float_as_uint(c.w[i]);
+        const uint32_t up = (b & kInf) == kInf ? 0u : mix(noise[i] + 0x9E3779B9u) & 0xFFFFu;
+        // cut to BF16; a NaN stays one
+        const uint32_t lost = (b & 0x7FFFFFFFu) > kInf ? 0x7FC00000u : b + up;
+        c.w[i] = __uint_as_float(lost & 0xFFFF0000u);
+      }
+    }
+    if (whole) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const long long j = e0 + 128 * h + 4 * lane;
+        const float* x = c.w + 4 * h;
+        if constexpr (sizeof(W) == 4)
+          *reinterpret_cast<float4*>(static_cast<float*>(t.w) + j) =
+              make_float4(x[0], x[1], x[2], x[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.w) + j) =
+              make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        if (t.half != nullptr)
+          *reinterpret_cast<uint2*>(t.half + j) =
+              make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        if constexpr (k8) {
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + j) = mo[h];
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + j) = vo[h];
+        } else {
+          *reinterpret_cast<float4*>(static_cast<float*>(t.m) + j) =
+              make_float4(c.m[4 * h], c.m[4 * h + 1], c.m[4 * h + 2], c.m[4 * h + 3]);
+          *reinterpret_cast<float4*>(static_cast<float*>(t.v) + j) =
+              make_float4(c.v[4 * h], c.v[4 * h + 1], c.v[4 * h + 2], c.v[4 * h + 3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = 32 * i + lane;
+        if (k >= n) continue;
+        const long long j = e0 + k;
+        if constexpr (sizeof(W) == 4)
+          static_cast<float*>(t.w)[j] = c.w[i];
+        else
+          static_cast<uint16_t*>(t.w)[j] = __bfloat16_as_ushort(__float2bfloat16_rn(c.w[i]));
+        if (t.half != nullptr) t.half[j] = __bfloat16_as_ushort(__float2bfloat16_rn(c.w[i]));
+        if constexpr (k8) {
+          static_cast<uint8_t*>(t.m)[j] = static_cast<uint8_t>(mo[i / 4] >> (8 * (i % 4)));
+          static_cast<uint8_t*>(t.v)[j] = static_cast<uint8_t>(vo[i / 4] >> (8 * (i % 4)));
+        } else {
+          static_cast<float*>(t.m)[j] = c.m[i];
+          static_cast<float*>(t.v)[j] = c.v[i];
+        }
+      }
+    }
+  }
+}
+
+template <int kCap, typename W, typename G, bool k8>
+cudaError_t launch_step_t(const List<kMany>& all, const StepParams& p, int sm_count,
+                          cudaStream_t stream) {
+  List<kCap> list;
+  for (int i = 0; i < p.count; ++i) list.t[i] = all.t[i];
+  for (int i = p.count; i < kCap; ++i) list.t[i] = Entry{};
+  const long long most = static_cast<long long>(sm_count) * 8;
+  const unsigned grid = static_cast<unsigned>(p.turns < most ? p.turns : most);
+  adamw_kernel<kCap, W, G, k8><<<grid, kThreads, 0, stream>>>(list, p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <int kCap, typename W, typename G>
+cudaError_t launch_step_b(const List<kMany>& all, const StepParams& p, bool k8, int sm_count,
+                          cudaStream_t stream) {
+  return k8 ? launch_step_t<kCap, W, G, true>(all, p, sm_count, stream)
+            : launch_step_t<kCap, W, G, false>(all, p, sm_count, stream);
+}
+
+template <int kCap>
+cudaError_t launch_step_w(const List<kMany>& all, const StepParams& p, bool w32, bool g32, bool k8,
+                          int sm_count, cudaStream_t stream) {
+  if (w32)
+    return g32 ? launch_step_b<kCap, float, float>(all, p, k8, sm_count, stream)
+               : launch_step_b<kCap, float, gg_bf16>(all, p, k8, sm_count, stream);
+  return g32 ? launch_step_b<kCap, gg_bf16, float>(all, p, k8, sm_count, stream)
+             : launch_step_b<kCap, gg_bf16, gg_bf16>(all, p, k8, sm_count, stream);
+}
+
+// ------------------------------------------------------------------- the norm
+
+constexpr int kNormEach = 32;                    // elements per thread and turn
+constexpr int kNormTurn = kThreads * kNormEach;  // and per block
+constexpr int kNormList = 1024;                  // tensors in a launch's parameters
+constexpr int kNormBlocks = 1024;                // most blocks of a launch
+
+struct NormEntry {
+  const void* g;
+  long long n;
+  long long first;  // turns before this tensor's; its lowest bit: unaligned
+};
+
+template <int kCap>
+struct NormList {
+  NormEntry t[kCap];
+};
+
+__device__ __forceinline__ void put_norm(double sum, float max_norm, float* out) {
+  const double norm = sqrt(sum);
+  const float n = static_cast<float>(norm);
+  out[0] = n;
+  float scale = 1.0f;
+  if ((__float_as_uint(n) & kInf) == kInf)
+    scale = __uint_as_float(0x7FC00000u);
+  else if (max_norm > 0.0f)
+    scale = static_cast<float>(fmin(1.0, static_cast<double>(max_norm) / (norm + 1e-6)));
+  out[1] = scale;
+}
+
+// Sum of a block's values in a fixed order, in thread 0.
+__device__ __forceinline__ double block_sum(double x) {
+  __shared__ double part[kWarps];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(kFull, x, d);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+  __syncthreads();
+  double s = 0.0;
+  if (threadIdx.x == 0)
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) s += part[i];
+  return s;
+}
+
+// Squares are added in fp32, 32 at a time, and those sums in 64 bits.
+template <int kCap, typename G>
+__global__ void __launch_bounds__(kThreads)
+norm_kernel(const __grid_constant__ NormList<kCap> list, int count, long long turns,
+            double* partial, float max_norm, float* out) {
+  grid_dependents_launch();
+  constexpr int kVec = 16 / static_cast<int>(sizeof(G));
+  constexpr int kLoads = kNormEach / kVec;
+  double sum = 0.0;
+  int at = 0;
+  for (long long turn = blockIdx.x; turn < turns; turn += gridDim.x) {
+    while (at + 1 < count && (list.t[at + 1].first >> 1) <= turn) ++at;
+    const NormEntry& t = list.t[at];
+    const long long e0 = (turn - (t.first >> 1)) * kNormTurn;
+    float s = 0.0f;
+    if ((t.first & 1) == 0 && e0 + kNormTurn <= t.n) {
+      const uint4* from =
+          reinterpret_cast<const uint4*>(static_cast<const G*>(t.g) + e0) + threadIdx.x;
+      uint4 x[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) x[i] = __ldcs(from + i * kThreads);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (sizeof(G) == 4) {
+            s = fmaf(__uint_as_float(u[j]), __uint_as_float(u[j]), s);
+          } else {
+            s = fmaf(bf16_lo(u[j]), bf16_lo(u[j]), s);
+            s = fmaf(bf16_hi(u[j]), bf16_hi(u[j]), s);
+          }
+        }
+      }
+    } else {
+#pragma unroll 8
+      for (int i = 0; i < kNormEach; ++i) {
+        const long long e = e0 + i * kThreads + threadIdx.x;
+        const float x = e < t.n ? load1<G>(t.g, e) : 0.0f;
+        s = fmaf(x, x, s);
+      }
+    }
+    sum += s;
+  }
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) {
+    if (out != nullptr)
+      put_norm(sum, max_norm, out);
+    else
+      partial[blockIdx.x] = sum;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads)
+norm_join_kernel(const double* partial, int count, float max_norm, float* out) {
+  grid_dependency_wait();
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < count; i += kThreads) sum += partial[i];
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) put_norm(sum, max_norm, out);
+}
+
+template <int kCap, typename G>
+cudaError_t launch_norm_t(const NormList<kNormList>& all, int count, long long turns, int grid,
+                          double* partial, float max_norm, float* out, cudaStream_t stream) {
+  NormList<kCap> list;
+  for (int i = 0; i < kCap; ++i) list.t[i] = i < count ? all.t[i] : NormEntry{};
+  norm_kernel<kCap, G><<<grid, kThreads, 0, stream>>>(list, count, turns, partial, max_norm, out);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const gg_adamw_tensor* tensors, int n, const gg_adamw_options& o,
+                         const DeviceInfo& dev, cudaStream_t stream) {
+  const bool w32 = o.w_dtype == GG_DTYPE_F32, g32 = o.g_dtype == GG_DTYPE_F32;
+  const bool k8 = o.state_bits == 8;
+  StepParams p{};
+  const Factors f = factors(o.lr, o.beta1, o.beta2, o.step > 0 ? o.step : 1);
+  p.b1 = static_cast<float>(o.beta1);
+  p.b2 = static_cast<float>(o.beta2);
+  p.ib1 = static_cast<float>(1.0 - o.beta1);
+  p.ib2 = static_cast<float>(1.0 - o.beta2);
+  p.c2 = f.c2;
+  p.eps = static_cast<float>(o.eps);
+  p.seed_key = mix(o.seed);
+  p.run_key = mix(p.seed_key + static_cast<uint32_t>(o.step));
+  p.grad_scale = o.grad_scale;
+  p.lr_dev = o.lr_dev;
+  p.step_dev = o.step_dev;
+  p.lr = o.lr;
+  p.beta1 = o.beta1;
+  p.beta2 = o.beta2;
+  p.step = o.step;
+  List<kMany> list;
+  int i = 0;
+  while (i < n) {
+    p.count = 0;
+    p.turns = 0;
+    for (; i < n && p.count < kMany; ++i) {
+      const gg_adamw_tensor& t = tensors[i];
+      if (t.n == 0) continue;
+      Entry& e = list.t[p.count++];
+      e.w = t.w;
+      e.g = t.g;
+      e.m = t.m;
+      e.v = t.v;
+      e.ms = t.m_scale;
+      e.vs = t.v_scale;
+      e.half = t.half;
+      e.n = t.n;
+      e.first = p.turns;
+      e.lr_scale = t.lr_scale;
+      e.decay = t.weight_decay;
+      e.c1 = c1_of(f, t.lr_scale);
+      e.kept = kept_of(f, t.lr_scale, t.weight_decay);
+      e.position = i;
+      const auto fits = [](const void* q, size_t bytes) {
+        return (reinterpret_cast<uintptr_t>(q) & (4 * bytes - 1)) == 0;
+      };
+      e.wide = fits(t.w, w32 ? 4 : 2) && fits(t.g, g32 ? 4 : 2) && fits(t.m, k8 ? 1 : 4) &&
+               fits(t.v, k8 ? 1 : 4) && fits(t.half, 2);
+      const long long cells = (t.n + kCell - 1) / kCell;
+      p.turns += (cells + kWarps - 1) / kWarps;
+    }
+    if (p.count == 0) break;
+    const cudaError_t e = p.count <= kFew
+                              ? launch_step_w<kFew>(list, p, w32, g32, k8, dev.sm_count, stream)
+                              : launch_step_w<kMany>(list, p, w32, g32, k8, dev.sm_count, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+size_t grad_norm_scratch(int n) {
+  const size_t launches = (static_cast<size_t>(n) + kNormList - 1) / kNormList;
+  return sizeof(double) * kNormBlocks * (launches < 1 ? 1 : launches);
+}
+
+cudaError_t launch_grad_norm(const gg_grad_tensor* tensors, int n, bool f32, float max_norm,
+                             float* out, double* partial, const DeviceInfo& dev,
+                             cudaStream_t stream) {
+  NormList<kNormList> list;
+  int i = 0, written = 0;
+  bool done = false;
+  const long long most = static_cast<long long>(dev.sm_count) * 6 < kNormBlocks
+                             ? static_cast<long long>(dev.sm_count) * 6
+                             : kNormBlocks;
+  do {
+    int count = 0;
+    long long turns = 0;
+    for (; i < n && count < kNormList; ++i) {
+      if (tensors[i].n == 0) continue;
+      NormEntry& e = list.t[count++];
+      e.g = tensors[i].g;
+      e.n = tensors[i].n;
+      e.first = 2 * turns + ((reinterpret_cast<uintptr_t>(e.g) & 15u) != 0 ? 1 : 0);
+      turns += (e.n + kNormTurn - 1) / kNormTurn;
+    }
+    const int grid = static_cast<int>(turns < 1 ? 1 : (turns < most ? turns : most));
+    done = i == n && written == 0 && grid == 1;  // one block: it writes the result
+    float* to = done ? out : nullptr;
+    cudaError_t e;
+    if (count <= kFew)
+      e = f32 ? launch_norm_t<kFew, float>(list, count, turns, grid, partial + written, max_norm,
+                                           to, stream)
+              : launch_norm_t<kFew, gg_bf16>(list, count, turns, grid, partial + written,
+                                             max_norm, to, stream);
+    else
+      e = f32 ? launch_norm_t<kNormList, float>(list, count, turns, grid, partial + written,
+                                                max_norm, to, stream)
+              : launch_norm_t<kNormList, gg_bf16>(list, count, turns, grid, partial + written,
+                                                  max_norm, to, stream);
+    if (e != cudaSuccess) return e;
+    written += grid;
+  } while (i < n);
+  if (done) return cudaSuccess;
+  const cudaError_t e = launch_early(norm_join_kernel, dim3(1), dim3(kThreads), 0, stream,
+                                     static_cast<const double*>(partial), written, max_norm, out);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace gg

@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -1088,6 +1089,72 @@ gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
   }
   return gg_grouped_wgrad(buf->dYp, buf->A, buf->offsets, E, R_cap, H, F, out_dtype, base2, dW2,
                           ws, ws_bytes, stream);
+}
+
+gg_status gg_adamw_step(const gg_adamw_tensor* tensors, int n, const gg_adamw_options* options,
+                        gg_stream_t stream) {
+  if (n < 0 || options == nullptr || (n > 0 && tensors == nullptr)) return GG_ERR_INVALID_ARG;
+  const gg_adamw_options& o = *options;
+  const bool w32 = o.w_dtype == GG_DTYPE_F32, g32 = o.g_dtype == GG_DTYPE_F32;
+  if ((!w32 && o.w_dtype != GG_DTYPE_BF16) || (!g32 && o.g_dtype != GG_DTYPE_BF16))
+    return GG_ERR_INVALID_ARG;
+  if (o.state_bits != 8 && o.state_bits != 32) return GG_ERR_INVALID_ARG;
+  if (o.step_dev == nullptr && o.step < 1) return GG_ERR_INVALID_ARG;
+  // negated, so that a NaN is refused too
+  if (!(o.beta1 >= 0.0 && o.beta1 < 1.0) || !(o.beta2 >= 0.0 && o.beta2 < 1.0) ||
+      !(o.eps > 0.0) || static_cast<float>(o.eps) == 0.0f || !std::isfinite(o.eps) ||
+      (o.lr_dev == nullptr && !std::isfinite(o.lr)))
+    return GG_ERR_INVALID_ARG;
+  if (!aligned_to(o.grad_scale, 4) || !aligned_to(o.lr_dev, 4) || !aligned_to(o.step_dev, 4))
+    return GG_ERR_MISALIGNED;
+  const bool k8 = o.state_bits == 8;
+  for (int i = 0; i < n; ++i) {
+    const gg_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || !std::isfinite(t.lr_scale) || !std::isfinite(t.weight_decay))
+      return GG_ERR_INVALID_ARG;
+    if (t.n >= (1ll << 40)) return GG_ERR_UNSUPPORTED_SHAPE;
+    if (t.half != nullptr && !w32) return GG_ERR_INVALID_ARG;
+    if (!k8 && (t.m_scale != nullptr || t.v_scale != nullptr)) return GG_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    if (t.w == nullptr || t.g == nullptr || t.m == nullptr || t.v == nullptr)
+      return GG_ERR_INVALID_ARG;
+    if (k8 && (t.m_scale == nullptr || t.v_scale == nullptr)) return GG_ERR_INVALID_ARG;
+    if (!aligned_to(t.w, w32 ? 4 : 2) || !aligned_to(t.g, g32 ? 4 : 2) ||
+        (!k8 && (!aligned_to(t.m, 4) || !aligned_to(t.v, 4))) || !aligned_to(t.m_scale, 4) ||
+        !aligned_to(t.v_scale, 4) || !aligned_to(t.half, 2))
+      return GG_ERR_MISALIGNED;
+  }
+  DeviceInfo dev;
+  const gg_status s = device_ok(&dev);
+  if (s != GG_OK) return s;
+  return from_cuda(launch_adamw(tensors, n, o, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t gg_grad_norm_workspace_size(int n) {
+  return n < 0 ? 0 : kWsHeader + align256(grad_norm_scratch(n));
+}
+
+gg_status gg_grad_norm(const gg_grad_tensor* tensors, int n, int g_dtype, float max_norm,
+                       float* out, void* ws, size_t ws_bytes, gg_stream_t stream) {
+  if (n < 0 || out == nullptr || (n > 0 && tensors == nullptr)) return GG_ERR_INVALID_ARG;
+  const bool g32 = g_dtype == GG_DTYPE_F32;
+  if (!g32 && g_dtype != GG_DTYPE_BF16) return GG_ERR_INVALID_ARG;
+  if (max_norm != max_norm) return GG_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) {
+    if (tensors[i].n < 0 || (tensors[i].n > 0 && tensors[i].g == nullptr))
+      return GG_ERR_INVALID_ARG;
+    if (tensors[i].n >= (1ll << 40)) return GG_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned_to(tensors[i].g, g32 ? 4 : 2)) return GG_ERR_MISALIGNED;
+  }
+  if (!aligned_to(out, 4)) return GG_ERR_MISALIGNED;
+  gg_status s = check_ws(ws, ws_bytes, gg_grad_norm_workspace_size(n));
+  if (s != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  return from_cuda(launch_grad_norm(
+      tensors, n, g32, max_norm, out,
+      reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kWsHeader), dev,
+      reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t gg_q8_workspace_size(int R_cap, int K) {

@@ -223,6 +223,15 @@ int wgrad_slots(int R_cap, int N, int K);
 size_t wgrad_slot_bytes();
 cudaError_t launch_wgrad(const WgradArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
+// ------------------------------------------------------------------ gg_adamw.cu
+cudaError_t launch_adamw(const gg_adamw_tensor* tensors, int n, const gg_adamw_options& o,
+                         const DeviceInfo& dev, cudaStream_t stream);
+// `partial`: grad_norm_scratch(n) bytes.
+size_t grad_norm_scratch(int n);
+cudaError_t launch_grad_norm(const gg_grad_tensor* tensors, int n, bool f32, float max_norm,
+                             float* out, double* partial, const DeviceInfo& dev,
+                             cudaStream_t stream);
+
 // ------------------------------------------------------------------ gg_q8_quant.cu
 // Codes Q and scales S of `rows` source rows (no more than offsets[E] when
 // offsets is not null). With row_of_slot, source row t goes to the rows

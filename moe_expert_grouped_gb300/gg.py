@@ -9,6 +9,7 @@ is no CPU fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -82,6 +83,9 @@ SIGNATURES = [
     ("gg_grouped_wgrad", _I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
     ("gg_moe_mlp_wgrad", _I,
      [_I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    ("gg_adamw_step", _I, [_P, _I, _P, _P]),
+    ("gg_grad_norm_workspace_size", _Z, [_I]),
+    ("gg_grad_norm", _I, [_P, _I, _I, _F, _P, _P, _Z, _P]),
     ("gg_q8_buffers_size", _Z, [_I, _I, _I, _I, _I]),
     ("gg_q8_buffers_bind", _I, [_P, _Z, _I, _I, _I, _I, _I, _P]),
     ("gg_moe_mlp_fwd_q8", _I,
@@ -142,6 +146,29 @@ class GGQ8Buffers(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "Xq", "Xs", "A", "Aq", "As", "Yp", "offsets", "row_of_slot", "slot_of_row",
         "prob_of_row", "ws")] + [("ws_bytes", ctypes.c_size_t)]
+
+
+class GGAdamwTensor(ctypes.Structure):
+    """Mirror of struct gg_adamw_tensor."""
+
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "w", "g", "m", "v", "m_scale", "v_scale", "half")] + [
+        ("n", ctypes.c_int64), ("lr_scale", ctypes.c_double), ("weight_decay", ctypes.c_double)]
+
+
+class GGAdamwOptions(ctypes.Structure):
+    """Mirror of struct gg_adamw_options."""
+
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + [
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint32), ("w_dtype", ctypes.c_int),
+        ("g_dtype", ctypes.c_int), ("state_bits", ctypes.c_int)] + [
+        (n, ctypes.c_void_p) for n in ("grad_scale", "lr_dev", "step_dev")]
+
+
+class GGGradTensor(ctypes.Structure):
+    """Mirror of struct gg_grad_tensor."""
+
+    _fields_ = [("g", ctypes.c_void_p), ("n", ctypes.c_int64)]
 
 
 class GGError(RuntimeError):
@@ -830,6 +857,191 @@ def grouped_wgrad(dC, A, offsets, base=None, dB=None, out_dtype=torch.bfloat16, 
                                 _ptr(base), _ptr(dB), _ptr(ws), ws.numel(), _stream(dC.device)),
            "gg_grouped_wgrad")
     return dB
+
+
+# ---------------------------------------------------------------- optimizer step
+
+STATE_CELL = 256  # elements of an 8-bit state that share a scale
+
+
+def _guard(device: torch.device):
+    """The device made current for a call, where it is not."""
+    here = device.index is None or device.index == torch.cuda.current_device()
+    return contextlib.nullcontext() if here else torch.cuda.device(device)
+
+
+def _alike(tensors, name: str, dtype=None, numels=None):
+    """Checks a list of contiguous CUDA tensors of one type and device."""
+    tensors = list(tensors)
+    if numels is not None and len(tensors) != len(numels):
+        raise ValueError(f"{name}: expected {len(numels)} tensors, got {len(tensors)}")
+    for i, t in enumerate(tensors):
+        if dtype is None:
+            dtype = t.dtype
+        if t.dtype != dtype:
+            raise TypeError(f"{name}[{i}]: expected {dtype}, got {t.dtype}")
+        if numels is not None and t.numel() != numels[i]:
+            raise ValueError(f"{name}[{i}]: expected {numels[i]} elements, got {t.numel()}")
+        _ptr(t)
+        if t.device != tensors[0].device:
+            raise ValueError(f"{name}[{i}]: on {t.device}, the first on {tensors[0].device}")
+    return tensors
+
+
+class GradPlan:
+    """Gradients whose norm is taken together (grad_norm), with the call's workspace. Calls
+    that overlap need a plan each."""
+
+    def __init__(self, grads):
+        self.grads = _alike(grads, "grads")
+        if not self.grads:
+            raise ValueError("grads: at least one tensor expected")
+        self.device = self.grads[0].device
+        self.dtype = _dtype(self.grads[0], "grads[0]")
+        self.table = (GGGradTensor * len(self.grads))(
+            *[GGGradTensor(t.data_ptr(), t.numel()) for t in self.grads])
+        n = int(LIB.gg_grad_norm_workspace_size(len(self.grads)))
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+
+def grad_norm(grads, max_norm: float = 0.0, out=None):
+    """gg_grad_norm over a list of gradients (fp32 or BF16) or a GradPlan: out [2] fp32, the
+    norm and the factor that clips it to max_norm (1 for max_norm <= 0, NaN for gradients that
+    are not finite); out[1:] is AdamW.step's grad_scale."""
+    plan = grads if isinstance(grads, GradPlan) else GradPlan(grads)
+    if out is None:
+        out = torch.empty((2,), dtype=torch.float32, device=plan.device)
+    else:
+        _need(out, torch.float32, (2,), "out")
+        if out.device != plan.device:
+            raise ValueError(f"out: on {out.device}, the gradients on {plan.device}")
+    with _guard(plan.device):
+        _check(LIB.gg_grad_norm(plan.table, len(plan.grads), plan.dtype, max_norm, _ptr(out),
+                                plan.ws.data_ptr(), plan.ws.numel(), _stream(plan.device)),
+               "gg_grad_norm")
+    return out
+
+
+class AdamW:
+    """AdamW over a list of weights (gg_adamw_step), updated in place.
+
+    weights are fp32 or BF16 and grads fp32 or BF16, each list of one type; half are BF16 copies
+    of fp32 weights that every step writes. The states m and v are made here, zero, in fp32 or,
+    with state_bits=8, as E4M3 codes with a scale per STATE_CELL elements; or passed (8-bit ones
+    with their scales m_scale and v_scale, 1-D, one element per cell). weight_decay and lr_scale:
+    one number, or one per tensor."""
+
+    def __init__(self, weights, grads, half=None, state_bits=None, m=None, v=None, m_scale=None,
+                 v_scale=None, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0,
+                 lr_scale=1.0, seed: int = 0):
+        self.weights = _alike(weights, "weights")
+        if not self.weights:
+            raise ValueError("weights: at least one tensor expected")
+        n = [t.numel() for t in self.weights]
+        self.device = self.weights[0].device
+        self._numels = n
+        if (m is None) != (v is None) or (m_scale is None) != (v_scale is None):
+            raise ValueError("states are passed together: m and v, m_scale and v_scale")
+        if m is not None:
+            m = list(m)
+            given = 8 if m and m[0].dtype == torch.float8_e4m3fn else 32
+            if state_bits not in (None, given):
+                raise ValueError(f"m: {state_bits}-bit states asked for, {given}-bit ones passed")
+            state_bits = given
+        state_bits = 32 if state_bits is None else state_bits
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits: 8 or 32")
+        stype = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        cells = [-(-k // STATE_CELL) for k in n]
+
+        def states(given, name):
+            if given is None:
+                return [torch.zeros(t.shape, dtype=stype, device=self.device)
+                        for t in self.weights]
+            return _alike(given, name, stype, n)
+
+        def scales(given, name):
+            if state_bits == 32:
+                if given is not None:
+                    raise ValueError(f"{name}: fp32 states have no scales")
+                return None
+            if given is None:
+                if m is not None:
+                    raise ValueError(f"{name}: 8-bit states are passed with their scales")
+                return [torch.zeros(c, dtype=torch.float32, device=self.device) for c in cells]
+            return _alike(given, name, torch.float32, cells)
+
+        self.m, self.v = states(m, "m"), states(v, "v")
+        self.m_scale, self.v_scale = scales(m_scale, "m_scale"), scales(v_scale, "v_scale")
+        self.half = None if half is None else _alike(half, "half", torch.bfloat16, n)
+        for name in ("m", "v", "m_scale", "v_scale", "half"):
+            got = getattr(self, name)
+            if got and got[0].device != self.device:
+                raise ValueError(f"{name}: on {got[0].device}, the weights on {self.device}")
+        per = [x if isinstance(x, (list, tuple)) else [x] * len(n)
+               for x in (lr_scale, weight_decay)]
+        if any(len(x) != len(n) for x in per):
+            raise ValueError(f"lr_scale, weight_decay: one number or {len(n)} of them expected")
+        self.table = (GGAdamwTensor * len(n))()
+        for i, row in enumerate(self.table):
+            row.w, row.n = self.weights[i].data_ptr(), n[i]
+            row.m, row.v = self.m[i].data_ptr(), self.v[i].data_ptr()
+            if state_bits == 8:
+                row.m_scale = self.m_scale[i].data_ptr()
+                row.v_scale = self.v_scale[i].data_ptr()
+            if self.half is not None:
+                row.half = self.half[i].data_ptr()
+            row.lr_scale, row.weight_decay = float(per[0][i]), float(per[1][i])
+        self.opt = GGAdamwOptions(beta1=betas[0], beta2=betas[1], eps=eps, seed=seed & 0xFFFFFFFF,
+                                  w_dtype=_dtype(self.weights[0], "weights[0]"),
+                                  state_bits=state_bits)
+        self.t = 0  # steps taken
+        self.set_grads(grads)
+        written = [t for x in (self.weights, self.m, self.v, self.m_scale, self.v_scale,
+                               self.half) if x is not None for t in x if t.numel()]
+        ends = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                      for t in written)
+        if any(a[1] > b[0] for a, b in zip(ends, ends[1:])):
+            raise ValueError("weights, states and copies may not overlap")
+
+    def set_grads(self, grads) -> None:
+        """The gradients that the steps from now on read."""
+        grads = _alike(grads, "grads", None, self._numels)
+        if grads[0].device != self.device:
+            raise ValueError(f"grads: on {grads[0].device}, the weights on {self.device}")
+        self.opt.g_dtype = _dtype(grads[0], "grads[0]")
+        self.grads = grads
+        for row, t in zip(self.table, grads):
+            row.g = t.data_ptr()
+
+    def _scalar(self, t, dtype, name):
+        if t.dtype != dtype or t.numel() != 1 or t.device != self.device:
+            raise ValueError(f"{name}: one {dtype} on {self.device} expected")
+        return _ptr(t)
+
+    def step(self, lr, step=None, grad_scale=None) -> None:
+        """One step. lr: a number, or a one-element fp32 tensor that is read when the step runs.
+        step: the step's number from 1 on (by default one more than the last call's), or a
+        one-element int32 tensor read when the step runs. grad_scale (one fp32 on the device,
+        as out[1:] of grad_norm) multiplies the gradients; one that is not finite skips the
+        step on the device, which the count of steps here does not see."""
+        o = self.opt
+        o.lr_dev = o.step_dev = o.grad_scale = None
+        if isinstance(lr, torch.Tensor):
+            o.lr, o.lr_dev = 0.0, self._scalar(lr, torch.float32, "lr")
+        else:
+            o.lr = lr
+        if isinstance(step, torch.Tensor):
+            o.step, o.step_dev = 1, self._scalar(step, torch.int32, "step")
+        else:
+            o.step = self.t + 1 if step is None else step
+        if grad_scale is not None:
+            o.grad_scale = self._scalar(grad_scale, torch.float32, "grad_scale")
+        with _guard(self.device):
+            _check(LIB.gg_adamw_step(self.table, len(self.weights), ctypes.byref(o),
+                                     _stream(self.device)), "gg_adamw_step")
+        if not isinstance(step, torch.Tensor):
+            self.t = int(o.step)
 
 
 # ---------------------------------------------------------------- 8-bit expert weights
