@@ -783,6 +783,76 @@ gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
                            void* ws, size_t ws_bytes, gg_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * E4M3 expert weights with one fp32 scale for every 128 x 128 block, and
+ * activations with one for every 128 columns of a row: grouped linear layers
+ * and their input gradient on ONE set of codes of the weight.
+ * A block of a row, or of a weight, is held as
+ *   a = max(max |x|, 2^-100), q = e4m3(x * (448 * (1 / a))), s = a * (1 / 448)
+ * in fp32, q rounded to nearest even. A block with a NaN or an infinity gets
+ * the codes 0 and the scale NaN: its products are NaN. The last block of a
+ * width that is no multiple of 128 is narrower.
+ *   weight codes Wq[E][N][K], scales Ws[E][ceil(N / 128)][ceil(K / 128)];
+ *   row codes Q[R_cap][K], scales S[ceil(K / 128)][R_cap] (the scales of one
+ *   block of columns lie together).
+ * Codes and scales made elsewhere are accepted: any E4M3 code, any fp32 scale;
+ * the product of a row's and a weight's scale has to lie in fp32's range.
+ *
+ * gg_f8_prepare_weight — Wq and Ws of a BF16 weight W[E][N][K].
+ *
+ * gg_f8_quantize_rows — codes Q and scales S of src[T][K] (BF16). With
+ * row_of_slot[T*k] (k <= 32) the codes of token t go to rows row_of_slot[t*k]
+ * .. of Q and S, -1: nowhere; a row outside [-1, R_cap) sets
+ * GG_ERR_DEVICE_BAD_ROW and is skipped. Without it (NULL) they go to row t,
+ * T <= R_cap. Other rows are left as they were.
+ *
+ * gg_f8_grouped_gemm — for every expert e and row r of its own,
+ *   acc[r][n] = sum_b S[b][r] Ws[e][n / 128][b] sum_{k in block b} Q[r][k] Wq[e][n][k]
+ * in fp32.
+ *   GG_EPI_NONE:    C[R_cap][N] = bf16(acc).
+ *   GG_EPI_SWIGLU, GG_EPI_QGEGLU: N = 2F, g = acc[:, :F], u = acc[:, F:];
+ *     C[R_cap][F] = bf16([prob_of_row[r] *] act(g) * u), and, when H1_save is
+ *     not NULL, H1_save[R_cap][2F] = bf16([g, u]). The activation takes the
+ *     unrounded sums.
+ * gg_f8_grouped_fwd — the same from BF16 rows A[R_cap][K], quantised into ws.
+ *
+ * gg_f8_grouped_dgrad — input gradient: dC[R_cap][N] (BF16) is quantised along
+ * N into ws, and
+ *   acc[r][c] = sum_b S[b][r] Ws[e][b][c / 128] sum_{n in block b} Q[r][n] Wq[e][n][c]
+ * with the epilogues, H1, prob_of_row and rowdot of gg_grouped_dgrad, but that
+ * rowdot pairs acc with act(g) * u in fp32, unrounded, and that GG_EPI_NONE
+ * takes no prob_of_row.
+ *
+ * Rows outside [0, offsets[E]) are neither read into a result nor written.
+ * Results are bitwise repeatable for the same offsets and sizes. N and K
+ * multiples of 64, gated N of 128, E <= 1024; pointers 16-byte aligned but
+ * for scales, prob_of_row and offsets (4) and rowdot (32). Offsets that are
+ * not a valid prefix sum set GG_ERR_DEVICE_BAD_OFFSETS and nothing is
+ * computed. Workspace: gg_f8_workspace_size(R_cap, K) bytes for
+ * gg_f8_grouped_fwd, (R_cap, N) for gg_f8_grouped_dgrad, 256 bytes otherwise.
+ * ------------------------------------------------------------------------- */
+size_t gg_f8_workspace_size(int R_cap, int width);
+gg_status gg_f8_prepare_weight(const gg_bf16* W, int E, int N, int K, uint8_t* Wq, float* Ws,
+                               gg_stream_t stream);
+gg_status gg_f8_quantize_rows(const gg_bf16* src, int T, int K, const int32_t* row_of_slot, int k,
+                              int R_cap, uint8_t* Q, float* S, void* ws, size_t ws_bytes,
+                              gg_stream_t stream);
+gg_status gg_f8_grouped_gemm(const uint8_t* Aq, const float* As, const uint8_t* Wq,
+                             const float* Ws, const int32_t* offsets, int E, int R_cap, int K,
+                             int N, gg_epilogue epi, gg_bf16* C, gg_bf16* H1_save,
+                             const float* prob_of_row, void* ws, size_t ws_bytes,
+                             gg_stream_t stream);
+gg_status gg_f8_grouped_fwd(const gg_bf16* A, const uint8_t* Wq, const float* Ws,
+                            const int32_t* offsets, int E, int R_cap, int K, int N,
+                            gg_epilogue epi, gg_bf16* C, gg_bf16* H1_save,
+                            const float* prob_of_row, void* ws, size_t ws_bytes,
+                            gg_stream_t stream);
+gg_status gg_f8_grouped_dgrad(const gg_bf16* dC, const uint8_t* Wq, const float* Ws,
+                              const int32_t* offsets, int E, int R_cap, int K, int N,
+                              gg_epilogue epi, const gg_bf16* H1, const float* prob_of_row,
+                              gg_bf16* dA, float* rowdot, void* ws, size_t ws_bytes,
+                              gg_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * gg_adamw_step — one AdamW step over many tensors, in one launch for every
  * 310 of them. For each element, every operation rounded to fp32:
  *   g' = s g                          s = *grad_scale, 1 if that is NULL

@@ -1091,6 +1091,163 @@ gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
                           ws, ws_bytes, stream);
 }
 
+size_t gg_f8_workspace_size(int R_cap, int width) {
+  if (R_cap < 0 || width <= 0) return 0;
+  const size_t blocks = (static_cast<size_t>(width) + 127) / 128;
+  return kWsHeader + align256(sizeof(float) * blocks * static_cast<size_t>(R_cap)) +
+         align256(static_cast<size_t>(R_cap) * static_cast<size_t>(width));
+}
+
+gg_status gg_f8_prepare_weight(const gg_bf16* W, int E, int N, int K, uint8_t* Wq, float* Ws,
+                               gg_stream_t stream) {
+  if (E <= 0 || N <= 0 || K <= 0) return GG_ERR_INVALID_ARG;
+  if (W == nullptr || Wq == nullptr || Ws == nullptr) return GG_ERR_INVALID_ARG;
+  // blocks of rows are counted in a grid dimension of 16 bits
+  if (E > kMaxExperts || N % 64 != 0 || K % 64 != 0 || N > 65535 * 128)
+    return GG_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(W) || !aligned16(Wq) || !aligned_to(Ws, 4)) return GG_ERR_MISALIGNED;
+  DeviceInfo dev;
+  const gg_status s = device_ok(&dev);
+  if (s != GG_OK) return s;
+  return from_cuda(
+      launch_f8_weight(W, E, N, K, Wq, Ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gg_status gg_f8_quantize_rows(const gg_bf16* src, int T, int K, const int32_t* row_of_slot, int k,
+                              int R_cap, uint8_t* Q, float* S, void* ws, size_t ws_bytes,
+                              gg_stream_t stream) {
+  if (T < 0 || K <= 0 || R_cap < 0) return GG_ERR_INVALID_ARG;
+  if (row_of_slot != nullptr ? (k <= 0 || k > 32) : T > R_cap) return GG_ERR_INVALID_ARG;
+  if (K % 64 != 0) return GG_ERR_UNSUPPORTED_SHAPE;
+  if (T > 0 && R_cap > 0 && (src == nullptr || Q == nullptr || S == nullptr))
+    return GG_ERR_INVALID_ARG;
+  if (!aligned16(src) || !aligned16(Q) || !aligned_to(S, 4) || !aligned_to(row_of_slot, 4))
+    return GG_ERR_MISALIGNED;
+  gg_status s = check_ws(ws, ws_bytes, kWsHeader);
+  if (s != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  if (R_cap == 0) return GG_OK;
+  return from_cuda(launch_f8_quantize(src, T, K, nullptr, 0, row_of_slot, k, R_cap, Q, S,
+                                      status_ptr(ws), dev.sm_count,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// `out`: channels of the product, N or, for the gradient, K.
+static gg_status f8_gemm_checks(const void* A, const uint8_t* Wq, const float* Ws,
+                                const int32_t* offsets, int E, int R_cap, int K, int N, int out,
+                                const float* prob_of_row, const gg_bf16* C) {
+  if (E <= 0 || R_cap < 0 || K <= 0 || N <= 0) return GG_ERR_INVALID_ARG;
+  if (Wq == nullptr || Ws == nullptr || offsets == nullptr) return GG_ERR_INVALID_ARG;
+  if (R_cap > 0 && (A == nullptr || C == nullptr)) return GG_ERR_INVALID_ARG;
+  if (E > kMaxExperts || K % 64 != 0 || N % 64 != 0) return GG_ERR_UNSUPPORTED_SHAPE;
+  // work items and an expert's weight scales are counted in an int
+  if ((static_cast<long long>(R_cap) / 256 + E) * ((out + 127LL) / 128) > 0x3FFFFFFFLL ||
+      ((N + 127LL) / 128) * ((K + 127LL) / 128) > 0x3FFFFFFFLL)
+    return GG_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(A) || !aligned16(Wq) || !aligned_to(Ws, 4) || !aligned16(C) ||
+      !aligned_to(prob_of_row, 4) || !aligned_to(offsets, 4))
+    return GG_ERR_MISALIGNED;
+  return GG_OK;
+}
+
+static F8GemmArgs f8_args(bool grad, const uint8_t* Aq, const float* As, const uint8_t* Wq,
+                          const float* Ws, const int32_t* offsets, int E, int R_cap, int K, int N,
+                          gg_epilogue epi, const float* prob_of_row, gg_bf16* C, void* ws) {
+  F8GemmArgs a{};
+  a.grad = grad;
+  a.A = Aq;
+  a.As = As;
+  a.B = Wq;
+  a.Bs = Ws;
+  a.offsets = offsets;
+  a.E = E;
+  a.R_cap = R_cap;
+  a.K = K;
+  a.N = N;
+  a.alpha = glu_alpha(epi);
+  a.row_scale = prob_of_row;
+  a.C = C;
+  a.status = status_ptr(ws);
+  return a;
+}
+
+gg_status gg_f8_grouped_gemm(const uint8_t* Aq, const float* As, const uint8_t* Wq,
+                             const float* Ws, const int32_t* offsets, int E, int R_cap, int K,
+                             int N, gg_epilogue epi, gg_bf16* C, gg_bf16* H1_save,
+                             const float* prob_of_row, void* ws, size_t ws_bytes,
+                             gg_stream_t stream) {
+  gg_status s = f8_gemm_checks(Aq, Wq, Ws, offsets, E, R_cap, K, N, N, prob_of_row, C);
+  if (s != GG_OK) return s;
+  if ((s = fwd_epilogue_checks(epi, N, H1_save, prob_of_row)) != GG_OK) return s;
+  if (R_cap > 0 && As == nullptr) return GG_ERR_INVALID_ARG;
+  if (!aligned_to(As, 4)) return GG_ERR_MISALIGNED;
+  if ((s = check_ws(ws, ws_bytes, kWsHeader)) != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  if (R_cap == 0) return GG_OK;
+  F8GemmArgs a =
+      f8_args(false, Aq, As, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws);
+  a.H1_save = H1_save;
+  return from_cuda(launch_f8_gemm(a, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Rows of `width` columns quantised into the workspace, which then holds A and As of `a`.
+static cudaError_t f8_rows_to_ws(const gg_bf16* rows, int width, F8GemmArgs* a, void* ws,
+                                 const DeviceInfo& dev, cudaStream_t stream) {
+  const size_t blocks = (static_cast<size_t>(width) + 127) / 128;
+  float* S = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsHeader);
+  uint8_t* Q =
+      reinterpret_cast<uint8_t*>(S) + align256(sizeof(float) * blocks * static_cast<size_t>(a->R_cap));
+  a->A = Q;
+  a->As = S;
+  return launch_f8_quantize(rows, a->R_cap, width, a->offsets, a->E, nullptr, 1, a->R_cap, Q, S,
+                            a->status, dev.sm_count, stream);
+}
+
+gg_status gg_f8_grouped_fwd(const gg_bf16* A, const uint8_t* Wq, const float* Ws,
+                            const int32_t* offsets, int E, int R_cap, int K, int N,
+                            gg_epilogue epi, gg_bf16* C, gg_bf16* H1_save,
+                            const float* prob_of_row, void* ws, size_t ws_bytes,
+                            gg_stream_t stream) {
+  gg_status s = f8_gemm_checks(A, Wq, Ws, offsets, E, R_cap, K, N, N, prob_of_row, C);
+  if (s != GG_OK) return s;
+  if ((s = fwd_epilogue_checks(epi, N, H1_save, prob_of_row)) != GG_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, gg_f8_workspace_size(R_cap, K))) != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  if (R_cap == 0) return GG_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  F8GemmArgs a =
+      f8_args(false, nullptr, nullptr, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws);
+  a.H1_save = H1_save;
+  if (f8_rows_to_ws(A, K, &a, ws, dev, st) != cudaSuccess) return GG_ERR_CUDA;
+  return from_cuda(launch_f8_gemm(a, dev, st));
+}
+
+gg_status gg_f8_grouped_dgrad(const gg_bf16* dC, const uint8_t* Wq, const float* Ws,
+                              const int32_t* offsets, int E, int R_cap, int K, int N,
+                              gg_epilogue epi, const gg_bf16* H1, const float* prob_of_row,
+                              gg_bf16* dA, float* rowdot, void* ws, size_t ws_bytes,
+                              gg_stream_t stream) {
+  gg_status s = f8_gemm_checks(dC, Wq, Ws, offsets, E, R_cap, K, N, K, prob_of_row, dA);
+  if (s != GG_OK) return s;
+  if ((s = dgrad_epilogue_checks(epi, H1, rowdot)) != GG_OK) return s;
+  // the plain gradient has no place for a scale of its rows
+  if (epi == GG_EPI_NONE && prob_of_row != nullptr) return GG_ERR_INVALID_ARG;
+  if ((s = check_ws(ws, ws_bytes, gg_f8_workspace_size(R_cap, N))) != GG_OK) return s;
+  DeviceInfo dev;
+  if ((s = device_ok(&dev)) != GG_OK) return s;
+  if (R_cap == 0) return GG_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  F8GemmArgs a =
+      f8_args(true, nullptr, nullptr, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, dA, ws);
+  a.H1 = H1;
+  a.rowdot = rowdot;
+  if (f8_rows_to_ws(dC, N, &a, ws, dev, st) != cudaSuccess) return GG_ERR_CUDA;
+  return from_cuda(launch_f8_gemm(a, dev, st));
+}
+
 gg_status gg_adamw_step(const gg_adamw_tensor* tensors, int n, const gg_adamw_options* options,
                         gg_stream_t stream) {
   if (n < 0 || options == nullptr || (n > 0 && tensors == nullptr)) return GG_ERR_INVALID_ARG;

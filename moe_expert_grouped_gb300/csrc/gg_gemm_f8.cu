@@ -1,0 +1,749 @@
+// gg_gemm_f8.cu — grouped linear layers on E4M3 codes with an fp32 scale for
+// every 128 columns of a token's row and every 128 x 128 block of a weight, on
+// sm_103a; forward and input gradient on the same codes:
+//   C[r][n]  = sum_b s[b][r] t[e][n / 128][b] sum_{k in block b} q[r][k] w[e][n][k]
+//   dA[r][c] = sum_b s[b][r] t[e][b][c / 128] sum_{n in block b} d[r][n] w[e][n][c]
+// with the gated activations, and their gradients, fused.
+//
+// Scales change every 128 of the reduction, so the tensor cores sum 128 codes
+// (four MMAs) into one of two TMEM buffers, and eight warps add each buffer,
+// scaled, to fp32 sums in registers while the other one is filled. Products of
+// two E4M3 codes are exact in fp32.
+//
+// The weights are the tensor core's A operand (M = 256 channels per pair of
+// CTAs), the tokens its B operand (N = up to 256 tokens, in steps of 32): an
+// expert's ragged token count costs what it has, and the weight's scale is one
+// number per TMEM lane quarter, the tokens' scales one per column. For the
+// input gradient the weights are read as they lie, reduction outermost
+// ("MN-major"): one set of codes serves both directions.
+//
+// One CTA per SM in clusters of two (one tcgen05 MMA pair, 384 threads per
+// CTA, warp-specialised):
+//   warp 0      TMA producer: per step of 128 its 128 channels of the weight
+//               (gated forward: 64 gate rows and the matching 64 up rows) and
+//               half the tokens, 128-byte swizzle;
+//   warp 1      allocates TMEM; in the even CTA one lane issues
+//               tcgen05.mma.cta_group::2.kind::f8f6f4 (M = 256, K = 32);
+//   warp 2      finds the work items ahead of the others;
+//   warp 3      writes each step's scales, token times weight block, one row
+//               per half of the CTA's channels, into a ring;
+//   warps 4-11  sums and epilogue: one TMEM lane = one channel, one column =
+//               one token; two groups of four take half the columns each.
+// The epilogue turns chunks of 32 tokens x 32 channels in shared memory, so
+// that a lane has eight neighbouring channels of a token: 16-byte stores, and
+// gate and up values side by side.
+//
+// Every wait is bounded (gg_ptx.cuh); a wait that runs out records
+// GG_ERR_DEVICE_TIMEOUT, raises a CTA-wide abort flag, and the CTA drains
+// what is in flight, frees TMEM and exits after a final cluster barrier.
+
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "gg_f8.cuh"
+#include "gg_internal.h"
+#include "gg_launch.cuh"
+#include "gg_ptx.cuh"
+
+namespace gg {
+namespace {
+
+enum F8Mode : int { kFwd = 0, kFwdGated = 1, kGrad = 2, kGradGated = 3 };
+
+constexpr int BM = 128;       // channels per CTA
+constexpr int BN = 256;       // most tokens per work item
+constexpr int BK = kF8Block;  // codes per step
+constexpr int kStages = 5;
+constexpr int kScales = 4;    // steps of scales ahead
+constexpr int kItems = 4;     // work items found ahead
+constexpr int kItemWarp = 2, kFirstSum = 4;
+constexpr int kSumWarps = 8;
+constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
+constexpr int kMostChunks = BN / 32 / 2;  // of a summing warp
+constexpr uint16_t kPairMask = 0x3;
+constexpr uint32_t A_BYTES = BM * BK;
+constexpr uint32_t STAGE_BYTES = A_BYTES + BN / 2 * BK;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int kBoxes = 3;     // heights of token boxes: 64, 32 and 16 rows
+// Registers per thread of the two roles: the launch has 168 for each of 384
+// threads, and 56 + 2 * 216 is less than three times that.
+constexpr int kFewRegs = 56, kManyRegs = 216;
+static_assert(128 * (kFewRegs + 2 * kManyRegs) <= kThreads * 168, "register split");
+
+// A work item: expert, block of channels, its tokens (first row, number; rows
+// < 0: there are no more items), in `cols` columns, a multiple of 32.
+struct alignas(16) Item {
+  int e, nt, row0, rows;
+  int cols;
+  int pad_[3];
+};
+
+struct SmemTail {
+  Item item[kItems];
+  uint64_t item_full[kItems];
+  uint64_t item_empty[kItems];
+  uint64_t full[kStages];    // even CTA: both CTAs' loads have landed
+  uint64_t empty[kStages];
+  uint64_t scale_full[kScales];
+  uint64_t scale_empty[kScales];
+  uint64_t tfull[2];
+  uint64_t tempty[2];        // even CTA
+  uint64_t pair[2][2];       // per group: warps of gate rows and of the matching up rows
+  uint64_t group[2];         // the four warps of a group
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int total_tiles;
+  float dots[4][BN];         // row sums of each lane quadrant's 32 channels
+  int tiles_before[kMaxExperts + 1];
+  int row_start[kMaxExperts + 1];
+};
+
+constexpr uint32_t kScaleAt = kStages * STAGE_BYTES;
+constexpr uint32_t kScaleBytes = 2 * BN * 4;       // a step's: [half of the channels][token]
+constexpr uint32_t kStagingAt = kScaleAt + kScales * kScaleBytes;
+constexpr uint32_t kWarpStaging = 32 * 32 * 4;
+constexpr uint32_t kTailAt = kStagingAt + kSumWarps * kWarpStaging;
+constexpr size_t kSmemBytes = 1024 + kTailAt + sizeof(SmemTail);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+static_assert(kTailAt % 16 == 0 && kScaleAt % 16 == 0, "16-byte reads");
+
+struct F8Params {
+  const int32_t* offsets;
+  int E, R_cap;
+  int red;             // length of the reduction
+  int width;           // channels of an output half: N, F, K or F
+  int F;               // gated: channels from gate to up
+  int NT;              // blocks of channels
+  const float* S;      // [ceil(red / 128)][R_cap]
+  const float* T;      // weight scales of an expert: [.. channel block .. reduction block ..]
+  int t_expert, t_chan, t_red;  // their strides
+  const float* row_scale;
+  float alpha;
+  gg_bf16* C;
+  gg_bf16* H1_save;    // gated forward, or null
+  const gg_bf16* H1;   // gated gradient
+  float* rowdot;       // gated gradient, or null
+  int rowdot_stride;
+  int32_t* status;
+};
+
+__device__ __forceinline__ int token_blocks(int rows) { return (rows + BN - 1) / BN; }
+
+__device__ __forceinline__ Item item_of(int tile, const F8Params& p, const SmemTail& st) {
+  Item it;
+  int lo = 0, hi = p.E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (st.tiles_before[mid] <= tile)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  it.e = lo;
+  const int first = st.row_start[lo];
+  const int rows = st.row_start[lo + 1] - first;
+  const int blocks = token_blocks(rows);
+  const int local = tile - st.tiles_before[lo];
+  it.nt = local / blocks;
+  const int tb = local - it.nt * blocks;
+  const int each = ((rows + blocks - 1) / blocks + 31) / 32 * 32;  // as even as 32s allow
+  it.row0 = first + tb * each;
+  it.rows = min(each, rows - tb * each);  // each <= BN: no block is empty
+  it.cols = (it.rows + 31) & ~31;
+  return it;
+}
+
+// The reader's side of the item ring (a whole warp or one thread; `arriver`
+// reports the slot free, once per reader). False: no more items.
+struct ItemReader {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ bool next(SmemTail& st, Item& it, bool warp, bool arriver,
+                                       volatile int* abort_flag, int32_t* status) {
+    if (!mbar_wait_bounded(smem_u32(&st.item_full[slot]), phase, abort_flag, status)) return false;
+    it = st.item[slot];
+    if (warp) __syncwarp();
+    if (arriver) mbar_arrive(smem_u32(&st.item_empty[slot]));
+    if (++slot == kItems) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    return it.rows >= 0;
+  }
+};
+
+// E4M3 operands (format fields 0), fp32 sums, M = 256, N = n; the weights
+// MN-major for the input gradient.
+__device__ __forceinline__ uint32_t idesc_f8(int n, bool a_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((static_cast<uint32_t>(n) >> 3) << 17) |
+         ((static_cast<uint32_t>(2 * BM) >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+struct TokenMaps {
+  CUtensorMap box[kBoxes];
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ CUtensorMap mapW,
+               const F8Params p) {
+  constexpr bool kGated = MODE == kFwdGated;
+  constexpr bool kMN = MODE == kGrad || MODE == kGradGated;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sbase = raw_addr + pad;
+  SmemTail& st = *reinterpret_cast<SmemTail*>(smem + kTailAt);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int E = p.E;
+  const uint32_t crank = cluster_ctarank();
+  const bool leader = crank == 0;
+
+  if (warp == 0) {
+    bool bad = false;
+    int carry = 0;
+    for (int base = 0; base < E; base += 32) {
+      const int e = base + lane;
+      int tiles = 0;
+      if (e < E) {
+        const int o0 = p.offsets[e];
+        const int o1 = p.offsets[e + 1];
+        if (o1 < o0 || o0 < 0 || o1 > p.R_cap) bad = true;
+        tiles = o1 > o0 ? token_blocks(o1 - o0) * p.NT : 0;
+        st.row_start[e] = o0;
+      }
+      int incl = tiles;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int n = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += n;
+      }
+      if (e < E) st.tiles_before[e] = carry + incl - tiles;
+      carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    if (lane == 0) {
+      const int o_last = p.offsets[E];
+      if (p.offsets[0] != 0 || o_last > p.R_cap || o_last < 0) bad = true;
+      st.row_start[E] = o_last;
+      st.tiles_before[E] = carry;
+    }
+    bad = __any_sync(0xFFFFFFFFu, bad);
+    if (lane == 0) {
+      st.total_tiles = bad ? 0 : carry;
+      st.abort_flag = 0;
+      if (bad && blockIdx.x == 0) set_status(p.status, GG_ERR_DEVICE_BAD_OFFSETS);
+      for (int s = 0; s < kStages; ++s) {
+        mbar_init(smem_u32(&st.full[s]), 1);
+        mbar_init(smem_u32(&st.empty[s]), 1);
+      }
+      for (int s = 0; s < kScales; ++s) {
+        mbar_init(smem_u32(&st.scale_full[s]), 1);
+        mbar_init(smem_u32(&st.scale_empty[s]), kSumWarps);
+      }
+      for (int a = 0; a < 2; ++a) {
+        mbar_init(smem_u32(&st.tfull[a]), 1);
+        mbar_init(smem_u32(&st.tempty[a]), 2 * kSumWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&st.pair[a][i]), 2);
+        mbar_init(smem_u32(&st.group[a]), 4);
+      }
+      for (int i = 0; i < kItems; ++i) {
+        mbar_init(smem_u32(&st.item_full[i]), 1);
+        // readers: producer, scale and summing warps, and the even CTA's issuer
+        mbar_init(smem_u32(&st.item_empty[i]), 2 + kSumWarps + (leader ? 1 : 0));
+      }
+      mbar_init(smem_u32(&st.mma_done), 1);
+      mbar_fence_init();
+      fence_proxy_async();
+    }
+  } else if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&st.tmem_base), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();  // both CTAs' barriers exist before anything can arrive on them
+
+  const int first = static_cast<int>(blockIdx.x) / 2;
+  const int step = static_cast<int>(gridDim.x) / 2;
+  const uint32_t tmem_base = st.tmem_base;
+  const int total = st.total_tiles;
+  const int KB = (p.red + BK - 1) / BK;
+  volatile int* abort_flag = &st.abort_flag;
+
+  if (warp < kFirstSum) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if (warp == 0) {
+      if (lane == 0) {
+        // -------------------------------------------------- TMA producer
+        for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&mapT.box[i]);
+        tma_prefetch_desc(&mapW);
+        const int h = static_cast<int>(crank);
+        int stage = 0;
+        uint32_t phase = 0, used = 0, last_phase = 0;
+        bool ok = true;
+        Item it;
+        ItemReader items;
+        while (ok && items.next(st, it, false, true, abort_flag, p.status)) {
+          const int n0 = kGated ? it.nt * BM + h * (BM / 2) : it.nt * 2 * BM + h * BM;
+          const int half = it.cols / 2;  // this CTA's tokens, a multiple of 16
+          const int r0 = it.row0 + h * half;
+          for (int kb = 0; kb < KB; ++kb) {
+            if (!mbar_wait_bounded(smem_u32(&st.empty[stage]), phase ^ 1u, abort_flag,
+                                   p.status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t fb = mapa_shared(smem_u32(&st.full[stage]), 0);
+            const uint32_t sa = sbase + stage * STAGE_BYTES;
+            const int c = kb * BK;
+            // the even CTA's barrier counts the bytes of both CTAs' loads
+            if (leader)
+              mbar_arrive_expect_tx(smem_u32(&st.full[stage]), 2 * (A_BYTES + half * BK));
+            if (kMN) {
+              tma_load_3d_pair(sa, &mapW, fb, n0, c, it.e);
+            } else {
+              tma_load_3d_pair(sa, &mapW, fb, c, n0, it.e);
+              tma_load_3d_pair(sa + A_BYTES / 2, &mapW, fb, c, kGated ? p.F + n0 : n0 + BM / 2,
+                               it.e);
+            }
+            int i = 0;
+            for (; i + 64 <= half; i += 64)
+              tma_load_2d_pair(sa + A_BYTES + i * BK, &mapT.box[0], fb, c, r0 + i);
+            if (i + 32 <= half) {
+              tma_load_2d_pair(sa + A_BYTES + i * BK, &mapT.box[1], fb, c, r0 + i);
+              i += 32;
+            }
+            if (i < half) tma_load_2d_pair(sa + A_BYTES + i * BK, &mapT.box[2], fb, c, r0 + i);
+            used |= 1u << stage;
+            last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        // Before the CTA may exit, the pair's MMAs must have consumed (and so
+        // the loads must have landed in) every stage this producer filled.
+        for (int s = 0; s < kStages; ++s)
+          if (used & (1u << s)) {
+            if (leader)
+              (void)mbar_wait_bounded(smem_u32(&st.full[s]), (last_phase >> s) & 1u, nullptr,
+                                      p.status);
+            (void)mbar_wait_bounded(smem_u32(&st.empty[s]), (last_phase >> s) & 1u, nullptr,
+                                    p.status);
+          }
+      }
+    } else if (warp == 1) {
+      if (leader) {
+        // ------------------------------------------ MMA issuer (even CTA)
+        // The whole warp runs the loop and one lane issues. All of TMEM is
+        // ours, so it starts at column 0.
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, buf_phase = 0;
+        bool ok = tmem_base == 0;
+        // one group of 128 channels: the MN-major leading offset is not used
+        const uint64_t adesc0 = make_sdesc(sbase, kMN ? A_BYTES : 16, 1024);
+        const uint64_t bdesc0 = make_sdesc(sbase + A_BYTES, 16, 1024);
+        constexpr uint64_t kAStep = (kMN ? 32 * BM : 32) >> 4;
+        Item it;
+        ItemReader items;
+        while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
+          // a reduction, for its result is in a uniform register
+          const uint32_t idesc = idesc_f8(__reduce_max_sync(0xFFFFFFFFu, it.cols), kMN);
+          for (int kb = 0; kb < KB; ++kb) {
+            if (!mbar_wait_bounded(smem_u32(&st.tempty[buf]), buf_phase ^ 1u, abort_flag,
+                                   p.status) ||
+                !mbar_wait_bounded(smem_u32(&st.full[stage]), phase, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t at = stage * (STAGE_BYTES >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < BK / 32; ++kk)
+                tc_mma_f8_pair(buf * BN, adesc0 + at + kk * kAStep, bdesc0 + at + kk * 2, idesc,
+                               kk != 0 ? 1u : 0u);
+              tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
+              tc_commit_pair_mc(smem_u32(&st.tfull[buf]), kPairMask);
+            }
+            __syncwarp();
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            buf ^= 1;
+            if (buf == 0) buf_phase ^= 1u;
+          }
+        }
+        // All MMAs of the pair must retire before TMEM is freed.
+        if (elect_one()) {
+          tc_commit_pair(smem_u32(&st.mma_done));
+          (void)mbar_wait_bounded(smem_u32(&st.mma_done), 0, nullptr, p.status);
+        }
+        __syncwarp();
+      }
+    } else if (warp == kItemWarp) {
+      if (lane == 0) {
+        // ---------------------------------------------------- work items
+        int slot = 0;
+        uint32_t phase = 0;
+        for (int i = first;; i += step) {
+          Item it{0, 0, 0, -1, 0};
+          if (i < total) it = item_of(i, p, st);
+          if (!mbar_wait_bounded(smem_u32(&st.item_empty[slot]), phase ^ 1u, abort_flag, p.status))
+            break;
+          st.item[slot] = it;
+          mbar_arrive(smem_u32(&st.item_full[slot]));
+          if (i >= total) break;
+          if (++slot == kItems) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ scales
+      // Loaded two steps ahead of their use.
+      struct Ahead {
+        float s[BN / 32];
+        float t0, t1;
+      };
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      Item it;
+      ItemReader items;
+      while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
+        const int h = static_cast<int>(crank);
+        const int n0 = kGated ? it.nt * BM + h * (BM / 2) : it.nt * 2 * BM + h * BM;
+        const int n1 = kGated ? p.F + n0 : n0 + BM / 2;
+        const int most = kGated ? 2 * p.F : p.width;
+        const float* t = p.T + static_cast<long long>(it.e) * p.t_expert;
+        // channels that do not exist have a tile of zeros: any scale will do
+        const float* t0 = t + static_cast<long long>(min(n0, most - 1) / kF8Block) * p.t_chan;
+        const float* t1 = t + static_cast<long long>(min(n1, most - 1) / kF8Block) * p.t_chan;
+        const auto load = [&](int kb, Ahead& a) {
+          if (kb >= KB) return;
+          const float* s = p.S + static_cast<long long>(kb) * p.R_cap + it.row0;
+#pragma unroll
+          for (int j = 0; j < BN / 32; ++j) {
+            const int i = 32 * j + lane;
+            a.s[j] = i < it.rows ? __ldg(s + i) : 0.0f;
+          }
+          a.t0 = __ldg(t0 + static_cast<long long>(kb) * p.t_red);
+          a.t1 = __ldg(t1 + static_cast<long long>(kb) * p.t_red);
+        };
+        const auto put = [&](int kb, const Ahead& a) {
+          if (!ok || kb >= KB) return;
+          if (!mbar_wait_bounded(smem_u32(&st.scale_empty[slot]), phase ^ 1u, abort_flag,
+                                 p.status)) {
+            ok = false;
+            return;
+          }
+          float* to = reinterpret_cast<float*>(smem + kScaleAt + slot * kScaleBytes);
+#pragma unroll
+          for (int j = 0; j < BN / 32; ++j) {
+            if (32 * j >= it.cols) break;
+            to[32 * j + lane] = a.s[j] * a.t0;
+            to[BN + 32 * j + lane] = a.s[j] * a.t1;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&st.scale_full[slot]));
+          if (++slot == kScales) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        };
+        Ahead a, b;
+        load(0, a);
+        load(1, b);
+        for (int kb = 0; kb < KB && ok; kb += 2) {
+          put(kb, a);
+          load(kb + 2, a);
+          put(kb + 1, b);
+          load(kb + 3, b);
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+    // ---------------------------------------------------- sums and epilogue
+    const int q = warp & 3;
+    const int group = (warp - kFirstSum) >> 2;
+    const int half = q >> 1;  // of the CTA's channels
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    float* stg = reinterpret_cast<float*>(smem + kStagingAt + (warp - kFirstSum) * kWarpStaging);
+    const float* other = reinterpret_cast<const float*>(
+        smem + kStagingAt + ((warp - kFirstSum) ^ 2) * kWarpStaging);
+    const uint32_t tempty = mapa_shared(smem_u32(&st.tempty[0]), 0);
+    // What these warps wait for each other at: a barrier that a warp whose wait
+    // ran out does not leave the others in.
+    const uint32_t meet = smem_u32(kGated ? &st.pair[group][q & 1] : &st.group[group]);
+    uint32_t meet_phase = 0;
+    const auto met = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(meet);
+      const bool in_time = mbar_wait_bounded(meet, meet_phase, abort_flag, p.status);
+      meet_phase ^= 1u;
+      return in_time;
+    };
+    int slot = 0, buf = 0;
+    uint32_t slot_phase = 0, buf_phase = 0;
+    bool ok = true;
+    Item it;
+    ItemReader items;
+    while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
+      const int chunks = it.cols / 32;
+      const int mine0 = group == 0 ? 0 : (chunks + 1) / 2;
+      const int mine = group == 0 ? (chunks + 1) / 2 : chunks / 2;
+      float acc[kMostChunks][32];
+#pragma unroll
+      for (int c = 0; c < kMostChunks; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!mbar_wait_bounded(smem_u32(&st.scale_full[slot]), slot_phase, abort_flag, p.status) ||
+            !mbar_wait_bounded(smem_u32(&st.tfull[buf]), buf_phase, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float4* f =
+            reinterpret_cast<const float4*>(smem + kScaleAt + slot * kScaleBytes) +
+            (half * BN + 32 * mine0) / 4;
+#pragma unroll
+        for (int c = 0; c < kMostChunks; ++c) {
+          if (c < mine) {
+            float v[32];
+            tmem_ld32(lanes + buf * BN + 32 * (mine0 + c), v);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 s = f[8 * c + i / 4];
+              float2* to = reinterpret_cast<float2*>(&acc[c][i]);
+              to[0] = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(s.x, s.y), to[0]);
+              to[1] = __ffma2_rn(make_float2(v[i + 2], v[i + 3]), make_float2(s.z, s.w), to[1]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster_relaxed(tempty + 8 * buf);
+          mbar_arrive(smem_u32(&st.scale_empty[slot]));
+        }
+        if (++slot == kScales) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
+        buf ^= 1;
+        if (buf == 0) buf_phase ^= 1u;
+      }
+      if (!ok) break;
+      // Chunk by chunk through the warp's staging buffer, token i's 16-byte
+      // piece s at s ^ (i & 7): a lane then has channels 8 (lane % 4) .. + 7 of
+      // tokens 8 j + lane / 4.
+      const int ch0 = kGated ? it.nt * BM + static_cast<int>(crank) * (BM / 2) + (q & 1) * 32
+                             : it.nt * 2 * BM + static_cast<int>(crank) * BM + q * 32;
+      const bool exists = ch0 < p.width;  // 32 channels exist together: multiples of 64
+      const int ch = ch0 + 8 * (lane & 3);
+      const auto read8 = [&](const float* from, int i, float(&x)[8]) {
+        const float4* row = reinterpret_cast<const float4*>(from + 32 * i);
+        const int s = 2 * (lane & 3);
+        const float4 a = row[s ^ (i & 7)], b = row[(s + 1) ^ (i & 7)];
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+      };
+      const auto pack8 = [](const float(&x)[8]) {
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                          pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+      };
+#pragma unroll
+      for (int c = 0; c < kMostChunks; ++c) {
+        if (c >= mine || !ok) continue;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          stg[32 * i + (((lane >> 2) ^ (i & 7)) << 2) + (lane & 3)] = acc[c][i];
+        const int t0 = 32 * (mine0 + c);
+        if constexpr (kGated) {
+          // gate and up rows' warps (two lane quadrants apart) take half the
+          // chunk's tokens each, from both buffers
+          if (!(ok = met())) continue;
+          const float* gates = q < 2 ? stg : other;
+          const float* ups = q < 2 ? other : stg;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int i = 16 * half + 8 * j + (lane >> 2);
+            if (exists && t0 + i < it.rows) {
+              float g[8], u[8], v[8];
+              read8(gates, i, g);
+              read8(ups, i, u);
+              const long long r = static_cast<long long>(it.row0) + t0 + i;
+              const bool scaled = p.row_scale != nullptr;
+              const float w = scaled ? __ldg(p.row_scale + r) : 1.0f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = glu_mul(g[k], u[k], p.alpha, scaled, w);
+              *reinterpret_cast<uint4*>(p.C + r * p.width + ch) = pack8(v);
+              if (p.H1_save != nullptr) {
+                gg_bf16* h1 = p.H1_save + r * (2LL * p.F) + ch;
+                *reinterpret_cast<uint4*>(h1) = pack8(g);
+                *reinterpret_cast<uint4*>(h1 + p.F) = pack8(u);
+              }
+            }
+          }
+          ok = met();
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = 8 * j + (lane >> 2);
+            const bool there = exists && t0 + i < it.rows;
+            const long long r = static_cast<long long>(it.row0) + t0 + i;
+            float v[8];
+            read8(stg, i, v);
+            if constexpr (MODE == kGradGated) {
+              float dot = 0.0f;
+              if (there) {
+                const gg_bf16* h1 = p.H1 + r * (2LL * p.F) + ch;
+                const uint4 gw = __ldg(reinterpret_cast<const uint4*>(h1));
+                const uint4 uw = __ldg(reinterpret_cast<const uint4*>(h1 + p.F));
+                const float w = p.row_scale != nullptr ? __ldg(p.row_scale + r) : 1.0f;
+                const uint32_t gx[4] = {gw.x, gw.y, gw.z, gw.w};
+                const uint32_t ux[4] = {uw.x, uw.y, uw.z, uw.w};
+                float dg[8], du[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float g = k & 1 ? bf16_hi(gx[k / 2]) : bf16_lo(gx[k / 2]);
+                  const float u = k & 1 ? bf16_hi(ux[k / 2]) : bf16_lo(ux[k / 2]);
+                  const float ag = p.alpha * g;
+                  const float s = __fdividef(1.0f, 1.0f + __expf(-ag));
+                  const float gs = g * s;
+                  const float d = v[k] * w;
+                  dg[k] = (d * u) * (s * fmaf(ag, 1.0f - s, 1.0f));
+                  du[k] = d * gs;
+                  dot = fmaf(v[k], gs * u, dot);
+                }
+                gg_bf16* to = p.C + r * (2LL * p.F) + ch;
+                *reinterpret_cast<uint4*>(to) = pack8(dg);
+                *reinterpret_cast<uint4*>(to + p.F) = pack8(du);
+              }
+              dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
+              dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
+              if ((lane & 3) == 0) st.dots[q][t0 + i] = dot;
+            } else {
+              if (there) *reinterpret_cast<uint4*>(p.C + r * p.width + ch) = pack8(v);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if constexpr (MODE == kGradGated) {
+        if (p.rowdot != nullptr) {
+          // the CTA's 128 channels are one block of the row sums
+          if (!(ok = met())) break;
+          const int i = 32 * mine0 + 32 * q + lane;
+          if (q < mine && i < it.rows) {
+            const float sum = (st.dots[0][i] + st.dots[1][i]) + (st.dots[2][i] + st.dots[3][i]);
+            p.rowdot[(static_cast<long long>(it.row0) + i) * p.rowdot_stride + 2 * it.nt +
+                     static_cast<int>(crank)] = sum;
+          }
+          ok = met();
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+  cluster_sync();
+}
+
+template <int MODE>
+cudaError_t launch_f8_t(const TokenMaps& mt, const CUtensorMap& mw, const F8Params& p,
+                        const DeviceInfo& dev, cudaStream_t stream) {
+  static std::atomic<int> resident[kMaxDevices];
+  // no more clusters than there can be work items
+  const long long items =
+      (static_cast<long long>(p.R_cap) / BN + (p.R_cap < p.E ? p.R_cap : p.E)) * p.NT;
+  const int most = static_cast<int>(items < 1 ? 1 : (items < 0x7FFFFFFF ? items : 0x7FFFFFFF));
+  return launch_pairs(f8_gemm_kernel<MODE>, resident, kThreads, kSmemBytes, most, dev, stream, mt,
+                      mw, p);
+}
+
+}  // namespace
+
+cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  const int red = a.grad ? a.N : a.K;
+  const int out = a.grad ? a.K : a.N;
+  TokenMaps mt;
+  CUtensorMap mw;
+  const cuuint64_t td[2] = {static_cast<cuuint64_t>(red), static_cast<cuuint64_t>(a.R_cap)};
+  const cuuint64_t ts[1] = {static_cast<cuuint64_t>(red)};
+  for (int i = 0; i < kBoxes; ++i) {
+    const cuuint32_t tbox[2] = {BK, 64u >> i};
+    if (!encode_map(&mt.box[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, 2, td, ts, tbox,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  const cuuint64_t wd[3] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.N),
+                            static_cast<cuuint64_t>(a.E)};
+  const cuuint64_t ws[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.K) * a.N};
+  // forward: 64 channels x 128 codes; gradient: 128 rows of 128 channels
+  const cuuint32_t wbox[3] = {BK, a.grad ? static_cast<cuuint32_t>(BK) : BM / 2u, 1};
+  if (!encode_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, wd, ws, wbox,
+                  CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const int NB = (a.N + kF8Block - 1) / kF8Block, KB = (a.K + kF8Block - 1) / kF8Block;
+  F8Params p{};
+  p.offsets = a.offsets;
+  p.E = a.E;
+  p.R_cap = a.R_cap;
+  p.red = red;
+  p.S = a.As;
+  p.T = a.Bs;
+  p.t_expert = NB * KB;
+  p.t_chan = a.grad ? 1 : KB;
+  p.t_red = a.grad ? KB : 1;
+  p.row_scale = a.row_scale;
+  p.alpha = a.alpha;
+  p.C = a.C;
+  p.H1_save = a.H1_save;
+  p.H1 = a.H1;
+  p.rowdot = a.rowdot;
+  p.status = a.status;
+  const bool gated = a.alpha != 0.0f;
+  if (!a.grad && gated) {
+    p.F = a.N / 2;
+    p.width = p.F;
+    p.NT = (p.F + BM - 1) / BM;
+    return launch_f8_t<kFwdGated>(mt, mw, p, dev, stream);
+  }
+  p.width = out;
+  p.NT = (out + 2 * BM - 1) / (2 * BM);
+  if (!a.grad) return launch_f8_t<kFwd>(mt, mw, p, dev, stream);
+  if (!gated) return launch_f8_t<kGrad>(mt, mw, p, dev, stream);
+  p.F = a.K;
+  p.rowdot_stride = (2 * p.NT + 7) / 8 * 8;
+  return launch_f8_t<kGradGated>(mt, mw, p, dev, stream);
+}
+
+}  // namespace gg

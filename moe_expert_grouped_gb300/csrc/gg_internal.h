@@ -262,6 +262,34 @@ bool q8_rows_fits(int R_cap, int E);
 cudaError_t launch_q8_rows(const Q8GemmArgs& a, bool early, const DeviceInfo& dev,
                            cudaStream_t stream);
 
+// ------------------------------------------------------------------ gg_f8_quant.cu
+// Codes Q [..][K] and scales S [ceil(K / 128)][R_cap] of `rows` source rows; rows, offsets and
+// row_of_slot as launch_q8_quantize.
+cudaError_t launch_f8_quantize(const gg_bf16* src, long long rows, int K, const int32_t* offsets,
+                               int E, const int32_t* row_of_slot, int k, int R_cap, uint8_t* Q,
+                               float* S, int32_t* status, int sm_count, cudaStream_t stream);
+cudaError_t launch_f8_weight(const gg_bf16* W, int E, int N, int K, uint8_t* Wq, float* Ws,
+                             cudaStream_t stream);
+
+// ------------------------------------------------------------------ gg_gemm_f8.cu
+struct F8GemmArgs {
+  bool grad;               // dA = dC W instead of C = A W^T
+  const uint8_t* A;        // [R_cap][K], grad: dC's [R_cap][N]
+  const float* As;         // [blocks of the reduction][R_cap]
+  const uint8_t* B;        // [E][N][K]
+  const float* Bs;         // [E][ceil(N / 128)][ceil(K / 128)]
+  const int32_t* offsets;
+  int E, R_cap, K, N;
+  float alpha;             // of the gated activation, 0: none
+  const float* row_scale;  // gated: [R_cap] or null
+  gg_bf16* C;
+  gg_bf16* H1_save;        // gated forward: [R_cap][N] or null
+  const gg_bf16* H1;       // gated grad: [R_cap][2K]
+  float* rowdot;           // gated grad: partial sums as GemmArgs, or null
+  int32_t* status;
+};
+cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
 // ------------------------------------------------------------------ gg_route.cu
 // Blocks that accumulate the router's batch statistics (two per SM of a
 // 152-SM device): rows of the scratch below.

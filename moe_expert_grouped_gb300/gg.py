@@ -83,6 +83,14 @@ SIGNATURES = [
     ("gg_grouped_wgrad", _I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
     ("gg_moe_mlp_wgrad", _I,
      [_I, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    ("gg_f8_workspace_size", _Z, [_I, _I]),
+    ("gg_f8_prepare_weight", _I, [_P, _I, _I, _I, _P, _P, _P]),
+    ("gg_f8_quantize_rows", _I, [_P, _I, _I, _P, _I, _I, _P, _P, _P, _Z, _P]),
+    ("gg_f8_grouped_gemm", _I,
+     [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
+    ("gg_f8_grouped_fwd", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
+    ("gg_f8_grouped_dgrad", _I,
+     [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P]),
     ("gg_adamw_step", _I, [_P, _I, _P, _P]),
     ("gg_grad_norm_workspace_size", _Z, [_I]),
     ("gg_grad_norm", _I, [_P, _I, _I, _F, _P, _P, _Z, _P]),
@@ -857,6 +865,161 @@ def grouped_wgrad(dC, A, offsets, base=None, dB=None, out_dtype=torch.bfloat16, 
                                 _ptr(base), _ptr(dB), _ptr(ws), ws.numel(), _stream(dC.device)),
            "gg_grouped_wgrad")
     return dB
+
+
+# ---------------------------------------------------------------- E4M3, scales per block of 128
+
+F8_BLOCK = 128  # columns, and rows of a weight, that share a scale
+
+
+def _blocks(n: int) -> int:
+    return -(-n // F8_BLOCK)
+
+
+def f8_workspace(R_cap: int, width: int, device) -> torch.Tensor:
+    """A zeroed workspace (status word first) for f8_grouped_fwd on up to R_cap x width rows A,
+    or f8_grouped_dgrad on rows dC."""
+    return torch.zeros(int(LIB.gg_f8_workspace_size(R_cap, width)), dtype=torch.uint8,
+                       device=device)
+
+
+def f8_prepare_weight(W, Wq=None, Ws=None):
+    """gg_f8_prepare_weight: (codes [E, N, K] float8_e4m3fn, scales [E, ceil(N / 128),
+    ceil(K / 128)] fp32) of W [E, N, K] BF16."""
+    E, N, K = W.shape
+    _need(W, torch.bfloat16, (E, N, K), "W")
+    if Wq is None:
+        Wq = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=W.device)
+    if Ws is None:
+        Ws = torch.empty((E, _blocks(N), _blocks(K)), dtype=torch.float32, device=W.device)
+    _need_f8_weight(Wq, Ws, (E, N, K), W.device)
+    with _guard(W.device):
+        _check(LIB.gg_f8_prepare_weight(_ptr(W), E, N, K, _ptr(Wq), _ptr(Ws), _stream(W.device)),
+               "gg_f8_prepare_weight")
+    return Wq, Ws
+
+
+def _on(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _need_f8_weight(Wq, Ws, shape, device) -> None:
+    E, N, K = shape
+    _need(Wq, torch.float8_e4m3fn, (E, N, K), "Wq")
+    _need(Ws, torch.float32, (E, _blocks(N), _blocks(K)), "Ws")
+    _on(device, Wq=Wq, Ws=Ws)
+
+
+def f8_quantize_rows(src, ws, row_of_slot=None, k: int = 1, R_cap=None, Q=None, S=None):
+    """gg_f8_quantize_rows: (codes [R_cap, K] float8_e4m3fn, scales [ceil(K / 128), R_cap] fp32)
+    of src [T, K]; with row_of_slot [T*k] each token's codes go to its k rows."""
+    T, K = src.shape
+    _need(src, torch.bfloat16, (T, K), "src")
+    if row_of_slot is not None:
+        _need(row_of_slot, torch.int32, (T * k,), "row_of_slot")
+    if R_cap is None:
+        R_cap = T if row_of_slot is None else T * k
+    dev = src.device
+    Q = torch.empty((R_cap, K), dtype=torch.float8_e4m3fn, device=dev) if Q is None else Q
+    S = torch.empty((_blocks(K), R_cap), dtype=torch.float32, device=dev) if S is None else S
+    _need(Q, torch.float8_e4m3fn, (R_cap, K), "Q")
+    _need(S, torch.float32, (_blocks(K), R_cap), "S")
+    _on(dev, ws=ws, row_of_slot=row_of_slot, Q=Q, S=S)
+    with _guard(dev):
+        _check(LIB.gg_f8_quantize_rows(_ptr(src), T, K, _ptr(row_of_slot), k, R_cap, _ptr(Q),
+                                       _ptr(S), _ptr(ws), ws.numel(), _stream(dev)),
+               "gg_f8_quantize_rows")
+    return Q, S
+
+
+def _f8_fwd_out(R_cap, Wq, Ws, offsets, epilogue, prob_of_row, C, H1_save, dev):
+    E, N, K = Wq.shape
+    _need_f8_weight(Wq, Ws, (E, N, K), dev)
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    if prob_of_row is not None:
+        _need(prob_of_row, torch.float32, (R_cap,), "prob_of_row")
+    if H1_save is not None:
+        _need(H1_save, torch.bfloat16, (R_cap, N), "H1_save")
+    shape = (R_cap, N // 2 if epilogue in _GATED_FWD else N)
+    if C is None:
+        C = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _need(C, torch.bfloat16, shape, "C")
+    _on(dev, offsets=offsets, prob_of_row=prob_of_row, H1_save=H1_save, C=C)
+    return C
+
+
+def f8_grouped_gemm(Aq, As, Wq, Ws, offsets, epilogue: int = GG_EPI_NONE, prob_of_row=None,
+                    C=None, H1_save=None, ws=None):
+    """gg_f8_grouped_gemm on codes Aq [R_cap, K] with scales As [ceil(K / 128), R_cap] and a
+    weight Wq [E, N, K], Ws [E, ceil(N / 128), ceil(K / 128)]; returns C ([R_cap, N] or, gated,
+    [R_cap, N/2]). H1_save [R_cap, N] receives a gated activation's input."""
+    R_cap = Aq.shape[0]
+    E, N, K = Wq.shape
+    dev = Aq.device
+    _need(Aq, torch.float8_e4m3fn, (R_cap, K), "Aq")
+    _need(As, torch.float32, (_blocks(K), R_cap), "As")
+    C = _f8_fwd_out(R_cap, Wq, Ws, offsets, epilogue, prob_of_row, C, H1_save, dev)
+    ws = workspace(0, 1, E, dev) if ws is None else ws
+    _on(dev, As=As, ws=ws)
+    with _guard(dev):
+        _check(LIB.gg_f8_grouped_gemm(_ptr(Aq), _ptr(As), _ptr(Wq), _ptr(Ws), _ptr(offsets), E,
+                                      R_cap, K, N, epilogue, _ptr(C), _ptr(H1_save),
+                                      _ptr(prob_of_row), _ptr(ws), ws.numel(), _stream(dev)),
+               "gg_f8_grouped_gemm")
+    return C
+
+
+def f8_grouped_fwd(A, Wq, Ws, offsets, epilogue: int = GG_EPI_NONE, prob_of_row=None, C=None,
+                   H1_save=None, ws=None):
+    """gg_f8_grouped_fwd: quantises the rows of A [R_cap, K] (BF16) and multiplies them with the
+    weight as f8_grouped_gemm; ws from f8_workspace(R_cap, K)."""
+    R_cap = A.shape[0]
+    E, N, K = Wq.shape
+    dev = A.device
+    _need(A, torch.bfloat16, (R_cap, K), "A")
+    C = _f8_fwd_out(R_cap, Wq, Ws, offsets, epilogue, prob_of_row, C, H1_save, dev)
+    ws = f8_workspace(R_cap, K, dev) if ws is None else ws
+    _on(dev, ws=ws)
+    with _guard(dev):
+        _check(LIB.gg_f8_grouped_fwd(_ptr(A), _ptr(Wq), _ptr(Ws), _ptr(offsets), E, R_cap, K, N,
+                                     epilogue, _ptr(C), _ptr(H1_save), _ptr(prob_of_row),
+                                     _ptr(ws), ws.numel(), _stream(dev)),
+               "gg_f8_grouped_fwd")
+    return C
+
+
+def f8_grouped_dgrad(dC, Wq, Ws, offsets, epilogue: int = GG_EPI_NONE, H1=None, prob_of_row=None,
+                     dA=None, rowdot=None, ws=None):
+    """gg_f8_grouped_dgrad: dA [R_cap, K] (gated: [R_cap, 2K], through the activation of H1
+    [R_cap, 2K]) from dC [R_cap, N] and the forward weight Wq [E, N, K], Ws; rowdot [R_cap,
+    rowdot_stride(K)] fp32 receives the partial sums of the probabilities' gradient; ws from
+    f8_workspace(R_cap, N)."""
+    R_cap = dC.shape[0]
+    E, N, K = Wq.shape
+    dev = dC.device
+    _need(dC, torch.bfloat16, (R_cap, N), "dC")
+    _need_f8_weight(Wq, Ws, (E, N, K), dev)
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    shape = (R_cap, 2 * K if epilogue in _GATED_BWD else K)
+    if H1 is not None:
+        _need(H1, torch.bfloat16, (R_cap, 2 * K), "H1")
+    if prob_of_row is not None:
+        _need(prob_of_row, torch.float32, (R_cap,), "prob_of_row")
+    if rowdot is not None:
+        _need(rowdot, torch.float32, (R_cap, rowdot_stride(K)), "rowdot")
+    if dA is None:
+        dA = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _need(dA, torch.bfloat16, shape, "dA")
+    ws = f8_workspace(R_cap, N, dev) if ws is None else ws
+    _on(dev, offsets=offsets, H1=H1, prob_of_row=prob_of_row, rowdot=rowdot, dA=dA, ws=ws)
+    with _guard(dev):
+        _check(LIB.gg_f8_grouped_dgrad(_ptr(dC), _ptr(Wq), _ptr(Ws), _ptr(offsets), E, R_cap, K,
+                                       N, epilogue, _ptr(H1), _ptr(prob_of_row), _ptr(dA),
+                                       _ptr(rowdot), _ptr(ws), ws.numel(), _stream(dev)),
+               "gg_f8_grouped_dgrad")
+    return dA
 
 
 # ---------------------------------------------------------------- optimizer step
