@@ -10,28 +10,35 @@
 // scaled, to fp32 sums in registers while the other one is filled. Products of
 // two E4M3 codes are exact in fp32.
 //
-// The weights are the tensor core's A operand (M = 256 channels per pair of
-// CTAs), the tokens its B operand (N = up to 256 tokens, in steps of 32): an
-// expert's ragged token count costs what it has, and the weight's scale is one
-// number per TMEM lane quarter, the tokens' scales one per column. For the
-// input gradient the weights are read as they lie, reduction outermost
+// A work item is a block of 256 channels (gated forward: 128, gate and up) and
+// up to 256 tokens of an expert, in one of two orientations:
+//   - more than 128 tokens: tokens are the MMA's rows (M = 256, 128 per CTA),
+//     channels its columns (N = 256). A TMEM lane is a token, so a step's scale
+//     is one number per thread and 64 columns, a gate value and its up value
+//     meet in one thread, and a thread has its row's channels together;
+//   - up to 128 tokens (an expert's last ones, or all it has): channels are the
+//     rows, tokens the columns, in steps of 32, so that a ragged count costs
+//     what it has. The tokens' scales then differ by column, and reading them
+//     from shared memory is what a step costs: with 256 tokens 750 ns of it
+//     where the MMAs take 290, which is why long blocks are not done this way.
+// Both find the same tiles in shared memory; the MMA's operands change places.
+// For the input gradient the weights are read as they lie, reduction outermost
 // ("MN-major"): one set of codes serves both directions.
 //
 // One CTA per SM in clusters of two (one tcgen05 MMA pair, 384 threads per
 // CTA, warp-specialised):
-//   warp 0      TMA producer: per step of 128 its 128 channels of the weight
-//               (gated forward: 64 gate rows and the matching 64 up rows) and
-//               half the tokens, 128-byte swizzle;
+//   warp 0      TMA producer: per step of 128 its half of the channels (gated
+//               forward: the even CTA gate rows, the odd one up rows, or, few
+//               tokens, 64 of each) and half the tokens, 128-byte swizzle;
 //   warp 1      allocates TMEM; in the even CTA one lane issues
 //               tcgen05.mma.cta_group::2.kind::f8f6f4 (M = 256, K = 32);
 //   warp 2      finds the work items ahead of the others;
-//   warp 3      writes each step's scales, token times weight block, one row
-//               per half of the CTA's channels, into a ring;
-//   warps 4-11  sums and epilogue: one TMEM lane = one channel, one column =
-//               one token; two groups of four take half the columns each.
-// The epilogue turns chunks of 32 tokens x 32 channels in shared memory, so
-// that a lane has eight neighbouring channels of a token: 16-byte stores, and
-// gate and up values side by side.
+//   warp 3      writes each step's scales, token times weight block, into a
+//               ring;
+//   warps 4-11  sums and epilogue; two groups of four take half the columns
+//               each.
+// The epilogues pass their chunks through shared memory, so that stores write
+// whole 128-byte (few tokens: 64-byte) pieces of rows.
 //
 // Every wait is bounded (gg_ptx.cuh); a wait that runs out records
 // GG_ERR_DEVICE_TIMEOUT, raises a CTA-wide abort flag, and the CTA drains
@@ -41,6 +48,7 @@
 
 #include <atomic>
 
+#include "gg_epilogue.cuh"
 #include "gg_f8.cuh"
 #include "gg_internal.h"
 #include "gg_launch.cuh"
@@ -60,23 +68,25 @@ constexpr int kItems = 4;     // work items found ahead
 constexpr int kItemWarp = 2, kFirstSum = 4;
 constexpr int kSumWarps = 8;
 constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
-constexpr int kMostChunks = BN / 32 / 2;  // of a summing warp
+constexpr int kChunks = 4;    // of 32 columns, that a summing warp has at most
+constexpr int kFewTokens = 128;  // tokens up to which they are the columns
 constexpr uint16_t kPairMask = 0x3;
 constexpr uint32_t A_BYTES = BM * BK;
 constexpr uint32_t STAGE_BYTES = A_BYTES + BN / 2 * BK;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int kBoxes = 3;     // heights of token boxes: 64, 32 and 16 rows
 // Registers per thread of the two roles: the launch has 168 for each of 384
-// threads, and 56 + 2 * 216 is less than three times that.
-constexpr int kFewRegs = 56, kManyRegs = 216;
+// threads, and 72 + 2 * 216 is three times that.
+constexpr int kFewRegs = 72, kManyRegs = 216;
 static_assert(128 * (kFewRegs + 2 * kManyRegs) <= kThreads * 168, "register split");
 
 // A work item: expert, block of channels, its tokens (first row, number; rows
-// < 0: there are no more items), in `cols` columns, a multiple of 32.
+// < 0: there are no more items); few: channels are the MMA's rows and the
+// tokens its columns, in `cols` of them, a multiple of 32.
 struct alignas(16) Item {
   int e, nt, row0, rows;
-  int cols;
-  int pad_[3];
+  int few, cols;
+  int pad_[2];
 };
 
 struct SmemTail {
@@ -95,13 +105,15 @@ struct SmemTail {
   uint32_t tmem_base;
   int abort_flag;
   int total_tiles;
-  float dots[4][BN];         // row sums of each lane quadrant's 32 channels
+  float dots[4][kFewTokens];  // row sums of each lane quadrant's 32 channels
   int tiles_before[kMaxExperts + 1];
   int row_start[kMaxExperts + 1];
 };
 
 constexpr uint32_t kScaleAt = kStages * STAGE_BYTES;
-constexpr uint32_t kScaleBytes = 2 * BN * 4;       // a step's: [half of the channels][token]
+// A step's scales: [64 channels][this CTA's 128 tokens], or, few tokens, [this
+// CTA's half of 64 channels][128 tokens].
+constexpr uint32_t kScaleBytes = 4 * BM * 4;
 constexpr uint32_t kStagingAt = kScaleAt + kScales * kScaleBytes;
 constexpr uint32_t kWarpStaging = 32 * 32 * 4;
 constexpr uint32_t kTailAt = kStagingAt + kSumWarps * kWarpStaging;
@@ -148,10 +160,10 @@ __device__ __forceinline__ Item item_of(int tile, const F8Params& p, const SmemT
   const int local = tile - st.tiles_before[lo];
   it.nt = local / blocks;
   const int tb = local - it.nt * blocks;
-  const int each = ((rows + blocks - 1) / blocks + 31) / 32 * 32;  // as even as 32s allow
-  it.row0 = first + tb * each;
-  it.rows = min(each, rows - tb * each);  // each <= BN: no block is empty
-  it.cols = (it.rows + 31) & ~31;
+  it.row0 = first + tb * BN;
+  it.rows = min(BN, rows - tb * BN);
+  it.few = it.rows <= kFewTokens;
+  it.cols = it.few ? (it.rows + 31) & ~31 : BN;
   return it;
 }
 
@@ -174,11 +186,99 @@ struct ItemReader {
   }
 };
 
-// E4M3 operands (format fields 0), fp32 sums, M = 256, N = n; the weights
-// MN-major for the input gradient.
-__device__ __forceinline__ uint32_t idesc_f8(int n, bool a_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((static_cast<uint32_t>(n) >> 3) << 17) |
-         ((static_cast<uint32_t>(2 * BM) >> 4) << 24);
+// E4M3 operands (format fields 0), fp32 sums, M = 256, N = n.
+__device__ __forceinline__ uint32_t idesc_f8(int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((static_cast<uint32_t>(n) >> 3) << 17) | ((static_cast<uint32_t>(2 * BM) >> 4) << 24);
+}
+
+// 32 lanes x 32 columns: a thread gets its lane's 32. Valid after tmem_wait().
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Names the registers that the loads write, so that no use moves ahead of it.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// acc += v * (s, s), pairs of columns.
+__device__ __forceinline__ void add_scaled(float (&acc)[32], const uint32_t (&v)[32], float s) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float2* to = reinterpret_cast<float2*>(&acc[i]);
+    *to = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
+                     make_float2(s, s), *to);
+  }
+}
+
+// 32 rows x 64 BF16 in a warp's staging buffer: 16-byte piece c (0..7) of row r
+// at r * 8 + (c ^ (r & 7)), so that every eight lanes of a row, or of a piece
+// of eight rows, hit all banks.
+__device__ __forceinline__ int wide_slot(int r, int c) { return r * 8 + (c ^ (r & 7)); }
+
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+// Warp-collective store of 32 rows x 64 columns of BF16: lane i has row i in
+// lo and hi. Row r of them starts at row0 + r * ld; rows below `have` and
+// columns below `cols` (a multiple of 32) exist.
+__device__ __forceinline__ void store_wide(uint4* stg, const float (&lo)[32],
+                                           const float (&hi)[32], gg_bf16* row0, long long ld,
+                                           int have, int cols) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    stg[wide_slot(lane, c)] = pack8(&lo[8 * c]);
+    stg[wide_slot(lane, 4 + c)] = pack8(&hi[8 * c]);
+  }
+  __syncwarp();
+  const int c = lane & 7;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = 4 * j + (lane >> 3);
+    const uint4 x = stg[wide_slot(r, c)];
+    if (r < have && 8 * c < cols) reinterpret_cast<uint4*>(row0 + r * ld)[c] = x;
+  }
+  __syncwarp();
+}
+
+// load_chunk_raw's rows handed to the lanes, in place.
+__device__ __forceinline__ void turn_chunk(uint4* stg, uint4 (&w)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) stg[stage_slot(8 * j + (lane >> 2), lane & 3)] = w[j];
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) w[c] = stg[stage_slot(lane, c)];
+  __syncwarp();
+}
+
+// Gradient of act(g) u at acc * w, act(g) = g s with s = sigmoid(alpha g), and
+// dot + acc * act(g) u.
+__device__ __forceinline__ void glu_grad(float acc, float w, float g, float u, float alpha,
+                                         float& dg, float& du, float& dot) {
+  const float ag = alpha * g;
+  const float s = __fdividef(1.0f, 1.0f + __expf(-ag));
+  const float gs = g * s;
+  const float d = acc * w;
+  dg = (d * u) * (s * fmaf(ag, 1.0f - s, 1.0f));
+  du = d * gs;
+  dot = fmaf(acc, gs * u, dot);
 }
 
 __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
@@ -299,7 +399,12 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
         Item it;
         ItemReader items;
         while (ok && items.next(st, it, false, true, abort_flag, p.status)) {
-          const int n0 = kGated ? it.nt * BM + h * (BM / 2) : it.nt * 2 * BM + h * BM;
+          // two boxes of 64 weight rows
+          int n0 = it.nt * 2 * BM + h * BM, n1 = n0 + BM / 2;
+          if (kGated) {
+            n0 = it.few ? it.nt * BM + h * (BM / 2) : h * p.F + it.nt * BM;
+            n1 = it.few ? p.F + n0 : n0 + BM / 2;
+          }
           const int half = it.cols / 2;  // this CTA's tokens, a multiple of 16
           const int r0 = it.row0 + h * half;
           for (int kb = 0; kb < KB; ++kb) {
@@ -318,8 +423,7 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
               tma_load_3d_pair(sa, &mapW, fb, n0, c, it.e);
             } else {
               tma_load_3d_pair(sa, &mapW, fb, c, n0, it.e);
-              tma_load_3d_pair(sa + A_BYTES / 2, &mapW, fb, c, kGated ? p.F + n0 : n0 + BM / 2,
-                               it.e);
+              tma_load_3d_pair(sa + A_BYTES / 2, &mapW, fb, c, n1, it.e);
             }
             int i = 0;
             for (; i + 64 <= half; i += 64)
@@ -357,14 +461,18 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
         uint32_t phase = 0, buf_phase = 0;
         bool ok = tmem_base == 0;
         // one group of 128 channels: the MN-major leading offset is not used
-        const uint64_t adesc0 = make_sdesc(sbase, kMN ? A_BYTES : 16, 1024);
-        const uint64_t bdesc0 = make_sdesc(sbase + A_BYTES, 16, 1024);
-        constexpr uint64_t kAStep = (kMN ? 32 * BM : 32) >> 4;
+        const uint64_t wdesc = make_sdesc(sbase, kMN ? A_BYTES : 16, 1024);
+        const uint64_t tdesc = make_sdesc(sbase + A_BYTES, 16, 1024);
+        constexpr uint64_t kWStep = (kMN ? 32 * BM : 32) >> 4, kTStep = 32 >> 4;
         Item it;
         ItemReader items;
         while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
-          // a reduction, for its result is in a uniform register
-          const uint32_t idesc = idesc_f8(__reduce_max_sync(0xFFFFFFFFu, it.cols), kMN);
+          // reductions, for their results are in uniform registers
+          const int few = __reduce_max_sync(0xFFFFFFFFu, it.few);
+          const int n = __reduce_max_sync(0xFFFFFFFFu, it.cols);
+          const uint32_t idesc = idesc_f8(n, few && kMN, !few && kMN);
+          const uint64_t a0 = few ? wdesc : tdesc, b0 = few ? tdesc : wdesc;
+          const uint64_t as = few ? kWStep : kTStep, bs = few ? kTStep : kWStep;
           for (int kb = 0; kb < KB; ++kb) {
             if (!mbar_wait_bounded(smem_u32(&st.tempty[buf]), buf_phase ^ 1u, abort_flag,
                                    p.status) ||
@@ -377,7 +485,7 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < BK / 32; ++kk)
-                tc_mma_f8_pair(buf * BN, adesc0 + at + kk * kAStep, bdesc0 + at + kk * 2, idesc,
+                tc_mma_f8_pair(buf * BN, a0 + at + kk * as, b0 + at + kk * bs, idesc,
                                kk != 0 ? 1u : 0u);
               tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
               tc_commit_pair_mc(smem_u32(&st.tfull[buf]), kPairMask);
@@ -404,7 +512,7 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
         int slot = 0;
         uint32_t phase = 0;
         for (int i = first;; i += step) {
-          Item it{0, 0, 0, -1, 0};
+          Item it{0, 0, 0, -1, 0, 0};
           if (i < total) it = item_of(i, p, st);
           if (!mbar_wait_bounded(smem_u32(&st.item_empty[slot]), phase ^ 1u, abort_flag, p.status))
             break;
@@ -421,8 +529,8 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
       // ------------------------------------------------------------ scales
       // Loaded two steps ahead of their use.
       struct Ahead {
-        float s[BN / 32];
-        float t0, t1;
+        float s[BM / 32];
+        float t[4];  // of 64 channels each; few tokens: two
       };
       int slot = 0;
       uint32_t phase = 0;
@@ -431,23 +539,34 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
       ItemReader items;
       while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
         const int h = static_cast<int>(crank);
-        const int n0 = kGated ? it.nt * BM + h * (BM / 2) : it.nt * 2 * BM + h * BM;
-        const int n1 = kGated ? p.F + n0 : n0 + BM / 2;
-        const int most = kGated ? 2 * p.F : p.width;
+        const bool few = it.few != 0;
+        const int own = few ? 0 : h * BM;  // first token
+        const int most = (kGated ? 2 * p.F : p.width) - 1;
         const float* t = p.T + static_cast<long long>(it.e) * p.t_expert;
-        // channels that do not exist have a tile of zeros: any scale will do
-        const float* t0 = t + static_cast<long long>(min(n0, most - 1) / kF8Block) * p.t_chan;
-        const float* t1 = t + static_cast<long long>(min(n1, most - 1) / kF8Block) * p.t_chan;
+        const float* ts[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          int n;
+          if (few)  // this CTA's halves of 64
+            n = kGated ? (k & 1) * p.F + it.nt * BM + h * (BM / 2)
+                       : it.nt * 2 * BM + h * BM + (k & 1) * (BM / 2);
+          else
+            n = kGated ? (k >> 1) * p.F + it.nt * BM + (k & 1) * (BM / 2)
+                       : it.nt * 2 * BM + k * (BM / 2);
+          // channels that do not exist have a tile of zeros: any scale will do
+          ts[k] = t + static_cast<long long>(min(n, most) / kF8Block) * p.t_chan;
+        }
         const auto load = [&](int kb, Ahead& a) {
           if (kb >= KB) return;
-          const float* s = p.S + static_cast<long long>(kb) * p.R_cap + it.row0;
+          const float* s = p.S + static_cast<long long>(kb) * p.R_cap + it.row0 + own;
 #pragma unroll
-          for (int j = 0; j < BN / 32; ++j) {
+          for (int j = 0; j < BM / 32; ++j) {
             const int i = 32 * j + lane;
-            a.s[j] = i < it.rows ? __ldg(s + i) : 0.0f;
+            a.s[j] = own + i < it.rows ? __ldg(s + i) : 0.0f;
           }
-          a.t0 = __ldg(t0 + static_cast<long long>(kb) * p.t_red);
-          a.t1 = __ldg(t1 + static_cast<long long>(kb) * p.t_red);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < 2 || !few) a.t[k] = __ldg(ts[k] + static_cast<long long>(kb) * p.t_red);
         };
         const auto put = [&](int kb, const Ahead& a) {
           if (!ok || kb >= KB) return;
@@ -458,10 +577,10 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
           }
           float* to = reinterpret_cast<float*>(smem + kScaleAt + slot * kScaleBytes);
 #pragma unroll
-          for (int j = 0; j < BN / 32; ++j) {
-            if (32 * j >= it.cols) break;
-            to[32 * j + lane] = a.s[j] * a.t0;
-            to[BN + 32 * j + lane] = a.s[j] * a.t1;
+          for (int k = 0; k < 4; ++k) {
+            if (k >= 2 && few) break;
+#pragma unroll
+            for (int j = 0; j < BM / 32; ++j) to[k * BM + 32 * j + lane] = a.s[j] * a.t[k];
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&st.scale_full[slot]));
@@ -488,9 +607,7 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
     const int group = (warp - kFirstSum) >> 2;
     const int half = q >> 1;  // of the CTA's channels
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    float* stg = reinterpret_cast<float*>(smem + kStagingAt + (warp - kFirstSum) * kWarpStaging);
-    const float* other = reinterpret_cast<const float*>(
-        smem + kStagingAt + ((warp - kFirstSum) ^ 2) * kWarpStaging);
+    uint8_t* staging = smem + kStagingAt + (warp - kFirstSum) * kWarpStaging;
     const uint32_t tempty = mapa_shared(smem_u32(&st.tempty[0]), 0);
     // What these warps wait for each other at: a barrier that a warp whose wait
     // ran out does not leave the others in.
@@ -508,51 +625,156 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
     bool ok = true;
     Item it;
     ItemReader items;
+    // a step's sums and scales are there
+    const auto enter = [&]() {
+      ok = mbar_wait_bounded(smem_u32(&st.scale_full[slot]), slot_phase, abort_flag, p.status) &&
+           mbar_wait_bounded(smem_u32(&st.tfull[buf]), buf_phase, abort_flag, p.status);
+      tc_fence_after();
+      return ok;
+    };
+    // and have been read
+    const auto leave = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_cluster_relaxed(tempty + 8 * buf);
+        mbar_arrive(smem_u32(&st.scale_empty[slot]));
+      }
+      if (++slot == kScales) {
+        slot = 0;
+        slot_phase ^= 1u;
+      }
+      buf ^= 1;
+      if (buf == 0) buf_phase ^= 1u;
+    };
+    const auto scales_of = [&]() {
+      return reinterpret_cast<const float*>(smem + kScaleAt + slot * kScaleBytes);
+    };
     while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
+      if (it.few == 0) {
+        // Lane: token; registers: channels, in four chunks of 32.
+        const auto column_of = [&](int c) {
+          return kGated ? (c >> 1) * BM + group * 64 + (c & 1) * 32 : group * BM + c * 32;
+        };
+        float acc[kChunks][32];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
+        for (int kb = 0; kb < KB && enter(); ++kb) {
+          // the token's scales for the two blocks of 64 channels of this warp
+          const float* own = scales_of() + q * 32 + lane;
+          const float s0 = own[(kGated ? group : 2 * group) * BM];
+          const float s1 = own[(kGated ? 2 + group : 2 * group + 1) * BM];
+          const uint32_t from = lanes + buf * BN;
+          uint32_t v[2][32];
+          tmem_ld32_start(from + column_of(0), v[0]);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            tmem_wait(v[c & 1]);
+            if (c + 1 < kChunks) tmem_ld32_start(from + column_of(c + 1), v[(c + 1) & 1]);
+            add_scaled(acc[c], v[c & 1], c < 2 ? s0 : s1);
+          }
+          leave();
+        }
+        if (!ok) break;
+        const int row = it.row0 + static_cast<int>(crank) * BM + q * 32;  // the warp's first
+        const int have = it.row0 + it.rows - row;
+        const bool there = lane < have;
+        uint4* stage = reinterpret_cast<uint4*>(staging);
+        const long long r = row;
+        if constexpr (kGated) {
+          const int ch = it.nt * BM + group * 64;
+          const int cols = min(64, p.width - ch);
+          if (p.H1_save != nullptr) {
+            gg_bf16* h1 = p.H1_save + r * (2LL * p.F) + ch;
+            store_wide(stage, acc[0], acc[1], h1, 2LL * p.F, have, cols);
+            store_wide(stage, acc[2], acc[3], h1 + p.F, 2LL * p.F, have, cols);
+          }
+          const bool scaled = p.row_scale != nullptr;
+          const float w = scaled && there ? __ldg(p.row_scale + r + lane) : 1.0f;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              acc[c][i] = glu_mul(acc[c][i], acc[2 + c][i], p.alpha, scaled, w);
+          store_wide(stage, acc[0], acc[1], p.C + r * p.width + ch, p.width, have, cols);
+        } else if constexpr (MODE == kGradGated) {
+          const float w = p.row_scale != nullptr && there ? __ldg(p.row_scale + r + lane) : 1.0f;
+          float dot = 0.0f;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            const int ch = it.nt * 2 * BM + group * BM + c * 32;
+            if (ch >= p.width) continue;
+            uint4 g[4], u[4];
+            const gg_bf16* h1 = p.H1 + r * (2LL * p.F) + ch;
+            load_chunk_raw(g, h1, 2LL * p.F, have);
+            load_chunk_raw(u, h1 + p.F, 2LL * p.F, have);
+            turn_chunk(stage, g);
+            turn_chunk(stage, u);
+            // pairs of dg replace g, pairs of du replace u
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              uint32_t& gw = (&g[i / 8].x)[i / 2 % 4];
+              uint32_t& uw = (&u[i / 8].x)[i / 2 % 4];
+              float g0, g1, u0, u1;
+              glu_grad(acc[c][i], w, bf16_lo(gw), bf16_lo(uw), p.alpha, g0, u0, dot);
+              glu_grad(acc[c][i + 1], w, bf16_hi(gw), bf16_hi(uw), p.alpha, g1, u1, dot);
+              gw = pack_bf16x2(g0, g1);
+              uw = pack_bf16x2(u0, u1);
+            }
+            gg_bf16* to = p.C + r * (2LL * p.F) + ch;
+            store_chunk(stage, g, to, 2LL * p.F, have);
+            store_chunk(stage, u, to + p.F, 2LL * p.F, have);
+          }
+          if (p.rowdot != nullptr && there)
+            p.rowdot[(r + lane) * p.rowdot_stride + 2 * it.nt + group] = dot;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int ch = it.nt * 2 * BM + group * BM + c * 64;
+            store_wide(stage, acc[2 * c], acc[2 * c + 1], p.C + r * p.width + ch, p.width, have,
+                       min(64, p.width - ch));
+          }
+        }
+        continue;
+      }
+      // Few tokens. Lane: channel; registers: tokens, in chunks [mine0, mine0 + mine).
+      // `at` is the lane, made anew here: its address arithmetic, kept in
+      // registers over the loop above, spilled that loop's sums.
+      int at = lane;
+      asm volatile("" : "+r"(at));
+      float* stg = reinterpret_cast<float*>(staging);
+      const float* other = reinterpret_cast<const float*>(
+          smem + kStagingAt + ((warp - kFirstSum) ^ 2) * kWarpStaging);
       const int chunks = it.cols / 32;
       const int mine0 = group == 0 ? 0 : (chunks + 1) / 2;
       const int mine = group == 0 ? (chunks + 1) / 2 : chunks / 2;
-      float acc[kMostChunks][32];
+      float acc[kFewTokens / 64][32];
 #pragma unroll
-      for (int c = 0; c < kMostChunks; ++c)
+      for (int c = 0; c < kFewTokens / 64; ++c)
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!mbar_wait_bounded(smem_u32(&st.scale_full[slot]), slot_phase, abort_flag, p.status) ||
-            !mbar_wait_bounded(smem_u32(&st.tfull[buf]), buf_phase, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float4* f =
-            reinterpret_cast<const float4*>(smem + kScaleAt + slot * kScaleBytes) +
-            (half * BN + 32 * mine0) / 4;
+      for (int kb = 0; kb < KB && enter(); ++kb) {
+        const float4* f = reinterpret_cast<const float4*>(scales_of() + half * BM + 32 * mine0);
+        const uint32_t from = lanes + buf * BN + 32 * mine0;
 #pragma unroll
-        for (int c = 0; c < kMostChunks; ++c) {
-          if (c < mine) {
-            float v[32];
-            tmem_ld32(lanes + buf * BN + 32 * (mine0 + c), v);
+        for (int c = 0; c < kFewTokens / 64; ++c) {
+          if (c >= mine) continue;
+          uint32_t v[32];
+          tmem_ld32_start(from + 32 * c, v);
+          tmem_wait(v);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 s = f[8 * c + i / 4];
-              float2* to = reinterpret_cast<float2*>(&acc[c][i]);
-              to[0] = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(s.x, s.y), to[0]);
-              to[1] = __ffma2_rn(make_float2(v[i + 2], v[i + 3]), make_float2(s.z, s.w), to[1]);
-            }
+          for (int i = 0; i < 32; i += 4) {
+            const float4 s = f[8 * c + i / 4];
+            float2* to = reinterpret_cast<float2*>(&acc[c][i]);
+            to[0] = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
+                               make_float2(s.x, s.y), to[0]);
+            to[1] = __ffma2_rn(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])),
+                               make_float2(s.z, s.w), to[1]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster_relaxed(tempty + 8 * buf);
-          mbar_arrive(smem_u32(&st.scale_empty[slot]));
-        }
-        if (++slot == kScales) {
-          slot = 0;
-          slot_phase ^= 1u;
-        }
-        buf ^= 1;
-        if (buf == 0) buf_phase ^= 1u;
+        leave();
       }
       if (!ok) break;
       // Chunk by chunk through the warp's staging buffer, token i's 16-byte
@@ -561,24 +783,20 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
       const int ch0 = kGated ? it.nt * BM + static_cast<int>(crank) * (BM / 2) + (q & 1) * 32
                              : it.nt * 2 * BM + static_cast<int>(crank) * BM + q * 32;
       const bool exists = ch0 < p.width;  // 32 channels exist together: multiples of 64
-      const int ch = ch0 + 8 * (lane & 3);
+      const int ch = ch0 + 8 * (at & 3);
       const auto read8 = [&](const float* from, int i, float(&x)[8]) {
         const float4* row = reinterpret_cast<const float4*>(from + 32 * i);
-        const int s = 2 * (lane & 3);
+        const int s = 2 * (at & 3);
         const float4 a = row[s ^ (i & 7)], b = row[(s + 1) ^ (i & 7)];
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
         x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
       };
-      const auto pack8 = [](const float(&x)[8]) {
-        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                          pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-      };
 #pragma unroll
-      for (int c = 0; c < kMostChunks; ++c) {
+      for (int c = 0; c < kFewTokens / 64; ++c) {
         if (c >= mine || !ok) continue;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          stg[32 * i + (((lane >> 2) ^ (i & 7)) << 2) + (lane & 3)] = acc[c][i];
+          stg[32 * i + (((at >> 2) ^ (i & 7)) << 2) + (at & 3)] = acc[c][i];
         const int t0 = 32 * (mine0 + c);
         if constexpr (kGated) {
           // gate and up rows' warps (two lane quadrants apart) take half the
@@ -588,7 +806,7 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
           const float* ups = q < 2 ? other : stg;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int i = 16 * half + 8 * j + (lane >> 2);
+            const int i = 16 * half + 8 * j + (at >> 2);
             if (exists && t0 + i < it.rows) {
               float g[8], u[8], v[8];
               read8(gates, i, g);
@@ -611,7 +829,7 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int i = 8 * j + (lane >> 2);
+            const int i = 8 * j + (at >> 2);
             const bool there = exists && t0 + i < it.rows;
             const long long r = static_cast<long long>(it.row0) + t0 + i;
             float v[8];
@@ -630,13 +848,7 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
                 for (int k = 0; k < 8; ++k) {
                   const float g = k & 1 ? bf16_hi(gx[k / 2]) : bf16_lo(gx[k / 2]);
                   const float u = k & 1 ? bf16_hi(ux[k / 2]) : bf16_lo(ux[k / 2]);
-                  const float ag = p.alpha * g;
-                  const float s = __fdividef(1.0f, 1.0f + __expf(-ag));
-                  const float gs = g * s;
-                  const float d = v[k] * w;
-                  dg[k] = (d * u) * (s * fmaf(ag, 1.0f - s, 1.0f));
-                  du[k] = d * gs;
-                  dot = fmaf(v[k], gs * u, dot);
+                  glu_grad(v[k], w, g, u, p.alpha, dg[k], du[k], dot);
                 }
                 gg_bf16* to = p.C + r * (2LL * p.F) + ch;
                 *reinterpret_cast<uint4*>(to) = pack8(dg);
@@ -644,7 +856,7 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
               }
               dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
               dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
-              if ((lane & 3) == 0) st.dots[q][t0 + i] = dot;
+              if ((at & 3) == 0) st.dots[q][t0 + i] = dot;
             } else {
               if (there) *reinterpret_cast<uint4*>(p.C + r * p.width + ch) = pack8(v);
             }
