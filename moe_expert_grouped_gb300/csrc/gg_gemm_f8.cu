@@ -62,9 +62,10 @@ enum F8Mode : int { kFwd = 0, kFwdGated = 1, kGrad = 2, kGradGated = 3 };
 constexpr int BM = 128;       // channels per CTA
 constexpr int BN = 256;       // most tokens per work item
 constexpr int BK = kF8Block;  // codes per step
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr int kScales = 4;    // steps of scales ahead
 constexpr int kItems = 4;     // work items found ahead
+constexpr int kRaster = 8;    // token blocks that go through the channels together
 constexpr int kItemWarp = 2, kFirstSum = 4;
 constexpr int kSumWarps = 8;
 constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
@@ -115,11 +116,12 @@ constexpr uint32_t kScaleAt = kStages * STAGE_BYTES;
 // CTA's half of 64 channels][128 tokens].
 constexpr uint32_t kScaleBytes = 4 * BM * 4;
 constexpr uint32_t kStagingAt = kScaleAt + kScales * kScaleBytes;
-constexpr uint32_t kWarpStaging = 32 * 32 * 4;
+constexpr uint32_t kWarpStaging = 2 * 32 * 64 * 2;  // two buffers of 32 rows x 64 BF16
 constexpr uint32_t kTailAt = kStagingAt + kSumWarps * kWarpStaging;
 constexpr size_t kSmemBytes = 1024 + kTailAt + sizeof(SmemTail);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(kTailAt % 16 == 0 && kScaleAt % 16 == 0, "16-byte reads");
+static_assert(kStagingAt % 1024 == 0 && kWarpStaging % 1024 == 0, "128-byte swizzle");
 
 struct F8Params {
   const int32_t* offsets;
@@ -157,9 +159,14 @@ __device__ __forceinline__ Item item_of(int tile, const F8Params& p, const SmemT
   const int first = st.row_start[lo];
   const int rows = st.row_start[lo + 1] - first;
   const int blocks = token_blocks(rows);
+  // eight token blocks at a time, the token block fastest: what runs side by
+  // side shares its weights and its tokens
   const int local = tile - st.tiles_before[lo];
-  it.nt = local / blocks;
-  const int tb = local - it.nt * blocks;
+  const int from = local / (kRaster * p.NT) * kRaster;
+  const int wide = min(kRaster, blocks - from);
+  const int at = local - from * p.NT;
+  it.nt = at / wide;
+  const int tb = from + at - it.nt * wide;
   it.row0 = first + tb * BN;
   it.rows = min(BN, rows - tb * BN);
   it.few = it.rows <= kFewTokens;
@@ -224,48 +231,86 @@ __device__ __forceinline__ void add_scaled(float (&acc)[32], const uint32_t (&v)
   }
 }
 
-// 32 rows x 64 BF16 in a warp's staging buffer: 16-byte piece c (0..7) of row r
-// at r * 8 + (c ^ (r & 7)), so that every eight lanes of a row, or of a piece
-// of eight rows, hit all banks.
-__device__ __forceinline__ int wide_slot(int r, int c) { return r * 8 + (c ^ (r & 7)); }
-
 __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                     pack_bf16x2(x[6], x[7]));
 }
 
-// Warp-collective store of 32 rows x 64 columns of BF16: lane i has row i in
-// lo and hi. Row r of them starts at row0 + r * ld; rows below `have` and
-// columns below `cols` (a multiple of 32) exist.
-__device__ __forceinline__ void store_wide(uint4* stg, const float (&lo)[32],
-                                           const float (&hi)[32], gg_bf16* row0, long long ld,
-                                           int have, int cols) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    stg[wide_slot(lane, c)] = pack8(&lo[8 * c]);
-    stg[wide_slot(lane, 4 + c)] = pack8(&hi[8 * c]);
-  }
-  __syncwarp();
-  const int c = lane & 7;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = 4 * j + (lane >> 3);
-    const uint4 x = stg[wide_slot(r, c)];
-    if (r < have && 8 * c < cols) reinterpret_cast<uint4*>(row0 + r * ld)[c] = x;
-  }
-  __syncwarp();
+// 16-byte piece c of row r in a buffer of 32 rows x 64 BF16 (8 pieces) or 32 x
+// 32 (4): TMA's 128-byte and 64-byte swizzles, which also spread eight lanes
+// that touch one piece of eight rows over all banks. stage_slot() is the
+// latter.
+__device__ __forceinline__ int wide_slot(int r, int c) { return r * 8 + (c ^ (r & 7)); }
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
 }
 
-// load_chunk_raw's rows handed to the lanes, in place.
-__device__ __forceinline__ void turn_chunk(uint4* stg, uint4 (&w)[4]) {
+// A warp's results on their way to memory: two buffers, filled in turn, each
+// written by one TMA store where all 32 rows belong to the expert. Stores of
+// the warp's own held it up behind those of all other SMs, which reach their
+// epilogues together (131072 x 1536 x 2048: 362 us of 299 without any).
+struct Outbox {
+  uint8_t* at;   // the warp's buffers
+  int turn = 0;
+  // The buffer to fill next, once the store that read it last is done.
+  __device__ __forceinline__ uint4* open() {
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+    uint4* buf = reinterpret_cast<uint4*>(at + turn * (kWarpStaging / 2));
+    turn ^= 1;
+    return buf;
+  }
+  // No store reads a buffer any more.
+  __device__ __forceinline__ void drain() {
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+  }
+};
+
+// Every store of a buffer, or of none, is a group of its own.
+__device__ __forceinline__ void end_group() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Warp-collective: 32 rows x 64 columns, lane i with row i in lo and hi, to
+// rows row.. and columns col.. of out (ld wide). Rows below `have` exist, and
+// columns below ld - col or `cols`, a multiple of 64.
+__device__ __forceinline__ void send_wide(Outbox& box, const CUtensorMap* map,
+                                          const float (&lo)[32], const float (&hi)[32],
+                                          gg_bf16* out, long long ld, int row, int col, int have,
+                                          int cols) {
   const int lane = threadIdx.x & 31;
+  uint4* buf = box.open();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) stg[stage_slot(8 * j + (lane >> 2), lane & 3)] = w[j];
+  for (int c = 0; c < 4; ++c) {
+    buf[wide_slot(lane, c)] = pack8(&lo[8 * c]);
+    buf[wide_slot(lane, 4 + c)] = pack8(&hi[8 * c]);
+  }
+  if (have >= 32) {
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      if (cols > 0) tma_store_2d(map, smem_u32(buf), col, row);
+      end_group();
+    }
+    return;
+  }
   __syncwarp();
-#pragma unroll
-  for (int c = 0; c < 4; ++c) w[c] = stg[stage_slot(lane, c)];
+  if (cols > 0) {
+#pragma unroll 2
+    for (int j = 0; j < 8; ++j) {
+      const int r = 4 * j + (lane >> 3);
+      if (r < have)
+        reinterpret_cast<uint4*>(out + (row + r) * ld + col)[lane & 7] =
+            buf[wide_slot(r, lane & 7)];
+    }
+  }
   __syncwarp();
+  if (lane == 0) end_group();
 }
 
 // Gradient of act(g) u at acc * w, act(g) = g s with s = sigmoid(alpha g), and
@@ -291,14 +336,16 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t adesc, 
       : "memory");
 }
 
-struct TokenMaps {
-  CUtensorMap box[kBoxes];
+struct F8Maps {
+  CUtensorMap tokens[kBoxes];
+  CUtensorMap weights;
+  CUtensorMap out;  // C: 32 rows x 64 columns, gated gradient x 32
+  CUtensorMap h1;   // H1_save: 32 x 64
 };
 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
-f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ CUtensorMap mapW,
-               const F8Params p) {
+f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
   constexpr bool kGated = MODE == kFwdGated;
   constexpr bool kMN = MODE == kGrad || MODE == kGradGated;
   extern __shared__ uint8_t smem_raw[];
@@ -390,8 +437,9 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
     if (warp == 0) {
       if (lane == 0) {
         // -------------------------------------------------- TMA producer
-        for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&mapT.box[i]);
-        tma_prefetch_desc(&mapW);
+        for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.tokens[i]);
+        tma_prefetch_desc(&maps.weights);
+        tma_prefetch_desc(&maps.out);
         const int h = static_cast<int>(crank);
         int stage = 0;
         uint32_t phase = 0, used = 0, last_phase = 0;
@@ -420,19 +468,19 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
             if (leader)
               mbar_arrive_expect_tx(smem_u32(&st.full[stage]), 2 * (A_BYTES + half * BK));
             if (kMN) {
-              tma_load_3d_pair(sa, &mapW, fb, n0, c, it.e);
+              tma_load_3d_pair(sa, &maps.weights, fb, n0, c, it.e);
             } else {
-              tma_load_3d_pair(sa, &mapW, fb, c, n0, it.e);
-              tma_load_3d_pair(sa + A_BYTES / 2, &mapW, fb, c, n1, it.e);
+              tma_load_3d_pair(sa, &maps.weights, fb, c, n0, it.e);
+              tma_load_3d_pair(sa + A_BYTES / 2, &maps.weights, fb, c, n1, it.e);
             }
             int i = 0;
             for (; i + 64 <= half; i += 64)
-              tma_load_2d_pair(sa + A_BYTES + i * BK, &mapT.box[0], fb, c, r0 + i);
+              tma_load_2d_pair(sa + A_BYTES + i * BK, &maps.tokens[0], fb, c, r0 + i);
             if (i + 32 <= half) {
-              tma_load_2d_pair(sa + A_BYTES + i * BK, &mapT.box[1], fb, c, r0 + i);
+              tma_load_2d_pair(sa + A_BYTES + i * BK, &maps.tokens[1], fb, c, r0 + i);
               i += 32;
             }
-            if (i < half) tma_load_2d_pair(sa + A_BYTES + i * BK, &mapT.box[2], fb, c, r0 + i);
+            if (i < half) tma_load_2d_pair(sa + A_BYTES + i * BK, &maps.tokens[2], fb, c, r0 + i);
             used |= 1u << stage;
             last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
             if (++stage == kStages) {
@@ -556,6 +604,20 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
           // channels that do not exist have a tile of zeros: any scale will do
           ts[k] = t + static_cast<long long>(min(n, most) / kF8Block) * p.t_chan;
         }
+        if constexpr (MODE == kGradGated) {
+          // the epilogue's H1 on its way to L2
+          const int lines = few ? 2 : 4;  // of 64 channels
+          const int ch = it.nt * 2 * BM + (few ? h * BM : 0);
+          for (int j = 0; j < BM / 32; ++j) {
+            const int i = own + 32 * j + lane;
+            if (i >= it.rows) continue;
+            const gg_bf16* g = p.H1 + (static_cast<long long>(it.row0) + i) * (2LL * p.F) + ch;
+            for (int k = 0; k < lines && ch + 64 * k < p.width; ++k) {
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(g + 64 * k));
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(g + p.F + 64 * k));
+            }
+          }
+        }
         const auto load = [&](int kb, Ahead& a) {
           if (kb >= KB) return;
           const float* s = p.S + static_cast<long long>(kb) * p.R_cap + it.row0 + own;
@@ -608,6 +670,8 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
     const int half = q >> 1;  // of the CTA's channels
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     uint8_t* staging = smem + kStagingAt + (warp - kFirstSum) * kWarpStaging;
+    Outbox box;
+    box.at = staging;
     const uint32_t tempty = mapa_shared(smem_u32(&st.tempty[0]), 0);
     // What these warps wait for each other at: a barrier that a warp whose wait
     // ran out does not leave the others in.
@@ -681,60 +745,102 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
         const int row = it.row0 + static_cast<int>(crank) * BM + q * 32;  // the warp's first
         const int have = it.row0 + it.rows - row;
         const bool there = lane < have;
-        uint4* stage = reinterpret_cast<uint4*>(staging);
-        const long long r = row;
         if constexpr (kGated) {
           const int ch = it.nt * BM + group * 64;
-          const int cols = min(64, p.width - ch);
+          const int cols = p.width - ch;
           if (p.H1_save != nullptr) {
-            gg_bf16* h1 = p.H1_save + r * (2LL * p.F) + ch;
-            store_wide(stage, acc[0], acc[1], h1, 2LL * p.F, have, cols);
-            store_wide(stage, acc[2], acc[3], h1 + p.F, 2LL * p.F, have, cols);
+            send_wide(box, &maps.h1, acc[0], acc[1], p.H1_save, 2LL * p.F, row, ch, have, cols);
+            send_wide(box, &maps.h1, acc[2], acc[3], p.H1_save, 2LL * p.F, row, p.F + ch, have,
+                      cols);
           }
           const bool scaled = p.row_scale != nullptr;
-          const float w = scaled && there ? __ldg(p.row_scale + r + lane) : 1.0f;
+          const float w = scaled && there ? __ldg(p.row_scale + row + lane) : 1.0f;
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               acc[c][i] = glu_mul(acc[c][i], acc[2 + c][i], p.alpha, scaled, w);
-          store_wide(stage, acc[0], acc[1], p.C + r * p.width + ch, p.width, have, cols);
+          send_wide(box, &maps.out, acc[0], acc[1], p.C, p.width, row, ch, have, cols);
         } else if constexpr (MODE == kGradGated) {
-          const float w = p.row_scale != nullptr && there ? __ldg(p.row_scale + r + lane) : 1.0f;
+          const float w = p.row_scale != nullptr && there ? __ldg(p.row_scale + row + lane) : 1.0f;
           float dot = 0.0f;
+          const int ch0 = it.nt * 2 * BM + group * BM;
+          const gg_bf16* h1 = p.H1 + static_cast<long long>(row) * (2LL * p.F) + ch0;
+          uint4 rg[4], ru[4];  // a chunk's rows as loads bring them, ahead of its use
+          if (ch0 < p.width) {
+            load_chunk_raw(rg, h1, 2LL * p.F, have);
+            load_chunk_raw(ru, h1 + p.F, 2LL * p.F, have);
+          }
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            const int ch = it.nt * 2 * BM + group * BM + c * 32;
+            const int ch = ch0 + 32 * c;
             if (ch >= p.width) continue;
-            uint4 g[4], u[4];
-            const gg_bf16* h1 = p.H1 + r * (2LL * p.F) + ch;
-            load_chunk_raw(g, h1, 2LL * p.F, have);
-            load_chunk_raw(u, h1 + p.F, 2LL * p.F, have);
-            turn_chunk(stage, g);
-            turn_chunk(stage, u);
-            // pairs of dg replace g, pairs of du replace u
+            // gate and up rows are turned in a buffer's halves, and replaced
+            // there by their gradients
+            uint4* gs = box.open();
+            uint4* us = gs + 32 * 4;
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              uint32_t& gw = (&g[i / 8].x)[i / 2 % 4];
-              uint32_t& uw = (&u[i / 8].x)[i / 2 % 4];
-              float g0, g1, u0, u1;
-              glu_grad(acc[c][i], w, bf16_lo(gw), bf16_lo(uw), p.alpha, g0, u0, dot);
-              glu_grad(acc[c][i + 1], w, bf16_hi(gw), bf16_hi(uw), p.alpha, g1, u1, dot);
-              gw = pack_bf16x2(g0, g1);
-              uw = pack_bf16x2(u0, u1);
+            for (int j = 0; j < 4; ++j) {
+              const int to = stage_slot(8 * j + (lane >> 2), lane & 3);
+              gs[to] = rg[j];
+              us[to] = ru[j];
             }
-            gg_bf16* to = p.C + r * (2LL * p.F) + ch;
-            store_chunk(stage, g, to, 2LL * p.F, have);
-            store_chunk(stage, u, to + p.F, 2LL * p.F, have);
+            __syncwarp();
+            if (c + 1 < kChunks && ch + 32 < p.width) {
+              load_chunk_raw(rg, h1 + 32 * (c + 1), 2LL * p.F, have);
+              load_chunk_raw(ru, h1 + p.F + 32 * (c + 1), 2LL * p.F, have);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int own = stage_slot(lane, k);
+              uint4 g = gs[own], u = us[own];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t& gw = (&g.x)[i];
+                uint32_t& uw = (&u.x)[i];
+                float g0, g1, u0, u1;
+                glu_grad(acc[c][8 * k + 2 * i], w, bf16_lo(gw), bf16_lo(uw), p.alpha, g0, u0, dot);
+                glu_grad(acc[c][8 * k + 2 * i + 1], w, bf16_hi(gw), bf16_hi(uw), p.alpha, g1, u1,
+                         dot);
+                gw = pack_bf16x2(g0, g1);
+                uw = pack_bf16x2(u0, u1);
+              }
+              gs[own] = g;
+              us[own] = u;
+            }
+            if (have >= 32) {
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&maps.out, smem_u32(gs), ch, row);
+                tma_store_2d(&maps.out, smem_u32(us), p.F + ch, row);
+                end_group();
+              }
+            } else {
+              __syncwarp();
+              gg_bf16* to = p.C + static_cast<long long>(row) * (2LL * p.F) + ch;
+              for (int j = 0; j < 4; ++j) {
+                const int i = 8 * j + (lane >> 2);
+                if (i < have) {
+                  reinterpret_cast<uint4*>(to + i * (2LL * p.F))[lane & 3] =
+                      gs[stage_slot(i, lane & 3)];
+                  reinterpret_cast<uint4*>(to + i * (2LL * p.F) + p.F)[lane & 3] =
+                      us[stage_slot(i, lane & 3)];
+                }
+              }
+              __syncwarp();
+              if (lane == 0) end_group();
+            }
           }
           if (p.rowdot != nullptr && there)
-            p.rowdot[(r + lane) * p.rowdot_stride + 2 * it.nt + group] = dot;
+            p.rowdot[static_cast<long long>(row + lane) * p.rowdot_stride + 2 * it.nt + group] =
+                dot;
         } else {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int ch = it.nt * 2 * BM + group * BM + c * 64;
-            store_wide(stage, acc[2 * c], acc[2 * c + 1], p.C + r * p.width + ch, p.width, have,
-                       min(64, p.width - ch));
+            send_wide(box, &maps.out, acc[2 * c], acc[2 * c + 1], p.C, p.width, row, ch, have,
+                      p.width - ch);
           }
         }
         continue;
@@ -777,6 +883,7 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
         leave();
       }
       if (!ok) break;
+      box.drain();
       // Chunk by chunk through the warp's staging buffer, token i's 16-byte
       // piece s at s ^ (i & 7): a lane then has channels 8 (lane % 4) .. + 7 of
       // tokens 8 j + lane / 4.
@@ -880,6 +987,8 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
     }
   }
 
+  // shared memory stays until the last stores have read it
+  if (warp >= kFirstSum && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -890,15 +999,15 @@ f8_gemm_kernel(const __grid_constant__ TokenMaps mapT, const __grid_constant__ C
 }
 
 template <int MODE>
-cudaError_t launch_f8_t(const TokenMaps& mt, const CUtensorMap& mw, const F8Params& p,
-                        const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_f8_t(const F8Maps& maps, const F8Params& p, const DeviceInfo& dev,
+                        cudaStream_t stream) {
   static std::atomic<int> resident[kMaxDevices];
   // no more clusters than there can be work items
   const long long items =
       (static_cast<long long>(p.R_cap) / BN + (p.R_cap < p.E ? p.R_cap : p.E)) * p.NT;
   const int most = static_cast<int>(items < 1 ? 1 : (items < 0x7FFFFFFF ? items : 0x7FFFFFFF));
-  return launch_pairs(f8_gemm_kernel<MODE>, resident, kThreads, kSmemBytes, most, dev, stream, mt,
-                      mw, p);
+  return launch_pairs(f8_gemm_kernel<MODE>, resident, kThreads, kSmemBytes, most, dev, stream,
+                      maps, p);
 }
 
 }  // namespace
@@ -906,13 +1015,12 @@ cudaError_t launch_f8_t(const TokenMaps& mt, const CUtensorMap& mw, const F8Para
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
   const int red = a.grad ? a.N : a.K;
   const int out = a.grad ? a.K : a.N;
-  TokenMaps mt;
-  CUtensorMap mw;
+  F8Maps maps;
   const cuuint64_t td[2] = {static_cast<cuuint64_t>(red), static_cast<cuuint64_t>(a.R_cap)};
   const cuuint64_t ts[1] = {static_cast<cuuint64_t>(red)};
   for (int i = 0; i < kBoxes; ++i) {
     const cuuint32_t tbox[2] = {BK, 64u >> i};
-    if (!encode_map(&mt.box[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, 2, td, ts, tbox,
+    if (!encode_map(&maps.tokens[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, 2, td, ts, tbox,
                     CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
@@ -921,9 +1029,27 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStrea
   const cuuint64_t ws[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.K) * a.N};
   // forward: 64 channels x 128 codes; gradient: 128 rows of 128 channels
   const cuuint32_t wbox[3] = {BK, a.grad ? static_cast<cuuint32_t>(BK) : BM / 2u, 1};
-  if (!encode_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, wd, ws, wbox,
+  if (!encode_map(&maps.weights, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, wd, ws, wbox,
                   CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  // results, in pieces of 32 rows
+  const bool gated = a.alpha != 0.0f;
+  const bool narrow = a.grad && gated;
+  const cuuint64_t width = narrow ? 2ull * a.K : a.grad ? a.K : gated ? a.N / 2 : a.N;
+  const cuuint64_t od[2] = {width, static_cast<cuuint64_t>(a.R_cap)};
+  const cuuint64_t os[1] = {2 * width};
+  const cuuint32_t obox[2] = {narrow ? 32u : 64u, 32u};
+  if (!encode_map(&maps.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.C, 2, od, os, obox,
+                  narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  maps.h1 = maps.out;
+  if (a.H1_save != nullptr) {
+    const cuuint64_t hd[2] = {static_cast<cuuint64_t>(a.N), static_cast<cuuint64_t>(a.R_cap)};
+    const cuuint64_t hs[1] = {2ull * a.N};
+    if (!encode_map(&maps.h1, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.H1_save, 2, hd, hs, obox,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
   const int NB = (a.N + kF8Block - 1) / kF8Block, KB = (a.K + kF8Block - 1) / kF8Block;
   F8Params p{};
   p.offsets = a.offsets;
@@ -942,20 +1068,19 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStrea
   p.H1 = a.H1;
   p.rowdot = a.rowdot;
   p.status = a.status;
-  const bool gated = a.alpha != 0.0f;
   if (!a.grad && gated) {
     p.F = a.N / 2;
     p.width = p.F;
     p.NT = (p.F + BM - 1) / BM;
-    return launch_f8_t<kFwdGated>(mt, mw, p, dev, stream);
+    return launch_f8_t<kFwdGated>(maps, p, dev, stream);
   }
   p.width = out;
   p.NT = (out + 2 * BM - 1) / (2 * BM);
-  if (!a.grad) return launch_f8_t<kFwd>(mt, mw, p, dev, stream);
-  if (!gated) return launch_f8_t<kGrad>(mt, mw, p, dev, stream);
+  if (!a.grad) return launch_f8_t<kFwd>(maps, p, dev, stream);
+  if (!gated) return launch_f8_t<kGrad>(maps, p, dev, stream);
   p.F = a.K;
   p.rowdot_stride = (2 * p.NT + 7) / 8 * 8;
-  return launch_f8_t<kGradGated>(mt, mw, p, dev, stream);
+  return launch_f8_t<kGradGated>(maps, p, dev, stream);
 }
 
 }  // namespace gg
