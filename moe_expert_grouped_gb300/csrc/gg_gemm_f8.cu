@@ -47,6 +47,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "gg_epilogue.cuh"
 #include "gg_f8.cuh"
@@ -63,6 +64,8 @@ constexpr int BM = 128;       // channels per CTA
 constexpr int BN = 256;       // most tokens per work item
 constexpr int BK = kF8Block;  // codes per step
 constexpr int kStages = 4;
+constexpr int kBufs = 2;      // of sums in TMEM
+constexpr int kBufCols = 256;
 constexpr int kScales = 4;    // steps of scales ahead
 constexpr int kItems = 4;     // work items found ahead
 constexpr int kRaster = 8;    // token blocks that go through the channels together
@@ -76,10 +79,15 @@ constexpr uint32_t A_BYTES = BM * BK;
 constexpr uint32_t STAGE_BYTES = A_BYTES + BN / 2 * BK;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int kBoxes = 3;     // heights of token boxes: 64, 32 and 16 rows
-// Registers per thread of the two roles: the launch has 168 for each of 384
-// threads, and 72 + 2 * 216 is three times that.
-constexpr int kFewRegs = 72, kManyRegs = 216;
-static_assert(128 * (kFewRegs + 2 * kManyRegs) <= kThreads * 168, "register split");
+// Registers per thread of the two roles. The launch has 168 for each of 384
+// threads; either split, of the first four warps and the other eight, is three
+// times that.
+template <int MODE>
+struct Regs {
+  static constexpr int kFew = MODE == kGradGated ? 56 : 72;
+  static constexpr int kMany = MODE == kGradGated ? 224 : 216;
+  static_assert(128 * (kFew + 2 * kMany) <= kThreads * 168, "register split");
+};
 
 // A work item: expert, block of channels, its tokens (first row, number; rows
 // < 0: there are no more items); few: channels are the MMA's rows and the
@@ -98,15 +106,18 @@ struct SmemTail {
   uint64_t empty[kStages];
   uint64_t scale_full[kScales];
   uint64_t scale_empty[kScales];
-  uint64_t tfull[2];
-  uint64_t tempty[2];        // even CTA
+  uint64_t tfull[kBufs];
+  uint64_t tempty[kBufs];    // even CTA
   uint64_t pair[2][2];       // per group: warps of gate rows and of the matching up rows
   uint64_t group[2];         // the four warps of a group
+  uint64_t all;              // all summing warps
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
   int total_tiles;
-  float dots[4][kFewTokens];  // row sums of each lane quadrant's 32 channels
+  // Row sums: of each lane quadrant's 32 channels (few tokens), or of 64, for
+  // items in turn.
+  float dots[2][4][kFewTokens];
   int tiles_before[kMaxExperts + 1];
   int row_start[kMaxExperts + 1];
 };
@@ -249,6 +260,14 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
                : "memory");
 }
 
+// The lane, made anew: address arithmetic on it is done where it is used, not
+// kept in registers over the loops, where it spilled their sums.
+__device__ __forceinline__ int lane_here() {
+  int lane = threadIdx.x & 31;
+  asm volatile("" : "+r"(lane));
+  return lane;
+}
+
 // A warp's results on their way to memory: two buffers, filled in turn, each
 // written by one TMA store where all 32 rows belong to the expert. Stores of
 // the warp's own held it up behind those of all other SMs, which reach their
@@ -283,7 +302,7 @@ __device__ __forceinline__ void send_wide(Outbox& box, const CUtensorMap* map,
                                           const float (&lo)[32], const float (&hi)[32],
                                           gg_bf16* out, long long ld, int row, int col, int have,
                                           int cols) {
-  const int lane = threadIdx.x & 31;
+  const int lane = lane_here();
   uint4* buf = box.open();
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -326,13 +345,22 @@ __device__ __forceinline__ void glu_grad(float acc, float w, float g, float u, f
   dot = fmaf(acc, gs * u, dot);
 }
 
-__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                               uint32_t idesc, uint32_t accumulate) {
+// make_sdesc with the 64-byte swizzle (layout 4).
+__device__ __forceinline__ uint64_t sdesc64(uint32_t saddr, uint32_t lbo_bytes,
+                                            uint32_t sbo_bytes) {
+  return (make_sdesc(saddr, lbo_bytes, sbo_bytes) & ~(static_cast<uint64_t>(7) << 61)) |
+         static_cast<uint64_t>(4) << 61;
+}
+
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                               uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                               bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 
@@ -401,9 +429,12 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         mbar_init(smem_u32(&st.scale_full[s]), 1);
         mbar_init(smem_u32(&st.scale_empty[s]), kSumWarps);
       }
-      for (int a = 0; a < 2; ++a) {
+      for (int a = 0; a < kBufs; ++a) {
         mbar_init(smem_u32(&st.tfull[a]), 1);
         mbar_init(smem_u32(&st.tempty[a]), 2 * kSumWarps);
+      }
+      mbar_init(smem_u32(&st.all), kSumWarps);
+      for (int a = 0; a < 2; ++a) {
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&st.pair[a][i]), 2);
         mbar_init(smem_u32(&st.group[a]), 4);
       }
@@ -433,7 +464,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
   volatile int* abort_flag = &st.abort_flag;
 
   if (warp < kFirstSum) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<MODE>::kFew));
     if (warp == 0) {
       if (lane == 0) {
         // -------------------------------------------------- TMA producer
@@ -447,12 +478,10 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         Item it;
         ItemReader items;
         while (ok && items.next(st, it, false, true, abort_flag, p.status)) {
-          // two boxes of 64 weight rows
-          int n0 = it.nt * 2 * BM + h * BM, n1 = n0 + BM / 2;
-          if (kGated) {
-            n0 = it.few ? it.nt * BM + h * (BM / 2) : h * p.F + it.nt * BM;
-            n1 = it.few ? p.F + n0 : n0 + BM / 2;
-          }
+          // two boxes of 64 channels: of either half of the block's, or, few
+          // tokens, neighbours
+          const int n0 = kGated ? it.nt * BM + h * 64 : it.nt * 2 * BM + h * (it.few ? BM : 64);
+          const int n1 = kGated ? p.F + n0 : n0 + (it.few ? 64 : BM);
           const int half = it.cols / 2;  // this CTA's tokens, a multiple of 16
           const int r0 = it.row0 + h * half;
           for (int kb = 0; kb < KB; ++kb) {
@@ -469,6 +498,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
               mbar_arrive_expect_tx(smem_u32(&st.full[stage]), 2 * (A_BYTES + half * BK));
             if (kMN) {
               tma_load_3d_pair(sa, &maps.weights, fb, n0, c, it.e);
+              tma_load_3d_pair(sa + A_BYTES / 2, &maps.weights, fb, n1, c, it.e);
             } else {
               tma_load_3d_pair(sa, &maps.weights, fb, c, n0, it.e);
               tma_load_3d_pair(sa + A_BYTES / 2, &maps.weights, fb, c, n1, it.e);
@@ -508,44 +538,59 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         int stage = 0, buf = 0;
         uint32_t phase = 0, buf_phase = 0;
         bool ok = tmem_base == 0;
-        // one group of 128 channels: the MN-major leading offset is not used
-        const uint64_t wdesc = make_sdesc(sbase, kMN ? A_BYTES : 16, 1024);
+        // Weights: 64 channels are 8 KB. K-major: 128-byte rows; MN-major: 64
+        // bytes of channels to each row of the reduction, 64-byte swizzle. Of
+        // a descriptor only the address, in the lower half, changes.
+        const uint64_t wdesc = kMN ? sdesc64(sbase, A_BYTES / 2, 512) : make_sdesc(sbase, 16, 1024);
         const uint64_t tdesc = make_sdesc(sbase + A_BYTES, 16, 1024);
-        constexpr uint64_t kWStep = (kMN ? 32 * BM : 32) >> 4, kTStep = 32 >> 4;
-        Item it;
-        ItemReader items;
-        while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
-          // reductions, for their results are in uniform registers
-          const int few = __reduce_max_sync(0xFFFFFFFFu, it.few);
-          const int n = __reduce_max_sync(0xFFFFFFFFu, it.cols);
-          const uint32_t idesc = idesc_f8(n, few && kMN, !few && kMN);
-          const uint64_t a0 = few ? wdesc : tdesc, b0 = few ? tdesc : wdesc;
-          const uint64_t as = few ? kWStep : kTStep, bs = few ? kTStep : kWStep;
+        constexpr uint32_t kWStep = (kMN ? 32 * 64 : 32) >> 4, kTStep = 32 >> 4;
+        // waits end in a vote: what depends on them stays in uniform registers
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+          return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(bar), parity, abort_flag,
+                                                           p.status)) != 0;
+        };
+        const auto run = [&](auto few, uint32_t idesc) {
+          constexpr bool kFew = decltype(few)::value;
+          const uint64_t a = kFew ? wdesc : tdesc, b = kFew ? tdesc : wdesc;
+          constexpr uint32_t kA = kFew ? kWStep : kTStep, kB = kFew ? kTStep : kWStep;
+          const uint32_t a_hi = static_cast<uint32_t>(a >> 32);
+          const uint32_t b_hi = static_cast<uint32_t>(b >> 32);
           for (int kb = 0; kb < KB; ++kb) {
-            if (!mbar_wait_bounded(smem_u32(&st.tempty[buf]), buf_phase ^ 1u, abort_flag,
-                                   p.status) ||
-                !mbar_wait_bounded(smem_u32(&st.full[stage]), phase, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
+            if (!wait(&st.full[stage], phase)) return false;
+            if (!wait(&st.tempty[buf], buf_phase ^ 1u)) return false;
             tc_fence_after();
-            const uint64_t at = stage * (STAGE_BYTES >> 4);
+            const uint32_t at = stage * (STAGE_BYTES >> 4);
+            const uint32_t a_lo = static_cast<uint32_t>(a) + at;
+            const uint32_t b_lo = static_cast<uint32_t>(b) + at;
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < BK / 32; ++kk)
-                tc_mma_f8_pair(buf * BN, a0 + at + kk * as, b0 + at + kk * bs, idesc,
-                               kk != 0 ? 1u : 0u);
-              tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
+                tc_mma_f8_pair(buf * kBufCols, a_lo + kk * kA, a_hi, b_lo + kk * kB, b_hi, idesc,
+                               kk != 0);
               tc_commit_pair_mc(smem_u32(&st.tfull[buf]), kPairMask);
+              tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
             }
             __syncwarp();
+            if (++buf == kBufs) {
+              buf = 0;
+              buf_phase ^= 1u;
+            }
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1u;
             }
-            buf ^= 1;
-            if (buf == 0) buf_phase ^= 1u;
           }
+          return true;
+        };
+        Item it;
+        ItemReader items;
+        while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
+          // a reduction, for its result is in a uniform register
+          const int n = __reduce_max_sync(0xFFFFFFFFu, it.cols);
+          if (__any_sync(0xFFFFFFFFu, it.few))
+            ok = run(std::true_type{}, idesc_f8(n, kMN, false));
+          else
+            ok = run(std::false_type{}, idesc_f8(BN, false, kMN));
         }
         // All MMAs of the pair must retire before TMEM is freed.
         if (elect_one()) {
@@ -663,7 +708,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<MODE>::kMany));
     // ---------------------------------------------------- sums and epilogue
     const int q = warp & 3;
     const int group = (warp - kFirstSum) >> 2;
@@ -684,64 +729,84 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
       meet_phase ^= 1u;
       return in_time;
     };
+    uint32_t all_phase = 0;
+    const auto met_all = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&st.all));
+      const bool in_time = mbar_wait_bounded(smem_u32(&st.all), all_phase, abort_flag, p.status);
+      all_phase ^= 1u;
+      return in_time;
+    };
     int slot = 0, buf = 0;
     uint32_t slot_phase = 0, buf_phase = 0;
     bool ok = true;
     Item it;
     ItemReader items;
-    // a step's sums and scales are there
-    const auto enter = [&]() {
-      ok = mbar_wait_bounded(smem_u32(&st.scale_full[slot]), slot_phase, abort_flag, p.status) &&
-           mbar_wait_bounded(smem_u32(&st.tfull[buf]), buf_phase, abort_flag, p.status);
-      tc_fence_after();
-      return ok;
+    const auto scales_there = [&]() {
+      ok = mbar_wait_bounded(smem_u32(&st.scale_full[slot]), slot_phase, abort_flag, p.status);
+      return reinterpret_cast<const float*>(smem + kScaleAt + slot * kScaleBytes);
     };
-    // and have been read
-    const auto leave = [&]() {
-      tc_fence_before();
+    const auto scales_read = [&]() {
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_cluster_relaxed(tempty + 8 * buf);
-        mbar_arrive(smem_u32(&st.scale_empty[slot]));
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&st.scale_empty[slot]));
       if (++slot == kScales) {
         slot = 0;
         slot_phase ^= 1u;
       }
-      buf ^= 1;
-      if (buf == 0) buf_phase ^= 1u;
     };
-    const auto scales_of = [&]() {
-      return reinterpret_cast<const float*>(smem + kScaleAt + slot * kScaleBytes);
+    const auto sums_there = [&]() {
+      ok = mbar_wait_bounded(smem_u32(&st.tfull[buf]), buf_phase, abort_flag, p.status);
+      tc_fence_after();
+      return lanes + buf * kBufCols;
     };
+    // they are in registers: the next MMAs may have the buffer
+    const auto sums_read = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(tempty + 8 * buf);
+      if (++buf == kBufs) {
+        buf = 0;
+        buf_phase ^= 1u;
+      }
+    };
+    int item_turn = 0;
     while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
       if (it.few == 0) {
-        // Lane: token; registers: channels, in four chunks of 32.
-        const auto column_of = [&](int c) {
-          return kGated ? (c >> 1) * BM + group * 64 + (c & 1) * 32 : group * BM + c * 32;
-        };
+        // Lane: token; registers: 64 channels (two chunks) of either half of
+        // the block's; gated forward: gate values, then up values.
         float acc[kChunks][32];
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
-        for (int kb = 0; kb < KB && enter(); ++kb) {
-          // the token's scales for the two blocks of 64 channels of this warp
-          const float* own = scales_of() + q * 32 + lane;
-          const float s0 = own[(kGated ? group : 2 * group) * BM];
-          const float s1 = own[(kGated ? 2 + group : 2 * group + 1) * BM];
-          const uint32_t from = lanes + buf * BN;
-          uint32_t v[2][32];
-          tmem_ld32_start(from + column_of(0), v[0]);
+        for (int kb = 0; kb < KB; ++kb) {
+          // the token's scales for either 64 channels
+          const float* own = scales_there() + group * BM + q * 32 + lane;
+          if (!ok) break;
+          const float s[2] = {own[0], own[2 * BM]};
+          scales_read();
+          const uint32_t from = sums_there() + BM * group;
+          if (!ok) break;
+          // The buffer is free as soon as the last loads are done. The branch
+          // between the halves keeps the second one's loads behind the first
+          // one's sums: moved ahead, they spilled them.
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            tmem_wait(v[c & 1]);
-            if (c + 1 < kChunks) tmem_ld32_start(from + column_of(c + 1), v[(c + 1) & 1]);
-            add_scaled(acc[c], v[c & 1], c < 2 ? s0 : s1);
+          for (int hb = 0; hb < 2; ++hb) {
+            uint32_t v0[32], v1[32];
+            tmem_ld32_start(from + 64 * hb, v0);
+            tmem_ld32_start(from + 64 * hb + 32, v1);
+            tmem_wait(v0);
+            tmem_wait(v1);
+            if (hb == 1) sums_read();
+            add_scaled(acc[2 * hb], v0, s[hb]);
+            add_scaled(acc[2 * hb + 1], v1, s[hb]);
+            if (hb == 0 && *abort_flag) ok = false;
+            if (!ok) break;
           }
-          leave();
+          if (!ok) break;
         }
         if (!ok) break;
+        const int lane = lane_here();
         const int row = it.row0 + static_cast<int>(crank) * BM + q * 32;  // the warp's first
         const int have = it.row0 + it.rows - row;
         const bool there = lane < have;
@@ -764,16 +829,21 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         } else if constexpr (MODE == kGradGated) {
           const float w = p.row_scale != nullptr && there ? __ldg(p.row_scale + row + lane) : 1.0f;
           float dot = 0.0f;
-          const int ch0 = it.nt * 2 * BM + group * BM;
+          const int ch0 = it.nt * 2 * BM + group * 64;
           const gg_bf16* h1 = p.H1 + static_cast<long long>(row) * (2LL * p.F) + ch0;
           uint4 rg[4], ru[4];  // a chunk's rows as loads bring them, ahead of its use
+          const auto channel = [&](int c) { return (c >> 1) * BM + (c & 1) * 32; };
           if (ch0 < p.width) {
             load_chunk_raw(rg, h1, 2LL * p.F, have);
             load_chunk_raw(ru, h1 + p.F, 2LL * p.F, have);
           }
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            const int ch = ch0 + 32 * c;
+            const int ch = ch0 + channel(c);
+            if (c == 2) {
+              st.dots[item_turn][group][q * 32 + lane] = dot;
+              dot = 0.0f;
+            }
             if (ch >= p.width) continue;
             // gate and up rows are turned in a buffer's halves, and replaced
             // there by their gradients
@@ -786,9 +856,9 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
               us[to] = ru[j];
             }
             __syncwarp();
-            if (c + 1 < kChunks && ch + 32 < p.width) {
-              load_chunk_raw(rg, h1 + 32 * (c + 1), 2LL * p.F, have);
-              load_chunk_raw(ru, h1 + p.F + 32 * (c + 1), 2LL * p.F, have);
+            if (c + 1 < kChunks && ch0 + channel(c + 1) < p.width) {
+              load_chunk_raw(rg, h1 + channel(c + 1), 2LL * p.F, have);
+              load_chunk_raw(ru, h1 + p.F + channel(c + 1), 2LL * p.F, have);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -832,13 +902,20 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
               if (lane == 0) end_group();
             }
           }
-          if (p.rowdot != nullptr && there)
-            p.rowdot[static_cast<long long>(row + lane) * p.rowdot_stride + 2 * it.nt + group] =
-                dot;
+          if (p.rowdot != nullptr) {
+            // 64 channels of either group to a block of the row sums
+            st.dots[item_turn][2 + group][q * 32 + lane] = dot;
+            if (!(ok = met_all())) break;
+            if (there)
+              p.rowdot[static_cast<long long>(row + lane) * p.rowdot_stride + 2 * it.nt + group] =
+                  st.dots[item_turn][2 * group][q * 32 + lane] +
+                  st.dots[item_turn][2 * group + 1][q * 32 + lane];
+            item_turn ^= 1;
+          }
         } else {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int ch = it.nt * 2 * BM + group * BM + c * 64;
+            const int ch = it.nt * 2 * BM + c * BM + group * 64;
             send_wide(box, &maps.out, acc[2 * c], acc[2 * c + 1], p.C, p.width, row, ch, have,
                       p.width - ch);
           }
@@ -846,10 +923,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         continue;
       }
       // Few tokens. Lane: channel; registers: tokens, in chunks [mine0, mine0 + mine).
-      // `at` is the lane, made anew here: its address arithmetic, kept in
-      // registers over the loop above, spilled that loop's sums.
-      int at = lane;
-      asm volatile("" : "+r"(at));
+      const int at = lane_here();
       float* stg = reinterpret_cast<float*>(staging);
       const float* other = reinterpret_cast<const float*>(
           smem + kStagingAt + ((warp - kFirstSum) ^ 2) * kWarpStaging);
@@ -861,26 +935,34 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
       for (int c = 0; c < kFewTokens / 64; ++c)
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
-      for (int kb = 0; kb < KB && enter(); ++kb) {
-        const float4* f = reinterpret_cast<const float4*>(scales_of() + half * BM + 32 * mine0);
-        const uint32_t from = lanes + buf * BN + 32 * mine0;
+      for (int kb = 0; kb < KB; ++kb) {
+        const float4* f = reinterpret_cast<const float4*>(scales_there() + half * BM + 32 * mine0);
+        if (!ok) break;
+        const uint32_t from = sums_there() + 32 * mine0;
+        if (!ok) break;
+        uint32_t v[kFewTokens / 64][32];
+        // columns that no token has too: loads under a condition made v live over
+        // the whole kernel, and spilled the other loop's sums
+#pragma unroll
+        for (int c = 0; c < kFewTokens / 64; ++c) tmem_ld32_start(from + 32 * c, v[c]);
+#pragma unroll
+        for (int c = 0; c < kFewTokens / 64; ++c) tmem_wait(v[c]);
+        sums_read();
 #pragma unroll
         for (int c = 0; c < kFewTokens / 64; ++c) {
           if (c >= mine) continue;
-          uint32_t v[32];
-          tmem_ld32_start(from + 32 * c, v);
-          tmem_wait(v);
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             const float4 s = f[8 * c + i / 4];
             float2* to = reinterpret_cast<float2*>(&acc[c][i]);
-            to[0] = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
+            const uint32_t* x = &v[c][i];
+            to[0] = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
                                make_float2(s.x, s.y), to[0]);
-            to[1] = __ffma2_rn(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])),
+            to[1] = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
                                make_float2(s.z, s.w), to[1]);
           }
         }
-        leave();
+        scales_read();
       }
       if (!ok) break;
       box.drain();
@@ -963,7 +1045,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
               }
               dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
               dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
-              if ((at & 3) == 0) st.dots[q][t0 + i] = dot;
+              if ((at & 3) == 0) st.dots[0][q][t0 + i] = dot;
             } else {
               if (there) *reinterpret_cast<uint4*>(p.C + r * p.width + ch) = pack8(v);
             }
@@ -977,7 +1059,8 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
           if (!(ok = met())) break;
           const int i = 32 * mine0 + 32 * q + lane;
           if (q < mine && i < it.rows) {
-            const float sum = (st.dots[0][i] + st.dots[1][i]) + (st.dots[2][i] + st.dots[3][i]);
+            const float sum = (st.dots[0][0][i] + st.dots[0][1][i]) +
+                              (st.dots[0][2][i] + st.dots[0][3][i]);
             p.rowdot[(static_cast<long long>(it.row0) + i) * p.rowdot_stride + 2 * it.nt +
                      static_cast<int>(crank)] = sum;
           }
@@ -1027,10 +1110,11 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStrea
   const cuuint64_t wd[3] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.N),
                             static_cast<cuuint64_t>(a.E)};
   const cuuint64_t ws[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.K) * a.N};
-  // forward: 64 channels x 128 codes; gradient: 128 rows of 128 channels
-  const cuuint32_t wbox[3] = {BK, a.grad ? static_cast<cuuint32_t>(BK) : BM / 2u, 1};
+  // forward: 64 channels x 128 codes; gradient: 128 rows of 64 channels
+  const cuuint32_t wbox[3] = {a.grad ? 64u : static_cast<cuuint32_t>(BK),
+                              a.grad ? static_cast<cuuint32_t>(BK) : 64u, 1};
   if (!encode_map(&maps.weights, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, wd, ws, wbox,
-                  CU_TENSOR_MAP_SWIZZLE_128B))
+                  a.grad ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   // results, in pieces of 32 rows
   const bool gated = a.alpha != 0.0f;
