@@ -64,9 +64,7 @@ constexpr int BM = 128;       // channels per CTA
 constexpr int BN = 256;       // most tokens per work item
 constexpr int BK = kF8Block;  // codes per step
 constexpr int kStages = 4;
-constexpr int kBufs = 2;      // of sums in TMEM
-constexpr int kBufCols = 256;
-constexpr int kScales = 4;    // steps of scales ahead
+constexpr int kScales = 4;    // steps of scales ready
 constexpr int kItems = 4;     // work items found ahead
 constexpr int kRaster = 8;    // token blocks that go through the channels together
 constexpr int kItemWarp = 2, kFirstSum = 4;
@@ -78,12 +76,14 @@ constexpr uint16_t kPairMask = 0x3;
 constexpr uint32_t A_BYTES = BM * BK;
 constexpr uint32_t STAGE_BYTES = A_BYTES + BN / 2 * BK;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int kBoxes = 3;     // heights of token boxes: 64, 32 and 16 rows
+constexpr int kBoxes = 4;     // heights of token boxes: 128, 64, 32 and 16 rows
 // Registers per thread of the two roles. The launch has 168 for each of 384
 // threads; either split, of the first four warps and the other eight, is three
 // times that.
+// And the steps of scales on their way (registers of the warp that loads them).
 template <int MODE>
 struct Regs {
+  static constexpr int kAhead = MODE == kGradGated ? 2 : 4;
   static constexpr int kFew = MODE == kGradGated ? 56 : 72;
   static constexpr int kMany = MODE == kGradGated ? 224 : 216;
   static_assert(128 * (kFew + 2 * kMany) <= kThreads * 168, "register split");
@@ -106,18 +106,16 @@ struct SmemTail {
   uint64_t empty[kStages];
   uint64_t scale_full[kScales];
   uint64_t scale_empty[kScales];
-  uint64_t tfull[kBufs];
-  uint64_t tempty[kBufs];    // even CTA
+  uint64_t tfull[2];
+  uint64_t tempty[2];        // even CTA
   uint64_t pair[2][2];       // per group: warps of gate rows and of the matching up rows
   uint64_t group[2];         // the four warps of a group
-  uint64_t all;              // all summing warps
+  uint64_t h1_full[kSumWarps];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
   int total_tiles;
-  // Row sums: of each lane quadrant's 32 channels (few tokens), or of 64, for
-  // items in turn.
-  float dots[2][4][kFewTokens];
+  float dots[4][kFewTokens];  // row sums of each lane quadrant's 32 channels
   int tiles_before[kMaxExperts + 1];
   int row_start[kMaxExperts + 1];
 };
@@ -268,6 +266,13 @@ __device__ __forceinline__ int lane_here() {
   return lane;
 }
 
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
 // A warp's results on their way to memory: two buffers, filled in turn, each
 // written by one TMA store where all 32 rows belong to the expert. Stores of
 // the warp's own held it up behind those of all other SMs, which reach their
@@ -345,13 +350,6 @@ __device__ __forceinline__ void glu_grad(float acc, float w, float g, float u, f
   dot = fmaf(acc, gs * u, dot);
 }
 
-// make_sdesc with the 64-byte swizzle (layout 4).
-__device__ __forceinline__ uint64_t sdesc64(uint32_t saddr, uint32_t lbo_bytes,
-                                            uint32_t sbo_bytes) {
-  return (make_sdesc(saddr, lbo_bytes, sbo_bytes) & ~(static_cast<uint64_t>(7) << 61)) |
-         static_cast<uint64_t>(4) << 61;
-}
-
 __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
                                                uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                                bool accumulate) {
@@ -368,7 +366,7 @@ struct F8Maps {
   CUtensorMap tokens[kBoxes];
   CUtensorMap weights;
   CUtensorMap out;  // C: 32 rows x 64 columns, gated gradient x 32
-  CUtensorMap h1;   // H1_save: 32 x 64
+  CUtensorMap h1;   // H1_save: 32 x 64; gated gradient's H1: 32 x 32
 };
 
 template <int MODE>
@@ -429,15 +427,13 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         mbar_init(smem_u32(&st.scale_full[s]), 1);
         mbar_init(smem_u32(&st.scale_empty[s]), kSumWarps);
       }
-      for (int a = 0; a < kBufs; ++a) {
+      for (int a = 0; a < 2; ++a) {
         mbar_init(smem_u32(&st.tfull[a]), 1);
         mbar_init(smem_u32(&st.tempty[a]), 2 * kSumWarps);
-      }
-      mbar_init(smem_u32(&st.all), kSumWarps);
-      for (int a = 0; a < 2; ++a) {
         for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&st.pair[a][i]), 2);
         mbar_init(smem_u32(&st.group[a]), 4);
       }
+      for (int w = 0; w < kSumWarps; ++w) mbar_init(smem_u32(&st.h1_full[w]), 1);
       for (int i = 0; i < kItems; ++i) {
         mbar_init(smem_u32(&st.item_full[i]), 1);
         // readers: producer, scale and summing warps, and the even CTA's issuer
@@ -478,10 +474,8 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         Item it;
         ItemReader items;
         while (ok && items.next(st, it, false, true, abort_flag, p.status)) {
-          // two boxes of 64 channels: of either half of the block's, or, few
-          // tokens, neighbours
-          const int n0 = kGated ? it.nt * BM + h * 64 : it.nt * 2 * BM + h * (it.few ? BM : 64);
-          const int n1 = kGated ? p.F + n0 : n0 + (it.few ? 64 : BM);
+          // 128 channels; gated forward: 64 gate rows and the matching up rows
+          const int n0 = it.nt * (kGated ? BM : 2 * BM) + h * (kGated ? 64 : BM);
           const int half = it.cols / 2;  // this CTA's tokens, a multiple of 16
           const int r0 = it.row0 + h * half;
           for (int kb = 0; kb < KB; ++kb) {
@@ -498,19 +492,20 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
               mbar_arrive_expect_tx(smem_u32(&st.full[stage]), 2 * (A_BYTES + half * BK));
             if (kMN) {
               tma_load_3d_pair(sa, &maps.weights, fb, n0, c, it.e);
-              tma_load_3d_pair(sa + A_BYTES / 2, &maps.weights, fb, n1, c, it.e);
             } else {
               tma_load_3d_pair(sa, &maps.weights, fb, c, n0, it.e);
-              tma_load_3d_pair(sa + A_BYTES / 2, &maps.weights, fb, c, n1, it.e);
+              if (kGated)
+                tma_load_3d_pair(sa + A_BYTES / 2, &maps.weights, fb, c, p.F + n0, it.e);
             }
+            // few boxes: each costs this thread about 100 cycles of a step's 520
             int i = 0;
-            for (; i + 64 <= half; i += 64)
-              tma_load_2d_pair(sa + A_BYTES + i * BK, &maps.tokens[0], fb, c, r0 + i);
-            if (i + 32 <= half) {
-              tma_load_2d_pair(sa + A_BYTES + i * BK, &maps.tokens[1], fb, c, r0 + i);
-              i += 32;
+#pragma unroll
+            for (int k = 0; k < kBoxes; ++k) {
+              if (half & (BM >> k)) {
+                tma_load_2d_pair(sa + A_BYTES + i * BK, &maps.tokens[k], fb, c, r0 + i);
+                i += BM >> k;
+              }
             }
-            if (i < half) tma_load_2d_pair(sa + A_BYTES + i * BK, &maps.tokens[2], fb, c, r0 + i);
             used |= 1u << stage;
             last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
             if (++stage == kStages) {
@@ -538,12 +533,11 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         int stage = 0, buf = 0;
         uint32_t phase = 0, buf_phase = 0;
         bool ok = tmem_base == 0;
-        // Weights: 64 channels are 8 KB. K-major: 128-byte rows; MN-major: 64
-        // bytes of channels to each row of the reduction, 64-byte swizzle. Of
-        // a descriptor only the address, in the lower half, changes.
-        const uint64_t wdesc = kMN ? sdesc64(sbase, A_BYTES / 2, 512) : make_sdesc(sbase, 16, 1024);
+        // One group of 128 channels: the MN-major leading offset is not used.
+        // Of a descriptor only the address, in the lower half, changes.
+        const uint64_t wdesc = make_sdesc(sbase, kMN ? A_BYTES : 16, 1024);
         const uint64_t tdesc = make_sdesc(sbase + A_BYTES, 16, 1024);
-        constexpr uint32_t kWStep = (kMN ? 32 * 64 : 32) >> 4, kTStep = 32 >> 4;
+        constexpr uint32_t kWStep = (kMN ? 32 * BM : 32) >> 4, kTStep = 32 >> 4;
         // waits end in a vote: what depends on them stays in uniform registers
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
           return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(bar), parity, abort_flag,
@@ -565,16 +559,14 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < BK / 32; ++kk)
-                tc_mma_f8_pair(buf * kBufCols, a_lo + kk * kA, a_hi, b_lo + kk * kB, b_hi, idesc,
+                tc_mma_f8_pair(buf * BN, a_lo + kk * kA, a_hi, b_lo + kk * kB, b_hi, idesc,
                                kk != 0);
               tc_commit_pair_mc(smem_u32(&st.tfull[buf]), kPairMask);
               tc_commit_pair_mc(smem_u32(&st.empty[stage]), kPairMask);
             }
             __syncwarp();
-            if (++buf == kBufs) {
-              buf = 0;
-              buf_phase ^= 1u;
-            }
+            buf ^= 1;
+            if (buf == 0) buf_phase ^= 1u;
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1u;
@@ -620,7 +612,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
       }
     } else {
       // ------------------------------------------------------------ scales
-      // Loaded two steps ahead of their use.
+      // Loaded kAhead steps ahead of their use: their latency is 1000 cycles and more.
       struct Ahead {
         float s[BM / 32];
         float t[4];  // of 64 channels each; few tokens: two
@@ -648,20 +640,6 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
                        : it.nt * 2 * BM + k * (BM / 2);
           // channels that do not exist have a tile of zeros: any scale will do
           ts[k] = t + static_cast<long long>(min(n, most) / kF8Block) * p.t_chan;
-        }
-        if constexpr (MODE == kGradGated) {
-          // the epilogue's H1 on its way to L2
-          const int lines = few ? 2 : 4;  // of 64 channels
-          const int ch = it.nt * 2 * BM + (few ? h * BM : 0);
-          for (int j = 0; j < BM / 32; ++j) {
-            const int i = own + 32 * j + lane;
-            if (i >= it.rows) continue;
-            const gg_bf16* g = p.H1 + (static_cast<long long>(it.row0) + i) * (2LL * p.F) + ch;
-            for (int k = 0; k < lines && ch + 64 * k < p.width; ++k) {
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(g + 64 * k));
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(g + p.F + 64 * k));
-            }
-          }
         }
         const auto load = [&](int kb, Ahead& a) {
           if (kb >= KB) return;
@@ -696,14 +674,16 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
             phase ^= 1u;
           }
         };
-        Ahead a, b;
-        load(0, a);
-        load(1, b);
-        for (int kb = 0; kb < KB && ok; kb += 2) {
-          put(kb, a);
-          load(kb + 2, a);
-          put(kb + 1, b);
-          load(kb + 3, b);
+        constexpr int kAhead = Regs<MODE>::kAhead;
+        Ahead a[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) load(j, a[j]);
+        for (int kb = 0; kb < KB && ok; kb += kAhead) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            put(kb + j, a[j]);
+            load(kb + j + kAhead, a[j]);
+          }
         }
       }
     }
@@ -717,6 +697,9 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
     uint8_t* staging = smem + kStagingAt + (warp - kFirstSum) * kWarpStaging;
     Outbox box;
     box.at = staging;
+    int h1_chunks = 0;  // gated gradient: the item's chunks
+    bool h1_pending = false;
+    uint32_t h1_phase = 0;
     const uint32_t tempty = mapa_shared(smem_u32(&st.tempty[0]), 0);
     // What these warps wait for each other at: a barrier that a warp whose wait
     // ran out does not leave the others in.
@@ -727,14 +710,6 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
       if (lane == 0) mbar_arrive(meet);
       const bool in_time = mbar_wait_bounded(meet, meet_phase, abort_flag, p.status);
       meet_phase ^= 1u;
-      return in_time;
-    };
-    uint32_t all_phase = 0;
-    const auto met_all = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&st.all));
-      const bool in_time = mbar_wait_bounded(smem_u32(&st.all), all_phase, abort_flag, p.status);
-      all_phase ^= 1u;
       return in_time;
     };
     int slot = 0, buf = 0;
@@ -757,23 +732,46 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
     const auto sums_there = [&]() {
       ok = mbar_wait_bounded(smem_u32(&st.tfull[buf]), buf_phase, abort_flag, p.status);
       tc_fence_after();
-      return lanes + buf * kBufCols;
+      return lanes + buf * BN;
     };
     // they are in registers: the next MMAs may have the buffer
     const auto sums_read = [&]() {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(tempty + 8 * buf);
-      if (++buf == kBufs) {
-        buf = 0;
-        buf_phase ^= 1u;
-      }
+      buf ^= 1;
+      if (buf == 0) buf_phase ^= 1u;
     };
-    int item_turn = 0;
     while (ok && items.next(st, it, true, lane == 0, abort_flag, p.status)) {
       if (it.few == 0) {
-        // Lane: token; registers: 64 channels (two chunks) of either half of
-        // the block's; gated forward: gate values, then up values.
+        // Lane: token; registers: 128 channels of the CTA `group`, in four
+        // chunks of 32; gated forward: 64 gate values, then their up values.
+        if constexpr (MODE == kGradGated) {
+          // H1 of the first two chunks into the idle buffers, of the others
+          // into L2, while the products run: the epilogue read it from memory
+          // chunk by chunk, 13 us an item
+          const int row = it.row0 + static_cast<int>(crank) * BM + q * 32;
+          const int ch = it.nt * 2 * BM + group * BM;
+          h1_chunks = row < it.row0 + it.rows ? max(0, min(kChunks, (p.width - ch) / 32)) : 0;
+          if (h1_chunks > 0) {
+            box.drain();
+            if (lane == 0) {
+              const uint32_t bar = smem_u32(&st.h1_full[warp - kFirstSum]);
+              fence_proxy_async();
+              mbar_arrive_expect_tx(bar, kWarpStaging);  // widths are multiples of 64
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t to = smem_u32(staging) + c * (kWarpStaging / 2);
+                tma_load_2d(to, &maps.h1, bar, ch + 32 * c, row);
+                tma_load_2d(to + kWarpStaging / 4, &maps.h1, bar, p.F + ch + 32 * c, row);
+              }
+              for (int c = 2; c < h1_chunks; ++c) {
+                tma_prefetch_2d(&maps.h1, ch + 32 * c, row);
+                tma_prefetch_2d(&maps.h1, p.F + ch + 32 * c, row);
+              }
+            }
+            h1_pending = true;
+          }
+        }
         float acc[kChunks][32];
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
@@ -781,9 +779,10 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
           for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
         for (int kb = 0; kb < KB; ++kb) {
           // the token's scales for either 64 channels
-          const float* own = scales_there() + group * BM + q * 32 + lane;
+          const float* own = scales_there() + q * 32 + lane;
           if (!ok) break;
-          const float s[2] = {own[0], own[2 * BM]};
+          const float s[2] = {own[(kGated ? group : 2 * group) * BM],
+                              own[(kGated ? 2 + group : 2 * group + 1) * BM]};
           scales_read();
           const uint32_t from = sums_there() + BM * group;
           if (!ok) break;
@@ -829,36 +828,41 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         } else if constexpr (MODE == kGradGated) {
           const float w = p.row_scale != nullptr && there ? __ldg(p.row_scale + row + lane) : 1.0f;
           float dot = 0.0f;
-          const int ch0 = it.nt * 2 * BM + group * 64;
+          const int ch0 = it.nt * 2 * BM + group * BM;
           const gg_bf16* h1 = p.H1 + static_cast<long long>(row) * (2LL * p.F) + ch0;
-          uint4 rg[4], ru[4];  // a chunk's rows as loads bring them, ahead of its use
-          const auto channel = [&](int c) { return (c >> 1) * BM + (c & 1) * 32; };
-          if (ch0 < p.width) {
-            load_chunk_raw(rg, h1, 2LL * p.F, have);
-            load_chunk_raw(ru, h1 + p.F, 2LL * p.F, have);
+          if (h1_chunks > 0) {
+            if (!(ok = mbar_wait_bounded(smem_u32(&st.h1_full[warp - kFirstSum]), h1_phase,
+                                         abort_flag, p.status)))
+              break;
+            h1_phase ^= 1u;
+            h1_pending = false;
           }
+          uint4 rg[4], ru[4];  // a later chunk's rows as loads bring them
+          if (h1_chunks > 2) {
+            load_chunk_raw(rg, h1 + 64, 2LL * p.F, have);
+            load_chunk_raw(ru, h1 + p.F + 64, 2LL * p.F, have);
+          }
+          box.turn = 0;
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            const int ch = ch0 + channel(c);
-            if (c == 2) {
-              st.dots[item_turn][group][q * 32 + lane] = dot;
-              dot = 0.0f;
-            }
-            if (ch >= p.width) continue;
-            // gate and up rows are turned in a buffer's halves, and replaced
-            // there by their gradients
+            const int ch = ch0 + 32 * c;
+            if (c >= h1_chunks) continue;
+            // gate and up rows lie in a buffer's halves, and are replaced there
+            // by their gradients
             uint4* gs = box.open();
             uint4* us = gs + 32 * 4;
+            if (c >= 2) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int to = stage_slot(8 * j + (lane >> 2), lane & 3);
-              gs[to] = rg[j];
-              us[to] = ru[j];
-            }
-            __syncwarp();
-            if (c + 1 < kChunks && ch0 + channel(c + 1) < p.width) {
-              load_chunk_raw(rg, h1 + channel(c + 1), 2LL * p.F, have);
-              load_chunk_raw(ru, h1 + p.F + channel(c + 1), 2LL * p.F, have);
+              for (int j = 0; j < 4; ++j) {
+                const int to = stage_slot(8 * j + (lane >> 2), lane & 3);
+                gs[to] = rg[j];
+                us[to] = ru[j];
+              }
+              __syncwarp();
+              if (c == 2 && h1_chunks > 3) {
+                load_chunk_raw(rg, h1 + 96, 2LL * p.F, have);
+                load_chunk_raw(ru, h1 + p.F + 96, 2LL * p.F, have);
+              }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -902,20 +906,14 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
               if (lane == 0) end_group();
             }
           }
-          if (p.rowdot != nullptr) {
-            // 64 channels of either group to a block of the row sums
-            st.dots[item_turn][2 + group][q * 32 + lane] = dot;
-            if (!(ok = met_all())) break;
-            if (there)
-              p.rowdot[static_cast<long long>(row + lane) * p.rowdot_stride + 2 * it.nt + group] =
-                  st.dots[item_turn][2 * group][q * 32 + lane] +
-                  st.dots[item_turn][2 * group + 1][q * 32 + lane];
-            item_turn ^= 1;
-          }
+          // the group's 128 channels are one block of the row sums
+          if (p.rowdot != nullptr && there)
+            p.rowdot[static_cast<long long>(row + lane) * p.rowdot_stride + 2 * it.nt + group] =
+                dot;
         } else {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int ch = it.nt * 2 * BM + c * BM + group * 64;
+            const int ch = it.nt * 2 * BM + group * BM + c * 64;
             send_wide(box, &maps.out, acc[2 * c], acc[2 * c + 1], p.C, p.width, row, ch, have,
                       p.width - ch);
           }
@@ -1045,7 +1043,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
               }
               dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
               dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
-              if ((at & 3) == 0) st.dots[0][q][t0 + i] = dot;
+              if ((at & 3) == 0) st.dots[q][t0 + i] = dot;
             } else {
               if (there) *reinterpret_cast<uint4*>(p.C + r * p.width + ch) = pack8(v);
             }
@@ -1059,8 +1057,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
           if (!(ok = met())) break;
           const int i = 32 * mine0 + 32 * q + lane;
           if (q < mine && i < it.rows) {
-            const float sum = (st.dots[0][0][i] + st.dots[0][1][i]) +
-                              (st.dots[0][2][i] + st.dots[0][3][i]);
+            const float sum = (st.dots[0][i] + st.dots[1][i]) + (st.dots[2][i] + st.dots[3][i]);
             p.rowdot[(static_cast<long long>(it.row0) + i) * p.rowdot_stride + 2 * it.nt +
                      static_cast<int>(crank)] = sum;
           }
@@ -1068,8 +1065,14 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         }
       }
     }
+    // (after an abort) H1 that is still on its way to shared memory
+    if (h1_pending)
+      (void)mbar_wait_bounded(smem_u32(&st.h1_full[warp - kFirstSum]), h1_phase, nullptr,
+                              p.status);
   }
 
+  // (after an abort) no load of TMEM is under way when it is freed
+  if (warp >= kFirstSum) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
   // shared memory stays until the last stores have read it
   if (warp >= kFirstSum && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tc_fence_before();
@@ -1102,7 +1105,7 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStrea
   const cuuint64_t td[2] = {static_cast<cuuint64_t>(red), static_cast<cuuint64_t>(a.R_cap)};
   const cuuint64_t ts[1] = {static_cast<cuuint64_t>(red)};
   for (int i = 0; i < kBoxes; ++i) {
-    const cuuint32_t tbox[2] = {BK, 64u >> i};
+    const cuuint32_t tbox[2] = {BK, static_cast<cuuint32_t>(BM) >> i};
     if (!encode_map(&maps.tokens[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, 2, td, ts, tbox,
                     CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
@@ -1110,11 +1113,10 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStrea
   const cuuint64_t wd[3] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.N),
                             static_cast<cuuint64_t>(a.E)};
   const cuuint64_t ws[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.K) * a.N};
-  // forward: 64 channels x 128 codes; gradient: 128 rows of 64 channels
-  const cuuint32_t wbox[3] = {a.grad ? 64u : static_cast<cuuint32_t>(BK),
-                              a.grad ? static_cast<cuuint32_t>(BK) : 64u, 1};
+  // 128 channels x 128 codes (gated forward 64); gradient: 128 rows of 128 channels
+  const cuuint32_t wbox[3] = {BK, !a.grad && a.alpha != 0.0f ? 64u : 128u, 1};
   if (!encode_map(&maps.weights, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, wd, ws, wbox,
-                  a.grad ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   // results, in pieces of 32 rows
   const bool gated = a.alpha != 0.0f;
@@ -1127,6 +1129,9 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStrea
                   narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   maps.h1 = maps.out;
+  if (narrow && !encode_map(&maps.h1, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.H1, 2, od, os, obox,
+                            CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
   if (a.H1_save != nullptr) {
     const cuuint64_t hd[2] = {static_cast<cuuint64_t>(a.N), static_cast<cuuint64_t>(a.R_cap)};
     const cuuint64_t hs[1] = {2ull * a.N};
