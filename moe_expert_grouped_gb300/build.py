@@ -20,8 +20,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libgg.so")
 SOURCES = ["gg_api.cu", "gg_permute.cu", "gg_gemm.cu", "gg_gemm_mx.cu", "gg_mx_quant.cu",
-           "gg_route.cu", "gg_wgrad.cu", "gg_adamw.cu",
-           "gg_f8_quant.cu", "gg_gemm_f8.cu", "gg_q8_quant.cu", "gg_gemm_q8.cu", "gg_q8_rows.cu"]
+           "gg_route.cu", "gg_wgrad.cu", "gg_q8_quant.cu", "gg_gemm_q8.cu", "gg_q8_rows.cu",
+           "gg_f8_quant.cu", "gg_gemm_f8.cu", "gg_f8_rows.cu", "gg_adamw.cu"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

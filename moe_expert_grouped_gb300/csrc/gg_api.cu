@@ -1189,7 +1189,9 @@ gg_status gg_f8_grouped_gemm(const uint8_t* Aq, const float* As, const uint8_t* 
   F8GemmArgs a =
       f8_args(false, Aq, As, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws);
   a.H1_save = H1_save;
-  return from_cuda(launch_f8_gemm(a, dev, reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return from_cuda(f8_rows_fits(R_cap, E) ? launch_f8_rows(a, nullptr, dev, st)
+                                          : launch_f8_gemm(a, dev, st));
 }
 
 // Rows of `width` columns quantised into the workspace, which then holds A and As of `a`.
@@ -1221,6 +1223,7 @@ gg_status gg_f8_grouped_fwd(const gg_bf16* A, const uint8_t* Wq, const float* Ws
   F8GemmArgs a =
       f8_args(false, nullptr, nullptr, Wq, Ws, offsets, E, R_cap, K, N, epi, prob_of_row, C, ws);
   a.H1_save = H1_save;
+  if (f8_rows_fits(R_cap, E)) return from_cuda(launch_f8_rows(a, A, dev, st));
   if (f8_rows_to_ws(A, K, &a, ws, dev, st) != cudaSuccess) return GG_ERR_CUDA;
   return from_cuda(launch_f8_gemm(a, dev, st));
 }

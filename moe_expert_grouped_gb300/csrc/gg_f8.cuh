@@ -24,10 +24,8 @@ __device__ __forceinline__ void f8_scale(uint32_t top, float& inv, float& scale)
 
 // Codes of (lo, hi), to nearest even.
 __device__ __forceinline__ uint32_t f8_codes2(float lo, float hi, float inv) {
-  // a NaN times 0 stays one: E4M3 has it, the codes of such a block are 0
-  return inv == 0.0f ? 0u
-                     : __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(lo, inv), __fmul_rn(hi, inv)),
-                                                __NV_SATFINITE, __NV_E4M3);
+  return __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(lo, inv), __fmul_rn(hi, inv)),
+                                  __NV_SATFINITE, __NV_E4M3);
 }
 
 }  // namespace

@@ -4,8 +4,8 @@
 // elements of a weight. Rounded to nearest even; |x| 448 / a is at most 448
 // but for its rounding, and saturates there.
 //
-// Rows: one warp per source row, half a warp per block, the row in registers
-// up to 4096 columns so that all its loads are in flight together. The scales
+// Rows: one warp per source row, eight lanes per block (32 bytes each), the row
+// in registers up to 4096 columns so that all its loads are in flight together. The scales
 // of one block of columns lie together, S[ceil(K / 128)][R_cap]: the products'
 // tiles take a block of rows for one block of columns at a time.
 //
@@ -31,6 +31,8 @@ __device__ __forceinline__ uint32_t top_of(uint4 w) {  // largest |BF16|, as its
 }
 
 __device__ __forceinline__ uint2 codes8(uint4 w, float inv) {
+  // a NaN times 0 stays one, and E4M3 has it: the codes of such a block are 0
+  if (inv == 0.0f) return make_uint2(0u, 0u);
   uint2 q;
   q.x = f8_codes2(bf16_lo(w.x), bf16_hi(w.x), inv) |
         f8_codes2(bf16_lo(w.y), bf16_hi(w.y), inv) << 16;
@@ -39,16 +41,16 @@ __device__ __forceinline__ uint2 codes8(uint4 w, float inv) {
   return q;
 }
 
-// V: 16-byte pieces of a row per lane.
+// V: 32-byte pieces (16 columns) of a row per lane; eight lanes share a scale.
 template <int V>
 __global__ void __launch_bounds__(32 * kWarps)
 f8_quantize_kernel(const uint4* __restrict__ src, long long rows, int K,
                    const int32_t* __restrict__ offsets, int E,
                    const int32_t* __restrict__ row_of_slot, int k, int R_cap,
-                   uint2* __restrict__ Q, float* __restrict__ S, int32_t* status) {
+                   uint4* __restrict__ Q, float* __restrict__ S, int32_t* status) {
   grid_dependents_launch();  // the product's set-up need not wait for the codes
   const int lane = threadIdx.x & 31;
-  const int vec = K / 8;
+  const int vec = K / 16;
   if (offsets != nullptr) {
     const int used = offsets[E];
     rows = used < 0 ? 0 : (used < rows ? used : rows);
@@ -64,30 +66,33 @@ f8_quantize_kernel(const uint4* __restrict__ src, long long rows, int K,
       }
     }
     const int copies = row_of_slot != nullptr ? k : 1;
-    for (int c0 = 0; c0 < vec; c0 += 32 * V) {  // once, up to 256 V columns
-      const uint4* x = src + r * vec + c0;
-      uint4 held[V];
+    for (int c0 = 0; c0 < vec; c0 += 32 * V) {  // once, up to 512 V columns
+      const uint4* x = src + 2 * (r * vec + c0 + lane);
+      uint4 held[V][2];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = lane + 32 * i;
-        held[i] = c0 + c < vec ? x[c] : make_uint4(0u, 0u, 0u, 0u);
+        const bool there = c0 + 32 * i + lane < vec;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          held[i][h] = there ? __ldcs(x + 64 * i + h) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = c0 + 32 * i + lane;
         if (c - lane >= vec) break;
-        uint32_t top = top_of(held[i]);
+        uint32_t top = max(top_of(held[i][0]), top_of(held[i][1]));
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(kFull, top, d));
+        for (int d = 4; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(kFull, top, d));
         float inv, scale;
         f8_scale(top << 16, inv, scale);
-        const uint2 q = codes8(held[i], inv);
-        const int block = c >> 4;
+        const uint2 lo = codes8(held[i][0], inv), hi = codes8(held[i][1], inv);
+        const uint4 q = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        const int block = c >> 3;
         for (int j = 0; j < copies; ++j) {
           const long long to = row_of_slot != nullptr ? __shfl_sync(kFull, dst, j) : r;
           if (to < 0 || c >= vec) continue;
           Q[to * vec + c] = q;
-          if ((lane & 15) == 0) S[static_cast<long long>(block) * R_cap + to] = scale;
+          if ((lane & 7) == 0) S[static_cast<long long>(block) * R_cap + to] = scale;
         }
       }
     }
@@ -137,17 +142,16 @@ cudaError_t launch_f8_quantize(const gg_bf16* src, long long rows, int K, const 
   long long blocks = (rows + kWarps - 1) / kWarps;
   const long long cap = static_cast<long long>(sm_count) * 8;
   if (blocks > cap) blocks = cap;
-  const int pieces = (K / 8 + 31) / 32;  // per lane
+  const int pieces = (K / 16 + 31) / 32;  // per lane
   const auto go = [&](auto kernel) {
     kernel<<<static_cast<int>(blocks), 32 * kWarps, 0, stream>>>(
         reinterpret_cast<const uint4*>(src), rows, K, offsets, E, row_of_slot, k, R_cap,
-        reinterpret_cast<uint2*>(Q), S, status);
+        reinterpret_cast<uint4*>(Q), S, status);
   };
   if (pieces <= 1) go(f8_quantize_kernel<1>);
   else if (pieces <= 2) go(f8_quantize_kernel<2>);
   else if (pieces <= 4) go(f8_quantize_kernel<4>);
-  else if (pieces <= 8) go(f8_quantize_kernel<8>);
-  else go(f8_quantize_kernel<16>);
+  else go(f8_quantize_kernel<8>);
   count_launch();
   return cudaGetLastError();
 }

@@ -1,0 +1,465 @@
+// gg_f8_rows.cu — the forward product of gg_gemm_f8.cu for few rows per expert
+// (tokens being decoded), where reading the weights is all that costs:
+//   C[r][n] = sum_b s[b][r] t[e][n / 128][b] sum_{k in block b} q[r][k] w[e][n][k],
+// gated activations fused, in one launch: BF16 rows are quantised where they
+// are used.
+//
+// A tile is 32 rows of one live expert's weight (gated: 16 gate rows and the
+// matching 16 up rows). One block of 16 warps per SM; kParts warps share a
+// tile, each taking every kParts-th block of 128 codes. Every warp has a ring
+// of its own in shared memory that TMA fills with 32 x 128 weight codes per
+// stage, so 192 KB of weights per SM are always on their way, across tiles too.
+//
+// A lane reads 16 consecutive codes of four weight rows at a time and widens
+// them to FP16 (exact); its own token's codes it makes in registers, 32 columns
+// of one of up to eight tokens, with the block's maximum from the other three
+// lanes of the token. So both have the fragments of mma.m16n8k16: which k of a
+// fragment a code stands for does not matter as long as both operands agree.
+// The sums of a block are scaled and added up in fp32; the other parts' go
+// through shared memory to the first, which adds them in order.
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "gg_f8.cuh"
+#include "gg_internal.h"
+#include "gg_launch.cuh"
+#include "gg_ptx.cuh"
+
+namespace gg {
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTurns = kMaxExperts / 32;  // groups of 32 experts
+static_assert(kTurns <= 32 && kMaxExperts % kThreads == 0, "one warp scans the groups");
+constexpr int kRows = 32;          // weight rows per tile
+constexpr int kChunk = kF8Block;   // codes of K per stage
+constexpr int kTokens = 8;         // tokens multiplied with each piece of weight
+constexpr uint32_t kStageBytes = kRows * kChunk;
+constexpr int kStages = 3;         // of a warp's ring
+constexpr uint32_t kWarpBytes = kStages * kStageBytes;
+
+struct SmemTail {
+  uint64_t full[kWarps][kStages];
+  int abort_flag;
+  int bad;
+  int n_live;
+  int in_turn[kTurns];
+  uint16_t live[kMaxExperts];  // experts that have rows
+  float part[kWarps][8][32];   // sums of the parts but the first, as their lanes hold them
+};
+
+constexpr size_t kSmemBytes = 1024 + kWarps * kWarpBytes + sizeof(SmemTail);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+struct RowsParams {
+  const gg_bf16* x;     // BF16 rows, or null:
+  const uint8_t* A;     // codes
+  const float* As;      // and scales [ceil(K / 128)][R_cap]
+  const float* Bs;
+  const int32_t* offsets;
+  int E, R_cap, K, N, F;
+  float alpha;
+  const float* row_scale;
+  gg_bf16* C;
+  gg_bf16* H1_save;
+  int32_t* status;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four E4M3 codes -> four FP16 of the same value.
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu),
+                                                    __NV_E4M3);
+  const __half2_raw hi =
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
+  return make_uint2(static_cast<uint32_t>(lo.x) | static_cast<uint32_t>(lo.y) << 16,
+                    static_cast<uint32_t>(hi.x) | static_cast<uint32_t>(hi.y) << 16);
+}
+
+__device__ __forceinline__ uint32_t top_of(uint4 w) {  // largest |BF16|, as its bits
+  const uint32_t a = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                              __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+  return max(a & 0xFFFFu, a >> 16);
+}
+
+// Where a warp is in its stages: tile, first token of the pass, block of K.
+struct Cursor {
+  int tile, first, chunk;
+  int e, n0;       // the tile's expert and first weight row
+  int row0, rows;  // the expert's rows
+};
+
+// A lane's 32 columns of its token as they come from memory.
+template <bool kBf16>
+struct Token {
+  uint4 v[kBf16 ? 4 : 2];
+  float s;      // codes: the block's scale of this lane's token
+};
+
+template <bool kGated, bool kBf16, int kParts>
+__global__ void __launch_bounds__(kThreads, 1)
+f8_rows_kernel(const __grid_constant__ CUtensorMap mapB, const RowsParams p) {
+  constexpr int kGroups = kWarps / kParts;  // tiles at a time
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  SmemTail& st = *reinterpret_cast<SmemTail*>(smem + kWarps * kWarpBytes);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+
+  // The live experts, in order: 32 experts per warp and turn, so that all
+  // offsets are on their way at once.
+  if (threadIdx.x == 0) {
+    st.abort_flag = 0;
+    st.bad = 0;
+    tma_prefetch_desc(&mapB);
+  }
+  for (int i = threadIdx.x; i < kWarps * kStages; i += kThreads)
+    mbar_init(smem_u32(&st.full[i / kStages][i % kStages]), 1);
+  mbar_fence_init();
+  fence_proxy_async();
+  __syncthreads();
+  uint32_t live[kMaxExperts / kThreads];  // of the warp's turns: lanes with rows
+#pragma unroll
+  for (int i = 0; i < kMaxExperts / kThreads; ++i) {
+    const int e = i * kThreads + threadIdx.x;
+    const int o0 = e < p.E ? p.offsets[e] : 0;
+    const int o1 = e < p.E ? p.offsets[e + 1] : 0;
+    if (o1 < o0 || o0 < 0 || o1 > p.R_cap || (e == 0 && o0 != 0)) st.bad = 1;
+    live[i] = __ballot_sync(0xFFFFFFFFu, o1 > o0);
+    if (lane == 0) st.in_turn[i * kWarps + warp] = __popc(live[i]);
+  }
+  __syncthreads();
+  {
+    // experts of the turns before each of this warp's
+    const int mine = lane < kTurns ? st.in_turn[lane] : 0;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int n = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += n;
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / kThreads; ++i) {
+      const int before = __shfl_sync(0xFFFFFFFFu, upto - mine, i * kWarps + warp);
+      if (live[i] >> lane & 1u)
+        st.live[before + __popc(live[i] & ((1u << lane) - 1u))] =
+            static_cast<uint16_t>(i * kThreads + threadIdx.x);
+    }
+    const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    if (threadIdx.x == 0) {
+      st.n_live = st.bad ? 0 : all;
+      if (st.bad && blockIdx.x == 0) set_status(p.status, GG_ERR_DEVICE_BAD_OFFSETS);
+    }
+  }
+  __syncthreads();
+
+  volatile int* abort_flag = &st.abort_flag;
+  constexpr int kOut = kGated ? kRows / 2 : kRows;  // outputs per tile and token
+  const int per = (kGated ? p.F : p.N) / kOut;      // tiles per expert
+  const int total = st.n_live * per;
+  const int chunks = (p.K + kChunk - 1) / kChunk;
+  const int NB = (p.N + kF8Block - 1) / kF8Block;
+  const int group = warp / kParts, part_of = warp % kParts;
+  const int first_tile = group * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  const int tile_step = kGroups * static_cast<int>(gridDim.x);
+  uint8_t* ring = smem + warp * kWarpBytes;
+  const uint32_t ring_addr = raw_addr + pad + warp * kWarpBytes;
+
+  const auto enter = [&](Cursor& c) {  // c.tile has changed
+    if (c.tile >= total) return;
+    const int a = c.tile / per;
+    c.e = st.live[a];
+    c.n0 = (c.tile - a * per) * kOut;
+    c.row0 = p.offsets[c.e];
+    c.rows = p.offsets[c.e + 1] - c.row0;
+  };
+  const auto advance = [&](Cursor& c) {
+    c.chunk += kParts;
+    if (c.chunk < chunks) return;
+    c.chunk = part_of;
+    c.first += kTokens;
+    if (c.first < c.rows) return;
+    c.first = 0;
+    c.tile += tile_step;
+    enter(c);
+  };
+  const auto load_weights = [&](const Cursor& c, int s) {
+    const uint32_t bar = smem_u32(&st.full[warp][s]);
+    const uint32_t dst = ring_addr + s * kStageBytes;
+    mbar_arrive_expect_tx(bar, kStageBytes);
+    tma_load_3d(dst, &mapB, bar, c.chunk * kChunk, c.n0, c.e);
+    if (kGated)
+      tma_load_3d(dst + kStageBytes / 2, &mapB, bar, c.chunk * kChunk, p.F + c.n0, c.e);
+  };
+  // this lane's columns 32 t .. + 31 of a block of token g
+  const auto load_token = [&](const Cursor& c, Token<kBf16>& to) {
+    const int col = c.chunk * kChunk + 32 * t;  // K is a multiple of 64: all 32 exist or none
+    const bool there = c.tile < total && c.first + g < c.rows && col < p.K;
+    const long long row = static_cast<long long>(c.row0) + c.first + g;
+    constexpr int kPieces = kBf16 ? 4 : 2;
+    const uint4* from = kBf16 ? reinterpret_cast<const uint4*>(p.x + row * p.K + col)
+                              : reinterpret_cast<const uint4*>(p.A + row * p.K + col);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) to.v[i] = there ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+    if (!kBf16)
+      to.s = c.tile < total && c.first + g < c.rows
+                 ? __ldg(p.As + static_cast<long long>(c.chunk) * p.R_cap + row)
+                 : 0.0f;
+  };
+  // the weight's scales of a block: of the first and of the second 16 rows
+  const auto load_scales = [&](const Cursor& c, float& t0, float& t1) {
+    if (c.tile >= total) return;
+    const float* b = p.Bs + (static_cast<long long>(c.e) * NB + c.n0 / kF8Block) * chunks + c.chunk;
+    t0 = __ldg(b);
+    t1 = kGated ? __ldg(p.Bs +
+                        (static_cast<long long>(c.e) * NB + (p.F + c.n0) / kF8Block) * chunks +
+                        c.chunk)
+                : t0;
+  };
+
+  Cursor at{first_tile, 0, part_of, 0, 0, 0, 0};  // of the stage consumed next
+  enter(at);
+  Cursor ahead = at;                    // of the stage loaded next
+  uint32_t pending = 0;                 // stages with a load that was not waited for
+  const bool works = part_of < chunks;  // short K: the later parts have nothing
+  if (works) {
+    for (int s = 0; s < kStages && ahead.tile < total; ++s) {
+      if (lane == 0) load_weights(ahead, s);
+      pending |= 1u << s;
+      advance(ahead);
+    }
+  }
+  // tokens and scales one block ahead of their use
+  Cursor next = at;
+  Token<kBf16> held;
+  float t0 = 0.0f, t1 = 0.0f;
+  if (works) {
+    load_token(next, held);
+    load_scales(next, t0, t1);
+    advance(next);
+  }
+
+  bool ok = true;
+  int s = 0;
+  uint32_t phase = 0;
+  int failed = 0;
+  uint32_t failed_phase = 0;
+  for (; at.tile < total; at.tile += tile_step, enter(at)) {
+    for (int first = 0; first < at.rows; first += kTokens) {
+      float sum[2][4] = {};
+      for (int chunk = part_of; chunk < chunks; chunk += kParts) {
+        // codes of this lane's columns as FP16, and the scale of the token
+        uint2 b[8];
+        float scale;
+        if constexpr (kBf16) {
+          uint32_t top = max(max(top_of(held.v[0]), top_of(held.v[1])),
+                             max(top_of(held.v[2]), top_of(held.v[3])));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          float inv;
+          f8_scale(top << 16, inv, scale);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {held.v[i].x, held.v[i].y, held.v[i].z, held.v[i].w};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t q = f8_codes2(bf16_lo(w[2 * j]), bf16_hi(w[2 * j]), inv) |
+                           f8_codes2(bf16_lo(w[2 * j + 1]), bf16_hi(w[2 * j + 1]), inv) << 16;
+              if (inv == 0.0f) q = 0u;  // a block with a NaN: its codes are 0
+              b[2 * i + j] = widen4(q);
+            }
+          }
+        } else {
+          scale = held.s;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) b[i] = widen4((&held.v[i / 4].x)[i % 4]);
+        }
+        const float w0 = t0, w1 = t1;
+        load_token(next, held);
+        load_scales(next, t0, t1);
+        advance(next);
+        if (ok) {
+          ok = mbar_wait_bounded(smem_u32(&st.full[warp][s]), phase, abort_flag, p.status);
+          if (ok)
+            pending &= ~(1u << s);
+          else
+            failed = s, failed_phase = phase;
+        }
+        const uint8_t* stage = ring + s * kStageBytes;
+        float acc[2][4] = {};
+        // 16-byte piece 2t + h of the swizzled 128-byte rows: the eight lanes
+        // of an access, two neighbouring rows, then hit all banks
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t piece = ((2 * t + h) ^ g) << 4;
+          uint4 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = *reinterpret_cast<const uint4*>(stage + (8 * i + g) * kChunk + piece);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint2 r0 = widen4((&w[0].x)[q]), r1 = widen4((&w[1].x)[q]);
+            const uint2 r2 = widen4((&w[2].x)[q]), r3 = widen4((&w[3].x)[q]);
+            const uint32_t a0[4] = {r0.x, r1.x, r0.y, r1.y};
+            const uint32_t a1[4] = {r2.x, r3.x, r2.y, r3.y};
+            const uint2 x = b[4 * h + q];
+            mma_f16(acc[0], a0, x.x, x.y);
+            mma_f16(acc[1], a1, x.x, x.y);
+          }
+        }
+        __syncwarp();  // every lane has read the stage
+        if (ok && ahead.tile < total) {
+          if (lane == 0) {
+            fence_proxy_async();
+            load_weights(ahead, s);
+          }
+          pending |= 1u << s;
+          advance(ahead);
+        }
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1u;
+        }
+        // D fragment: rows g (values 0, 1) and g + 8 (2, 3), tokens 2t and 2t + 1
+        const float s0 = __shfl_sync(0xFFFFFFFFu, scale, 8 * t);
+        const float s1 = __shfl_sync(0xFFFFFFFFu, scale, 8 * t + 4);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float f = v & 1 ? s1 : s0;
+          sum[0][v] = fmaf(acc[0][v], f * w0, sum[0][v]);
+          sum[1][v] = fmaf(acc[1][v], f * w1, sum[1][v]);
+        }
+      }
+      if (part_of != 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) st.part[warp][i][lane] = sum[i / 4][i % 4];
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kParts) : "memory");
+      if (part_of == 0) {
+#pragma unroll
+        for (int w = 1; w < kParts; ++w)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i / 4][i % 4] += st.part[warp + w][i][lane];
+        const int have = ok ? min(kTokens, at.rows - first) : 0;
+        const long long width = kGated ? p.F : p.N;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int tok = 2 * t + (v & 1), c = g + (v & 2 ? 8 : 0);
+          if (tok >= have) continue;
+          const long long r = static_cast<long long>(at.row0) + first + tok;
+          gg_bf16* out = p.C + r * width + at.n0 + c;
+          const float lo = sum[0][v], hi = sum[1][v];
+          if (kGated) {
+            const bool scaled = p.row_scale != nullptr;
+            *out = __bfloat16_as_ushort(__float2bfloat16_rn(
+                glu_mul(lo, hi, p.alpha, scaled, scaled ? p.row_scale[r] : 1.0f)));
+            if (p.H1_save != nullptr) {
+              gg_bf16* h1 = p.H1_save + r * p.N + at.n0 + c;
+              h1[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
+              h1[p.F] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
+            }
+          } else {
+            out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
+            out[16] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
+          }
+        }
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kParts) : "memory");
+    }
+  }
+  // after a wait that ran out: no load may still be on its way at the exit
+  if (!ok)
+    for (int i = 0; i < kStages; ++i)
+      if (pending & (1u << i))
+        (void)mbar_wait_bounded(smem_u32(&st.full[warp][i]),
+                                i >= failed ? failed_phase : failed_phase ^ 1u, nullptr,
+                                p.status);
+}
+
+template <bool kGated, bool kBf16, int kParts>
+cudaError_t launch_rows_t(const CUtensorMap& mb, const RowsParams& p, int grid,
+                          const DeviceInfo& dev, cudaStream_t stream) {
+  static std::atomic<int> opted[kMaxDevices];
+  if (opted[dev.device].load(std::memory_order_relaxed) == 0) {
+    const cudaError_t o = cudaFuncSetAttribute(f8_rows_kernel<kGated, kBf16, kParts>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kSmemBytes));
+    if (o != cudaSuccess) return o;
+    opted[dev.device].store(1, std::memory_order_relaxed);
+  }
+  f8_rows_kernel<kGated, kBf16, kParts><<<grid, kThreads, kSmemBytes, stream>>>(mb, p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <bool kGated, bool kBf16>
+cudaError_t launch_rows_p(const CUtensorMap& mb, const RowsParams& p, const DeviceInfo& dev,
+                          cudaStream_t stream) {
+  const int experts = p.R_cap < p.E ? p.R_cap : p.E;  // that can have rows
+  const long long tiles = static_cast<long long>(p.N / kRows) * experts;
+  const int grid = static_cast<int>(tiles < dev.sm_count ? tiles : dev.sm_count);
+  // as many warps to a tile as leave every tile its own
+  const long long warps = static_cast<long long>(dev.sm_count) * kWarps;
+  if (tiles * 8 <= warps) return launch_rows_t<kGated, kBf16, 8>(mb, p, grid, dev, stream);
+  if (tiles * 4 <= warps) return launch_rows_t<kGated, kBf16, 4>(mb, p, grid, dev, stream);
+  return launch_rows_t<kGated, kBf16, 2>(mb, p, grid, dev, stream);
+}
+
+}  // namespace
+
+bool f8_rows_fits(int R_cap, int E) {
+  const int experts = R_cap < E ? R_cap : E;
+  return R_cap <= 4 * experts;
+}
+
+cudaError_t launch_f8_rows(const F8GemmArgs& a, const gg_bf16* x, const DeviceInfo& dev,
+                           cudaStream_t stream) {
+  const bool gated = a.alpha != 0.0f;
+  CUtensorMap mb;
+  const cuuint64_t bd[3] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.N),
+                            static_cast<cuuint64_t>(a.E)};
+  const cuuint64_t bs[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.K) * a.N};
+  const cuuint32_t bbox[3] = {kChunk, gated ? kRows / 2u : static_cast<cuuint32_t>(kRows), 1};
+  if (!encode_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, bd, bs, bbox,
+                  CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  RowsParams p{};
+  p.x = x;
+  p.A = a.A;
+  p.As = a.As;
+  p.Bs = a.Bs;
+  p.offsets = a.offsets;
+  p.E = a.E;
+  p.R_cap = a.R_cap;
+  p.K = a.K;
+  p.N = a.N;
+  p.F = a.N / 2;
+  p.alpha = a.alpha;
+  p.row_scale = a.row_scale;
+  p.C = a.C;
+  p.H1_save = a.H1_save;
+  p.status = a.status;
+  if (x != nullptr)
+    return gated ? launch_rows_p<true, true>(mb, p, dev, stream)
+                 : launch_rows_p<false, true>(mb, p, dev, stream);
+  return gated ? launch_rows_p<true, false>(mb, p, dev, stream)
+               : launch_rows_p<false, false>(mb, p, dev, stream);
+}
+
+}  // namespace gg

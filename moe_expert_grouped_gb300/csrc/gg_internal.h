@@ -290,6 +290,13 @@ struct F8GemmArgs {
 };
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
+// ------------------------------------------------------------------ gg_f8_rows.cu
+// The forward for few rows per expert (f8_rows_fits), from BF16 rows x or, x
+// null, from A and As.
+bool f8_rows_fits(int R_cap, int E);
+cudaError_t launch_f8_rows(const F8GemmArgs& a, const gg_bf16* x, const DeviceInfo& dev,
+                           cudaStream_t stream);
+
 // ------------------------------------------------------------------ gg_route.cu
 // Blocks that accumulate the router's batch statistics (two per SM of a
 // 152-SM device): rows of the scratch below.

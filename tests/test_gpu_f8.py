@@ -125,7 +125,7 @@ def test_weight_codes(gg, E, N, K):
 
 COUNTS = [
     [1], [0, 5, 0, 0, 1], [33, 31, 32, 64], [255, 256, 257], [1000, 0, 3, 300], [2] * 40,
-    [129, 513, 90],
+    [129, 513, 90], [20, 0] + [1] * 9,
 ]
 SHAPES = [(64, 64), (128, 128), (256, 192), (320, 448), (576, 1024), (1088, 64)]
 
@@ -159,7 +159,8 @@ def test_forward_plain(gg, counts, N, K):
 @pytest.mark.parametrize("epi", [1, 3])
 @pytest.mark.parametrize("keep,weighted", [(True, True), (False, False), (True, False)])
 @pytest.mark.parametrize("N,K", [(128, 64), (256, 192), (384, 320), (640, 1024)])
-@pytest.mark.parametrize("counts", [[1], [0, 33, 300, 2], [257, 64, 0]], ids=_ids)
+@pytest.mark.parametrize("counts", [[1], [0, 33, 300, 2], [257, 64, 0], [3, 0, 12, 1, 2, 1]],
+                         ids=_ids)
 def test_forward_gated(gg, counts, N, K, keep, weighted, epi):
     E, spare, F = len(counts), 5, N // 2
     R = sum(counts) + spare
