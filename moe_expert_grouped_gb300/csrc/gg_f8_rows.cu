@@ -7,19 +7,21 @@
 // A tile is 32 rows of one live expert's weight (gated: 16 gate rows and the
 // matching 16 up rows). One block of 16 warps per SM; kParts warps share a
 // tile, each taking every kParts-th block of 128 codes. Every warp has a ring
-// of its own in shared memory that TMA fills with 32 x 128 weight codes per
-// stage, so 192 KB of weights per SM are always on their way, across tiles too.
+// of its own in shared memory that TMA fills with 32 x 128 weight codes and
+// the same columns of up to eight tokens per stage, so 128 KB of weights per SM
+// are always on their way, across tiles too.
 //
-// A lane reads 16 consecutive codes of four weight rows at a time and widens
-// them to FP16 (exact); its own token's codes it makes in registers, 32 columns
-// of one of up to eight tokens, with the block's maximum from the other three
-// lanes of the token. So both have the fragments of mma.m16n8k16: which k of a
-// fragment a code stands for does not matter as long as both operands agree.
-// The sums of a block are scaled and added up in fp32; the other parts' go
-// through shared memory to the first, which adds them in order.
+// A lane reads 16 consecutive codes of four weight rows at a time, and makes
+// the codes of 32 columns of one token in registers, with the block's maximum
+// from the other three lanes of the token. Both then have the fragments of
+// mma.m16n8k32 on E4M3: which k of a fragment a code stands for does not matter
+// as long as both operands agree. Its sums are good to 2^-24 of their largest
+// term (measured), like the tensor-memory path's. Widening to FP16 for
+// mma.m16n8k16 instead was bound by the conversions, 16 a clock and SM (512 rows
+// of 128 experts, 2048 x 768: 44 us from codes, 38 as it is). The sums of a
+// block are scaled and added up in fp32; the other parts' go through shared
+// memory to the first, which adds them in order.
 
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -39,8 +41,9 @@ static_assert(kTurns <= 32 && kMaxExperts % kThreads == 0, "one warp scans the g
 constexpr int kRows = 32;          // weight rows per tile
 constexpr int kChunk = kF8Block;   // codes of K per stage
 constexpr int kTokens = 8;         // tokens multiplied with each piece of weight
-constexpr uint32_t kStageBytes = kRows * kChunk;
-constexpr int kStages = 3;         // of a warp's ring
+constexpr uint32_t kWeightBytes = kRows * kChunk;
+constexpr int kStages = 2;         // of a warp's ring
+constexpr uint32_t kStageBytes = kWeightBytes + kTokens * kChunk * 2;  // tokens in BF16 at most
 constexpr uint32_t kWarpBytes = kStages * kStageBytes;
 
 struct SmemTail {
@@ -55,11 +58,10 @@ struct SmemTail {
 
 constexpr size_t kSmemBytes = 1024 + kWarps * kWarpBytes + sizeof(SmemTail);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+static_assert(kStageBytes % 1024 == 0, "128-byte swizzle");
 
 struct RowsParams {
-  const gg_bf16* x;     // BF16 rows, or null:
-  const uint8_t* A;     // codes
-  const float* As;      // and scales [ceil(K / 128)][R_cap]
+  const float* As;      // of codes: [ceil(K / 128)][R_cap]
   const float* Bs;
   const int32_t* offsets;
   int E, R_cap, K, N, F;
@@ -70,23 +72,14 @@ struct RowsParams {
   int32_t* status;
 };
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
+// D (+)= A[16 x 32] * B[32 x 8], E4M3 operands, fp32 sums.
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Four E4M3 codes -> four FP16 of the same value.
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
-  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu),
-                                                    __NV_E4M3);
-  const __half2_raw hi =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-  return make_uint2(static_cast<uint32_t>(lo.x) | static_cast<uint32_t>(lo.y) << 16,
-                    static_cast<uint32_t>(hi.x) | static_cast<uint32_t>(hi.y) << 16);
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t top_of(uint4 w) {  // largest |BF16|, as its bits
@@ -102,16 +95,10 @@ struct Cursor {
   int row0, rows;  // the expert's rows
 };
 
-// A lane's 32 columns of its token as they come from memory.
-template <bool kBf16>
-struct Token {
-  uint4 v[kBf16 ? 4 : 2];
-  float s;      // codes: the block's scale of this lane's token
-};
-
 template <bool kGated, bool kBf16, int kParts>
 __global__ void __launch_bounds__(kThreads, 1)
-f8_rows_kernel(const __grid_constant__ CUtensorMap mapB, const RowsParams p) {
+f8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+               const RowsParams p) {
   constexpr int kGroups = kWarps / kParts;  // tiles at a time
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -127,6 +114,7 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapB, const RowsParams p) {
   if (threadIdx.x == 0) {
     st.abort_flag = 0;
     st.bad = 0;
+    tma_prefetch_desc(&mapA);
     tma_prefetch_desc(&mapB);
   }
   for (int i = threadIdx.x; i < kWarps * kStages; i += kThreads)
@@ -199,32 +187,26 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapB, const RowsParams p) {
     c.tile += tile_step;
     enter(c);
   };
-  const auto load_weights = [&](const Cursor& c, int s) {
+  constexpr uint32_t kTokenBytes = kTokens * kChunk * (kBf16 ? 2 : 1);
+  const auto load = [&](const Cursor& c, int s) {
     const uint32_t bar = smem_u32(&st.full[warp][s]);
     const uint32_t dst = ring_addr + s * kStageBytes;
-    mbar_arrive_expect_tx(bar, kStageBytes);
-    tma_load_3d(dst, &mapB, bar, c.chunk * kChunk, c.n0, c.e);
-    if (kGated)
-      tma_load_3d(dst + kStageBytes / 2, &mapB, bar, c.chunk * kChunk, p.F + c.n0, c.e);
-  };
-  // this lane's columns 32 t .. + 31 of a block of token g
-  const auto load_token = [&](const Cursor& c, Token<kBf16>& to) {
-    const int col = c.chunk * kChunk + 32 * t;  // K is a multiple of 64: all 32 exist or none
-    const bool there = c.tile < total && c.first + g < c.rows && col < p.K;
-    const long long row = static_cast<long long>(c.row0) + c.first + g;
-    constexpr int kPieces = kBf16 ? 4 : 2;
-    const uint4* from = kBf16 ? reinterpret_cast<const uint4*>(p.x + row * p.K + col)
-                              : reinterpret_cast<const uint4*>(p.A + row * p.K + col);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) to.v[i] = there ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
-    if (!kBf16)
-      to.s = c.tile < total && c.first + g < c.rows
-                 ? __ldg(p.As + static_cast<long long>(c.chunk) * p.R_cap + row)
-                 : 0.0f;
+    const int k0 = c.chunk * kChunk;
+    mbar_arrive_expect_tx(bar, kWeightBytes + kTokenBytes);
+    tma_load_3d(dst, &mapB, bar, k0, c.n0, c.e);
+    if (kGated) tma_load_3d(dst + kWeightBytes / 2, &mapB, bar, k0, p.F + c.n0, c.e);
+    tma_load_2d(dst + kWeightBytes, &mapA, bar, k0, c.row0 + c.first);
+    if (kBf16)  // 128 bytes of a row at a time
+      tma_load_2d(dst + kWeightBytes + kTokenBytes / 2, &mapA, bar, k0 + kChunk / 2,
+                  c.row0 + c.first);
   };
   // the weight's scales of a block: of the first and of the second 16 rows
-  const auto load_scales = [&](const Cursor& c, float& t0, float& t1) {
+  const auto load_scales = [&](const Cursor& c, float& t0, float& t1, float& ts) {
     if (c.tile >= total) return;
+    if (!kBf16)  // of codes: token g's too
+      ts = c.first + g < c.rows
+               ? __ldg(p.As + static_cast<long long>(c.chunk) * p.R_cap + c.row0 + c.first + g)
+               : 0.0f;
     const float* b = p.Bs + (static_cast<long long>(c.e) * NB + c.n0 / kF8Block) * chunks + c.chunk;
     t0 = __ldg(b);
     t1 = kGated ? __ldg(p.Bs +
@@ -240,18 +222,16 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapB, const RowsParams p) {
   const bool works = part_of < chunks;  // short K: the later parts have nothing
   if (works) {
     for (int s = 0; s < kStages && ahead.tile < total; ++s) {
-      if (lane == 0) load_weights(ahead, s);
+      if (lane == 0) load(ahead, s);
       pending |= 1u << s;
       advance(ahead);
     }
   }
-  // tokens and scales one block ahead of their use
+  // scales one block ahead of their use
   Cursor next = at;
-  Token<kBf16> held;
-  float t0 = 0.0f, t1 = 0.0f;
+  float t0 = 0.0f, t1 = 0.0f, ts = 0.0f;
   if (works) {
-    load_token(next, held);
-    load_scales(next, t0, t1);
+    load_scales(next, t0, t1, ts);
     advance(next);
   }
 
@@ -264,35 +244,9 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapB, const RowsParams p) {
     for (int first = 0; first < at.rows; first += kTokens) {
       float sum[2][4] = {};
       for (int chunk = part_of; chunk < chunks; chunk += kParts) {
-        // codes of this lane's columns as FP16, and the scale of the token
-        uint2 b[8];
-        float scale;
-        if constexpr (kBf16) {
-          uint32_t top = max(max(top_of(held.v[0]), top_of(held.v[1])),
-                             max(top_of(held.v[2]), top_of(held.v[3])));
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          float inv;
-          f8_scale(top << 16, inv, scale);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {held.v[i].x, held.v[i].y, held.v[i].z, held.v[i].w};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t q = f8_codes2(bf16_lo(w[2 * j]), bf16_hi(w[2 * j]), inv) |
-                           f8_codes2(bf16_lo(w[2 * j + 1]), bf16_hi(w[2 * j + 1]), inv) << 16;
-              if (inv == 0.0f) q = 0u;  // a block with a NaN: its codes are 0
-              b[2 * i + j] = widen4(q);
-            }
-          }
-        } else {
-          scale = held.s;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[i] = widen4((&held.v[i / 4].x)[i % 4]);
-        }
         const float w0 = t0, w1 = t1;
-        load_token(next, held);
-        load_scales(next, t0, t1);
+        float scale = ts;
+        load_scales(next, t0, t1, ts);
         advance(next);
         if (ok) {
           ok = mbar_wait_bounded(smem_u32(&st.full[warp][s]), phase, abort_flag, p.status);
@@ -302,6 +256,34 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapB, const RowsParams p) {
             failed = s, failed_phase = phase;
         }
         const uint8_t* stage = ring + s * kStageBytes;
+        // codes of this lane's columns 32 t .. + 31 of token g
+        uint32_t b[8];
+        if constexpr (kBf16) {
+          const uint8_t* row = stage + kWeightBytes + (t >> 1) * (kTokenBytes / 2) + g * 128;
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = *reinterpret_cast<const uint4*>(row + (((4 * (t & 1) + i) ^ g) << 4));
+          uint32_t top = max(max(top_of(x[0]), top_of(x[1])), max(top_of(x[2]), top_of(x[3])));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          float inv;
+          f8_scale(top << 16, inv, scale);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t lo = (&x[i / 2].x)[2 * (i % 2)], hi = (&x[i / 2].x)[2 * (i % 2) + 1];
+            b[i] = f8_codes2(bf16_lo(lo), bf16_hi(lo), inv) |
+                   f8_codes2(bf16_lo(hi), bf16_hi(hi), inv) << 16;
+            if (inv == 0.0f) b[i] = 0u;  // a block with a NaN: its codes are 0
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + kWeightBytes + g * kChunk +
+                                                            (((2 * t + h) ^ g) << 4));
+            b[4 * h] = x.x, b[4 * h + 1] = x.y, b[4 * h + 2] = x.z, b[4 * h + 3] = x.w;
+          }
+        }
         float acc[2][4] = {};
         // 16-byte piece 2t + h of the swizzled 128-byte rows: the eight lanes
         // of an access, two neighbouring rows, then hit all banks
@@ -313,21 +295,18 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapB, const RowsParams p) {
           for (int i = 0; i < 4; ++i)
             w[i] = *reinterpret_cast<const uint4*>(stage + (8 * i + g) * kChunk + piece);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint2 r0 = widen4((&w[0].x)[q]), r1 = widen4((&w[1].x)[q]);
-            const uint2 r2 = widen4((&w[2].x)[q]), r3 = widen4((&w[3].x)[q]);
-            const uint32_t a0[4] = {r0.x, r1.x, r0.y, r1.y};
-            const uint32_t a1[4] = {r2.x, r3.x, r2.y, r3.y};
-            const uint2 x = b[4 * h + q];
-            mma_f16(acc[0], a0, x.x, x.y);
-            mma_f16(acc[1], a1, x.x, x.y);
+          for (int q = 0; q < 4; q += 2) {
+            const auto word = [&](int i, int k) { return (&w[i].x)[k]; };
+            const uint32_t b0 = b[4 * h + q], b1 = b[4 * h + q + 1];
+            mma_e4m3(acc[0], word(0, q), word(1, q), word(0, q + 1), word(1, q + 1), b0, b1);
+            mma_e4m3(acc[1], word(2, q), word(3, q), word(2, q + 1), word(3, q + 1), b0, b1);
           }
         }
         __syncwarp();  // every lane has read the stage
         if (ok && ahead.tile < total) {
           if (lane == 0) {
             fence_proxy_async();
-            load_weights(ahead, s);
+            load(ahead, s);
           }
           pending |= 1u << s;
           advance(ahead);
@@ -393,8 +372,8 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapB, const RowsParams p) {
 }
 
 template <bool kGated, bool kBf16, int kParts>
-cudaError_t launch_rows_t(const CUtensorMap& mb, const RowsParams& p, int grid,
-                          const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_rows_t(const CUtensorMap& ma, const CUtensorMap& mb, const RowsParams& p,
+                          int grid, const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<int> opted[kMaxDevices];
   if (opted[dev.device].load(std::memory_order_relaxed) == 0) {
     const cudaError_t o = cudaFuncSetAttribute(f8_rows_kernel<kGated, kBf16, kParts>,
@@ -403,22 +382,22 @@ cudaError_t launch_rows_t(const CUtensorMap& mb, const RowsParams& p, int grid,
     if (o != cudaSuccess) return o;
     opted[dev.device].store(1, std::memory_order_relaxed);
   }
-  f8_rows_kernel<kGated, kBf16, kParts><<<grid, kThreads, kSmemBytes, stream>>>(mb, p);
+  f8_rows_kernel<kGated, kBf16, kParts><<<grid, kThreads, kSmemBytes, stream>>>(ma, mb, p);
   count_launch();
   return cudaGetLastError();
 }
 
 template <bool kGated, bool kBf16>
-cudaError_t launch_rows_p(const CUtensorMap& mb, const RowsParams& p, const DeviceInfo& dev,
-                          cudaStream_t stream) {
+cudaError_t launch_rows_p(const CUtensorMap& ma, const CUtensorMap& mb, const RowsParams& p,
+                          const DeviceInfo& dev, cudaStream_t stream) {
   const int experts = p.R_cap < p.E ? p.R_cap : p.E;  // that can have rows
   const long long tiles = static_cast<long long>(p.N / kRows) * experts;
   const int grid = static_cast<int>(tiles < dev.sm_count ? tiles : dev.sm_count);
   // as many warps to a tile as leave every tile its own
   const long long warps = static_cast<long long>(dev.sm_count) * kWarps;
-  if (tiles * 8 <= warps) return launch_rows_t<kGated, kBf16, 8>(mb, p, grid, dev, stream);
-  if (tiles * 4 <= warps) return launch_rows_t<kGated, kBf16, 4>(mb, p, grid, dev, stream);
-  return launch_rows_t<kGated, kBf16, 2>(mb, p, grid, dev, stream);
+  if (tiles * 8 <= warps) return launch_rows_t<kGated, kBf16, 8>(ma, mb, p, grid, dev, stream);
+  if (tiles * 4 <= warps) return launch_rows_t<kGated, kBf16, 4>(ma, mb, p, grid, dev, stream);
+  return launch_rows_t<kGated, kBf16, 2>(ma, mb, p, grid, dev, stream);
 }
 
 }  // namespace
@@ -439,9 +418,17 @@ cudaError_t launch_f8_rows(const F8GemmArgs& a, const gg_bf16* x, const DeviceIn
   if (!encode_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, 3, bd, bs, bbox,
                   CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  CUtensorMap ma;
+  const cuuint64_t ad[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.R_cap)};
+  const cuuint64_t as[1] = {static_cast<cuuint64_t>(a.K) * (x != nullptr ? 2 : 1)};
+  const cuuint32_t abox[2] = {x != nullptr ? kChunk / 2u : static_cast<cuuint32_t>(kChunk),
+                              kTokens};
+  if (!encode_map(&ma, x != nullptr ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                  x != nullptr ? static_cast<const void*>(x) : a.A, 2, ad, as, abox,
+                  CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
   RowsParams p{};
-  p.x = x;
-  p.A = a.A;
   p.As = a.As;
   p.Bs = a.Bs;
   p.offsets = a.offsets;
@@ -456,10 +443,10 @@ cudaError_t launch_f8_rows(const F8GemmArgs& a, const gg_bf16* x, const DeviceIn
   p.H1_save = a.H1_save;
   p.status = a.status;
   if (x != nullptr)
-    return gated ? launch_rows_p<true, true>(mb, p, dev, stream)
-                 : launch_rows_p<false, true>(mb, p, dev, stream);
-  return gated ? launch_rows_p<true, false>(mb, p, dev, stream)
-               : launch_rows_p<false, false>(mb, p, dev, stream);
+    return gated ? launch_rows_p<true, true>(ma, mb, p, dev, stream)
+                 : launch_rows_p<false, true>(ma, mb, p, dev, stream);
+  return gated ? launch_rows_p<true, false>(ma, mb, p, dev, stream)
+               : launch_rows_p<false, false>(ma, mb, p, dev, stream);
 }
 
 }  // namespace gg
