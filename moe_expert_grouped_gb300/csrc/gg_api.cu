@@ -1191,7 +1191,7 @@ gg_status gg_f8_grouped_gemm(const uint8_t* Aq, const float* As, const uint8_t* 
   a.H1_save = H1_save;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return from_cuda(f8_rows_fits(R_cap, E) ? launch_f8_rows(a, nullptr, dev, st)
-                                          : launch_f8_gemm(a, dev, st));
+                                          : launch_f8_gemm(a, false, dev, st));
 }
 
 // Rows of `width` columns quantised into the workspace, which then holds A and As of `a`.
@@ -1225,7 +1225,7 @@ gg_status gg_f8_grouped_fwd(const gg_bf16* A, const uint8_t* Wq, const float* Ws
   a.H1_save = H1_save;
   if (f8_rows_fits(R_cap, E)) return from_cuda(launch_f8_rows(a, A, dev, st));
   if (f8_rows_to_ws(A, K, &a, ws, dev, st) != cudaSuccess) return GG_ERR_CUDA;
-  return from_cuda(launch_f8_gemm(a, dev, st));
+  return from_cuda(launch_f8_gemm(a, true, dev, st));
 }
 
 gg_status gg_f8_grouped_dgrad(const gg_bf16* dC, const uint8_t* Wq, const float* Ws,
@@ -1248,7 +1248,7 @@ gg_status gg_f8_grouped_dgrad(const gg_bf16* dC, const uint8_t* Wq, const float*
   a.H1 = H1;
   a.rowdot = rowdot;
   if (f8_rows_to_ws(dC, N, &a, ws, dev, st) != cudaSuccess) return GG_ERR_CUDA;
-  return from_cuda(launch_f8_gemm(a, dev, st));
+  return from_cuda(launch_f8_gemm(a, true, dev, st));
 }
 
 gg_status gg_adamw_step(const gg_adamw_tensor* tensors, int n, const gg_adamw_options* options,

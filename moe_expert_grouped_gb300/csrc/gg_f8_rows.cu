@@ -4,8 +4,11 @@
 // gated activations fused, in one launch: BF16 rows are quantised where they
 // are used.
 //
-// A tile is 32 rows of one live expert's weight (gated: 16 gate rows and the
-// matching 16 up rows). One block of 16 warps per SM; kParts warps share a
+// A tile is 32 rows of a live expert's weight (gated: 16 gate rows and the
+// matching 16 up rows) and up to eight of the expert's rows: a hot expert's
+// tiles find its weights in L2, on other SMs at the same time (one after the
+// other by the same warps, 256 rows of 128 experts by Zipf's law took 98 us
+// where even ones took 67). One block of 16 warps per SM; kParts warps share a
 // tile, each taking every kParts-th block of 128 codes. Every warp has a ring
 // of its own in shared memory that TMA fills with 32 x 128 weight codes and
 // the same columns of up to eight tokens per stage, so 128 KB of weights per SM
@@ -41,6 +44,8 @@ static_assert(kTurns <= 32 && kMaxExperts % kThreads == 0, "one warp scans the g
 constexpr int kRows = 32;          // weight rows per tile
 constexpr int kChunk = kF8Block;   // codes of K per stage
 constexpr int kTokens = 8;         // tokens multiplied with each piece of weight
+constexpr int kMostRows = 4;       // rows per expert, on average, that this is for
+constexpr int kMaxUnits = kMaxExperts + kMostRows * kMaxExperts / kTokens;
 constexpr uint32_t kWeightBytes = kRows * kChunk;
 constexpr int kStages = 2;         // of a warp's ring
 constexpr uint32_t kStageBytes = kWeightBytes + kTokens * kChunk * 2;  // tokens in BF16 at most
@@ -50,9 +55,9 @@ struct SmemTail {
   uint64_t full[kWarps][kStages];
   int abort_flag;
   int bad;
-  int n_live;
+  int n_units;
   int in_turn[kTurns];
-  uint16_t live[kMaxExperts];  // experts that have rows
+  uint32_t unit[kMaxUnits];    // an expert and, times 65536, eight of its rows
   float part[kWarps][8][32];   // sums of the parts but the first, as their lanes hold them
 };
 
@@ -88,11 +93,11 @@ __device__ __forceinline__ uint32_t top_of(uint4 w) {  // largest |BF16|, as its
   return max(a & 0xFFFFu, a >> 16);
 }
 
-// Where a warp is in its stages: tile, first token of the pass, block of K.
+// Where a warp is in its stages: tile, block of K.
 struct Cursor {
-  int tile, first, chunk;
+  int tile, chunk;
   int e, n0;       // the tile's expert and first weight row
-  int row0, rows;  // the expert's rows
+  int row0, rows;  // and rows
 };
 
 template <bool kGated, bool kBf16, int kParts>
@@ -109,8 +114,8 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
 
-  // The live experts, in order: 32 experts per warp and turn, so that all
-  // offsets are on their way at once.
+  // The units, in order of their experts: 32 experts per warp and turn, so that
+  // all offsets are on their way at once.
   if (threadIdx.x == 0) {
     st.abort_flag = 0;
     st.bad = 0;
@@ -122,36 +127,47 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   mbar_fence_init();
   fence_proxy_async();
   __syncthreads();
-  uint32_t live[kMaxExperts / kThreads];  // of the warp's turns: lanes with rows
+  int units[kMaxExperts / kThreads], upto[kMaxExperts / kThreads];  // of this thread's experts
 #pragma unroll
   for (int i = 0; i < kMaxExperts / kThreads; ++i) {
     const int e = i * kThreads + threadIdx.x;
     const int o0 = e < p.E ? p.offsets[e] : 0;
     const int o1 = e < p.E ? p.offsets[e + 1] : 0;
-    if (o1 < o0 || o0 < 0 || o1 > p.R_cap || (e == 0 && o0 != 0)) st.bad = 1;
-    live[i] = __ballot_sync(0xFFFFFFFFu, o1 > o0);
-    if (lane == 0) st.in_turn[i * kWarps + warp] = __popc(live[i]);
+    const bool bad = o1 < o0 || o0 < 0 || o1 > p.R_cap || (e == 0 && o0 != 0);
+    if (bad) st.bad = 1;
+    units[i] = bad ? 0 : (o1 - o0 + kTokens - 1) / kTokens;
+    upto[i] = units[i];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int n = __shfl_up_sync(0xFFFFFFFFu, upto[i], d);
+      if (lane >= d) upto[i] += n;
+    }
+    if (lane == 31) st.in_turn[i * kWarps + warp] = upto[i];
   }
   __syncthreads();
   {
-    // experts of the turns before each of this warp's
+    // units of the turns before each of this warp's
     const int mine = lane < kTurns ? st.in_turn[lane] : 0;
-    int upto = mine;
+    int sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int n = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-      if (lane >= d) upto += n;
+      const int n = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += n;
     }
+    // valid offsets give R_cap / 8 and one for every expert at most
+    const int all = st.bad ? 0 : __shfl_sync(0xFFFFFFFFu, sum, 31);
 #pragma unroll
     for (int i = 0; i < kMaxExperts / kThreads; ++i) {
-      const int before = __shfl_sync(0xFFFFFFFFu, upto - mine, i * kWarps + warp);
-      if (live[i] >> lane & 1u)
-        st.live[before + __popc(live[i] & ((1u << lane) - 1u))] =
-            static_cast<uint16_t>(i * kThreads + threadIdx.x);
+      const int before = __shfl_sync(0xFFFFFFFFu, sum - mine, i * kWarps + warp);
+      for (int u = 0; u < units[i]; ++u) {
+        const int to = before + upto[i] - units[i] + u;
+        if (to < all && to < kMaxUnits)
+          st.unit[to] = static_cast<uint32_t>(i * kThreads + threadIdx.x) |
+                        static_cast<uint32_t>(u) << 16;
+      }
     }
-    const int all = __shfl_sync(0xFFFFFFFFu, upto, 31);
     if (threadIdx.x == 0) {
-      st.n_live = st.bad ? 0 : all;
+      st.n_units = all;
       if (st.bad && blockIdx.x == 0) set_status(p.status, GG_ERR_DEVICE_BAD_OFFSETS);
     }
   }
@@ -159,8 +175,8 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
 
   volatile int* abort_flag = &st.abort_flag;
   constexpr int kOut = kGated ? kRows / 2 : kRows;  // outputs per tile and token
-  const int per = (kGated ? p.F : p.N) / kOut;      // tiles per expert
-  const int total = st.n_live * per;
+  const int per = (kGated ? p.F : p.N) / kOut;      // tiles per unit
+  const int total = st.n_units * per;
   const int chunks = (p.K + kChunk - 1) / kChunk;
   const int NB = (p.N + kF8Block - 1) / kF8Block;
   const int group = warp / kParts, part_of = warp % kParts;
@@ -172,18 +188,17 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   const auto enter = [&](Cursor& c) {  // c.tile has changed
     if (c.tile >= total) return;
     const int a = c.tile / per;
-    c.e = st.live[a];
+    const uint32_t unit = st.unit[a];
+    const int first = static_cast<int>(unit >> 16) * kTokens;
+    c.e = static_cast<int>(unit & 0xFFFFu);
     c.n0 = (c.tile - a * per) * kOut;
-    c.row0 = p.offsets[c.e];
-    c.rows = p.offsets[c.e + 1] - c.row0;
+    c.row0 = p.offsets[c.e] + first;
+    c.rows = min(kTokens, p.offsets[c.e + 1] - c.row0);
   };
   const auto advance = [&](Cursor& c) {
     c.chunk += kParts;
     if (c.chunk < chunks) return;
     c.chunk = part_of;
-    c.first += kTokens;
-    if (c.first < c.rows) return;
-    c.first = 0;
     c.tile += tile_step;
     enter(c);
   };
@@ -195,18 +210,17 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
     mbar_arrive_expect_tx(bar, kWeightBytes + kTokenBytes);
     tma_load_3d(dst, &mapB, bar, k0, c.n0, c.e);
     if (kGated) tma_load_3d(dst + kWeightBytes / 2, &mapB, bar, k0, p.F + c.n0, c.e);
-    tma_load_2d(dst + kWeightBytes, &mapA, bar, k0, c.row0 + c.first);
+    tma_load_2d(dst + kWeightBytes, &mapA, bar, k0, c.row0);
     if (kBf16)  // 128 bytes of a row at a time
       tma_load_2d(dst + kWeightBytes + kTokenBytes / 2, &mapA, bar, k0 + kChunk / 2,
-                  c.row0 + c.first);
+                  c.row0);
   };
   // the weight's scales of a block: of the first and of the second 16 rows
   const auto load_scales = [&](const Cursor& c, float& t0, float& t1, float& ts) {
     if (c.tile >= total) return;
     if (!kBf16)  // of codes: token g's too
-      ts = c.first + g < c.rows
-               ? __ldg(p.As + static_cast<long long>(c.chunk) * p.R_cap + c.row0 + c.first + g)
-               : 0.0f;
+      ts = g < c.rows ? __ldg(p.As + static_cast<long long>(c.chunk) * p.R_cap + c.row0 + g)
+                      : 0.0f;
     const float* b = p.Bs + (static_cast<long long>(c.e) * NB + c.n0 / kF8Block) * chunks + c.chunk;
     t0 = __ldg(b);
     t1 = kGated ? __ldg(p.Bs +
@@ -215,7 +229,7 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
                 : t0;
   };
 
-  Cursor at{first_tile, 0, part_of, 0, 0, 0, 0};  // of the stage consumed next
+  Cursor at{first_tile, part_of, 0, 0, 0, 0};  // of the stage consumed next
   enter(at);
   Cursor ahead = at;                    // of the stage loaded next
   uint32_t pending = 0;                 // stages with a load that was not waited for
@@ -241,126 +255,124 @@ f8_rows_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__
   int failed = 0;
   uint32_t failed_phase = 0;
   for (; at.tile < total; at.tile += tile_step, enter(at)) {
-    for (int first = 0; first < at.rows; first += kTokens) {
-      float sum[2][4] = {};
-      for (int chunk = part_of; chunk < chunks; chunk += kParts) {
-        const float w0 = t0, w1 = t1;
-        float scale = ts;
-        load_scales(next, t0, t1, ts);
-        advance(next);
-        if (ok) {
-          ok = mbar_wait_bounded(smem_u32(&st.full[warp][s]), phase, abort_flag, p.status);
-          if (ok)
-            pending &= ~(1u << s);
-          else
-            failed = s, failed_phase = phase;
+    float sum[2][4] = {};
+    for (int chunk = part_of; chunk < chunks; chunk += kParts) {
+      const float w0 = t0, w1 = t1;
+      float scale = ts;
+      load_scales(next, t0, t1, ts);
+      advance(next);
+      if (ok) {
+        ok = mbar_wait_bounded(smem_u32(&st.full[warp][s]), phase, abort_flag, p.status);
+        if (ok)
+          pending &= ~(1u << s);
+        else
+          failed = s, failed_phase = phase;
+      }
+      const uint8_t* stage = ring + s * kStageBytes;
+      // codes of this lane's columns 32 t .. + 31 of token g
+      uint32_t b[8];
+      if constexpr (kBf16) {
+        const uint8_t* row = stage + kWeightBytes + (t >> 1) * (kTokenBytes / 2) + g * 128;
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = *reinterpret_cast<const uint4*>(row + (((4 * (t & 1) + i) ^ g) << 4));
+        uint32_t top = max(max(top_of(x[0]), top_of(x[1])), max(top_of(x[2]), top_of(x[3])));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        float inv;
+        f8_scale(top << 16, inv, scale);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t lo = (&x[i / 2].x)[2 * (i % 2)], hi = (&x[i / 2].x)[2 * (i % 2) + 1];
+          b[i] = f8_codes2(bf16_lo(lo), bf16_hi(lo), inv) |
+                 f8_codes2(bf16_lo(hi), bf16_hi(hi), inv) << 16;
+          if (inv == 0.0f) b[i] = 0u;  // a block with a NaN: its codes are 0
         }
-        const uint8_t* stage = ring + s * kStageBytes;
-        // codes of this lane's columns 32 t .. + 31 of token g
-        uint32_t b[8];
-        if constexpr (kBf16) {
-          const uint8_t* row = stage + kWeightBytes + (t >> 1) * (kTokenBytes / 2) + g * 128;
-          uint4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[i] = *reinterpret_cast<const uint4*>(row + (((4 * (t & 1) + i) ^ g) << 4));
-          uint32_t top = max(max(top_of(x[0]), top_of(x[1])), max(top_of(x[2]), top_of(x[3])));
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          float inv;
-          f8_scale(top << 16, inv, scale);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t lo = (&x[i / 2].x)[2 * (i % 2)], hi = (&x[i / 2].x)[2 * (i % 2) + 1];
-            b[i] = f8_codes2(bf16_lo(lo), bf16_hi(lo), inv) |
-                   f8_codes2(bf16_lo(hi), bf16_hi(hi), inv) << 16;
-            if (inv == 0.0f) b[i] = 0u;  // a block with a NaN: its codes are 0
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + kWeightBytes + g * kChunk +
-                                                            (((2 * t + h) ^ g) << 4));
-            b[4 * h] = x.x, b[4 * h + 1] = x.y, b[4 * h + 2] = x.z, b[4 * h + 3] = x.w;
-          }
-        }
-        float acc[2][4] = {};
-        // 16-byte piece 2t + h of the swizzled 128-byte rows: the eight lanes
-        // of an access, two neighbouring rows, then hit all banks
+      } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t piece = ((2 * t + h) ^ g) << 4;
-          uint4 w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = *reinterpret_cast<const uint4*>(stage + (8 * i + g) * kChunk + piece);
-#pragma unroll
-          for (int q = 0; q < 4; q += 2) {
-            const auto word = [&](int i, int k) { return (&w[i].x)[k]; };
-            const uint32_t b0 = b[4 * h + q], b1 = b[4 * h + q + 1];
-            mma_e4m3(acc[0], word(0, q), word(1, q), word(0, q + 1), word(1, q + 1), b0, b1);
-            mma_e4m3(acc[1], word(2, q), word(3, q), word(2, q + 1), word(3, q + 1), b0, b1);
-          }
-        }
-        __syncwarp();  // every lane has read the stage
-        if (ok && ahead.tile < total) {
-          if (lane == 0) {
-            fence_proxy_async();
-            load(ahead, s);
-          }
-          pending |= 1u << s;
-          advance(ahead);
-        }
-        if (++s == kStages) {
-          s = 0;
-          phase ^= 1u;
-        }
-        // D fragment: rows g (values 0, 1) and g + 8 (2, 3), tokens 2t and 2t + 1
-        const float s0 = __shfl_sync(0xFFFFFFFFu, scale, 8 * t);
-        const float s1 = __shfl_sync(0xFFFFFFFFu, scale, 8 * t + 4);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float f = v & 1 ? s1 : s0;
-          sum[0][v] = fmaf(acc[0][v], f * w0, sum[0][v]);
-          sum[1][v] = fmaf(acc[1][v], f * w1, sum[1][v]);
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + kWeightBytes + g * kChunk +
+                                                          (((2 * t + h) ^ g) << 4));
+          b[4 * h] = x.x, b[4 * h + 1] = x.y, b[4 * h + 2] = x.z, b[4 * h + 3] = x.w;
         }
       }
-      if (part_of != 0) {
+      float acc[2][4] = {};
+      // 16-byte piece 2t + h of the swizzled 128-byte rows: the eight lanes
+      // of an access, two neighbouring rows, then hit all banks
 #pragma unroll
-        for (int i = 0; i < 8; ++i) st.part[warp][i][lane] = sum[i / 4][i % 4];
-      }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kParts) : "memory");
-      if (part_of == 0) {
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t piece = ((2 * t + h) ^ g) << 4;
+        uint4 w[4];
 #pragma unroll
-        for (int w = 1; w < kParts; ++w)
+        for (int i = 0; i < 4; ++i)
+          w[i] = *reinterpret_cast<const uint4*>(stage + (8 * i + g) * kChunk + piece);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i / 4][i % 4] += st.part[warp + w][i][lane];
-        const int have = ok ? min(kTokens, at.rows - first) : 0;
-        const long long width = kGated ? p.F : p.N;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int tok = 2 * t + (v & 1), c = g + (v & 2 ? 8 : 0);
-          if (tok >= have) continue;
-          const long long r = static_cast<long long>(at.row0) + first + tok;
-          gg_bf16* out = p.C + r * width + at.n0 + c;
-          const float lo = sum[0][v], hi = sum[1][v];
-          if (kGated) {
-            const bool scaled = p.row_scale != nullptr;
-            *out = __bfloat16_as_ushort(__float2bfloat16_rn(
-                glu_mul(lo, hi, p.alpha, scaled, scaled ? p.row_scale[r] : 1.0f)));
-            if (p.H1_save != nullptr) {
-              gg_bf16* h1 = p.H1_save + r * p.N + at.n0 + c;
-              h1[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
-              h1[p.F] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
-            }
-          } else {
-            out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
-            out[16] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
-          }
+        for (int q = 0; q < 4; q += 2) {
+          const auto word = [&](int i, int k) { return (&w[i].x)[k]; };
+          const uint32_t b0 = b[4 * h + q], b1 = b[4 * h + q + 1];
+          mma_e4m3(acc[0], word(0, q), word(1, q), word(0, q + 1), word(1, q + 1), b0, b1);
+          mma_e4m3(acc[1], word(2, q), word(3, q), word(2, q + 1), word(3, q + 1), b0, b1);
         }
       }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kParts) : "memory");
+      __syncwarp();  // every lane has read the stage
+      if (ok && ahead.tile < total) {
+        if (lane == 0) {
+          fence_proxy_async();
+          load(ahead, s);
+        }
+        pending |= 1u << s;
+        advance(ahead);
+      }
+      if (++s == kStages) {
+        s = 0;
+        phase ^= 1u;
+      }
+      // D fragment: rows g (values 0, 1) and g + 8 (2, 3), tokens 2t and 2t + 1
+      const float s0 = __shfl_sync(0xFFFFFFFFu, scale, 8 * t);
+      const float s1 = __shfl_sync(0xFFFFFFFFu, scale, 8 * t + 4);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float f = v & 1 ? s1 : s0;
+        sum[0][v] = fmaf(acc[0][v], f * w0, sum[0][v]);
+        sum[1][v] = fmaf(acc[1][v], f * w1, sum[1][v]);
+      }
     }
+    if (part_of != 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) st.part[warp][i][lane] = sum[i / 4][i % 4];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kParts) : "memory");
+    if (part_of == 0) {
+#pragma unroll
+      for (int w = 1; w < kParts; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i / 4][i % 4] += st.part[warp + w][i][lane];
+      const int have = ok ? at.rows : 0;
+      const long long width = kGated ? p.F : p.N;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int tok = 2 * t + (v & 1), c = g + (v & 2 ? 8 : 0);
+        if (tok >= have) continue;
+        const long long r = static_cast<long long>(at.row0) + tok;
+        gg_bf16* out = p.C + r * width + at.n0 + c;
+        const float lo = sum[0][v], hi = sum[1][v];
+        if (kGated) {
+          const bool scaled = p.row_scale != nullptr;
+          *out = __bfloat16_as_ushort(__float2bfloat16_rn(
+              glu_mul(lo, hi, p.alpha, scaled, scaled ? p.row_scale[r] : 1.0f)));
+          if (p.H1_save != nullptr) {
+            gg_bf16* h1 = p.H1_save + r * p.N + at.n0 + c;
+            h1[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
+            h1[p.F] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
+          }
+        } else {
+          out[0] = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
+          out[16] = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
+        }
+      }
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kParts) : "memory");
   }
   // after a wait that ran out: no load may still be on its way at the exit
   if (!ok)
@@ -391,8 +403,10 @@ template <bool kGated, bool kBf16>
 cudaError_t launch_rows_p(const CUtensorMap& ma, const CUtensorMap& mb, const RowsParams& p,
                           const DeviceInfo& dev, cudaStream_t stream) {
   const int experts = p.R_cap < p.E ? p.R_cap : p.E;  // that can have rows
+  // units at most; the parts go by the usual number, one for each expert
   const long long tiles = static_cast<long long>(p.N / kRows) * experts;
-  const int grid = static_cast<int>(tiles < dev.sm_count ? tiles : dev.sm_count);
+  const long long most = static_cast<long long>(p.N / kRows) * (experts + p.R_cap / kTokens);
+  const int grid = static_cast<int>(most < dev.sm_count ? most : dev.sm_count);
   // as many warps to a tile as leave every tile its own
   const long long warps = static_cast<long long>(dev.sm_count) * kWarps;
   if (tiles * 8 <= warps) return launch_rows_t<kGated, kBf16, 8>(ma, mb, p, grid, dev, stream);
@@ -402,9 +416,14 @@ cudaError_t launch_rows_p(const CUtensorMap& ma, const CUtensorMap& mb, const Ro
 
 }  // namespace
 
+// us here : quantiser and gg_gemm_f8.cu, rows dealt evenly, and by Zipf's law (1.2):
+//   rows per expert                     1                2               4               8
+//   128 experts, 1536 x 2048 gated  53:63   33:42    66:78   46:53   72:85   71:66  106:95  108:74
+//   128 experts, 2048 x 768         29:37   19:25    35:45   25:28   40:49   39:39   54:53   56:45
+//   32 experts, 4096 x 4096 gated   71:81   50:56    78:94   70:70   98:108  94:83  143:115 144:100
 bool f8_rows_fits(int R_cap, int E) {
   const int experts = R_cap < E ? R_cap : E;
-  return R_cap <= 4 * experts;
+  return R_cap <= kMostRows * experts;
 }
 
 cudaError_t launch_f8_rows(const F8GemmArgs& a, const gg_bf16* x, const DeviceInfo& dev,

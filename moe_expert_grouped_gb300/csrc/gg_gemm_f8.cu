@@ -465,6 +465,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
       if (lane == 0) {
         // -------------------------------------------------- TMA producer
         for (int i = 0; i < kBoxes; ++i) tma_prefetch_desc(&maps.tokens[i]);
+        grid_dependency_wait();  // the quantiser's codes
         tma_prefetch_desc(&maps.weights);
         tma_prefetch_desc(&maps.out);
         const int h = static_cast<int>(crank);
@@ -612,6 +613,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
       }
     } else {
       // ------------------------------------------------------------ scales
+      grid_dependency_wait();  // the quantiser's scales
       // Loaded kAhead steps ahead of their use: their latency is 1000 cycles and more.
       struct Ahead {
         float s[BM / 32];
@@ -1085,20 +1087,21 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
 }
 
 template <int MODE>
-cudaError_t launch_f8_t(const F8Maps& maps, const F8Params& p, const DeviceInfo& dev,
+cudaError_t launch_f8_t(const F8Maps& maps, const F8Params& p, bool early, const DeviceInfo& dev,
                         cudaStream_t stream) {
   static std::atomic<int> resident[kMaxDevices];
   // no more clusters than there can be work items
   const long long items =
       (static_cast<long long>(p.R_cap) / BN + (p.R_cap < p.E ? p.R_cap : p.E)) * p.NT;
   const int most = static_cast<int>(items < 1 ? 1 : (items < 0x7FFFFFFF ? items : 0x7FFFFFFF));
-  return launch_pairs(f8_gemm_kernel<MODE>, resident, kThreads, kSmemBytes, most, dev, stream,
-                      maps, p);
+  return launch_pairs_early(early, f8_gemm_kernel<MODE>, resident, kThreads, kSmemBytes, most, dev,
+                            stream, maps, p);
 }
 
 }  // namespace
 
-cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+cudaError_t launch_f8_gemm(const F8GemmArgs& a, bool early, const DeviceInfo& dev,
+                           cudaStream_t stream) {
   const int red = a.grad ? a.N : a.K;
   const int out = a.grad ? a.K : a.N;
   F8Maps maps;
@@ -1161,15 +1164,15 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStrea
     p.F = a.N / 2;
     p.width = p.F;
     p.NT = (p.F + BM - 1) / BM;
-    return launch_f8_t<kFwdGated>(maps, p, dev, stream);
+    return launch_f8_t<kFwdGated>(maps, p, early, dev, stream);
   }
   p.width = out;
   p.NT = (out + 2 * BM - 1) / (2 * BM);
-  if (!a.grad) return launch_f8_t<kFwd>(maps, p, dev, stream);
-  if (!gated) return launch_f8_t<kGrad>(maps, p, dev, stream);
+  if (!a.grad) return launch_f8_t<kFwd>(maps, p, early, dev, stream);
+  if (!gated) return launch_f8_t<kGrad>(maps, p, early, dev, stream);
   p.F = a.K;
   p.rowdot_stride = (2 * p.NT + 7) / 8 * 8;
-  return launch_f8_t<kGradGated>(maps, p, dev, stream);
+  return launch_f8_t<kGradGated>(maps, p, early, dev, stream);
 }
 
 }  // namespace gg

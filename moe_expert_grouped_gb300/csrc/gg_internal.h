@@ -288,7 +288,9 @@ struct F8GemmArgs {
   float* rowdot;           // gated grad: partial sums as GemmArgs, or null
   int32_t* status;
 };
-cudaError_t launch_f8_gemm(const F8GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+// early: launched right behind launch_f8_quantize, which makes A and As.
+cudaError_t launch_f8_gemm(const F8GemmArgs& a, bool early, const DeviceInfo& dev,
+                           cudaStream_t stream);
 
 // ------------------------------------------------------------------ gg_f8_rows.cu
 // The forward for few rows per expert (f8_rows_fits), from BF16 rows x or, x

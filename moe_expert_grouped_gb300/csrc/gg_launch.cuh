@@ -47,13 +47,15 @@ inline bool encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* b
 // many clusters as can be resident at once (at most `most`), found once per
 // device and kernel (`resident`: kMaxDevices entries of the kernel's own,
 // zero before the first call; host threads may race, every writer stores the
-// same value).
+// same value). early: as launch_early.
 template <typename... Params, typename... Args>
-cudaError_t launch_pairs(void (*kernel)(Params...), std::atomic<int>* resident, int threads,
-                         size_t smem, int most, const DeviceInfo& dev, cudaStream_t stream,
-                         Args... args) {
+cudaError_t launch_pairs_early(bool early, void (*kernel)(Params...), std::atomic<int>* resident,
+                               int threads, size_t smem, int most, const DeviceInfo& dev,
+                               cudaStream_t stream, Args... args) {
   if (dev.device < 0 || dev.device >= kMaxDevices) return cudaErrorInvalidDevice;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -77,9 +79,17 @@ cudaError_t launch_pairs(void (*kernel)(Params...), std::atomic<int>* resident, 
     resident[dev.device].store(n, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (n < most ? n : most)));
+  cfg.numAttrs = early ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_pairs(void (*kernel)(Params...), std::atomic<int>* resident, int threads,
+                         size_t smem, int most, const DeviceInfo& dev, cudaStream_t stream,
+                         Args... args) {
+  return launch_pairs_early(false, kernel, resident, threads, smem, most, dev, stream, args...);
 }
 
 }  // namespace gg
