@@ -39,7 +39,7 @@ namespace {
 constexpr int kCell = 256;        // elements that share a scale
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kFew = 8, kMany = 310;  // tensors in a launch's parameters (at most 32 KB)
+constexpr int kFew = 8, kSome = 64, kMany = 310;  // tensors in a launch's parameters (32 KB at most)
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr uint32_t kInf = 0x7F800000u;
 constexpr float kTop = 448.0f;                       // largest E4M3 value
@@ -134,62 +134,297 @@ __host__ __device__ inline float kept_of(const Factors& f, double lr_scale, doub
 
 // -------------------------------------------------------------- the elements
 
-__device__ __forceinline__ void e4m3_values(uint32_t codes, float* to) {
+// Rounded products of two elements at a time, and their sums one by one: packed
+// multiplications and additions came out fused, whatever rounding they named.
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 mul(float2 a, float b) { return mul(a, make_float2(b, b)); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
+// Values of four E4M3 codes.
+__device__ __forceinline__ void e4m3_values(uint32_t codes, float2* to) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(
         static_cast<__nv_fp8x2_storage_t>(codes >> (16 * h) & 0xFFFFu), __NV_E4M3);
-    const float2 f = __half22float2(__half2(r));
-    to[2 * h] = f.x;
-    to[2 * h + 1] = f.y;
+    to[h] = __half22float2(__half2(r));
   }
 }
 
 // E4M3 code of y in [0, 448], rounded up where the part cut off exceeds
-// 1 - bits16 / 65536. Below 2^-6 codes are 2^-9 apart, as mantissas of 3 bits
-// are from 2^-6 to 2^-5: y + 2^-6 is cut there.
-__device__ __forceinline__ uint32_t round_code(float y, uint32_t bits16) {
+// 1 - r / 2^20, r the random bits (16 of them, times 16). Below 2^-6 codes are
+// 2^-9 apart, as mantissas of 3 bits are from 2^-6 to 2^-5: y + 2^-6 is cut
+// there. y 448 / a may exceed 448 by its rounding: at most code 126.
+__device__ __forceinline__ uint32_t round_code(float y, uint32_t r) {
   const bool small = y < 0.015625f;
   const float z = small ? __fadd_rn(y, 0.015625f) : y;
-  const uint32_t t = (__float_as_uint(z) + (bits16 << 4)) >> 20;
-  return min(t - (small ? 968u : 960u), 126u);
+  const uint32_t less = small ? 968u << 20 : 960u << 20;
+  return min((__float_as_uint(z) + r - less) >> 20, 126u);
 }
 
-struct Cell {
-  float w[8], g[8], m[8], v[8];
-};
+// The low bytes of a, b, c, d as one word.
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
 
-template <typename T>
-__device__ __forceinline__ void load4(float* to, const void* from, long long at) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(from) + at);
-    to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// How a cell is read and written: four neighbours of a lane at a time, one
+// element of every 32 (arrays that are not aligned), and those below its end
+// (a tensor's last cell).
+enum Way : int { kWide = 0, kSingle = 1, kPartial = 2 };
+
+template <Way kWay>
+__device__ __forceinline__ int place(int i, int lane) {
+  return kWay == kWide ? 128 * (i / 4) + 4 * lane + i % 4 : 32 * i + lane;
+}
+
+// A lane's eight elements of 32-bit or BF16 values.
+template <Way kWay, typename T>
+__device__ __forceinline__ void load8(float2 (&x)[4], const void* base, long long e0, int n,
+                                      int lane) {
+  const T* from = static_cast<const T*>(base) + e0;
+  if constexpr (kWay == kWide) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = 128 * h + 4 * lane;
+      if constexpr (sizeof(T) == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(from + j);
+        x[2 * h] = make_float2(v.x, v.y);
+        x[2 * h + 1] = make_float2(v.z, v.w);
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(from + j);
+        x[2 * h] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+        x[2 * h + 1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+      }
+    }
   } else {
-    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(from) + at);
-    to[0] = bf16_lo(x.x), to[1] = bf16_hi(x.x), to[2] = bf16_lo(x.y), to[3] = bf16_hi(x.y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = place<kWay>(i, lane);
+      float v = 0.0f;
+      if (kWay == kSingle || j < n) {
+        if constexpr (sizeof(T) == 4)
+          v = from[j];
+        else
+          v = __uint_as_float(static_cast<uint32_t>(from[j]) << 16);
+      }
+      (i & 1 ? x[i / 2].y : x[i / 2].x) = v;
+    }
   }
 }
 
-template <typename T>
-__device__ __forceinline__ float load1(const void* from, long long at) {
-  if constexpr (sizeof(T) == 4)
-    return static_cast<const float*>(from)[at];
-  else
-    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(from)[at]) << 16);
+template <Way kWay>
+__device__ __forceinline__ void load_codes(uint32_t (&w)[2], const void* base, long long e0, int n,
+                                           int lane) {
+  const uint8_t* from = static_cast<const uint8_t*>(base) + e0;
+  if constexpr (kWay == kWide) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[h] = *reinterpret_cast<const uint32_t*>(from + 128 * h + 4 * lane);
+  } else {
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = place<kWay>(i, lane);
+      c[i] = kWay == kSingle || j < n ? from[j] : 0u;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) w[h] = bytes4(c[4 * h], c[4 * h + 1], c[4 * h + 2], c[4 * h + 3]);
+  }
+}
+
+template <Way kWay>
+__device__ __forceinline__ void store8(const float2 (&x)[4], void* base, long long e0, int n,
+                                       int lane) {
+  float* to = static_cast<float*>(base) + e0;
+  if constexpr (kWay == kWide) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<float4*>(to + 128 * h + 4 * lane) =
+          make_float4(x[2 * h].x, x[2 * h].y, x[2 * h + 1].x, x[2 * h + 1].y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = place<kWay>(i, lane);
+      if (kWay == kSingle || j < n) to[j] = i & 1 ? x[i / 2].y : x[i / 2].x;
+    }
+  }
+}
+
+// Pairs of BF16.
+template <Way kWay>
+__device__ __forceinline__ void store8_bf16(const uint32_t (&x)[4], gg_bf16* base, long long e0,
+                                            int n, int lane) {
+  gg_bf16* to = base + e0;
+  if constexpr (kWay == kWide) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<uint2*>(to + 128 * h + 4 * lane) = make_uint2(x[2 * h], x[2 * h + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = place<kWay>(i, lane);
+      if (kWay == kSingle || j < n)
+        to[j] = static_cast<gg_bf16>(i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xFFFFu);
+    }
+  }
+}
+
+template <Way kWay>
+__device__ __forceinline__ void store_codes(const uint32_t (&w)[2], void* base, long long e0,
+                                            int n, int lane) {
+  uint8_t* to = static_cast<uint8_t*>(base) + e0;
+  if constexpr (kWay == kWide) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<uint32_t*>(to + 128 * h + 4 * lane) = w[h];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = place<kWay>(i, lane);
+      if (kWay == kSingle || j < n) to[j] = static_cast<uint8_t>(w[i / 4] >> (8 * (i % 4)));
+    }
+  }
+}
+
+// What the elements of a tensor share.
+struct Shared {
+  float gs, b1, b2, ib1, ib2, c1, c2, eps, kept;
+  uint32_t key;  // of the cell
+};
+
+template <Way kWay, typename W, typename G, bool k8>
+__device__ __forceinline__ void step_cell(const Entry& t, long long cell, int n, int lane,
+                                          const Shared& k) {
+  const long long e0 = cell * kCell;
+  float2 w[4], g[4], m[4], v[4];
+  float ms = 0.0f, vs = 0.0f;
+  load8<kWay, W>(w, t.w, e0, n, lane);
+  load8<kWay, G>(g, t.g, e0, n, lane);
+  if constexpr (k8) {
+    uint32_t mw[2], vw[2];
+    load_codes<kWay>(mw, t.m, e0, n, lane);
+    load_codes<kWay>(vw, t.v, e0, n, lane);
+    ms = t.ms[cell];
+    vs = t.vs[cell];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      e4m3_values(mw[h], m + 2 * h);
+      e4m3_values(vw[h], v + 2 * h);
+    }
+  } else {
+    load8<kWay, float>(m, t.m, e0, n, lane);
+    load8<kWay, float>(v, t.v, e0, n, lane);
+  }
+  uint32_t mtop = 0, vtop = 0, wtop = 0;
+  float2 r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 gi = mul(g[i], k.gs);
+    if constexpr (k8) {
+      m[i] = mul(m[i], ms);
+      v[i] = mul(v[i], vs);
+      v[i] = mul(v[i], v[i]);
+    }
+    m[i] = add(mul(m[i], k.b1), mul(gi, k.ib1));
+    v[i] = add(mul(v[i], k.b2), mul(mul(gi, gi), k.ib2));
+    r[i] = make_float2(__fsqrt_rn(v[i].x), __fsqrt_rn(v[i].y));
+    const float2 up = mul(m[i], k.c1);
+    const float2 down = add(mul(r[i], k.c2), make_float2(k.eps, k.eps));
+    const float2 q = make_float2(-__fdiv_rn(up.x, down.x), -__fdiv_rn(up.y, down.y));
+    w[i] = add(mul(w[i], k.kept), q);
+    // as bits: ordered, a NaN above infinity. What is behind a tensor's end is
+    // all 0 and stays 0 in m and v.
+    if constexpr (k8) {
+      mtop = max(mtop, max(magnitude(m[i].x), magnitude(m[i].y)));
+      vtop = max(vtop, max(magnitude(r[i].x), magnitude(r[i].y)));
+    }
+    if constexpr (sizeof(W) == 2)
+      wtop = max(wtop, max(magnitude(w[i].x), magnitude(w[i].y)));
+  }
+  uint32_t noise[8];
+  if constexpr (k8 || sizeof(W) == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) noise[i] = mix(k.key + place<kWay>(i, lane));
+  }
+  if constexpr (k8) {
+    mtop = __reduce_max_sync(kFull, mtop);
+    vtop = __reduce_max_sync(kFull, vtop);
+    // a NaN or infinity makes the cell's scale NaN, and so all its values
+    const bool mfine = mtop < kInf, vfine = vtop < kInf;
+    const float ma = fmaxf(__uint_as_float(mtop), kAmaxFloor);
+    const float va = fmaxf(__uint_as_float(vtop), kAmaxFloor);
+    const float minv = __fmul_rn(__frcp_rn(ma), kTop);
+    const float vinv = __fmul_rn(__frcp_rn(va), kTop);
+    if (lane == 0) {
+      t.ms[cell] = mfine ? __fmul_rn(ma, 1.0f / kTop) : __uint_as_float(0x7FC00000u);
+      t.vs[cell] = vfine ? __fmul_rn(va, 1.0f / kTop) : __uint_as_float(0x7FC00000u);
+    }
+    uint32_t mo[2], vo[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 4 * h + j;
+        const float mi = i & 1 ? m[i / 2].y : m[i / 2].x, ri = i & 1 ? r[i / 2].y : r[i / 2].x;
+        a[j] = round_code(__fmul_rn(fabsf(mi), minv), noise[i] << 4 & 0xFFFF0u);
+        if (mi < 0.0f) a[j] |= 128u;
+        b[j] = max(round_code(__fmul_rn(ri, vinv), noise[i] >> 12 & 0xFFFF0u),
+                   min(__float_as_uint(ri), 1u));  // ri > 0
+      }
+      mo[h] = mfine ? bytes4(a[0], a[1], a[2], a[3]) : 0u;
+      vo[h] = vfine ? bytes4(b[0], b[1], b[2], b[3]) : 0u;
+    }
+    store_codes<kWay>(mo, t.m, e0, n, lane);
+    store_codes<kWay>(vo, t.v, e0, n, lane);
+  } else {
+    store8<kWay>(m, t.m, e0, n, lane);
+    store8<kWay>(v, t.v, e0, n, lane);
+  }
+  if constexpr (sizeof(W) == 2) {
+    uint32_t out[4];
+    uint32_t bits[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      bits[i] = __float_as_uint(i & 1 ? w[i / 2].y : w[i / 2].x);
+      const uint32_t up = mix(noise[i] + 0x9E3779B9u) & 0xFFFFu;
+      if (wtop < kInf) {
+        bits[i] += up;
+      } else if (magnitude(__uint_as_float(bits[i])) > kInf) {
+        bits[i] = 0x7FC00000u;  // a NaN stays one
+      } else if ((bits[i] & kInf) != kInf) {
+        bits[i] += up;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = __byte_perm(bits[2 * i], bits[2 * i + 1], 0x7632);
+    store8_bf16<kWay>(out, static_cast<gg_bf16*>(t.w), e0, n, lane);
+  } else {
+    store8<kWay>(w, t.w, e0, n, lane);
+    if (t.half != nullptr) {
+      uint32_t out[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[i] = pack_bf16x2(w[i].x, w[i].y);
+      store8_bf16<kWay>(out, t.half, e0, n, lane);
+    }
+  }
 }
 
 template <int kCap, typename W, typename G, bool k8>
 __global__ void __launch_bounds__(kThreads)
 adamw_kernel(const __grid_constant__ List<kCap> list, const __grid_constant__ StepParams p) {
-  float gs = 1.0f;
+  Shared k;
+  k.gs = 1.0f;
   if (p.grad_scale != nullptr) {
-    gs = *p.grad_scale;
-    if ((__float_as_uint(gs) & kInf) == kInf) return;  // the step is skipped
+    k.gs = *p.grad_scale;
+    if ((__float_as_uint(k.gs) & kInf) == kInf) return;  // the step is skipped
   }
   const bool on_device = p.lr_dev != nullptr || p.step_dev != nullptr;
   __shared__ Factors shared;
   uint32_t run_key = p.run_key;
-  float c2 = p.c2;
+  k.b1 = p.b1, k.b2 = p.b2, k.ib1 = p.ib1, k.ib2 = p.ib2, k.c2 = p.c2, k.eps = p.eps;
   if (on_device) {
     const long long t = p.step_dev != nullptr ? *p.step_dev : p.step;
     if (t < 1) return;
@@ -197,7 +432,7 @@ adamw_kernel(const __grid_constant__ List<kCap> list, const __grid_constant__ St
       shared = factors(p.lr_dev != nullptr ? static_cast<double>(*p.lr_dev) : p.lr, p.beta1,
                        p.beta2, t);
     __syncthreads();
-    c2 = shared.c2;
+    k.c2 = shared.c2;
     run_key = mix(p.seed_key + static_cast<uint32_t>(t));
   }
   const int warp = threadIdx.x >> 5;
@@ -207,179 +442,26 @@ adamw_kernel(const __grid_constant__ List<kCap> list, const __grid_constant__ St
     while (at + 1 < p.count && list.t[at + 1].first <= turn) ++at;
     const Entry& t = list.t[at];
     const long long cell = (turn - t.first) * kWarps + warp;
-    const long long e0 = cell * kCell;
-    if (e0 >= t.n) continue;
-    // The lane's elements: four neighbours of either half of the cell, or one of
-    // every 32, which loads and stores of single elements bring together.
-    const bool whole = t.wide && e0 + kCell <= t.n;
-    const int n = static_cast<int>(min(static_cast<long long>(kCell), t.n - e0));
-    const auto place = [&](int i) {
-      return whole ? 128 * (i / 4) + 4 * lane + i % 4 : 32 * i + lane;
-    };
-    Cell c;
-    float ms = 0.0f, vs = 0.0f;
-    if constexpr (k8) {
-      ms = t.ms[cell];
-      vs = t.vs[cell];
-    }
-    const uint8_t* mq = static_cast<const uint8_t*>(t.m) + e0;
-    const uint8_t* vq = static_cast<const uint8_t*>(t.v) + e0;
-    uint32_t mw[2] = {}, vw[2] = {};
-    if (whole) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = 128 * h + 4 * lane;
-        load4<W>(c.w + 4 * h, t.w, e0 + j);
-        load4<G>(c.g + 4 * h, t.g, e0 + j);
-        if constexpr (k8) {
-          mw[h] = *reinterpret_cast<const uint32_t*>(mq + j);
-          vw[h] = *reinterpret_cast<const uint32_t*>(vq + j);
-        } else {
-          load4<float>(c.m + 4 * h, t.m, e0 + j);
-          load4<float>(c.v + 4 * h, t.v, e0 + j);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = 32 * i + lane;
-        const bool there = j < n;
-        c.w[i] = there ? load1<W>(t.w, e0 + j) : 0.0f;
-        c.g[i] = there ? load1<G>(t.g, e0 + j) : 0.0f;
-        if constexpr (k8) {
-          mw[i / 4] |= (there ? static_cast<uint32_t>(mq[j]) : 0u) << (8 * (i % 4));
-          vw[i / 4] |= (there ? static_cast<uint32_t>(vq[j]) : 0u) << (8 * (i % 4));
-        } else {
-          c.m[i] = there ? load1<float>(t.m, e0 + j) : 0.0f;
-          c.v[i] = there ? load1<float>(t.v, e0 + j) : 0.0f;
-        }
-      }
-    }
-    const float c1 = on_device ? c1_of(shared, t.lr_scale) : t.c1;
-    const float kept = on_device ? kept_of(shared, t.lr_scale, t.decay) : t.kept;
-    uint32_t mtop = 0, vtop = 0;
-    float r[8];
-    if constexpr (k8) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        e4m3_values(mw[h], c.m + 4 * h);
-        e4m3_values(vw[h], c.v + 4 * h);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float g = __fmul_rn(c.g[i], gs);
-      if constexpr (k8) {
-        c.m[i] = __fmul_rn(c.m[i], ms);
-        const float old = __fmul_rn(c.v[i], vs);
-        c.v[i] = __fmul_rn(old, old);
-      }
-      c.m[i] = __fadd_rn(__fmul_rn(c.m[i], p.b1), __fmul_rn(g, p.ib1));
-      c.v[i] = __fadd_rn(__fmul_rn(c.v[i], p.b2), __fmul_rn(__fmul_rn(g, g), p.ib2));
-      r[i] = __fsqrt_rn(c.v[i]);
-      c.w[i] = __fadd_rn(__fmul_rn(c.w[i], kept),
-                         -__fdiv_rn(__fmul_rn(c.m[i], c1), __fadd_rn(__fmul_rn(r[i], c2), p.eps)));
-      if constexpr (k8) {
-        const bool there = whole || 32 * i + lane < n;
-        // as bits: ordered, a NaN above infinity
-        mtop = max(mtop, there ? __float_as_uint(c.m[i]) & 0x7FFFFFFFu : 0u);
-        vtop = max(vtop, there ? __float_as_uint(r[i]) & 0x7FFFFFFFu : 0u);
-      }
-    }
-    uint32_t noise[8];
-    if constexpr (k8 || sizeof(W) == 2) {
-      const uint32_t key = mix(mix(run_key + static_cast<uint32_t>(t.position)) +
-                               static_cast<uint32_t>(cell));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) noise[i] = mix(key + place(i));
-    }
-    uint32_t mo[2] = {}, vo[2] = {};
-    if constexpr (k8) {
-      mtop = __reduce_max_sync(kFull, mtop);
-      vtop = __reduce_max_sync(kFull, vtop);
-      // a NaN or infinity makes the cell's scale NaN, and so all its values
-      const bool mfine = mtop < kInf, vfine = vtop < kInf;
-      const float ma = fmaxf(__uint_as_float(mtop), kAmaxFloor);
-      const float va = fmaxf(__uint_as_float(vtop), kAmaxFloor);
-      const float minv = __fmul_rn(__frcp_rn(ma), kTop);
-      const float vinv = __fmul_rn(__frcp_rn(va), kTop);
-      if (lane == 0) {
-        t.ms[cell] = mfine ? __fmul_rn(ma, 1.0f / kTop) : __uint_as_float(0x7FC00000u);
-        t.vs[cell] = vfine ? __fmul_rn(va, 1.0f / kTop) : __uint_as_float(0x7FC00000u);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t a = round_code(__fmul_rn(fabsf(c.m[i]), minv), noise[i] & 0xFFFFu);
-        uint32_t b = round_code(__fmul_rn(r[i], vinv), noise[i] >> 16);
-        if (c.m[i] < 0.0f) a |= 128u;
-        if (r[i] > 0.0f) b = max(b, 1u);
-        mo[i / 4] |= (mfine ? a : 0u) << (8 * (i % 4));
-        vo[i / 4] |= (vfine ? b : 0u) << (8 * (i % 4));
-      }
-    }
-    if constexpr (sizeof(W) == 2) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __float_as_uint(c.w[i]);
-        const uint32_t up = (b & kInf) == kInf ? 0u : mix(noise[i] + 0x9E3779B9u) & 0xFFFFu;
-        // cut to BF16; a NaN stays one
-        const uint32_t lost = (b & 0x7FFFFFFFu) > kInf ? 0x7FC00000u : b + up;
-        c.w[i] = __uint_as_float(lost & 0xFFFF0000u);
-      }
-    }
-    if (whole) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const long long j = e0 + 128 * h + 4 * lane;
-        const float* x = c.w + 4 * h;
-        if constexpr (sizeof(W) == 4)
-          *reinterpret_cast<float4*>(static_cast<float*>(t.w) + j) =
-              make_float4(x[0], x[1], x[2], x[3]);
-        else
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.w) + j) =
-              make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-        if (t.half != nullptr)
-          *reinterpret_cast<uint2*>(t.half + j) =
-              make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-        if constexpr (k8) {
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + j) = mo[h];
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + j) = vo[h];
-        } else {
-          *reinterpret_cast<float4*>(static_cast<float*>(t.m) + j) =
-              make_float4(c.m[4 * h], c.m[4 * h + 1], c.m[4 * h + 2], c.m[4 * h + 3]);
-          *reinterpret_cast<float4*>(static_cast<float*>(t.v) + j) =
-              make_float4(c.v[4 * h], c.v[4 * h + 1], c.v[4 * h + 2], c.v[4 * h + 3]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = 32 * i + lane;
-        if (k >= n) continue;
-        const long long j = e0 + k;
-        if constexpr (sizeof(W) == 4)
-          static_cast<float*>(t.w)[j] = c.w[i];
-        else
-          static_cast<uint16_t*>(t.w)[j] = __bfloat16_as_ushort(__float2bfloat16_rn(c.w[i]));
-        if (t.half != nullptr) t.half[j] = __bfloat16_as_ushort(__float2bfloat16_rn(c.w[i]));
-        if constexpr (k8) {
-          static_cast<uint8_t*>(t.m)[j] = static_cast<uint8_t>(mo[i / 4] >> (8 * (i % 4)));
-          static_cast<uint8_t*>(t.v)[j] = static_cast<uint8_t>(vo[i / 4] >> (8 * (i % 4)));
-        } else {
-          static_cast<float*>(t.m)[j] = c.m[i];
-          static_cast<float*>(t.v)[j] = c.v[i];
-        }
-      }
-    }
+    const long long left = t.n - cell * kCell;
+    if (left <= 0) continue;
+    k.c1 = on_device ? c1_of(shared, t.lr_scale) : t.c1;
+    k.kept = on_device ? kept_of(shared, t.lr_scale, t.decay) : t.kept;
+    k.key = mix(mix(run_key + static_cast<uint32_t>(t.position)) + static_cast<uint32_t>(cell));
+    const int n = static_cast<int>(min(static_cast<long long>(kCell), left));
+    if (n < kCell)
+      step_cell<kPartial, W, G, k8>(t, cell, n, lane, k);
+    else if (t.wide)
+      step_cell<kWide, W, G, k8>(t, cell, n, lane, k);
+    else
+      step_cell<kSingle, W, G, k8>(t, cell, n, lane, k);
   }
 }
 
 template <int kCap, typename W, typename G, bool k8>
 cudaError_t launch_step_t(const List<kMany>& all, const StepParams& p, int sm_count,
                           cudaStream_t stream) {
-  List<kCap> list;
+  List<kCap> list;  // entries from p.count on are not read
   for (int i = 0; i < p.count; ++i) list.t[i] = all.t[i];
-  for (int i = p.count; i < kCap; ++i) list.t[i] = Entry{};
   const long long most = static_cast<long long>(sm_count) * 8;
   const unsigned grid = static_cast<unsigned>(p.turns < most ? p.turns : most);
   adamw_kernel<kCap, W, G, k8><<<grid, kThreads, 0, stream>>>(list, p);
@@ -448,6 +530,14 @@ __device__ __forceinline__ double block_sum(double x) {
   return s;
 }
 
+template <typename T>
+__device__ __forceinline__ float load1(const void* from, long long at) {
+  if constexpr (sizeof(T) == 4)
+    return static_cast<const float*>(from)[at];
+  else
+    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(from)[at]) << 16);
+}
+
 // Squares are added in fp32, 32 at a time, and those sums in 64 bits.
 template <int kCap, typename G>
 __global__ void __launch_bounds__(kThreads)
@@ -513,8 +603,8 @@ norm_join_kernel(const double* partial, int count, float max_norm, float* out) {
 template <int kCap, typename G>
 cudaError_t launch_norm_t(const NormList<kNormList>& all, int count, long long turns, int grid,
                           double* partial, float max_norm, float* out, cudaStream_t stream) {
-  NormList<kCap> list;
-  for (int i = 0; i < kCap; ++i) list.t[i] = i < count ? all.t[i] : NormEntry{};
+  NormList<kCap> list;  // entries from count on are not read
+  for (int i = 0; i < count; ++i) list.t[i] = all.t[i];
   norm_kernel<kCap, G><<<grid, kThreads, 0, stream>>>(list, count, turns, partial, max_norm, out);
   count_launch();
   return cudaGetLastError();
@@ -575,9 +665,12 @@ cudaError_t launch_adamw(const gg_adamw_tensor* tensors, int n, const gg_adamw_o
       p.turns += (cells + kWarps - 1) / kWarps;
     }
     if (p.count == 0) break;
-    const cudaError_t e = p.count <= kFew
-                              ? launch_step_w<kFew>(list, p, w32, g32, k8, dev.sm_count, stream)
-                              : launch_step_w<kMany>(list, p, w32, g32, k8, dev.sm_count, stream);
+    const auto go = [&](auto launch) {
+      return launch(list, p, w32, g32, k8, dev.sm_count, stream);
+    };
+    const cudaError_t e = p.count <= kFew    ? go(launch_step_w<kFew>)
+                          : p.count <= kSome ? go(launch_step_w<kSome>)
+                                             : go(launch_step_w<kMany>);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -611,17 +704,16 @@ cudaError_t launch_grad_norm(const gg_grad_tensor* tensors, int n, bool f32, flo
     const int grid = static_cast<int>(turns < 1 ? 1 : (turns < most ? turns : most));
     done = i == n && written == 0 && grid == 1;  // one block: it writes the result
     float* to = done ? out : nullptr;
+    const auto go = [&](auto launch) {
+      return launch(list, count, turns, grid, partial + written, max_norm, to, stream);
+    };
     cudaError_t e;
     if (count <= kFew)
-      e = f32 ? launch_norm_t<kFew, float>(list, count, turns, grid, partial + written, max_norm,
-                                           to, stream)
-              : launch_norm_t<kFew, gg_bf16>(list, count, turns, grid, partial + written,
-                                             max_norm, to, stream);
+      e = f32 ? go(launch_norm_t<kFew, float>) : go(launch_norm_t<kFew, gg_bf16>);
+    else if (count <= kSome)
+      e = f32 ? go(launch_norm_t<kSome, float>) : go(launch_norm_t<kSome, gg_bf16>);
     else
-      e = f32 ? launch_norm_t<kNormList, float>(list, count, turns, grid, partial + written,
-                                                max_norm, to, stream)
-              : launch_norm_t<kNormList, gg_bf16>(list, count, turns, grid, partial + written,
-                                                  max_norm, to, stream);
+      e = f32 ? go(launch_norm_t<kNormList, float>) : go(launch_norm_t<kNormList, gg_bf16>);
     if (e != cudaSuccess) return e;
     written += grid;
   } while (i < n);
