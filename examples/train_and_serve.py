@@ -1,6 +1,6 @@
 """Trains a small mixture-of-experts layer with its router, then serves it on 8-bit weights.
 
-    python examples/train_and_serve.py [--steps 60] [--tokens 2048]
+    python examples/train_and_serve.py [--steps 60] [--tokens 2048] [--f8]
 
 A student layer (router, E experts) learns to reproduce a fixed teacher layer. One training step:
 
@@ -10,6 +10,9 @@ A student layer (router, E experts) learns to reproduce a fixed teacher layer. O
     MoeLayer.weight_grads                   dW1, dW2 of the experts, in fp32
     route_bwd  -> dlogits                   from dprob and the balance and z losses
     grad_norm, AdamW.step                   all weights in one launch, skipped unless finite
+
+With --f8 the layer is F8MoeLayer: both directions on E4M3 codes of the BF16 weights with a scale
+for every 128 x 128 block, made anew after each step (f8_prepare_weight).
 
 Serving quantises the trained experts once (q8_prepare_weight) and runs Q8MoeLayer, for the whole
 batch and for a single token. Needs a GB300 and the built library.
@@ -36,7 +39,7 @@ def experts(g, scale):
             for s in ((E, 2 * F, H), (E, H, F))]
 
 
-def train(tokens: int, steps: int, seed: int = 0, log=print):
+def train(tokens: int, steps: int, seed: int = 0, log=print, f8: bool = False):
     """Returns dict(first, last, W1, W2, R, x, route, out): losses and the trained layer."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     x = torch.randn(tokens, H, generator=g, device="cuda").bfloat16()
@@ -49,6 +52,8 @@ def train(tokens: int, steps: int, seed: int = 0, log=print):
     weights.append(tr + 0.3 * torch.randn(H, E, generator=g, device="cuda") / H ** 0.5)
     R = weights[2]
     W1, W2, _ = half = [w.bfloat16() for w in weights]
+    w1, w2 = (gg.f8_prepare_weight(W1), gg.f8_prepare_weight(W2)) if f8 else (W1, W2)
+    student = gg.F8MoeLayer(tokens, H, F, K, E) if f8 else layer
     dW1, dW2, dR = grads = [torch.empty_like(w) for w in weights]
     opt = gg.AdamW(weights, grads, half=half, betas=(0.9, 0.99))
     norm = gg.GradPlan(grads)
@@ -57,21 +62,24 @@ def train(tokens: int, steps: int, seed: int = 0, log=print):
     for i in range(steps):
         logits = x.float() @ R
         r = gg.route(logits, K, renormalize=True, counts=True, losses=True, ws=ws)
-        out = layer.forward(x, r["idx"], r["prob"], W1, W2)
+        out = student.forward(x, r["idx"], r["prob"], w1, w2)
         err = out.float() - target
         losses.append(err.square().mean())
         dOut = (err * (2.0 / tokens)).bfloat16()
-        _, dprob = layer.backward(dOut, W1, W2, dprob=True)
-        layer.weight_grads(dW1, dW2)
+        _, dprob = student.backward(dOut, w1, w2, dprob=True)
+        student.weight_grads(dW1, dW2)
         dlogits = gg.route_bwd(logits, r["idx"], dprob, renormalize=True, counts=r["counts"],
                                aux_coef=AUX, z_coef=ZCO)
         torch.mm(x.float().t(), dlogits, out=dR)
         opt.step(LR, grad_scale=gg.grad_norm(norm)[1:])
+        if f8:
+            gg.f8_prepare_weight(W1, *w1)
+            gg.f8_prepare_weight(W2, *w2)
         if i % 20 == 0 or i == steps - 1:
             log(f"step {i:4d}  loss {losses[-1].item():.5f}  balance {r['losses'][0].item():.3f}"
                 f"  busiest expert {int(r['counts'].max())} of {tokens * K} pairs")
-    if layer.status() != 0:
-        raise RuntimeError(gg.status_string(layer.status()))
+    if student.status() != 0:
+        raise RuntimeError(gg.status_string(student.status()))
     r = gg.route(x.float() @ R, K, renormalize=True)
     out = layer.forward(x, r["idx"], r["prob"], W1, W2)
     return dict(first=losses[0].item(), last=losses[-1].item(), W1=W1, W2=W2, R=R,
@@ -98,8 +106,9 @@ def main():
                                  formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--tokens", type=int, default=2048)
+    ap.add_argument("--f8", action="store_true", help="train on E4M3 codes of the weights")
     a = ap.parse_args()
-    serve(train(a.tokens, a.steps))
+    serve(train(a.tokens, a.steps, f8=a.f8))
 
 
 if __name__ == "__main__":

@@ -852,6 +852,28 @@ gg_status gg_f8_grouped_dgrad(const gg_bf16* dC, const uint8_t* Wq, const float*
                               gg_bf16* dA, float* rowdot, void* ws, size_t ws_bytes,
                               gg_stream_t stream);
 
+/* The expert layer on such weights: gg_moe_mlp_fwd_ex and gg_moe_mlp_bwd_ex with
+ * their linear layers as gg_f8_grouped_fwd and gg_f8_grouped_dgrad, on the same
+ * buffers; W1q[E][2F][H], W2q[E][H][F] and their scales from
+ * gg_f8_prepare_weight serve both directions. gg_moe_mlp_wgrad follows
+ * unchanged: the weight gradients are of the BF16 rows. H and F multiples of 64;
+ * every prob_mode; recompute_h1 is refused (GG_ERR_INVALID_ARG). ws: scratch of
+ * gg_moe_f8_workspace_size(T, H, F, k, E, pad_multiple) bytes, status word
+ * first, for the codes of the rows; nothing in it is kept between calls. A
+ * device-side error is reported in buf->ws or in ws. */
+size_t gg_moe_f8_workspace_size(int T, int H, int F, int k, int E, int pad_multiple);
+gg_status gg_moe_mlp_fwd_f8(const gg_bf16* x, const int32_t* idx, const float* prob,
+                            const uint8_t* W1q, const float* W1s, const uint8_t* W2q,
+                            const float* W2s, int T, int H, int F, int k, int E, int pad_multiple,
+                            const gg_moe_options* opt, gg_bf16* out, const gg_moe_buffers* buf,
+                            void* ws, size_t ws_bytes, gg_stream_t stream);
+gg_status gg_moe_mlp_bwd_f8(const gg_bf16* dOut, const gg_bf16* x, const float* prob,
+                            const uint8_t* W1q, const float* W1s, const uint8_t* W2q,
+                            const float* W2s, int T, int H, int F, int k, int E, int pad_multiple,
+                            const gg_moe_options* opt, gg_bf16* dX, float* dprob,
+                            const gg_moe_buffers* buf, void* ws, size_t ws_bytes,
+                            gg_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * gg_adamw_step — one AdamW step over many tensors, in one launch for every
  * 310 of them. For each element, every operation rounded to fp32:

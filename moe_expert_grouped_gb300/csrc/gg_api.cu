@@ -13,6 +13,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -1249,6 +1250,114 @@ gg_status gg_f8_grouped_dgrad(const gg_bf16* dC, const uint8_t* Wq, const float*
   a.rowdot = rowdot;
   if (f8_rows_to_ws(dC, N, &a, ws, dev, st) != cudaSuccess) return GG_ERR_CUDA;
   return from_cuda(launch_f8_gemm(a, true, dev, st));
+}
+
+size_t gg_moe_f8_workspace_size(int T, int H, int F, int k, int E, int pad_multiple) {
+  if (T < 0 || H <= 0 || F <= 0 || k <= 0 || E <= 0 || pad_multiple <= 0) return 0;
+  const long long rc = r_cap_of(T, k, E, pad_multiple);
+  if (rc > 0x7FFFFFFFLL || F > 0x3FFFFFFF) return 0;
+  return gg_f8_workspace_size(static_cast<int>(rc), std::max(H, 2 * F));
+}
+
+// What both directions of the layer ask of their arguments, before either enqueues anything.
+static gg_status f8_layer_checks(int T, int H, int F, int k, int E, int P,
+                                 const gg_moe_options* opt, const uint8_t* W1q, const float* W1s,
+                                 const uint8_t* W2q, const float* W2s, const gg_moe_buffers* b,
+                                 const void* ws, size_t ws_bytes, gg_epilogue* fepi,
+                                 gg_epilogue* bepi, int* mode, int* R_cap) {
+  if (T < 0 || H <= 0 || F <= 0 || k <= 0 || E <= 0 || P <= 0) return GG_ERR_INVALID_ARG;
+  bool recompute;
+  gg_status s = read_options(opt, fepi, bepi, mode, &recompute);
+  if (s != GG_OK) return s;
+  if (recompute) return GG_ERR_INVALID_ARG;
+  if ((s = check_buffers(b, T, k, E)) != GG_OK) return s;
+  const long long rc = r_cap_of(T, k, E, P);
+  if (F > 0x3FFFFFFF || rc > 0x7FFFFFFFLL) return GG_ERR_UNSUPPORTED_SHAPE;
+  *R_cap = static_cast<int>(rc);
+  const float* p = b->prob_of_row;
+  if ((s = f8_gemm_checks(b->Xp, W1q, W1s, b->offsets, E, *R_cap, H, 2 * F, 2 * F, p, b->A)) !=
+          GG_OK ||
+      (s = f8_gemm_checks(b->A, W2q, W2s, b->offsets, E, *R_cap, F, H, H, p, b->Yp)) != GG_OK ||
+      (s = f8_gemm_checks(b->dYp, W2q, W2s, b->offsets, E, *R_cap, F, H, F, p, b->dH)) != GG_OK ||
+      (s = f8_gemm_checks(b->dH, W1q, W1s, b->offsets, E, *R_cap, H, 2 * F, H, p, b->dXp)) !=
+          GG_OK ||
+      (s = dgrad_epilogue_checks(*bepi, b->H1, b->rowdot)) != GG_OK)
+    return s;
+  if (!aligned_to(b->row_of_slot, 4) || !aligned_to(b->slot_of_row, 4)) return GG_ERR_MISALIGNED;
+  return check_ws(ws, ws_bytes, gg_moe_f8_workspace_size(T, H, F, k, E, P));
+}
+
+gg_status gg_moe_mlp_fwd_f8(const gg_bf16* x, const int32_t* idx, const float* prob,
+                            const uint8_t* W1q, const float* W1s, const uint8_t* W2q,
+                            const float* W2s, int T, int H, int F, int k, int E, int pad_multiple,
+                            const gg_moe_options* opt, gg_bf16* out, const gg_moe_buffers* buf,
+                            void* ws, size_t ws_bytes, gg_stream_t stream) {
+  gg_epilogue fepi, bepi;
+  int mode, R_cap;
+  gg_status s = f8_layer_checks(T, H, F, k, E, pad_multiple, opt, W1q, W1s, W2q, W2s, buf, ws,
+                                ws_bytes, &fepi, &bepi, &mode, &R_cap);
+  if (s != GG_OK) return s;
+  if (T > 0 && (x == nullptr || out == nullptr)) return GG_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(out)) return GG_ERR_MISALIGNED;
+  const bool pre = mode == GG_PROB_PRE_FC1;
+  // BF16 rows first, codes after: the weight gradients read the rows
+  s = gg_permute(x, idx, prob, T, H, k, E, pad_multiple, pre ? nullptr : buf->Xp, buf->offsets,
+                 buf->row_of_slot, buf->slot_of_row, buf->prob_of_row, buf->ws, buf->ws_bytes,
+                 stream);
+  if (s != GG_OK || T == 0) return s;
+  if (pre) {
+    s = gg_permute_rows(x, buf->row_of_slot, buf->slot_of_row, buf->offsets, T, H, k, E,
+                        pad_multiple, R_cap, prob, buf->Xp, buf->ws, buf->ws_bytes, stream);
+    if (s != GG_OK) return s;
+  }
+  s = gg_f8_grouped_fwd(buf->Xp, W1q, W1s, buf->offsets, E, R_cap, H, 2 * F, fepi, buf->A, buf->H1,
+                        mode == GG_PROB_ACTIVATION ? buf->prob_of_row : nullptr, ws, ws_bytes,
+                        stream);
+  if (s != GG_OK) return s;
+  s = gg_f8_grouped_fwd(buf->A, W2q, W2s, buf->offsets, E, R_cap, F, H, GG_EPI_NONE, buf->Yp,
+                        nullptr, nullptr, ws, ws_bytes, stream);
+  if (s != GG_OK) return s;
+  return gg_unpermute_combine(buf->Yp, buf->row_of_slot, mode == GG_PROB_COMBINE ? prob : nullptr,
+                              T, k, H, R_cap, out, nullptr, 0, nullptr, nullptr, buf->ws,
+                              buf->ws_bytes, stream);
+}
+
+gg_status gg_moe_mlp_bwd_f8(const gg_bf16* dOut, const gg_bf16* x, const float* prob,
+                            const uint8_t* W1q, const float* W1s, const uint8_t* W2q,
+                            const float* W2s, int T, int H, int F, int k, int E, int pad_multiple,
+                            const gg_moe_options* opt, gg_bf16* dX, float* dprob,
+                            const gg_moe_buffers* buf, void* ws, size_t ws_bytes,
+                            gg_stream_t stream) {
+  gg_epilogue fepi, bepi;
+  int mode, R_cap;
+  gg_status s = f8_layer_checks(T, H, F, k, E, pad_multiple, opt, W1q, W1s, W2q, W2s, buf, ws,
+                                ws_bytes, &fepi, &bepi, &mode, &R_cap);
+  if (s != GG_OK) return s;
+  if (T == 0) return GG_OK;
+  if (dOut == nullptr || dX == nullptr) return GG_ERR_INVALID_ARG;
+  const bool pre = mode == GG_PROB_PRE_FC1;
+  if (pre && (prob == nullptr || (dprob != nullptr && x == nullptr))) return GG_ERR_INVALID_ARG;
+  if (!aligned16(dOut) || !aligned16(x) || !aligned16(dX) || !aligned_to(dprob, 4) ||
+      !aligned_to(prob, 4))
+    return GG_ERR_MISALIGNED;
+  float* rowdot = dprob != nullptr && !pre ? buf->rowdot : nullptr;
+  s = gg_permute_rows(dOut, buf->row_of_slot, buf->slot_of_row, buf->offsets, T, H, k, E,
+                      pad_multiple, R_cap, nullptr, buf->dYp, buf->ws, buf->ws_bytes, stream);
+  if (s != GG_OK) return s;
+  // both gradients read the forward's codes: W2 as [E][H][F], W1 as [E][2F][H]
+  s = gg_f8_grouped_dgrad(buf->dYp, W2q, W2s, buf->offsets, E, R_cap, F, H, bepi, buf->H1,
+                          pre ? nullptr : buf->prob_of_row, buf->dH, rowdot, ws, ws_bytes, stream);
+  if (s != GG_OK) return s;
+  s = gg_f8_grouped_dgrad(buf->dH, W1q, W1s, buf->offsets, E, R_cap, H, 2 * F, GG_EPI_NONE,
+                          nullptr, nullptr, buf->dXp, nullptr, ws, ws_bytes, stream);
+  if (s != GG_OK) return s;
+  if (pre)  // Xp = prob * x: dX = sum_j prob * dXp[row], dprob = <x_t, dXp[row]>
+    return gg_unpermute_combine(buf->dXp, buf->row_of_slot, prob, T, k, H, R_cap, dX, nullptr, 0,
+                                dprob != nullptr ? x : nullptr, dprob, buf->ws, buf->ws_bytes,
+                                stream);
+  return gg_unpermute_combine(buf->dXp, buf->row_of_slot, nullptr, T, k, H, R_cap, dX, rowdot,
+                              gg_rowdot_blocks(F), nullptr, dprob, buf->ws, buf->ws_bytes,
+                              stream);
 }
 
 gg_status gg_adamw_step(const gg_adamw_tensor* tensors, int n, const gg_adamw_options* options,

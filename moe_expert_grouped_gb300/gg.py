@@ -91,6 +91,11 @@ SIGNATURES = [
     ("gg_f8_grouped_fwd", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
     ("gg_f8_grouped_dgrad", _I,
      [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P]),
+    ("gg_moe_f8_workspace_size", _Z, [_I, _I, _I, _I, _I, _I]),
+    ("gg_moe_mlp_fwd_f8", _I,
+     [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
+    ("gg_moe_mlp_bwd_f8", _I,
+     [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P]),
     ("gg_adamw_step", _I, [_P, _I, _P, _P]),
     ("gg_grad_norm_workspace_size", _Z, [_I]),
     ("gg_grad_norm", _I, [_P, _I, _I, _F, _P, _P, _Z, _P]),
@@ -1020,6 +1025,87 @@ def f8_grouped_dgrad(dC, Wq, Ws, offsets, epilogue: int = GG_EPI_NONE, H1=None, 
                                        _ptr(rowdot), _ptr(ws), ws.numel(), _stream(dev)),
                "gg_f8_grouped_dgrad")
     return dA
+
+
+class F8MoeLayer(MoeLayer):
+    """The whole expert layer on E4M3 weights with scales per block (gg_moe_mlp_fwd_f8 /
+    gg_moe_mlp_bwd_f8); weights as the (codes, scales) pairs of f8_prepare_weight, one pair for
+    both directions. weight_grads gives the gradients of the BF16 or fp32 weights they were
+    made from."""
+
+    def __init__(self, T: int, H: int, F: int, k: int, E: int, P: int = 1, device="cuda",
+                 activation: int = GG_ACT_SWIGLU, prob_mode: int = GG_PROB_COMBINE):
+        super().__init__(T, H, F, k, E, P, device, activation, prob_mode)
+        n = int(LIB.gg_moe_f8_workspace_size(T, H, F, k, E, P))
+        if n == 0:
+            raise GGError(2, "gg_moe_f8_workspace_size")
+        self.ws8 = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        self.device = self.ws8.device  # with its index
+
+    def _weights(self, W1, W2):
+        E, H, F = self.E, self.H, self.F
+        _need_f8_weight(*W1, (E, 2 * F, H), self.device)
+        _need_f8_weight(*W2, (E, H, F), self.device)
+        return (*map(_ptr, W1), *map(_ptr, W2))
+
+    def forward(self, x, idx, prob, W1, W2, out=None):
+        """out [T, H] for x [T, H]: T is the bound size or any smaller batch that fits."""
+        T = int(x.shape[0])
+        H, k = self.H, self.k
+        if not self.fits(T):
+            raise GGError(4, f"{T} tokens do not fit a layer bound for {self.T}")
+        _need(x, torch.bfloat16, (T, H), "x")
+        _need(idx, torch.int32, (T, k), "idx")
+        _need(prob, torch.float32, (T, k), "prob")
+        weights = self._weights(W1, W2)
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=self.device) if out is None else out
+        _need(out, torch.bfloat16, (T, H), "out")
+        _on(self.device, x=x, idx=idx, prob=prob, out=out)
+        with _guard(self.device):
+            _check(LIB.gg_moe_mlp_fwd_f8(_ptr(x), _ptr(idx), _ptr(prob), *weights, T, H, self.F, k,
+                                         self.E, self.P, ctypes.byref(self.opt), _ptr(out),
+                                         ctypes.byref(self.buf), _ptr(self.ws8),
+                                         self.ws8.numel(), _stream(self.device)),
+                   "gg_moe_mlp_fwd_f8")
+        self._saved = (x, prob)
+        self._rows = T
+        self._backward_rows = None
+        return out
+
+    def backward(self, dOut, W1, W2, dX=None, dprob=None):
+        """dX [T, H] of the last forward's batch; with dprob ([T, k] fp32, or True to allocate
+        one) also the probabilities' gradient, as (dX, dprob)."""
+        if self._rows is None:
+            raise GGError(1, "backward before forward")
+        T, H, k = self._rows, self.H, self.k
+        _need(dOut, torch.bfloat16, (T, H), "dOut")
+        weights = self._weights(W1, W2)
+        dX = torch.empty((T, H), dtype=torch.bfloat16, device=self.device) if dX is None else dX
+        _need(dX, torch.bfloat16, (T, H), "dX")
+        want = dprob is not None and dprob is not False
+        if dprob is True:
+            dprob = torch.empty((T, k), dtype=torch.float32, device=self.device)
+        if want:
+            _need(dprob, torch.float32, (T, k), "dprob")
+        x, prob = self._saved
+        _on(self.device, dOut=dOut, dX=dX, dprob=dprob if want else None)
+        with _guard(self.device):
+            _check(LIB.gg_moe_mlp_bwd_f8(_ptr(dOut), _ptr(x), _ptr(prob), *weights, T, H, self.F,
+                                         k, self.E, self.P, ctypes.byref(self.opt), _ptr(dX),
+                                         _ptr(dprob) if want else None, ctypes.byref(self.buf),
+                                         _ptr(self.ws8), self.ws8.numel(), _stream(self.device)),
+                   "gg_moe_mlp_bwd_f8")
+        self._backward_rows = T
+        return (dX, dprob) if want else dX
+
+    def weight_grads(self, dW1=None, dW2=None, base1=None, base2=None,
+                     out_dtype=torch.bfloat16):
+        _on(self.device, dW1=dW1, dW2=dW2, base1=base1, base2=base2)
+        with _guard(self.device):
+            return super().weight_grads(dW1, dW2, base1, base2, out_dtype)
+
+    def status(self) -> int:
+        return super().status() or read_status(self.ws8)
 
 
 # ---------------------------------------------------------------- optimizer step

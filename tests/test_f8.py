@@ -1,6 +1,8 @@
 """CPU checks of the E4M3 products with scales per block of 128: the oracle's codes against
 torch's E4M3, its gradient against differences, and the refusals that come before any launch."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -154,3 +156,53 @@ class TestRefusals:
         assert rows(src=None) == rows(T=5) == rows(ros=a, k=33) == rows(ros=a, k=0) == 1
         assert rows(ws=None) == rows(T=-1) == 1
         assert rows(K=72) == 2 and rows(S=a + 2) == 3 and rows(nbytes=8) == 4
+
+    def _layer(self, gg, backward=False, opt=(0, 0, 0), T=20, H=128, F=64, k=2, E=4, P=1, null=None,
+               buf=None, nbytes=None, **kw):
+        L, a = gg.LIB, 1 << 12
+        b = gg.GGBuffers()
+        assert L.gg_moe_buffers_bind(1 << 20, 1 << 40, 20, 128, 64, 2, 4, 1, ctypes.byref(b)) == 0
+        for name, v in (buf or {}).items():
+            setattr(b, name, v)
+        names = ["dOut", "x", "prob"] if backward else ["x", "idx", "prob"]
+        args = dict.fromkeys(names + ["W1q", "W1s", "W2q", "W2s"], a)
+        tail = dict.fromkeys(["dX", "dprob"] if backward else ["out"], a)
+        ws = dict(ws=a)
+        for d in (args, tail, ws):
+            d.update({n: v for n, v in kw.items() if n in d})
+            d.update({n: None for n in d if n == null})
+        need = L.gg_moe_f8_workspace_size(T, H, F, k, E, P) if nbytes is None else nbytes
+        o = gg.GGOptions(*opt)
+        f = L.gg_moe_mlp_bwd_f8 if backward else L.gg_moe_mlp_fwd_f8
+        return f(*args.values(), T, H, F, k, E, P, ctypes.byref(o), *tail.values(),
+                 ctypes.byref(b), ws["ws"], need, None)
+
+    @pytest.mark.parametrize("backward", [False, True])
+    @pytest.mark.parametrize("kw,code", [
+        (dict(null="W1q"), 1), (dict(null="W1s"), 1), (dict(null="W2q"), 1), (dict(null="W2s"), 1),
+        (dict(null="x", opt=(0, 2, 0)), 1), (dict(null="prob", opt=(0, 2, 0), back=True), 1),
+        (dict(null="out", fwd=True), 1), (dict(null="dOut", back=True), 1),
+        (dict(null="dX", back=True), 1), (dict(null="ws"), 1), (dict(opt=(0, 0, 1)), 1),
+        (dict(opt=(2, 0, 0)), 1), (dict(opt=(0, 3, 0)), 1), (dict(T=-1), 1), (dict(P=0), 1),
+        (dict(buf=dict(H1=None)), 1), (dict(buf=dict(rowdot=None)), 1), (dict(H=96), 2),
+        (dict(F=32), 2), (dict(T=1 << 30, k=4, E=1, buf=dict(ws_bytes=1 << 60), nbytes=0), 2),
+        (dict(buf=dict(dXp=(1 << 20) + 8)), 3), (dict(buf=dict(H1=(1 << 20) + 8)), 3),
+        (dict(W1q=4104), 3), (dict(W2s=4098), 3), (dict(out=4104, fwd=True), 3),
+        (dict(dX=4104, back=True), 3), (dict(ws=4104), 3), (dict(nbytes=255), 4)])
+    def test_layer(self, gg, backward, kw, code):
+        kw = dict(kw)
+        only = {"back": True, "fwd": False}
+        for name, side in only.items():
+            if kw.pop(name, False) and side != backward:
+                return
+        assert self._layer(gg, backward, **kw) == code
+
+    def test_layer_workspace(self, gg):
+        L = gg.LIB
+        rows = gg.r_cap(30, 2, 6, 16)
+        assert L.gg_moe_f8_workspace_size(30, 128, 192, 2, 6, 16) == L.gg_f8_workspace_size(
+            rows, 384)
+        assert L.gg_moe_f8_workspace_size(30, 512, 192, 2, 6, 16) == L.gg_f8_workspace_size(
+            rows, 512)
+        assert L.gg_moe_f8_workspace_size(30, 0, 192, 2, 6, 16) == 0
+        assert L.gg_moe_f8_workspace_size(1 << 30, 64, 64, 4, 1, 1) == 0
