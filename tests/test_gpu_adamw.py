@@ -271,7 +271,9 @@ def _step_at(g, first_cell, size):
 
 @pytest.mark.parametrize("g_bf16", [False, True])
 @pytest.mark.parametrize("sizes", [[1], [8192], [8193], [1, 3, 255, 4097, 100000], [3000000],
-                                   [7 + 13 * i for i in range(1500)], [0, 5, 0]],
+                                   [7 + 13 * i for i in range(1500)], [0, 5, 0],
+                                   [8192] * 2, [8192 * 64], [8192 * 64 + 1], [700] * 64, [700] * 65,
+                                   [1] + [20000] * 20, [9000] * 20 + [1] * 24],
                          ids=lambda s: f"{len(s)}x{max(s)}")
 @pytest.mark.parametrize("shift", [0, 1])
 def test_norm(gg, sizes, g_bf16, shift):
