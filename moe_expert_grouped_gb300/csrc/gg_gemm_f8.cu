@@ -266,13 +266,6 @@ __device__ __forceinline__ int lane_here() {
   return lane;
 }
 
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(c0), "r"(c1)
-               : "memory");
-}
-
 // A warp's results on their way to memory: two buffers, filled in turn, each
 // written by one TMA store where all 32 rows belong to the expert. Stores of
 // the warp's own held it up behind those of all other SMs, which reach their
@@ -348,6 +341,28 @@ __device__ __forceinline__ void glu_grad(float acc, float w, float g, float u, f
   dg = (d * u) * (s * fmaf(ag, 1.0f - s, 1.0f));
   du = d * gs;
   dot = fmaf(acc, gs * u, dot);
+}
+
+// The same for two channels, in packed multiplications and additions, which
+// take half the issue slots (FIGP).
+__device__ __forceinline__ void glu_grad2(float2 acc, float2 w, float2 g, float2 u, float2 alpha,
+                                          float2 to_exp, float2& dg, float2& du, float2& dot) {
+  const float2 one = make_float2(1.0f, 1.0f);
+  const float2 t = __fmul2_rn(g, to_exp);  // exp(-alpha g) = 2^t
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = __fadd2_rn(e, one);
+  float2 s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
+  const float2 gs = __fmul2_rn(g, s);
+  const float2 d = __fmul2_rn(acc, w);
+  const float2 rest = __ffma2_rn(s, make_float2(-1.0f, -1.0f), one);
+  const float2 slope = __fmul2_rn(s, __ffma2_rn(__fmul2_rn(alpha, g), rest, one));
+  dg = __fmul2_rn(__fmul2_rn(d, u), slope);
+  du = __fmul2_rn(d, gs);
+  dot = __ffma2_rn(acc, __fmul2_rn(gs, u), dot);
 }
 
 __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
@@ -749,9 +764,8 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
         // Lane: token; registers: 128 channels of the CTA `group`, in four
         // chunks of 32; gated forward: 64 gate values, then their up values.
         if constexpr (MODE == kGradGated) {
-          // H1 of the first two chunks into the idle buffers, of the others
-          // into L2, while the products run: the epilogue read it from memory
-          // chunk by chunk, 13 us an item
+          // H1 of the first two chunks into the idle buffers while the products
+          // run: the epilogue read it from memory chunk by chunk, 13 us an item
           const int row = it.row0 + static_cast<int>(crank) * BM + q * 32;
           const int ch = it.nt * 2 * BM + group * BM;
           h1_chunks = row < it.row0 + it.rows ? max(0, min(kChunks, (p.width - ch) / 32)) : 0;
@@ -765,10 +779,6 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
                 const uint32_t to = smem_u32(staging) + c * (kWarpStaging / 2);
                 tma_load_2d(to, &maps.h1, bar, ch + 32 * c, row);
                 tma_load_2d(to + kWarpStaging / 4, &maps.h1, bar, p.F + ch + 32 * c, row);
-              }
-              for (int c = 2; c < h1_chunks; ++c) {
-                tma_prefetch_2d(&maps.h1, ch + 32 * c, row);
-                tma_prefetch_2d(&maps.h1, p.F + ch + 32 * c, row);
               }
             }
             h1_pending = true;
@@ -829,7 +839,10 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
           send_wide(box, &maps.out, acc[0], acc[1], p.C, p.width, row, ch, have, cols);
         } else if constexpr (MODE == kGradGated) {
           const float w = p.row_scale != nullptr && there ? __ldg(p.row_scale + row + lane) : 1.0f;
-          float dot = 0.0f;
+          float2 dot = make_float2(0.0f, 0.0f);
+          const float2 w2 = make_float2(w, w), alpha2 = make_float2(p.alpha, p.alpha);
+          const float x = -1.4426950408889634f * p.alpha;
+          const float2 to_exp = make_float2(x, x);
           const int ch0 = it.nt * 2 * BM + group * BM;
           const gg_bf16* h1 = p.H1 + static_cast<long long>(row) * (2LL * p.F) + ch0;
           if (h1_chunks > 0) {
@@ -874,12 +887,12 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
               for (int i = 0; i < 4; ++i) {
                 uint32_t& gw = (&g.x)[i];
                 uint32_t& uw = (&u.x)[i];
-                float g0, g1, u0, u1;
-                glu_grad(acc[c][8 * k + 2 * i], w, bf16_lo(gw), bf16_lo(uw), p.alpha, g0, u0, dot);
-                glu_grad(acc[c][8 * k + 2 * i + 1], w, bf16_hi(gw), bf16_hi(uw), p.alpha, g1, u1,
-                         dot);
-                gw = pack_bf16x2(g0, g1);
-                uw = pack_bf16x2(u0, u1);
+                float2 dg, du;
+                glu_grad2(make_float2(acc[c][8 * k + 2 * i], acc[c][8 * k + 2 * i + 1]), w2,
+                          make_float2(bf16_lo(gw), bf16_hi(gw)),
+                          make_float2(bf16_lo(uw), bf16_hi(uw)), alpha2, to_exp, dg, du, dot);
+                gw = pack_bf16x2(dg.x, dg.y);
+                uw = pack_bf16x2(du.x, du.y);
               }
               gs[own] = g;
               us[own] = u;
@@ -911,7 +924,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
           // the group's 128 channels are one block of the row sums
           if (p.rowdot != nullptr && there)
             p.rowdot[static_cast<long long>(row + lane) * p.rowdot_stride + 2 * it.nt + group] =
-                dot;
+                dot.x + dot.y;
         } else {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
