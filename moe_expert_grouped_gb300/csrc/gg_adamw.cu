@@ -23,6 +23,12 @@
 // hold and not a launch each. The list of tensors travels in the launch's
 // parameters: nothing is copied to the device ahead of it, and a captured
 // launch keeps its own.
+//
+// What bounds it: memory with 32-bit states (120 M elements, fp32 weights with
+// BF16 copies: 500 us, 6.2 TB/s; arrays that are not aligned 551), the issue of
+// instructions with 8-bit ones, some 110 an element for the two divisions, the
+// square root, the hash and the two codes (fp32 weights 405 us, BF16 ones 420, 79 %
+// of the issue slots; 480 and 456 unaligned).
 
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -538,7 +544,10 @@ __device__ __forceinline__ float load1(const void* from, long long at) {
     return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(from)[at]) << 16);
 }
 
-// Squares are added in fp32, 32 at a time, and those sums in 64 bits.
+// Squares are added in fp32, 32 at a time, and those sums in 64 bits. Bound by
+// memory: 604 M BF16 elements in 172 us, 7.0 TB/s; small lists by the two
+// launches' host time, 9 to 15 us (one launch of a cluster that adds everything up
+// was no faster from the host and slower on the device).
 template <int kCap, typename G>
 __global__ void __launch_bounds__(kThreads)
 norm_kernel(const __grid_constant__ NormList<kCap> list, int count, long long turns,

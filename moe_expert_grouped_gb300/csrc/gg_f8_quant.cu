@@ -7,9 +7,11 @@
 // Rows: one warp per source row, eight lanes per block (32 bytes each), the row
 // in registers up to 4096 columns so that all its loads are in flight together. The scales
 // of one block of columns lie together, S[ceil(K / 128)][R_cap]: the products'
-// tiles take a block of rows for one block of columns at a time.
+// tiles take a block of rows for one block of columns at a time. Bound by memory:
+// 131072 x 2048 in 134 us, 6.0 TB/s; 16384 tokens to their 8 rows each, 69 us.
 //
-// Weights: one block of 256 threads for each 128 x 128.
+// Weights: one block of 256 threads for each 128 x 128; 128 of 1536 x 2048 in
+// 165 us, 7.3 TB/s.
 
 #include <cuda_runtime.h>
 
