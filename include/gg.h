@@ -824,7 +824,8 @@ gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
  *
  * Rows outside [0, offsets[E]) are neither read into a result nor written.
  * Results are bitwise repeatable for the same offsets and sizes. N and K
- * multiples of 64, gated N of 128, E <= 1024; pointers 16-byte aligned but
+ * multiples of 64, gated N of 128, E <= 1024, no size (a gated gradient's 2K
+ * among them) within 512 of 2^31; pointers 16-byte aligned but
  * for scales, prob_of_row and offsets (4) and rowdot (32). Offsets that are
  * not a valid prefix sum set GG_ERR_DEVICE_BAD_OFFSETS and nothing is
  * computed. Workspace: gg_f8_workspace_size(R_cap, K) bytes for

@@ -1142,8 +1142,11 @@ static gg_status f8_gemm_checks(const void* A, const uint8_t* Wq, const float* W
   if (Wq == nullptr || Ws == nullptr || offsets == nullptr) return GG_ERR_INVALID_ARG;
   if (R_cap > 0 && (A == nullptr || C == nullptr)) return GG_ERR_INVALID_ARG;
   if (E > kMaxExperts || K % 64 != 0 || N % 64 != 0) return GG_ERR_UNSUPPORTED_SHAPE;
-  // work items and an expert's weight scales are counted in an int
-  if ((static_cast<long long>(R_cap) / 256 + E) * ((out + 127LL) / 128) > 0x3FFFFFFFLL ||
+  // rows and columns up to a tile behind the last, work items and an expert's
+  // weight scales are counted in an int
+  constexpr int kMost = 0x7FFFFFFF - 512;
+  if (R_cap > kMost || K > kMost || N > kMost ||
+      (static_cast<long long>(R_cap) / 256 + E) * ((out + 127LL) / 128) > 0x3FFFFFFFLL ||
       ((N + 127LL) / 128) * ((K + 127LL) / 128) > 0x3FFFFFFFLL)
     return GG_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(A) || !aligned16(Wq) || !aligned_to(Ws, 4) || !aligned16(C) ||
@@ -1241,6 +1244,7 @@ gg_status gg_f8_grouped_dgrad(const gg_bf16* dC, const uint8_t* Wq, const float*
   gg_status s = f8_gemm_checks(dC, Wq, Ws, offsets, E, R_cap, K, N, K, prob_of_row, dA);
   if (s != GG_OK) return s;
   if ((s = dgrad_epilogue_checks(epi, H1, rowdot)) != GG_OK) return s;
+  if (epi != GG_EPI_NONE && K > 0x3FFFFFFF - 512) return GG_ERR_UNSUPPORTED_SHAPE;  // 2K columns
   // the plain gradient has no place for a scale of its rows
   if (epi == GG_EPI_NONE && prob_of_row != nullptr) return GG_ERR_INVALID_ARG;
   if ((s = check_ws(ws, ws_bytes, gg_f8_workspace_size(R_cap, N))) != GG_OK) return s;
@@ -1276,7 +1280,7 @@ static gg_status f8_layer_checks(int T, int H, int F, int k, int E, int P,
   if (recompute) return GG_ERR_INVALID_ARG;
   if ((s = check_buffers(b, T, k, E)) != GG_OK) return s;
   const long long rc = r_cap_of(T, k, E, P);
-  if (F > 0x3FFFFFFF || rc > 0x7FFFFFFFLL) return GG_ERR_UNSUPPORTED_SHAPE;
+  if (F > 0x3FFFFFFF - 512 || rc > 0x7FFFFFFFLL) return GG_ERR_UNSUPPORTED_SHAPE;
   *R_cap = static_cast<int>(rc);
   const float* p = b->prob_of_row;
   if ((s = f8_gemm_checks(b->Xp, W1q, W1s, b->offsets, E, *R_cap, H, 2 * F, 2 * F, p, b->A)) !=

@@ -126,7 +126,9 @@ struct SmemTail {
   uint32_t tmem_base;
   int abort_flag;
   int total_tiles;
-  float dots[4][kFewTokens];  // row sums of each lane quadrant's 32 channels
+  // row sums of each lane quadrant's 32 channels, for a group's own tokens: which
+  // those are differs from item to item, and the groups are not at the same one
+  float dots[2][4][kFewTokens / 2];
   int tiles_before[kMaxExperts + 1];
   int row_start[kMaxExperts + 1];
 };
@@ -1084,7 +1086,7 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
               }
               dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
               dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
-              if ((at & 3) == 0) st.dots[q][t0 + i] = dot;
+              if ((at & 3) == 0) st.dots[group][q][32 * c + i] = dot;
             } else {
               if (there) *reinterpret_cast<uint4*>(p.C + r * p.width + ch) = pack8(v);
             }
@@ -1098,7 +1100,9 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
           if (!(ok = met())) break;
           const int i = 32 * mine0 + 32 * q + lane;
           if (q < mine && i < it.rows) {
-            const float sum = (st.dots[0][i] + st.dots[1][i]) + (st.dots[2][i] + st.dots[3][i]);
+            const auto& d = st.dots[group];
+            const int own = 32 * q + lane;
+            const float sum = (d[0][own] + d[1][own]) + (d[2][own] + d[3][own]);
             p.rowdot[(static_cast<long long>(it.row0) + i) * p.rowdot_stride + 2 * it.nt +
                      static_cast<int>(crank)] = sum;
           }

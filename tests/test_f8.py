@@ -115,14 +115,17 @@ class TestRefusals:
         (dict(epi=1, N=192), 2), (dict(A=4104), 3), (dict(Wq=8200), 3), (dict(Ws=16386), 3),
         (dict(C=65544), 3), (dict(epi=1, H1=4104), 3), (dict(epi=3, prob=4098), 3),
         (dict(off=32770), 3), (dict(ws=131076), 3), (dict(nbytes=256), 4),
-        (dict(R=0x7FFFFFFF, N=1 << 22, E=1024), 2)])
+        (dict(R=0x7FFFFFFF, N=1 << 22, E=1024), 2), (dict(R=0x7FFFFFFF - 100, N=64), 2),
+        (dict(N=0x7FFFFFFF - 127, K=64), 2), (dict(N=64, K=0x7FFFFFFF - 63), 2)])
     def test_forward(self, gg, kw, code):
         assert self._fwd(gg, **kw) == code
 
     @pytest.mark.parametrize("kw,code", [
         (dict(dC=None), 1), (dict(dA=None), 1), (dict(Wq=None), 1), (dict(epi=1), 1),
         (dict(epi=2), 1), (dict(H1=1 << 12), 1), (dict(dot=1 << 12), 1), (dict(prob=1 << 12), 1),
-        (dict(K=32), 2), (dict(N=65), 2), (dict(dC=4100), 3), (dict(dA=65540), 3),
+        (dict(K=32), 2), (dict(N=65), 2),
+        (dict(epi=2, H1=1 << 12, K=(1 << 30) - 64, N=64), 2), (dict(K=0x7FFFFFFF - 63, N=64), 2),
+        (dict(dC=4100), 3), (dict(dA=65540), 3),
         (dict(epi=2, H1=4100), 3), (dict(epi=2, H1=1 << 12, dot=4112), 3), (dict(nbytes=300), 4)])
     def test_gradient(self, gg, kw, code):
         assert self._grad(gg, **kw) == code

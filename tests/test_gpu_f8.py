@@ -368,6 +368,70 @@ def test_many_experts_and_items(gg):
     _near(_np(dA), y, _sum_tol(mag, N) + 2.0 ** -8 * np.abs(y), "dA")
 
 
+@pytest.mark.parametrize("N,K", [(64, 1024), (192, 3904), (128, 64)])
+def test_row_sums_of_items_side_by_side(gg, N, K):
+    """Items of different heights, one after the other: the two halves of a block's tokens are
+    summed by warps that need not be at the same item."""
+    counts = [100, 40, 128, 33, 65, 1, 97, 64] * 6
+    R = sum(counts)
+    d, H1, off = _rows(R, N, 46), _rows(R, 2 * K, 47, 0.7), _offsets(counts)
+    p = torch.rand(R, generator=torch.Generator().manual_seed(48)).cuda()
+    Wq, Ws = _weight(gg, len(counts), N, K, 49)
+    blocks, stride = gg.rowdot_blocks(K), gg.rowdot_stride(K)
+    got = []
+    for _ in range(10):
+        rowdot = torch.zeros((R, stride), device="cuda")
+        gg.f8_grouped_dgrad(d, Wq, Ws, off, 2, H1, p, rowdot=rowdot)
+        got.append(rowdot[:, :blocks])
+    assert all(torch.equal(g, got[0]) for g in got)
+    q, s = of.quantize_rows(d.float().cpu().numpy())
+    y, mag = of.product(q, s, _codes(Wq), Ws.cpu().numpy(), off.cpu().numpy(), grad=True)
+    act = np.abs(_np(H1)[:, :K]) * np.abs(_np(H1)[:, K:])
+    _, _, dot = of.glu_bwd(y, _np(H1)[:, :K], _np(H1)[:, K:])
+    tol = _sum_tol(mag, N) * act + (2 * _act_tol(_np(H1)[:, :K]) + K * U) * np.abs(y) * act
+    _near(_np(got[0]).sum(axis=1), dot.sum(axis=1), tol.sum(axis=1), "rowdot")
+
+
+@pytest.mark.parametrize("most", [2, 12, 300])
+def test_most_experts(gg, most):
+    """1024 experts, some empty: the few-row kernel and both of the other's orientations."""
+    r = np.random.default_rng(most)
+    counts = r.integers(0, most, 1024)
+    counts[[0, 1023]] = 0, most
+    R, N, K = int(counts.sum()), 128, 192
+    x, off = _rows(R, K, 40), _offsets(counts)
+    Wq, Ws = _weight(gg, 1024, N, K, 41)
+    C = gg.f8_grouped_fwd(x, Wq, Ws, off)
+    q, s = of.quantize_rows(x.float().cpu().numpy())
+    y, mag = of.product(q, s, _codes(Wq), Ws.cpu().numpy(), off.cpu().numpy())
+    _near(_np(C), y, _sum_tol(mag, K) + 2.0 ** -8 * np.abs(y), "C")
+    d = _rows(R, N, 42)
+    dA = gg.f8_grouped_dgrad(d, Wq, Ws, off)
+    q, s = of.quantize_rows(d.float().cpu().numpy())
+    y, mag = of.product(q, s, _codes(Wq), Ws.cpu().numpy(), off.cpu().numpy(), grad=True)
+    _near(_np(dA), y, _sum_tol(mag, N) + 2.0 ** -8 * np.abs(y), "dA")
+
+
+def test_two_streams_with_workspaces_of_their_own(gg):
+    """Two calls under way at once, each with its own workspace and result."""
+    counts = [700, 0, 300, 24]
+    R, N, K = sum(counts), 512, 1024
+    off, (Wq, Ws) = _offsets(counts), _weight(gg, 4, N, K, 43)
+    xs = [_rows(R, K, 44), _rows(R, K, 45)]
+    want = [gg.f8_grouped_fwd(x, Wq, Ws, off) for x in xs]
+    ws = [gg.f8_workspace(R, K, "cuda") for _ in xs]
+    got = [torch.zeros_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                gg.f8_grouped_fwd(xs[i], Wq, Ws, off, C=got[i], ws=ws[i])
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+
+
 def test_binding_refuses(gg):
     R, N, K = 10, 128, 64
     x, off = _rows(R, K, 29), _offsets([4, 6])
