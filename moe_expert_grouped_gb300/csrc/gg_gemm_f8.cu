@@ -976,35 +976,44 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
       for (int c = 0; c < kFewTokens / 64; ++c)
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
-      for (int kb = 0; kb < KB; ++kb) {
-        const float4* f = reinterpret_cast<const float4*>(scales_there() + half * BM + 32 * mine0);
-        if (!ok) break;
-        const uint32_t from = sums_there() + 32 * mine0;
-        if (!ok) break;
-        uint32_t v[kFewTokens / 64][32];
-        // columns that no token has too: loads under a condition made v live over
-        // the whole kernel, and spilled the other loop's sums
+      // a loop for each number of chunks: loads under a condition made v live
+      // over the whole kernel, and spilled the other loop's sums
+      const auto add_steps = [&](auto of) {
+        constexpr int kMine = decltype(of)::value;
+        for (int kb = 0; kb < KB; ++kb) {
+          const float4* f =
+              reinterpret_cast<const float4*>(scales_there() + half * BM + 32 * mine0);
+          if (!ok) break;
+          const uint32_t from = sums_there() + 32 * mine0;
+          if (!ok) break;
+          uint32_t v[kMine + 1][32];
 #pragma unroll
-        for (int c = 0; c < kFewTokens / 64; ++c) tmem_ld32_start(from + 32 * c, v[c]);
+          for (int c = 0; c < kMine; ++c) tmem_ld32_start(from + 32 * c, v[c]);
 #pragma unroll
-        for (int c = 0; c < kFewTokens / 64; ++c) tmem_wait(v[c]);
-        sums_read();
+          for (int c = 0; c < kMine; ++c) tmem_wait(v[c]);
+          sums_read();
 #pragma unroll
-        for (int c = 0; c < kFewTokens / 64; ++c) {
-          if (c >= mine) continue;
+          for (int c = 0; c < kMine; ++c) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 s = f[8 * c + i / 4];
-            float2* to = reinterpret_cast<float2*>(&acc[c][i]);
-            const uint32_t* x = &v[c][i];
-            to[0] = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                               make_float2(s.x, s.y), to[0]);
-            to[1] = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                               make_float2(s.z, s.w), to[1]);
+            for (int i = 0; i < 32; i += 4) {
+              const float4 s = f[8 * c + i / 4];
+              float2* to = reinterpret_cast<float2*>(&acc[c][i]);
+              const uint32_t* x = &v[c][i];
+              to[0] = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                 make_float2(s.x, s.y), to[0]);
+              to[1] = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                 make_float2(s.z, s.w), to[1]);
+            }
           }
+          scales_read();
         }
-        scales_read();
-      }
+      };
+      if (mine == 2)
+        add_steps(std::integral_constant<int, 2>{});
+      else if (mine == 1)
+        add_steps(std::integral_constant<int, 1>{});
+      else
+        add_steps(std::integral_constant<int, 0>{});
       if (!ok) break;
       box.drain();
       // Chunk by chunk through the warp's staging buffer, token i's 16-byte
