@@ -1205,8 +1205,8 @@ static cudaError_t f8_rows_to_ws(const gg_bf16* rows, int width, F8GemmArgs* a, 
                                  const int32_t* row_of_slot = nullptr) {
   const size_t blocks = (static_cast<size_t>(width) + 127) / 128;
   float* S = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsHeader);
-  uint8_t* Q =
-      reinterpret_cast<uint8_t*>(S) + align256(sizeof(float) * blocks * static_cast<size_t>(a->R_cap));
+  uint8_t* Q = reinterpret_cast<uint8_t*>(S) +
+               align256(sizeof(float) * blocks * static_cast<size_t>(a->R_cap));
   a->A = Q;
   a->As = S;
   const bool tokens = row_of_slot != nullptr;

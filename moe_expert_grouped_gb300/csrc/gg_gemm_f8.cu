@@ -28,8 +28,8 @@
 // One CTA per SM in clusters of two (one tcgen05 MMA pair, 384 threads per
 // CTA, warp-specialised):
 //   warp 0      TMA producer: per step of 128 its half of the channels (gated
-//               forward: the even CTA gate rows, the odd one up rows, or, few
-//               tokens, 64 of each) and half the tokens, 128-byte swizzle;
+//               forward: 64 gate rows and the matching up rows) and half the
+//               tokens, 128-byte swizzle;
 //   warp 1      allocates TMEM; in the even CTA one lane issues
 //               tcgen05.mma.cta_group::2.kind::f8f6f4 (M = 256, K = 32);
 //   warp 2      finds the work items ahead of the others;

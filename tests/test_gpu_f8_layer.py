@@ -252,8 +252,8 @@ def test_training_step_against_its_oracle(gg):
     assert abs(norm - total) <= 2.0 ** -20 * total
     for i, (w, g) in enumerate(zip(before, grads)):
         zero = np.zeros(g.size, np.float32)
-        new = oa.step(w.ravel(), g.ravel(), zero, zero.copy(), lr=float(np.float32(1e-2)), t=1, beta1=0.9,
-                      beta2=0.99, weight_decay=0.01, grad_scale=scale)
+        new = oa.step(w.ravel(), g.ravel(), zero, zero.copy(), lr=float(np.float32(1e-2)), t=1,
+                      beta1=0.9, beta2=0.99, weight_decay=0.01, grad_scale=scale)
         np.testing.assert_array_equal(own["master"][i].cpu().numpy().ravel(), new[0])
     for (q, s), W in zip(own["w"], own["half"]):
         want = gg.f8_prepare_weight(W)
