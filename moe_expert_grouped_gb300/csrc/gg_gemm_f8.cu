@@ -689,7 +689,8 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
 #pragma unroll
           for (int j = 0; j < BM / 32; ++j) {
             const int i = 32 * j + lane;
-            a.s[j] = own + i < it.rows ? __ldg(s + i) : 0.0f;
+            // plain loads: the quantiser writes while this kernel already runs
+            a.s[j] = own + i < it.rows ? s[i] : 0.0f;
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k)
