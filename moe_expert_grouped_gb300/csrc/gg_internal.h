@@ -59,7 +59,7 @@ cudaError_t launch_permute(const gg_bf16* x, const int32_t* idx, const float* pr
 // null); with has_padding, rows below offsets[E] whose slot_of_row is -1 are
 // zeroed. after_maps: the launch directly follows the kernel that writes the
 // row maps, so it may start before that kernel ends (it waits for its
-// results before its first access).
+// results before its first access; with prob it starts after it).
 cudaError_t launch_gather_rows(const gg_bf16* src, const int32_t* row_of_slot,
                                const int32_t* slot_of_row, const int32_t* offsets, int H, int k,
                                int E, int R_cap, int T, bool has_padding, const float* prob,

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256)
 quantize_scatter_kernel(const uint4* __restrict__ src, const int32_t* __restrict__ row_of_slot,
                         const int32_t* __restrict__ slot_of_row, bool has_padding,
                         const float* __restrict__ prob,
-                        const int32_t* __restrict__ offsets, const int32_t* __restrict__ tb,
+                        const int32_t* __restrict__ offsets, const int32_t* tb,
                         int T, int k, int K, int E, int R_cap, int sf_tiles_cap,
                         uint8_t* __restrict__ Q, uint8_t* __restrict__ S, int32_t* status) {
   const int lane = threadIdx.x & 31;

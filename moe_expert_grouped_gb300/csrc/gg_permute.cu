@@ -91,7 +91,7 @@ permute_count_kernel(const int32_t* __restrict__ idx, long long R, int E, long l
 __global__ void __launch_bounds__(kPermuteBlockThreads)
 permute_scatter_kernel(const int32_t* __restrict__ idx, const float* __restrict__ prob,
                        long long R, int E, int P, long long ppb, int nb,
-                       const int32_t* __restrict__ block_hist, int32_t* __restrict__ offsets,
+                       const int32_t* block_hist, int32_t* __restrict__ offsets,
                        int32_t* __restrict__ row_of_slot, int32_t* __restrict__ slot_of_row,
                        float* __restrict__ prob_of_row) {
   extern __shared__ int sm[];
@@ -224,9 +224,8 @@ permute_scatter_kernel(const int32_t* __restrict__ idx, const float* __restrict_
 // multiple of 8, the warps of 256-thread blocks) takes the units
 // u = (w % 8) * (nw / 8) + w / 8 + i * nw, i = 0, 1, ..., which puts
 // neighbouring units in different blocks and so spreads a run over the SMs.
-__device__ __forceinline__ void zero_pad_rows(const int32_t* __restrict__ slot_of_row,
-                                              const int32_t* __restrict__ offsets, int E,
-                                              int R_cap, int vec_per_row,
+__device__ __forceinline__ void zero_pad_rows(const int32_t* slot_of_row, const int32_t* offsets,
+                                              int E, int R_cap, int vec_per_row,
                                               uint4* __restrict__ dst, long long w,
                                               long long nw) {
   constexpr int kSlice = 64;
@@ -262,10 +261,9 @@ __device__ __forceinline__ void zero_pad_rows(const int32_t* __restrict__ slot_o
 // below offsets[E] (each warp after its tokens, so the copy and the zeroing
 // overlap instead of running back to back).
 __global__ void __launch_bounds__(256)
-scatter_rows_kernel(const uint4* __restrict__ src, const int32_t* __restrict__ row_of_slot,
-                    int T, int k, int vec_per_row, int R_cap, uint4* __restrict__ dst,
-                    int32_t* status, const int32_t* __restrict__ pad_slot_of_row,
-                    const int32_t* __restrict__ offsets, int E) {
+scatter_rows_kernel(const uint4* __restrict__ src, const int32_t* row_of_slot, int T, int k,
+                    int vec_per_row, int R_cap, uint4* __restrict__ dst, int32_t* status,
+                    const int32_t* pad_slot_of_row, const int32_t* offsets, int E) {
   const int lane = threadIdx.x & 31;
   const long long warp0 = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
@@ -314,7 +312,6 @@ scatter_rows_scaled_kernel(const uint4* __restrict__ src, const int32_t* __restr
   const int lane = threadIdx.x & 31;
   const long long warp0 = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
-  grid_dependency_wait();  // the row maps, when launched behind their writer
   for (long long t = warp0; t < T; t += nwarps) {
     int my_row = -1;
     float my_p = 0.0f;
@@ -796,12 +793,9 @@ cudaError_t launch_gather_rows(const gg_bf16* src, const int32_t* row_of_slot,
   uint4* d4 = reinterpret_cast<uint4*>(dst);
   const dim3 grid(static_cast<unsigned>(blocks)), block(256);
   cudaError_t err;
-  if (after_maps) {
-    err = prob != nullptr
-              ? launch_early(scatter_rows_scaled_kernel, grid, block, 0, stream, s4, row_of_slot,
-                             prob, T, k, vec, R_cap, d4, status, pad_sor, offsets, E)
-              : launch_early(scatter_rows_kernel, grid, block, 0, stream, s4, row_of_slot, T, k,
-                             vec, R_cap, d4, status, pad_sor, offsets, E);
+  if (after_maps && prob == nullptr) {
+    err = launch_early(scatter_rows_kernel, grid, block, 0, stream, s4, row_of_slot, T, k, vec,
+                       R_cap, d4, status, pad_sor, offsets, E);
   } else {
     if (prob != nullptr)
       scatter_rows_scaled_kernel<<<grid, block, 0, stream>>>(s4, row_of_slot, prob, T, k, vec,

@@ -49,7 +49,9 @@ __device__ __forceinline__ bool elect_one() {
 // the kernel ahead of it in the stream is still running. grid_dependency_wait
 // returns once that kernel has completed and its writes are visible (at once
 // without such a predecessor); grid_dependents_launch lets the next kernel's
-// blocks be scheduled before this one ends.
+// blocks be scheduled before this one ends. What the kernel ahead writes is not
+// constant for this one's lifetime: no __ldg of it, and no pointer to const
+// that is __restrict__, which may become the same load.
 
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

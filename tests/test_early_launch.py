@@ -14,12 +14,16 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 
 # kernel, and the names by which it reads what the kernel ahead of it writes
 READ = [
+    ("gg_permute.cu", "permute_scatter_kernel", ["block_hist"]),
+    ("gg_permute.cu", "scatter_rows_kernel", ["row_of_slot", "pad_slot_of_row", "offsets"]),
+    ("gg_mx_quant.cu", "quantize_scatter_kernel", ["tb"]),
+    ("gg_route.cu", "route_finalise_kernel", ["part_p", "part_n", "part_z"]),
     ("gg_gemm_f8.cu", "f8_gemm_kernel", ["s"]),
     ("gg_adamw.cu", "norm_join_kernel", ["partial"]),
 ]
 
 
-def _kernel(path, name):
+def _text(path, name):
     with open(os.path.join(CSRC, path)) as f:
         src = re.sub(r"//[^\n]*", "", f.read())
     start = re.search(name + r"\s*\(\s*const", src).start()
@@ -29,7 +33,7 @@ def _kernel(path, name):
 
 @pytest.mark.parametrize("path,name,read", READ, ids=[n for _, n, _ in READ])
 def test_what_the_kernel_ahead_writes_is_not_read_as_constant(path, name, read):
-    text = _kernel(path, name)
+    text = _text(path, name)
     assert "grid_dependency_wait()" in text
     for pointer in read:
         assert re.search(r"\b%s\b" % pointer, text)
