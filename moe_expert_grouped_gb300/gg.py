@@ -9,6 +9,7 @@ is no CPU fallback.
 
 from __future__ import annotations
 
+import bisect
 import contextlib
 import ctypes
 import os
@@ -1119,6 +1120,11 @@ def _guard(device: torch.device):
     return contextlib.nullcontext() if here else torch.cuda.device(device)
 
 
+def _span(t):
+    """A contiguous tensor's first byte and the one behind its last."""
+    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+
 def _alike(tensors, name: str, dtype=None, numels=None):
     """Checks a list of contiguous CUDA tensors of one type and device."""
     tensors = list(tensors)
@@ -1245,19 +1251,24 @@ class AdamW:
                                   w_dtype=_dtype(self.weights[0], "weights[0]"),
                                   state_bits=state_bits)
         self.t = 0  # steps taken
-        self.set_grads(grads)
-        written = [t for x in (self.weights, self.m, self.v, self.m_scale, self.v_scale,
-                               self.half) if x is not None for t in x if t.numel()]
-        ends = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-                      for t in written)
-        if any(a[1] > b[0] for a, b in zip(ends, ends[1:])):
+        # where the steps write, in order
+        self._written = sorted(
+            _span(t) for x in (self.weights, self.m, self.v, self.m_scale, self.v_scale, self.half)
+            if x is not None for t in x if t.numel())
+        if any(a[1] > b[0] for a, b in zip(self._written, self._written[1:])):
             raise ValueError("weights, states and copies may not overlap")
+        self.set_grads(grads)
 
     def set_grads(self, grads) -> None:
         """The gradients that the steps from now on read."""
         grads = _alike(grads, "grads", None, self._numels)
         if grads[0].device != self.device:
             raise ValueError(f"grads: on {grads[0].device}, the weights on {self.device}")
+        for i, t in enumerate(grads):
+            lo, hi = _span(t)
+            before = bisect.bisect_left(self._written, (hi,)) - 1  # the last that starts below hi
+            if lo < hi and before >= 0 and self._written[before][1] > lo:
+                raise ValueError(f"grads[{i}]: overlaps a weight, a state or a copy")
         self.opt.g_dtype = _dtype(grads[0], "grads[0]")
         self.grads = grads
         for row, t in zip(self.table, grads):

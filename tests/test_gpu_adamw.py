@@ -371,3 +371,34 @@ def test_binding_refuses(gg):
         gg.GradPlan([])
     with pytest.raises(TypeError):
         gg.grad_norm([f, h])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_gradients_that_a_step_would_overwrite_are_refused(gg, bits):
+    n, cells = 600, 3
+    flat = torch.zeros(4 * n, device="cuda")
+    w, g = flat[n:2 * n], flat[2 * n:3 * n]  # neighbours do not overlap
+    half = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    opt = gg.AdamW([w, flat[:0]], [g, flat[:0]], half=[half, half[:0]], state_bits=bits)
+    opt.set_grads([flat[:n], w[:0]])
+    opt.set_grads([g, g[:0]])
+    parts = [w, flat[n + 1:2 * n + 1], flat[1:n + 1], flat[2 * n - 1:3 * n - 1]]
+    if bits == 32:
+        parts += [opt.m[0], opt.v[0]]
+    for x in parts:
+        with pytest.raises(ValueError):
+            opt.set_grads([x, x[:0]])
+        assert opt.grads[0] is g and opt.table[0].g == g.data_ptr()
+        with pytest.raises(ValueError):
+            gg.AdamW([w], [x], **({} if bits == 8 else dict(m=[opt.m[0]], v=[opt.v[0]])))
+    with pytest.raises(ValueError):
+        opt.set_grads([half, half[:0]])
+    if bits == 8:
+        small = gg.AdamW([flat[:cells]], [g[:cells]], m=[opt.m[0][:cells]], v=[opt.v[0][:cells]],
+                         m_scale=[opt.m_scale[0][:1]], v_scale=[opt.v_scale[0][:1]])
+        with pytest.raises(ValueError):  # a gradient that begins with a cell's scale
+            small.set_grads([opt.m_scale[0][:cells]])
+    two = gg.AdamW([w, flat[:n]], [g, g], state_bits=bits)  # a gradient may serve two weights
+    g.fill_(1.0)
+    two.step(lr=0.5)
+    assert torch.equal(w, flat[:n]) and float(w[0]) < 0
