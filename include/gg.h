@@ -945,9 +945,10 @@ gg_status gg_adamw_step(const gg_adamw_tensor* tensors, int n, const gg_adamw_op
  *   out[0] = sqrt(sum over all tensors and elements of g^2)
  *   out[1] = min(1, max_norm / (out[0] + 1e-6)), 1 for max_norm <= 0, NaN
  *            when out[0] is NaN or infinite
- * out: two floats on the device. Squares are taken in fp32 (beyond 1.8e19
- * they are infinite), added up 32 at a time in fp32 and from there on in 64
- * bits, in an order that depends on the sizes alone. g fp32 or BF16 (a
+ * out: two floats on the device. Squares are taken in fp32 (of elements
+ * beyond 1.8e19 they are infinite, of those below 2.6e-23 zero), added up 32 at
+ * a time in fp32 and from there on in 64 bits, in an order that depends on the
+ * sizes and on the device's number of SMs alone. g fp32 or BF16 (a
  * gg_dtype) at its type's alignment (faster: 16 bytes). `tensors` is host
  * memory; n = 0 gives out = {0, 1}. Workspace: gg_grad_norm_workspace_size(n)
  * bytes; overlapping calls need one each.

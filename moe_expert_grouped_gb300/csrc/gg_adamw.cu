@@ -582,11 +582,16 @@ norm_kernel(const __grid_constant__ NormList<kCap> list, int count, long long tu
         }
       }
     } else {
-#pragma unroll 8
-      for (int i = 0; i < kNormEach; ++i) {
-        const long long e = e0 + i * kThreads + threadIdx.x;
-        const float x = e < t.n ? load1<G>(t.g, e) : 0.0f;
-        s = fmaf(x, x, s);
+      // a thread's elements, and their order, as above: the same sum wherever
+      // the array starts
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const long long e = e0 + (i * kThreads + threadIdx.x) * kVec;
+        float x[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) x[j] = e + j < t.n ? load1<G>(t.g, e + j) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) s = fmaf(x[j], x[j], s);
       }
     }
     sum += s;

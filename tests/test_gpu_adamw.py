@@ -402,3 +402,31 @@ def test_gradients_that_a_step_would_overwrite_are_refused(gg, bits):
     g.fill_(1.0)
     two.step(lr=0.5)
     assert torch.equal(w, flat[:n]) and float(w[0]) < 0
+
+
+@pytest.mark.parametrize("g_bf16", [False, True])
+def test_norm_bits_do_not_depend_on_where_an_array_starts(gg, g_bf16):
+    dtype = torch.bfloat16 if g_bf16 else torch.float32
+    run = 8 if g_bf16 else 4  # elements of a 16-byte load
+
+    def norms(x):
+        got = []
+        for shift in (0, 1, run - 1):
+            at = torch.zeros(x.numel() + shift, dtype=dtype, device="cuda")[shift:]
+            at.copy_(x)
+            got.append(gg.grad_norm([at], 1.0))
+        return got
+
+    # a 1 and 31 squares of 2^-26 in one thread's sum, where each of them is rounded away; apart
+    # from the 1 they add up to two units of the last place of the result
+    x = torch.zeros(8192, dtype=dtype, device="cuda")
+    for i in range(32 // run):
+        x[256 * run * i:256 * run * i + run] = 2.0 ** -13
+    x[0] = 1.0
+    a, *others = norms(x)
+    assert a[0].item() == 1.0 and all(torch.equal(a, b) for b in others)
+    r = np.random.default_rng(21)
+    for n in [int(v) for v in r.integers(1, 60000, 40)] + [8192 * i for i in (1, 2, 7)] * 10:
+        x = torch.from_numpy(r.normal(size=n).astype(np.float32)).to(dtype).cuda()
+        a, *others = norms(x)
+        assert all(torch.equal(a, b) for b in others), n
