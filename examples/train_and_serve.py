@@ -40,7 +40,8 @@ def experts(g, scale):
 
 
 def train(tokens: int, steps: int, seed: int = 0, log=print, f8: bool = False):
-    """Returns dict(first, last, W1, W2, R, x, route, out): losses and the trained layer."""
+    """Returns dict(first, last, W1, W2, R, x, route, out, grads): losses, the trained layer, its
+    outputs (with f8 those on the codes of W1 and W2) and the last step's gradients."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     x = torch.randn(tokens, H, generator=g, device="cuda").bfloat16()
     t1, t2 = experts(g, 1.5)
@@ -81,13 +82,13 @@ def train(tokens: int, steps: int, seed: int = 0, log=print, f8: bool = False):
     if student.status() != 0:
         raise RuntimeError(gg.status_string(student.status()))
     r = gg.route(x.float() @ R, K, renormalize=True)
-    out = layer.forward(x, r["idx"], r["prob"], W1, W2)
+    out = student.forward(x, r["idx"], r["prob"], w1, w2)
     return dict(first=losses[0].item(), last=losses[-1].item(), W1=W1, W2=W2, R=R,
-                x=x, route=r, out=out)
+                x=x, route=r, out=out, grads=grads)
 
 
 def serve(trained, log=print):
-    """Returns the relative distance of the 8-bit layer's outputs from the BF16 layer's, for the
+    """Returns the relative distance of the 8-bit layer's outputs from the trained layer's, for the
     whole batch and for its first token alone."""
     W1, W2 = gg.q8_prepare_weight(trained["W1"]), gg.q8_prepare_weight(trained["W2"])
     x, r, ref = trained["x"], trained["route"], trained["out"].float()
@@ -97,7 +98,7 @@ def serve(trained, log=print):
     if layer.status() != 0:
         raise RuntimeError(gg.status_string(layer.status()))
     off = (float((out - ref).norm() / ref.norm()), float((one - ref[:1]).norm() / ref[:1].norm()))
-    log(f"8-bit outputs against BF16: {off[0]:.4f} (batch), {off[1]:.4f} (one token)")
+    log(f"8-bit outputs against the trained layer's: {off[0]:.4f} (batch), {off[1]:.4f} (one token)")
     return off
 
 

@@ -270,3 +270,32 @@ def test_example_trains_on_codes(gg):
     t = ex.train(256, 3, f8=True, log=lambda *_: None)
     for w in (t["W1"], t["W2"], t["R"], t["out"]):
         assert torch.isfinite(w.float()).all()
+
+
+def test_example_on_codes_takes_its_steps_on_them(gg):
+    """A step whose gradients are not finite is skipped and leaves the weights finite, so: the loss
+    is finite, every step moves the weights, and what is returned comes from the codes. The first
+    step's expert gradients stand beside those of BF16 at the same weights, three products down the
+    chain and behind a difference (outputs less the teacher's, which are independent of them, so that
+    it is no smaller than the outputs): 0.21 as above."""
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    try:
+        import train_and_serve as ex
+    finally:
+        sys.path.pop(0)
+    runs = [ex.train(256, n, f8=True, log=lambda *_: None) for n in (1, 2, 3)]
+    for t in runs:
+        assert np.isfinite([t["first"], t["last"]]).all()
+    assert runs[0]["first"] == runs[1]["first"] == runs[2]["first"]
+    assert len({t["last"] for t in runs}) == 3
+    for a, b in zip(runs, runs[1:]):
+        for w in ("W1", "W2", "R"):
+            assert float((a[w] != b[w]).float().mean()) > 0.2
+    t = runs[2]
+    layer = gg.F8MoeLayer(256, ex.H, ex.F, ex.K, ex.E)
+    want = layer.forward(t["x"], t["route"]["idx"], t["route"]["prob"],
+                         gg.f8_prepare_weight(t["W1"]), gg.f8_prepare_weight(t["W2"]))
+    assert torch.equal(t["out"], want)
+    bf16 = ex.train(256, 1, log=lambda *_: None)
+    for got, ref in zip(runs[0]["grads"][:2], bf16["grads"][:2]):
+        assert float((got - ref).norm() / ref.norm()) < 0.21
