@@ -1103,8 +1103,8 @@ gg_status gg_f8_prepare_weight(const gg_bf16* W, int E, int N, int K, uint8_t* W
                                gg_stream_t stream) {
   if (E <= 0 || N <= 0 || K <= 0) return GG_ERR_INVALID_ARG;
   if (W == nullptr || Wq == nullptr || Ws == nullptr) return GG_ERR_INVALID_ARG;
-  // blocks of rows are counted in a grid dimension of 16 bits
-  if (E > kMaxExperts || N % 64 != 0 || K % 64 != 0 || N > 65535 * 128)
+  // blocks of rows are counted in a grid dimension of 16 bits, columns in an int
+  if (E > kMaxExperts || N % 64 != 0 || K % 64 != 0 || N > 65535 * 128 || K > 0x7FFFFFFF - 512)
     return GG_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(W) || !aligned16(Wq) || !aligned_to(Ws, 4)) return GG_ERR_MISALIGNED;
   DeviceInfo dev;

@@ -160,6 +160,11 @@ class TestRefusals:
         assert rows(ws=None) == rows(T=-1) == 1
         assert rows(K=72) == 2 and rows(S=a + 2) == 3 and rows(nbytes=8) == 4
 
+    def test_weights_too_wide_to_count(self, gg):
+        a = 1 << 12
+        for K in (0x7FFFFFFF - 63, 0x7FFFFFFF - 511):
+            assert gg.LIB.gg_f8_prepare_weight(a, 1, 64, K, a, a, None) == 2
+
     def _layer(self, gg, backward=False, opt=(0, 0, 0), T=20, H=128, F=64, k=2, E=4, P=1, null=None,
                buf=None, nbytes=None, **kw):
         L, a = gg.LIB, 1 << 12
