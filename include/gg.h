@@ -823,7 +823,11 @@ gg_status gg_moe_mlp_wgrad(int T, int H, int F, int k, int E, int pad_multiple,
  * takes no prob_of_row.
  *
  * Rows outside [0, offsets[E]) are neither read into a result nor written.
- * Results are bitwise repeatable for the same offsets and sizes. N and K
+ * Results are bitwise repeatable for the same offsets and sizes. Unlike those of
+ * gg_grouped_fwd they are not batch invariant: with other rows beside it a row
+ * can be summed in another order, or take its activation by another formula,
+ * and differ in the last bits (few rows per expert, by R_cap and E, and an
+ * expert's last 128 rows or fewer have kernels and loops of their own). N and K
  * multiples of 64, gated N of 128, E <= 1024, no size (a gated gradient's 2K
  * among them) within 512 of 2^31; pointers 16-byte aligned but
  * for scales, prob_of_row and offsets (4) and rowdot (32). Offsets that are
@@ -900,7 +904,9 @@ gg_status gg_moe_mlp_bwd_f8(const gg_bf16* dOut, const gg_bf16* x, const float* 
  * weights) is rounded stochastically: up with the probability of the part cut
  * off, to within 2^-16 of a step, by bits that depend on (seed, step, the
  * tensor's place in the list, the element) alone; equal inputs give equal
- * bits. A positive sqrt(v) keeps at least the smallest code.
+ * bits. Every rounding by itself is unbiased, but elements of different cells
+ * can share their bits: of 400 M elements about one cell in six has some in common
+ * with another. A positive sqrt(v) keeps at least the smallest code.
  * grad_scale, lr_dev and step_dev (nullable, device) are read when the step
  * runs: a captured step follows their values, which take the place of lr and
  * step. A grad_scale that is NaN or infinite skips the step: nothing is

@@ -14,7 +14,9 @@
 // rounding to nearest would leave it where it is. So what is kept from one
 // step to the next in fewer than 32 bits, the states and BF16 weights, is
 // rounded up with the probability of the part cut off, by bits of a hash
-// (Wellons' two-multiplication mixer) of seed, step, tensor and element. A
+// (Wellons' two-multiplication mixer) of seed, step, tensor and element: 256 hashes
+// of neighbouring numbers from a cell's key on. In a large list two cells' keys
+// can lie closer than that, and then share words; each rounding stays unbiased. A
 // sqrt(v') above 0 keeps at least the smallest code: as 0 it would divide m'
 // by eps alone.
 //
@@ -24,11 +26,12 @@
 // parameters: nothing is copied to the device ahead of it, and a captured
 // launch keeps its own.
 //
-// What bounds it: memory with 32-bit states (120 M elements, fp32 weights with
-// BF16 copies: 500 us, 6.2 TB/s; arrays that are not aligned 551), the issue of
-// instructions with 8-bit ones, some 110 an element for the two divisions, the
-// square root, the hash and the two codes (fp32 weights 405 us, BF16 ones 420, 79 %
-// of the issue slots; 480 and 456 unaligned).
+// What bounds it: memory with 32-bit states (120 M elements, fp32 weights, BF16
+// gradients: 500 us, with BF16 copies 536, 6.2 TB/s; no array aligned 584 and
+// 630), the issue of instructions with 8-bit ones, some 110 an element: a
+// division and a square root, both rounded to nearest, the hash, two codes (their
+// cells' two reciprocals serve eight elements of a lane). fp32 weights 404 us,
+// BF16 ones 420, 79 % of the issue slots; no array aligned 485 and 456.
 
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -179,7 +182,8 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 // How a cell is read and written: four neighbours of a lane at once or one by
 // one (arrays that are not aligned), or those below its end (a tensor's last
 // cell). One by one, a lane's neighbours are still the better ones: 552 us where
-// an element of every 32 took 625 (120 M elements, fp32 states, unaligned).
+// an element of every 32 took 625 (120 M elements, fp32 states, weights and
+// gradients unaligned).
 enum Way : int { kWide = 0, kSingle = 1, kPartial = 2 };
 
 __device__ __forceinline__ int place(int i, int lane) {
@@ -545,9 +549,11 @@ __device__ __forceinline__ float load1(const void* from, long long at) {
 }
 
 // Squares are added in fp32, 32 at a time, and those sums in 64 bits. Bound by
-// memory: 604 M BF16 elements in 172 us, 7.0 TB/s; small lists by the two
-// launches' host time, 9 to 15 us (one launch of a cluster that adds everything up
-// was no faster from the host and slower on the device).
+// memory: 604 M BF16 elements in 172 us, 7.0 TB/s (200 M: 60 us, not 16-byte
+// aligned 105; fp32 115 and 124); small lists by the two launches, 9 to 16 us from
+// the host (60 odd tensors, 3 M elements: 9.5 us of it on the device). One launch of
+// a cluster that adds everything up was no faster from the host and slower on the
+// device.
 template <int kCap, typename G>
 __global__ void __launch_bounds__(kThreads)
 norm_kernel(const __grid_constant__ NormList<kCap> list, int count, long long turns,

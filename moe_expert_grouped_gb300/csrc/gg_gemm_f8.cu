@@ -47,9 +47,9 @@
 // wake-up, two TMEM loads and 128 additions a thread, release, wake-up. TMEM
 // holds no third buffer of 256 columns, and 128-column MMAs read shared memory
 // at its limit. 131072 rows, 128 experts, 1536 x 2048: 397 us forward (2080
-// TFLOP/s), 462 gated with H1 kept, 400 input gradient; one expert, 65536 rows,
-// 4096 x 4096: 2550 TFLOP/s. Gated gradient, 131072 rows, 2048 x 768: 339 us,
-// 1 GB of H1 and its gradient among them.
+// TFLOP/s), 463 gated with H1 kept, 400 input gradient; one expert, 65536 rows,
+// 4096 x 4096: 2550 TFLOP/s. Gated gradient, 131072 rows, 2048 x 768: 340 us,
+// 0.8 GB of H1 and its gradient among them.
 //
 // Every wait is bounded (gg_ptx.cuh); a wait that runs out records
 // GG_ERR_DEVICE_TIMEOUT, raises a CTA-wide abort flag, and the CTA drains
@@ -680,7 +680,8 @@ f8_gemm_kernel(const __grid_constant__ F8Maps maps, const F8Params p) {
           else
             n = kGated ? (k >> 1) * p.F + it.nt * BM + (k & 1) * (BM / 2)
                        : it.nt * 2 * BM + k * (BM / 2);
-          // channels that do not exist have a tile of zeros: any scale will do
+          // channels that do not exist are zeros in the tile, or past F another
+          // half's, and are not stored: any scale will do
           ts[k] = t + static_cast<long long>(min(n, most) / kF8Block) * p.t_chan;
         }
         const auto load = [&](int kb, Ahead& a) {
